@@ -257,6 +257,104 @@ tpmlp_status tpmlp_swiglu_pack(void* G, void* U, void* W_sh, int64_t rows, int64
                                int inverse, void* stream);
 
 /*
+ * MXFP4 operands (OCP Microscaling Formats v1.0; the pages have no counterpart, they name
+ * FP8 kernels as the step beyond bf16: Level 2, M040): 4-bit E2M1 values 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives, in blocks of 32 along the contraction that share one power of two:
+ *   e = clamp(floor(log2(max |x|)) - 2, -127, 125),
+ *   value = 2^e * round_to_nearest_even(x / 2^e), at most 6 * 2^e.
+ * A block with an infinity or a NaN gets the NaN scale, and so does what it is multiplied into.
+ * An operand [rows, K] is two arrays:
+ *   codes   [rows][ceil(K/32) * 16] bytes, the value of even k in the low half of a byte (bit 3 of
+ *           a half byte is the sign), zero past K;
+ *   scales  bytes e + 127 (255 = NaN), in tiles of 128 rows x 4 blocks of 512 bytes,
+ *           [ceil(rows/128)][ceil(K/128)]; in a tile, row r and block j at (r % 32) * 16 + (r / 32) * 4 + j.
+ *           Blocks past K must not hold 255 (the quantiser writes 0); rows past the last are not used.
+ * tpmlp_mxfp4_code_bytes / _scale_bytes give the sizes (-1 for a bad shape).
+ */
+int64_t tpmlp_mxfp4_code_bytes(int64_t rows, int64_t k);
+int64_t tpmlp_mxfp4_scale_bytes(int64_t rows, int64_t k);
+
+/*
+ * Quantises X, reading it once, along its columns, its rows, or both:
+ *   X   [p][rows][cols/p] dt (bf16 or fp32), row pitch ldx elements: column shards, or with p = 1 an
+ *       ordinary matrix; logically [rows, cols]
+ *   Q, S    operand [rows, cols]  (blocks of 32 columns), or both NULL
+ *   Qt, St  operand [cols, rows]  (blocks of 32 rows), or both NULL
+ * A weight shard A_sh [p][h][f] gives the operand of X A as (Qt, St) [p f, h] and that of dH A^T as
+ * (Q, S) [h, p f].  Requires cols % p == 0, for p > 1 cols/p a multiple of 32, ldx >= cols/p and ldx a
+ * multiple of 16 bytes.
+ */
+tpmlp_status tpmlp_mxfp4_quantize(const void* X, void* Q, void* S, void* Qt, void* St, int64_t rows, int64_t cols,
+                                  int64_t ldx, int p, tpmlp_dtype dt, void* stream);
+
+/* The values of an operand: out [rows, k] dt.  Exact, in bf16 too (below 2^128). */
+tpmlp_status tpmlp_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, tpmlp_dtype dt,
+                                    void* stream);
+
+/*
+ * Product of MXFP4 operands, accumulated in fp32:
+ *   D[m, n] = sum_k A[m, k] B[n, k] + bias[n]
+ *   A = (Aq, As) [m, k], B = (Bq, Bs) [n, k], bias [n] bf16 or NULL, D [m, n] out_dt.
+ * n must be a multiple of 8 (bf16 D) or 4 (fp32 D).  fp32 D without a bias is a rank's partial sum
+ * (tpmlp_sum_finish).
+ */
+tpmlp_status tpmlp_mxfp4_matmul(const void* Aq, const void* As, const void* Bq, const void* Bs, const void* bias, void* D,
+                                int64_t m, int64_t n, int64_t k, tpmlp_dtype out_dt, void* stream);
+
+/*
+ * The SwiGLU block (tpmlp_swiglu_mlp_fwd) on MXFP4 operands, Q(.) = quantised along the contraction:
+ *   [G | U] = Q(X) W + bw,   Y = silu(G) U,   Z = Q(Y) B + b2,
+ * as three launches: Q(X); one kernel for both projections, the activation, their product and Q(Y)
+ * (from fp32, Y itself is not stored); the row product with all shards in its K loop.
+ *   X [M, h] bf16
+ *   W = (Wq, Ws), operand [2 ffn, h]: W_sh [p][h][2 ffn/p] (tpmlp_swiglu_pack) quantised along its rows
+ *       (tpmlp_mxfp4_quantize(W_sh, NULL, NULL, Wq, Ws, h, 2 ffn, 2 ffn/p, p, ...))
+ *   B = (Bq, Bs), operand [h, ffn]: B_sh, the bytes of B [ffn, h], quantised along its rows
+ *   bw_sh [p][2 ffn/p] packed and b2 [h], bf16, or NULL;  Z [M, h] z_dt
+ *   H [M][2 ffn] bf16 or NULL: the packed pre-activations for the backward (bf16: the 4-bit operands'
+ *       own rounding is some thirty times coarser)
+ *   ws: tpmlp_mxfp4_swiglu_ws_bytes(s, b, h, ffn, p, 0) bytes.
+ * Shards are multiples of 128 features, so that no block spans two and results do not depend on p.
+ * Requires ffn % p == 0, h % p == 0, ffn/p a multiple of 128 and h a multiple of 8.
+ */
+tpmlp_status tpmlp_mxfp4_swiglu_mlp_fwd(const void* X, const void* Wq, const void* Ws, const void* bw_sh, const void* Bq,
+                                        const void* Bs, const void* b2, void* Z, void* H, void* ws, int64_t s, int64_t b,
+                                        int64_t h, int64_t ffn, int p, tpmlp_dtype z_dt, void* stream);
+
+/*
+ * Its backward from dZ, every product on MXFP4 operands quantised along its own contraction
+ * (Q_h, Q_f, Q_m: along h, the packed 2 ffn, the tokens) and the rounding taken as the identity:
+ *   dY = Q_h(dZ) Q_h(B)^T,  dG = dY U silu'(G),  dU = dY silu(G),  Y = silu(G) U   (fp32, G and U from H)
+ *   dB = Q_m(Y)^T Q_m(dZ),  dW = Q_m(X)^T Q_m([dG | dU]),  dX = Q_f([dG | dU]) Q_f(W)^T
+ *   dbw = 1^T [dG | dU] (before quantisation),  db2 = 1^T dZ
+ * One kernel computes dY and, from its fp32 accumulators, quantises dG and dU along both axes and Y
+ * along the tokens; none of them is stored in another form.
+ *   X [M, h], dZ [M, h], H (from the forward) bf16
+ *   W = (Wq, Ws), operand [h, 2 ffn]: W_sh quantised along its columns
+ *   B = (Bq, Bs), operand [ffn, h]: B quantised along its columns
+ *   dX [M, h] dx_dt;  dW_sh [p][h][2 ffn/p], dB_sh [p][ffn/p][h], dbw_sh [p][2 ffn/p] (or NULL),
+ *   db2 [h] (or NULL) grad_dt
+ *   ws: tpmlp_mxfp4_swiglu_ws_bytes(s, b, h, ffn, p, 1) bytes.
+ * Requirements as for the forward.
+ */
+tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const void* Ws, const void* Bq, const void* Bs,
+                                        const void* H, const void* dZ, void* dX, void* dW_sh, void* dB_sh, void* dbw_sh,
+                                        void* db2, void* ws, int64_t s, int64_t b, int64_t h, int64_t ffn, int p,
+                                        tpmlp_dtype dx_dt, tpmlp_dtype grad_dt, void* stream);
+
+/* Workspace of the two calls above, in bytes (-1 for a bad shape). */
+int64_t tpmlp_mxfp4_swiglu_ws_bytes(int64_t s, int64_t b, int64_t h, int64_t ffn, int p, int backward);
+
+/*
+ * Tiling of the MXFP4 products, process wide, for tuning and tests: 0 = automatic (default), 1 = single
+ * CTAs (128x128 tiles), 2 = CTA pairs (256x256), 3, 4, 5 = single CTAs with the K loop split 2, 4, 8 ways
+ * (fewer where K is too short or the exchange of the partial sums does not fit).  Results agree within
+ * fp32 rounding.  TPMLP_ERR_SHAPE for other values.
+ */
+tpmlp_status tpmlp_set_mxfp4_mode(int mode);
+int tpmlp_get_mxfp4_mode(void);
+
+/*
  * The MLP block forward without a caller workspace.  The pages have no
  * counterpart: this entry point exists for callers that cannot allocate device
  * memory where they run the block (for example an inference-engine plugin whose

@@ -101,6 +101,34 @@ tpmlp_status launch_sum_finish(const float* S, const void* bias, void* out, int6
 tpmlp_status launch_swiglu_pack(void* G, void* U, void* W_sh, int64_t rows, int64_t ffn, int p, int esize,
                                 bool inverse, cudaStream_t st);
 
+// An MXFP4 operand [rows, K]: codes and tiled scales (mxfp4.cuh).
+struct MxOperand {
+    const void* codes;
+    const void* scales;
+    int64_t rows;
+};
+// D[M,N] = sum_k A[M,k] B[N,k] on MXFP4 operands, and what its epilogue reads and writes.
+struct MxSpec {
+    int64_t M, N, K;
+    int epi;  // EPI_STORE (+ bias), EPI_SWIGLU, EPI_DSWIGLU
+    bool out_f32;
+    void* out; int64_t out_ld, out_ss, shard_cols;  // shard_cols 0: the columns are not sharded
+    const void* bias;                               // bf16, may be null
+    const void* h_in; void* h_out; int64_t h_ld;    // packed bf16 pre-activations
+    void* q; void* qs; int64_t q_cols;              // quantised along the columns
+    void* ht; void* hts; void* yt; void* yts;       // quantised along the rows
+    float* colsum;                                  // sums over blocks of 32 rows, may be null
+};
+tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev, cudaStream_t st);
+// X [p][rows][cols / p] (row pitch ldx) -> (Q, S) along the columns and / or (Qt, St) along the rows
+tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows,
+                                   int64_t cols, int p, bool f32, const DeviceInfo& dev, cudaStream_t st);
+tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
+                                     const DeviceInfo& dev, cudaStream_t st);
+// Process-wide kernel choice of the MXFP4 GEMM (see tpmlp_set_mxfp4_mode).
+void set_mxfp4_mode(int mode);
+int get_mxfp4_mode();
+
 // How a bf16 GEMM launch of launch_tc_gemm would run, by the same tiling decision (false when
 // no tcgen05 variant takes it); nothing is launched.  A K-chunked fp32 contraction reports its
 // first launch.

@@ -1,0 +1,104 @@
+// MXFP4 (OCP Microscaling Formats v1.0): 4-bit E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+// their negatives) in blocks of 32 consecutive values along the contraction, each block with one
+// E8M0 scale, a power of two 2^(byte - 127).
+//
+//   e    = clamp(floor(log2(max |x|)) - 2, -127, 125)        (2 = exponent of E2M1's largest, 6)
+//   code = round to nearest even E2M1 of x 2^-e, at most 6
+//
+// With x in fp32 everything but that last rounding is exact: floor(log2) is the exponent field,
+// and x 2^-e a multiplication by a normal power of two.  A block that holds an infinity or a NaN
+// gets the NaN scale (255) and zero codes, so that whatever it is multiplied into is NaN.
+//
+// Layouts of an operand [rows, K]:
+//   codes   [rows][ceil(K/32) * 16 bytes], the value of even k in the low half of a byte; values
+//           past K are zero.
+//   scales  tiles of 128 rows x 4 blocks, 512 bytes each, [ceil(rows/128)][ceil(K/128)]; in a
+//           tile the byte of row r, block j is at (r % 32) * 16 + (r / 32) * 4 + j, which is what
+//           tcgen05.cp 32x128b brings to tensor memory as the block-scaled MMA reads it.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+namespace tpmlp {
+namespace mx {
+
+// Byte of the scale of row `row`, block `blk` in the tiled layout with `k_tiles` = ceil(K/128).
+__host__ __device__ __forceinline__ long long scale_offset(long long row, long long blk, long long k_tiles) {
+    return ((row >> 7) * k_tiles + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
+}
+
+// |x| as ordered bits: finite < 0x7F800000 <= infinity and NaN, so that an integer maximum keeps a
+// NaN where a floating one would drop it.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Scale byte of a block whose largest |x| has the bits amax.
+__device__ __forceinline__ uint32_t scale_of(uint32_t amax) {
+    const uint32_t ex = amax >> 23;
+    return amax >= 0x7F800000u ? 255u : (ex > 2u ? ex - 2u : 0u);
+}
+// 2^-e of scale byte s <= 252: a normal fp32 number (2^127 .. 2^-125); 0 for the NaN scale.
+__device__ __forceinline__ float inverse_scale(uint32_t s) {
+    return s == 255u ? 0.0f : __uint_as_float((254u - s) << 23);
+}
+// 2^e of scale byte s: subnormal for 0, NaN for 255.
+__device__ __forceinline__ float scale_value(uint32_t s) {
+    return __uint_as_float(s == 0u ? 0x00400000u : (s == 255u ? 0x7FFFFFFFu : s << 23));
+}
+
+// Eight values (already scaled) to eight codes, v[0] in the lowest half byte.
+__device__ __forceinline__ uint32_t encode8(float v0, float v1, float v2, float v3, float v4, float v5, float v6,
+                                            float v7) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v0), "f"(v1), "f"(v2), "f"(v3), "f"(v4), "f"(v5), "f"(v6), "f"(v7));
+    return r;
+}
+// Eight codes to their values.
+__device__ __forceinline__ void decode8(uint32_t c, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// One block of 32 fp32 values of this thread: 16 bytes of codes and the scale byte.
+__device__ __forceinline__ uint32_t quantize32(const float (&v)[32], uint4& codes) {
+    uint32_t a[4] = {abs_bits(v[0]), abs_bits(v[1]), abs_bits(v[2]), abs_bits(v[3])};
+#pragma unroll
+    for (int j = 4; j < 32; j += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = max(a[i], abs_bits(v[j + i]));
+    }
+    const uint32_t s = scale_of(max(max(a[0], a[1]), max(a[2], a[3])));
+    const float inv = inverse_scale(s);
+    uint32_t c[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float* x = v + w * 8;
+        c[w] = encode8(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv, x[4] * inv, x[5] * inv, x[6] * inv,
+                       x[7] * inv);
+    }
+    codes = s == 255u ? make_uint4(0, 0, 0, 0) : make_uint4(c[0], c[1], c[2], c[3]);
+    return s;
+}
+
+}  // namespace mx
+}  // namespace tpmlp

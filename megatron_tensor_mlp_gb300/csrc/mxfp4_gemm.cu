@@ -1,0 +1,238 @@
+// Host side of the MXFP4 GEMM: tensor maps, choice of kernel and split, launch.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "mxfp4_gemm.cuh"
+
+namespace tpmlp {
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+            const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+    auto fn = encode_fn();
+    if (!fn) {
+        set_error("cuTensorMapEncodeTiled is not available from the driver");
+        return false;
+    }
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled (MXFP4) failed (%d): dims %llu x %llu x %llu", static_cast<int>(r),
+                  (unsigned long long)dims[0], (unsigned long long)dims[1], (unsigned long long)dims[2]);
+        return false;
+    }
+    return true;
+}
+
+// Codes [rows][pitch bytes]: boxes of 128 bytes (256 values of k) x box_rows.
+bool codes_map(CUtensorMap* map, const MxOperand& o, int64_t k, uint32_t box_rows) {
+    const uint64_t pitch = static_cast<uint64_t>((k + 31) / 32 * 16), rows = static_cast<uint64_t>(o.rows);
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.codes, {pitch, rows, 1}, {pitch, pitch * rows}, {128, box_rows, 1},
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Scales [ceil(rows/128)][ceil(k/128)][512 bytes]: boxes of box_tiles row tiles x 2 k tiles.
+bool scales_map(CUtensorMap* map, const MxOperand& o, int64_t k, uint32_t box_tiles) {
+    const uint64_t kt = static_cast<uint64_t>((k + 127) / 128), rt = static_cast<uint64_t>((o.rows + 127) / 128);
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, o.scales, {128, kt, rt}, {512, 512 * kt}, {128, 2, box_tiles},
+                  CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// 0 auto, 1 single CTAs without a split, 2 CTA pairs, 3 / 4 / 5 single CTAs with the K loop split 2 / 4 / 8 ways
+// (where the exchange of that many partial sums fits)
+std::atomic<int> g_mode{0};
+
+template <typename Kern>
+bool set_smem(Kern kern, int device, int bytes, bool (&done)[64]) {
+    if (device < 64 && done[device]) return true;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) {
+        set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        return false;
+    }
+    if (device < 64) done[device] = true;
+    return true;
+}
+
+template <typename Kern>
+tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const CUtensorMap (&m)[4],
+                    const mx::Args& k) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see griddep_wait
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], k);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        set_error("MXFP4 GEMM launch: %s", cudaGetErrorString(e));
+        return TPMLP_ERR_CUDA;
+    }
+    count_launch();
+    return TPMLP_OK;
+}
+
+template <int EPI>
+int pair_capacity(const DeviceInfo& dev) {
+    static int cap[64];
+    static bool done[64], attr_done[64];
+    if (dev.device >= 64) return 0;
+    if (done[dev.device]) return cap[dev.device];
+    auto kern = mx::mx_pair_kernel<EPI>;
+    int n = 0;
+    if (set_smem(kern, dev.device, mx::PairGeom<EPI>::smem, attr_done)) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (dev.sm_count / 2));
+        cfg.blockDim = dim3(mx::P_THREADS);
+        cfg.dynamicSmemBytes = mx::PairGeom<EPI>::smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+        cudaGetLastError();
+    }
+    cap[dev.device] = n;
+    done[dev.device] = true;
+    return n;
+}
+
+// Bytes that one CTA of a split tile receives: the chunks it finishes, from every other CTA.
+template <int EPI>
+int exchange_bytes(int split, int rows) {
+    constexpr int CH = EPI == EPI_SWIGLU ? 2 : 4, PARTS = EPI == EPI_SWIGLU ? 2 : 1;
+    const int owners = std::min(split, CH);
+    return (CH + owners - 1) / owners * (split - 1) * PARTS * 128 * rows;
+}
+template <int EPI>
+bool split_fits(int split, int rows, int kb) {
+    const int room = mx::S_RING - (EPI == EPI_DSWIGLU ? 4 * mx::TURN_WORDS * 4 : 0);
+    return split <= kb && exchange_bytes<EPI>(split, std::min((rows + 31) / 32 * 32, mx::BM)) <= room;
+}
+
+template <int EPI>
+tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec& g, mx::Args k, const DeviceInfo& dev,
+                            cudaStream_t st) {
+    constexpr bool GATED = EPI == EPI_SWIGLU;
+    const int mode = g_mode.load(std::memory_order_relaxed);
+    const int cap = pair_capacity<EPI>(dev);
+    const int64_t m_pairs = (g.M + 255) / 256, n_pairs = (g.N + 255) / 256;
+    const bool pair = cap > 0 && (mode == 2 || (mode == 0 && m_pairs * n_pairs >= cap));
+    CUtensorMap m[4];
+    if (pair) {
+        k.m_blocks = static_cast<int>(m_pairs);
+        k.n_blocks = static_cast<int>(n_pairs);
+        k.num_tiles = k.m_blocks * k.n_blocks;
+        if (!codes_map(&m[0], a, g.K, mx::BM) || !codes_map(&m[1], b, g.K, mx::BM) || !scales_map(&m[2], a, g.K, 1) ||
+            !scales_map(&m[3], b, g.K, 2))
+            return TPMLP_ERR_CUDA;
+        const int clusters = std::min(k.num_tiles, cap);
+        return launch(mx::mx_pair_kernel<EPI>, dim3(2 * clusters), mx::P_THREADS, mx::PairGeom<EPI>::smem, 2, st, m, k);
+    }
+    static bool attr_done[64];
+    auto kern = mx::mx_single_kernel<EPI>;
+    if (!set_smem(kern, dev.device, mx::S_SMEM, attr_done)) return TPMLP_ERR_CUDA;
+    k.a_box = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+    k.stages = mx::SingleGeom<EPI>::stages(k.a_box);
+    const int64_t n_blocks = GATED ? g.N / 128 : (g.N + 127) / 128, m_blocks = (g.M + 127) / 128;
+    const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
+    int split = 1;
+    if (mode >= 3) {
+        split = 2 << (mode - 3);
+        while (split > 1 && !split_fits<EPI>(split, rows, k.kb)) split /= 2;
+    } else if (mode == 0) {
+        while (split < 8 && split_fits<EPI>(split * 2, rows, k.kb) && n_blocks * m_blocks * split * 2 <= 2 * dev.sm_count) split *= 2;
+    }
+    if (m_blocks > 65535 || n_blocks * split > 0x7FFFFFFF) {
+        set_error("MXFP4 GEMM: %lld x %lld tiles", (long long)m_blocks, (long long)n_blocks);
+        return TPMLP_ERR_SHAPE;
+    }
+    if (!codes_map(&m[0], a, g.K, static_cast<uint32_t>(k.a_box)) || !codes_map(&m[1], b, g.K, GATED ? 64 : 128) ||
+        !scales_map(&m[2], a, g.K, 1) || !scales_map(&m[3], b, g.K, GATED ? 2 : 1))
+        return TPMLP_ERR_CUDA;
+    return launch(kern, dim3(static_cast<unsigned>(n_blocks * split), static_cast<unsigned>(m_blocks)), mx::S_THREADS, mx::S_SMEM,
+                  static_cast<unsigned>(split), st, m, k);
+}
+
+}  // namespace
+
+void set_mxfp4_mode(int mode) { g_mode.store(mode, std::memory_order_relaxed); }
+int get_mxfp4_mode() { return g_mode.load(std::memory_order_relaxed); }
+
+tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev, cudaStream_t st) {
+    mx::Args k{};
+    k.M = static_cast<int>(g.M);
+    k.N = static_cast<int>(g.N);
+    k.kb = static_cast<int>((g.K + mx::KC - 1) / mx::KC);
+    k.last_steps = static_cast<int>((g.K - static_cast<int64_t>(k.kb - 1) * mx::KC + 63) / 64);
+    k.group_m = 16;
+    k.out_f32 = g.out_f32 ? 1 : 0;
+    k.out = g.out;
+    k.out_ld = g.out_ld;
+    k.out_ss = g.out_ss;
+    k.shard_cols = static_cast<int>(g.shard_cols > 0 ? g.shard_cols : g.N);
+    k.bias = static_cast<const __nv_bfloat16*>(g.bias);
+    k.h_in = static_cast<const __nv_bfloat16*>(g.h_in);
+    k.h_out = static_cast<__nv_bfloat16*>(g.h_out);
+    k.h_ld = g.h_ld;
+    k.q = static_cast<uint8_t*>(g.q);
+    k.qs = static_cast<uint8_t*>(g.qs);
+    k.q_pitch = (g.q_cols + 31) / 32 * 16;
+    k.q_tiles = (g.q_cols + 127) / 128;
+    k.ht = static_cast<uint8_t*>(g.ht);
+    k.hts = static_cast<uint8_t*>(g.hts);
+    k.yt = static_cast<uint8_t*>(g.yt);
+    k.yts = static_cast<uint8_t*>(g.yts);
+    k.t_pitch = (g.M + 31) / 32 * 16;
+    k.t_tiles = (g.M + 127) / 128;
+    k.colsum = g.colsum;
+    k.status = dev.status;
+    k.timeout_ns = 2000000000ull;  // 2 s per wait
+    {
+        // 32-byte epilogue accesses: every row that they touch starts on a 32-byte boundary
+        auto rows32 = [](const void* ptr, int64_t pitch, int64_t shard) {
+            return ptr == nullptr || (reinterpret_cast<uintptr_t>(ptr) % 32 == 0 && pitch % 32 == 0 && shard % 32 == 0);
+        };
+        const int64_t es = g.out_f32 ? 4 : 2;
+        k.st32 = rows32(g.out, g.out_ld * es, g.out_ss * es) && rows32(g.h_in, g.h_ld * 2, 0) && rows32(g.h_out, g.h_ld * 2, 0);
+    }
+    switch (g.epi) {
+        case EPI_STORE: return launch_variant<EPI_STORE>(a, b, g, k, dev, st);
+        case EPI_SWIGLU: return launch_variant<EPI_SWIGLU>(a, b, g, k, dev, st);
+        case EPI_DSWIGLU: return launch_variant<EPI_DSWIGLU>(a, b, g, k, dev, st);
+    }
+    set_error("internal: no MXFP4 GEMM for epilogue %d", g.epi);
+    return TPMLP_ERR_CUDA;
+}
+
+}  // namespace tpmlp

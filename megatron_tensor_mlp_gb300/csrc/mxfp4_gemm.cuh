@@ -1,0 +1,732 @@
+// D[M,N] = sum_k A[M,k] B[N,k] on MXFP4 operands: block-scaled tcgen05.mma (kind::mxf4, 4-bit
+// elements, one E8M0 scale per 32 along k, fp32 accumulators in tensor memory), fed by TMA, with
+// the epilogues of the gated feed-forward block fused.
+//
+// One instruction contracts 64 values of k: 32 bytes of a row, the bytes (and the tensor-core
+// cycles) of a 16-deep bf16 instruction, so the pipeline has the shape of the bf16 GEMM's at a
+// quarter of the K loop.  A ring stage is 256 values of k: 128-byte rows of codes (K-major,
+// 128-byte swizzle) and the scale tiles (128 rows x 4 blocks, 512 bytes) of the same rows, which
+// tcgen05.cp copies to tensor memory ahead of the stage's MMAs.  Copies and MMAs of one thread
+// execute in issue order, so all stages share one place for their scales.
+//
+// Two kernels:
+//   mx_pair_kernel    CTA pairs (cta_group::2), 256x256 tiles, persistent.  Two 256-column
+//                     accumulators and 24 columns of scales do not fit 512 tensor-memory columns,
+//                     so the accumulators share 32: [0,256) and [224,480), scales from 480.  Each
+//                     epilogue reads the shared columns first and reports them free; the next
+//                     tile's MMAs start then, beside the rest of the epilogue.
+//   mx_single_kernel  one CTA per 128x128 tile (128 rows of A, 128 of B; for the gated forward 64
+//                     gate and 64 up columns), two CTAs an SM, not persistent: for few rows, where
+//                     reading B's codes bounds the time, and for GEMMs of few tiles.  Clusters of
+//                     up to 8 CTAs split the K loop and add their partial sums through distributed
+//                     shared memory in a fixed order.  With at most 64 rows of A only those rows
+//                     are copied: the MMA's other rows read whatever lies behind them in shared
+//                     memory, and their results are not stored.
+//
+// Every wait on an mbarrier is bounded (a status word records a timeout); no TMA load uses
+// cluster multicast.
+#pragma once
+#include "gemm_tc.cuh"
+#include "internal.h"
+#include "mxfp4.cuh"
+#include "ptx.cuh"
+
+namespace tpmlp {
+namespace mx {
+
+constexpr int BM = 128;           // rows of A (and of B) in one CTA's stage
+constexpr int KC = 256;           // k per ring stage: 128 bytes of codes a row
+constexpr int OP_BYTES = BM * 128;
+constexpr int SF_TILE = 512;      // scales of 128 rows x 128 k
+
+struct Args {
+    int M, N;
+    int kb;          // ring stages of K: ceil(K / 256)
+    int last_steps;  // MMAs (64 k each) of the last one: 1..4
+    int m_blocks, n_blocks, num_tiles, group_m;  // pair kernel
+    int a_box;       // single kernel: rows of A copied per stage (16, 32, 64 or 128)
+    int stages;      // single kernel: ring stages
+    int out_f32, st32;
+    // EPI_STORE: D + bias; column n is at out + (n / shard_cols) * out_ss + m * out_ld + n % shard_cols
+    void* out; long long out_ld, out_ss; int shard_cols;
+    const __nv_bfloat16* bias;   // EPI_STORE [N], EPI_SWIGLU [N] packed
+    // EPI_SWIGLU: h_out (optional) [M][2 ffn]; EPI_DSWIGLU: h_in
+    const __nv_bfloat16* h_in; __nv_bfloat16* h_out; long long h_ld;
+    // quantised outputs along the columns: EPI_SWIGLU y [M][ffn], EPI_DSWIGLU dH [M][2 ffn]
+    uint8_t* q; uint8_t* qs; long long q_pitch, q_tiles;
+    // EPI_DSWIGLU: along the rows (tokens), dH^T [2 ffn][M] and Y^T [ffn][M]
+    uint8_t* ht; uint8_t* hts; uint8_t* yt; uint8_t* yts; long long t_pitch, t_tiles;
+    float* colsum;   // EPI_DSWIGLU, optional: sums of dH over blocks of 32 tokens [ceil(M/32)][2 ffn]
+    uint32_t* status;
+    unsigned long long timeout_ns;
+};
+
+// ---------------------------------------------------------------- tcgen05, block scaled
+// Instruction descriptor, kind::mxf4: bits 4-5 B scale id, 7-9 A format (1 = E2M1), 10-12 B
+// format, 17-22 N >> 3, 23 scale format (1 = E8M0), 24-28 M >> 4, 29-30 A scale id.  The scale id
+// names the byte of the scale columns' 32-bit words that the instruction starts from: 0 for the
+// first 64 k of a scale tile, 2 for the second.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t sf_id) {
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(m >> 4) << 24) | (sf_id << 29);
+}
+// Shared-memory descriptor of a scale tile for tcgen05.cp: no swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+           (static_cast<uint64_t>(1) << 46);
+}
+template <int CG>
+__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t accumulate) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+// One scale tile (512 bytes) to 4 tensor-memory columns, the same 32 rows for every lane quarter.
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (CG == 2) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// ---------------------------------------------------------------- epilogues
+// EPI_STORE: 32 consecutive columns of a row.
+__device__ __forceinline__ void store_chunk(const Args& p, float (&v)[32], int gm, int gn0) {
+    const int nvalid = p.N - gn0;
+    if (gm >= p.M || nvalid <= 0) return;
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const __nv_bfloat16* bp = p.bias + gn0 + g * 8;
+            if ((g + 1) * 8 <= nvalid) {
+                float b[8];
+                tc::unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(bp)), b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[g * 8 + i] += b[i];
+            } else if (g * 8 < nvalid) {  // fp32 rows may end on a multiple of 4
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[g * 8 + i] += __bfloat162float(bp[i]);
+            }
+        }
+    }
+    const int sh = gn0 / p.shard_cols;
+    const long long at = sh * p.out_ss + gm * p.out_ld + (gn0 - sh * p.shard_cols);
+    if (p.out_f32) tc::store_f32x32(static_cast<float*>(p.out) + at, v, nvalid, p.st32 != 0);
+    else tc::store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + at, v, nvalid, p.st32 != 0);
+}
+
+// EPI_SWIGLU: y = silu(g) u for features f0..f0+31 of a row (one block), quantised from fp32.
+__device__ __forceinline__ void swiglu_chunk(const Args& p, float (&g)[32], float (&u)[32], int gm, int f0) {
+    if (gm >= p.M || 2 * f0 >= p.N) return;
+    const long long pg = (long long)(f0 >> 7) * 256 + (f0 & 127);
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float bg[8], bu[8];
+            tc::unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.bias + pg + j * 8)), bg);
+            tc::unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.bias + pg + 128 + j * 8)), bu);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                g[j * 8 + i] += bg[i];
+                u[j * 8 + i] += bu[i];
+            }
+        }
+    }
+    if (p.h_out != nullptr) {
+        __nv_bfloat16* d = p.h_out + gm * p.h_ld + pg;
+        tc::store_bf16x32(d, g, 32, p.st32 != 0);
+        tc::store_bf16x32(d + 128, u, 32, p.st32 != 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] = g[j] * tc::sigmoid_approx(g[j]) * u[j];
+    uint4 c;
+    const uint32_t s = quantize32(g, c);
+    *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + f0 / 2) = c;
+    p.qs[scale_offset(gm, f0 >> 5, p.q_tiles)] = static_cast<uint8_t>(s);
+}
+
+// A warp's 32 x 32 values, a row in each lane, turned so that each lane has a column.  buf: 32 rows
+// of 36 words of this warp's (both passes free of bank conflicts).
+constexpr int TURN_WORDS = 32 * 36;
+__device__ __forceinline__ void turn32(float* buf, const float (&v)[32], float (&w)[32], int lane) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(buf + lane * 36 + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int t = 0; t < 32; ++t) w[t] = buf[t * 36 + lane];
+    __syncwarp();
+}
+
+// One block of 32 tokens of column `col` of an array quantised along the tokens.
+__device__ __forceinline__ void put_token_block(const Args& p, uint8_t* q, uint8_t* qs, const float (&w)[32], long long col,
+                                                int tb) {
+    uint4 c;
+    const uint32_t s = quantize32(w, c);
+    if ((long long)tb * 16 < p.t_pitch) *reinterpret_cast<uint4*>(q + col * p.t_pitch + tb * 16) = c;
+    if (tb < p.t_tiles * 4) qs[scale_offset(col, tb, p.t_tiles)] = static_cast<uint8_t>(s);
+}
+
+// EPI_DSWIGLU: dY of features f0..f0+31 of this thread's row (token) and, from the saved bf16
+// pre-activations, dg = dY u silu'(g), du = dY silu(g) and y = silu(g) u, from fp32 quantised along the
+// columns (dg, du) and, turned through shared memory, along the tokens (dg, du, y).  tb: the warp's block of
+// 32 tokens.  Rows past M count as zero.
+__device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], int gm, int f0, int tb, float* buf, int lane) {
+    if (f0 >= p.N) return;  // (whole warp; features come in multiples of 128)
+    const long long pg = (long long)(f0 >> 7) * 256 + (f0 & 127);
+    const bool live = gm < p.M;
+    float g[32], u[32];
+    if (live) {
+        const __nv_bfloat16* hp = p.h_in + gm * p.h_ld + pg;
+        tc::load_bf16x32(hp, g, 32, p.st32 != 0);
+        tc::load_bf16x32(hp + 128, u, 32, p.st32 != 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float dy = v[j], gj = g[j], uj = u[j];
+        const float sg = tc::sigmoid_approx(gj), sl = gj * sg;
+        g[j] = live ? dy * uj * (sg * (1.0f + gj * (1.0f - sg))) : 0.0f;  // dg
+        u[j] = live ? dy * sl : 0.0f;                                     // du
+        v[j] = live ? sl * uj : 0.0f;                                     // y
+    }
+    if (live) {
+        uint4 c;
+        uint32_t s = quantize32(g, c);
+        *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + pg / 2) = c;
+        p.qs[scale_offset(gm, pg >> 5, p.q_tiles)] = static_cast<uint8_t>(s);
+        s = quantize32(u, c);
+        *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + pg / 2 + 64) = c;
+        p.qs[scale_offset(gm, (pg >> 5) + 4, p.q_tiles)] = static_cast<uint8_t>(s);
+    }
+    float w[32];
+    turn32(buf, v, w, lane);
+    put_token_block(p, p.yt, p.yts, w, f0 + lane, tb);
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        turn32(buf, part ? u : g, w, lane);
+        put_token_block(p, p.ht, p.hts, w, pg + part * 128 + lane, tb);
+        if (p.colsum != nullptr && (long long)tb * 16 < p.t_pitch) {
+            float s = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 32; ++t) s += w[t];
+            p.colsum[(long long)tb * (2 * p.N) + pg + part * 128 + lane] = s;
+        }
+    }
+}
+
+__device__ __forceinline__ void load_acc32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+
+// ---------------------------------------------------------------- pair kernel
+constexpr int P_BN = 256;
+constexpr int P_THREADS = 384;       // warp 0 TMA, warp 1 MMA, warps 4-11 epilogue
+constexpr int P_ACC1 = 224;          // second accumulator's first column
+constexpr int P_SFA = 480, P_SFB = 488;  // scales: 2 tiles of A (4 columns each), 2 of B (8 each)
+constexpr int P_SFA_BYTES = 2 * SF_TILE, P_SFB_BYTES = 4 * SF_TILE;
+constexpr int P_STAGE = 2 * OP_BYTES + P_SFA_BYTES + P_SFB_BYTES;
+template <int EPI>
+struct PairGeom {
+    static constexpr int turn = EPI == EPI_DSWIGLU ? 8 * TURN_WORDS * 4 : 0;
+    static constexpr int stages = EPI == EPI_DSWIGLU ? 5 : 6;
+    static constexpr int smem = 1024 + stages * P_STAGE + turn + 256;
+    static_assert(smem <= 227 * 1024, "pair kernel shared memory");
+};
+
+__device__ __forceinline__ void decode_tile(const Args& p, int t, int& mb, int& nb) {
+    const int per_group = p.group_m * p.n_blocks;
+    const int g = t / per_group;
+    const int first_m = g * p.group_m;
+    const int gm = min(p.m_blocks - first_m, p.group_m);
+    const int r = t - g * per_group;
+    mb = first_m + r % gm;
+    nb = r / gm;
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(P_THREADS, 1)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Args p) {
+    constexpr int STAGES = PairGeom<EPI>::stages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + STAGES * OP_BYTES;
+    uint8_t* sSA = sB + STAGES * OP_BYTES;
+    uint8_t* sSB = sSA + STAGES * P_SFA_BYTES;
+    float* turn = reinterpret_cast<float*>(sSB + STAGES * P_SFB_BYTES);
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(turn) + PairGeom<EPI>::turn);
+    uint64_t* empty = full + STAGES;
+    uint64_t* tfull = empty + STAGES;   // [2] accumulator complete
+    uint64_t* tempty = tfull + 2;       // [2] accumulator read
+    uint64_t* shared_free = tempty + 2; // the columns shared with the other accumulator read
+    uint64_t* drain = shared_free + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t prank = cluster_ctarank();
+    const bool leader = prank == 0;
+    const int cluster_id = blockIdx.x / 2;
+    const int n_clusters = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull + a, 1);
+            mbar_init(tempty + a, 16);  // 8 epilogue warps of either CTA
+        }
+        mbar_init(shared_free, 8);      // the 4 of either CTA that read the shared columns
+        mbar_init(drain, 1);
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSA);
+        tma_prefetch_desc(&tmSB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ producer (both CTAs)
+            int stage = 0;
+            uint32_t phase = 0, armed = 0, last_parity = 0;
+            bool ok = true;
+            const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+            for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters) {
+                int mb, nb;
+                decode_tile(p, t, mb, nb);
+                const int row_tile = mb * 2 + static_cast<int>(prank);
+                const int col0 = nb * P_BN + static_cast<int>(prank) * BM;
+                for (int it = 0; it < p.kb; ++it) {
+                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) {
+                        mbar_arrive_expect_tx(full + stage, 2 * P_STAGE);
+                        armed |= 1u << stage;
+                        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                    }
+                    const uint32_t bar = full0 + stage * 8;
+                    tma_load_3d_pair(sA + stage * OP_BYTES, &tmA, bar, it * 128, row_tile * BM, 0);
+                    tma_load_3d_pair(sB + stage * OP_BYTES, &tmB, bar, it * 128, col0, 0);
+                    tma_load_3d_pair(sSA + stage * P_SFA_BYTES, &tmSA, bar, 0, it * 2, row_tile);
+                    tma_load_3d_pair(sSB + stage * P_SFB_BYTES, &tmSB, bar, 0, it * 2, nb * 2);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (ok) {
+                // every stage's last release has arrived before this CTA can exit
+                for (int i = 0; i < STAGES; ++i) {
+                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereDrain)) break;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            } else {
+                if (leader) {
+                    for (int s = 0; s < STAGES; ++s)
+                        if (armed & (1u << s))
+                            mbar_wait_bounded(full + s, (last_parity >> s) & 1u, p.status, p.timeout_ns, kWhereDrain, false);
+                } else {
+                    spin_ns(200000);  // this CTA's last copies, counted on the leader's barriers, land
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            if (leader) {
+                // -------------------------------------------------------- MMA issuer (leader)
+                const uint64_t a0 = sdesc_sw128(smem_u32(sA), 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+                const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
+                int stage = 0;
+                uint32_t phase = 0;
+                int lt = 0;
+                bool ok = true;
+                for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters, ++lt) {
+                    const int acc = lt & 1;
+                    ok = mbar_wait_bounded(tempty + acc, ((lt >> 1) & 1) ^ 1u, p.status, p.timeout_ns, kWhereMma);
+                    if (ok && lt > 0) ok = mbar_wait_bounded(shared_free, (lt - 1) & 1, p.status, p.timeout_ns, kWhereMma);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + acc * P_ACC1;
+                    for (int it = 0; it < p.kb; ++it) {
+                        if (!mbar_wait_bounded(full + stage, phase, p.status, p.timeout_ns, kWhereMma)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = a0 + static_cast<uint64_t>(stage * (OP_BYTES >> 4));
+                        const uint64_t bd = b0 + static_cast<uint64_t>(stage * (OP_BYTES >> 4));
+                        const uint64_t sad = sa0 + static_cast<uint64_t>(stage * (P_SFA_BYTES >> 4));
+                        const uint64_t sbd = sb0 + static_cast<uint64_t>(stage * (P_SFB_BYTES >> 4));
+                        const int steps = it + 1 == p.kb ? p.last_steps : 4;
+#pragma unroll
+                        for (int kt = 0; kt < 2; ++kt) {
+                            if (kt * 2 < steps) {
+                                copy_scales<2>(tmem_base + P_SFA + kt * 4, sad + kt * (SF_TILE >> 4));
+                                copy_scales<2>(tmem_base + P_SFB + kt * 8, sbd + kt * (SF_TILE >> 4));
+                                copy_scales<2>(tmem_base + P_SFB + kt * 8 + 4, sbd + (2 + kt) * (SF_TILE >> 4));
+                            }
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (kk < steps)
+                                umma_mxf4<2>(d, ad + kk * 2, bd + kk * 2, idesc_mxf4(2 * BM, P_BN, (kk & 1) * 2),
+                                             tmem_base + P_SFA + (kk >> 1) * 4, tmem_base + P_SFB + (kk >> 1) * 8,
+                                             (it | kk) != 0 ? 1u : 0u);
+                        }
+                        umma_commit_pair_mc(empty + stage, 0x3);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (ok) umma_commit_pair_mc(tfull + acc, 0x3);
+                }
+                umma_commit_pair_mc(drain, 0x3);
+                // the last releases of the epilogue warps, some from the peer SM, land before this CTA can exit
+                if (ok && lt > 0) ok = mbar_wait_bounded(shared_free, (lt - 1) & 1, p.status, p.timeout_ns, kWhereDrain);
+                for (int i = 0; ok && i < 2; ++i, ++lt)
+                    ok = mbar_wait_bounded(tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, p.status, p.timeout_ns, kWhereDrain);
+            }
+            mbar_wait_bounded(drain, 0, p.status, p.timeout_ns, kWhereDrain, /*watch_status=*/false);
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------------- epilogue (both CTAs)
+        const int q = warp & 3;
+        const int half = (warp - 4) >> 2;
+        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0), shared0 = mapa_shared(smem_u32(shared_free), 0);
+        [[maybe_unused]] float* buf = turn + (warp - 4) * TURN_WORDS;
+        int lt = 0;
+        for (int t = cluster_id; t < p.num_tiles; t += n_clusters, ++lt) {
+            const int acc = lt & 1;
+            int okw = 0;
+            if (lane == 0) okw = mbar_wait_bounded(tfull + acc, (lt >> 1) & 1, p.status, p.timeout_ns, kWhereEpilogue);
+            okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
+            if (!okw) break;
+            tc_fence_after();
+            int mb, nb;
+            decode_tile(p, t, mb, nb);
+            const int row0 = mb * (2 * BM) + static_cast<int>(prank) * BM + q * 32;
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * P_ACC1;
+            // The first accumulator's shared columns are its last, the second's its first: walk the
+            // chunks so that they come first.  half 1 - acc holds them.
+            constexpr int CH = EPI == EPI_SWIGLU ? 2 : 4;
+#pragma unroll 1
+            for (int i = 0; i < CH; ++i) {
+                const int c = acc == 0 ? CH - 1 - i : i;
+                const int col = half * (CH * 32) + c * 32;
+                float v[32];
+                [[maybe_unused]] float u[32];
+                load_acc32(t_row + col, v);
+                if constexpr (EPI == EPI_SWIGLU) load_acc32(t_row + 128 + col, u);
+                if (i == 0 && half == 1 - acc) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(shared0);
+                }
+                if constexpr (EPI == EPI_SWIGLU) swiglu_chunk(p, v, u, row0 + lane, nb * 128 + col);
+                else if constexpr (EPI == EPI_DSWIGLU) dswiglu_chunk(p, v, row0 + lane, nb * P_BN + col, row0 >> 5, buf, lane);
+                else store_chunk(p, v, row0 + lane, nb * P_BN + col);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + acc * 8);
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while its peer may still touch its shared or tensor memory
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------- single kernel
+constexpr int S_BN = 128;
+constexpr int S_THREADS = 192;       // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
+constexpr int S_TMEM = 256;          // 128 accumulator columns, 24 of scales: two CTAs an SM
+constexpr int S_SFA = 128, S_SFB = 136;
+constexpr int S_MAX_STAGES = 6;
+constexpr int S_SMEM = 113 * 1024;   // two CTAs an SM
+constexpr int S_RING = S_SMEM - 1024 - 256;
+template <int EPI>
+struct SingleGeom {
+    static constexpr int sfb = EPI == EPI_SWIGLU ? 4 * SF_TILE : 2 * SF_TILE;
+    static __host__ __device__ constexpr int stage(int a_box) { return a_box * 128 + OP_BYTES + 2 * SF_TILE + sfb; }
+    // stages that fit with the MMA's reads past a narrow A box kept inside the ring
+    static __host__ __device__ constexpr int stages(int a_box) {
+        const int n = S_RING / stage(a_box);
+        return n < S_MAX_STAGES ? n : S_MAX_STAGES;
+    }
+};
+static_assert(SingleGeom<EPI_STORE>::stages(128) >= 3 && SingleGeom<EPI_SWIGLU>::stages(128) >= 3, "ring depth");
+
+template <int EPI>
+__global__ void __launch_bounds__(S_THREADS, 2)
+    mx_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Args p) {
+    constexpr bool GATED = EPI == EPI_SWIGLU;
+    constexpr int SFB = SingleGeom<EPI>::sfb;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int a_bytes = p.a_box * 128;
+    uint8_t* sA = smem;  // first, so that rows past a narrow box are still in the ring
+    uint8_t* sB = sA + p.stages * a_bytes;
+    uint8_t* sSA = sB + p.stages * OP_BYTES;
+    uint8_t* sSB = sSA + p.stages * 2 * SF_TILE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S_RING);
+    uint64_t* empty = full + S_MAX_STAGES;
+    uint64_t* tfull = empty + S_MAX_STAGES;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    uint32_t split, rank;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    rank = cluster_ctarank();
+    const int nb = blockIdx.x / split, mb = blockIdx.y;
+    const int it0 = static_cast<int>((long long)p.kb * rank / split), it1 = static_cast<int>((long long)p.kb * (rank + 1) / split);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(tfull, 1);
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSA);
+        tma_prefetch_desc(&tmSB);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, S_TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+
+    // the tile's columns: gated, 64 gate rows of B and the 64 up rows of the same features
+    const int f0 = nb * 64;
+    const int gate_row = (f0 >> 7) * 256 + (f0 & 127);
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ producer
+            int stage = 0;
+            uint32_t phase = 0, armed = 0, last_parity = 0;
+            bool ok = true;
+            const uint32_t bytes = static_cast<uint32_t>(a_bytes + OP_BYTES + 2 * SF_TILE + SFB);
+            for (int it = it0; it < it1; ++it) {
+                ok = mbar_wait_bounded(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereProducer);
+                if (!ok) break;
+                mbar_arrive_expect_tx(full + stage, bytes);
+                armed |= 1u << stage;
+                last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                uint8_t* b = sB + stage * OP_BYTES;
+                if constexpr (GATED) {
+                    tma_load_3d(b, &tmB, full + stage, it * 128, gate_row, 0);
+                    tma_load_3d(b + OP_BYTES / 2, &tmB, full + stage, it * 128, gate_row + 128, 0);
+                    tma_load_3d(sSB + stage * SFB, &tmSB, full + stage, 0, it * 2, (f0 >> 7) * 2);
+                } else {
+                    tma_load_3d(b, &tmB, full + stage, it * 128, nb * S_BN, 0);
+                    tma_load_3d(sSB + stage * SFB, &tmSB, full + stage, 0, it * 2, nb);
+                }
+                tma_load_3d(sA + stage * a_bytes, &tmA, full + stage, it * 128, mb * BM, 0);
+                tma_load_3d(sSA + stage * 2 * SF_TILE, &tmSA, full + stage, 0, it * 2, mb);
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            // all copies have landed before this CTA can reuse its ring or exit, also where a wait gave up
+            for (int s = 0; s < p.stages; ++s)
+                if (armed & (1u << s))
+                    mbar_wait_bounded(full + s, (last_parity >> s) & 1u, p.status, p.timeout_ns, kWhereDrain, false);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ MMA issuer
+            const uint64_t a0 = sdesc_sw128(smem_u32(sA), 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+            const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int it = it0; it < it1; ++it) {
+                if (!mbar_wait_bounded(full + stage, phase, p.status, p.timeout_ns, kWhereMma)) break;
+                tc_fence_after();
+                const uint64_t ad = a0 + static_cast<uint64_t>(stage * (a_bytes >> 4));
+                const uint64_t bd = b0 + static_cast<uint64_t>(stage * (OP_BYTES >> 4));
+                const uint64_t sad = sa0 + static_cast<uint64_t>(stage * (2 * SF_TILE >> 4));
+                const uint64_t sbd = sb0 + static_cast<uint64_t>(stage * (SFB >> 4));
+                const int steps = it + 1 == p.kb ? p.last_steps : 4;
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) {
+                    if (kt * 2 < steps) {
+                        copy_scales<1>(tmem_base + S_SFA + kt * 4, sad + kt * (SF_TILE >> 4));
+                        copy_scales<1>(tmem_base + S_SFB + kt * 4, sbd + kt * (SF_TILE >> 4));
+                        if constexpr (GATED) copy_scales<1>(tmem_base + S_SFB + 8 + kt * 4, sbd + (2 + kt) * (SF_TILE >> 4));
+                    }
+                }
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (kk < steps) {
+                        const uint32_t add = (it != it0 || kk != 0) ? 1u : 0u;
+                        const uint32_t sfa = tmem_base + S_SFA + (kk >> 1) * 4, sfb = tmem_base + S_SFB + (kk >> 1) * 4;
+                        if constexpr (GATED) {
+                            // 64 rows of a scale tile are two of its four columns
+                            const uint32_t id = idesc_mxf4(BM, 64, (kk & 1) * 2), odd = (f0 & 64) ? 2u : 0u;
+                            umma_mxf4<1>(tmem_base, ad + kk * 2, bd + kk * 2, id, sfa, sfb + odd, add);
+                            umma_mxf4<1>(tmem_base + 64, ad + kk * 2, bd + (OP_BYTES / 2 >> 4) + kk * 2, id, sfa, sfb + 8 + odd,
+                                         add);
+                        } else {
+                            umma_mxf4<1>(tmem_base, ad + kk * 2, bd + kk * 2, idesc_mxf4(BM, S_BN, (kk & 1) * 2), sfa, sfb, add);
+                        }
+                    }
+                }
+                umma_commit(empty + stage);
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            umma_commit(tfull);
+        }
+    }
+    __syncwarp();
+    const int q = warp & 3;
+    const int row0 = mb * BM + q * 32;
+    const bool epi = warp >= 2;
+    // Warps whose rows are all past M have nothing to do; the token-wise outputs also want the zeros
+    // of a last scale tile's blocks past M.
+    const bool work = epi && (EPI == EPI_DSWIGLU || row0 < p.M);
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    // every warp waits: nobody leaves (or lets its shared memory be written by a peer) while copies or
+    // MMAs are in flight
+    if (lane == 0) mbar_wait_bounded(tfull, 0, p.status, p.timeout_ns, kWhereEpilogue, /*watch_status=*/false);
+    __syncwarp();
+    tc_fence_after();
+    constexpr int CH = GATED ? 2 : 4;        // 32-column chunks (gated: of features)
+    constexpr int PARTS = GATED ? 2 : 1;     // accumulator chunks of one of them
+    const int owners = min(static_cast<int>(split), CH);
+    const int rows_in = min(BM, ((p.M - mb * BM) + 31) / 32 * 32);  // rows exchanged: whole warps
+    const int ethread = q * 32 + lane;       // row of this thread
+    uint4* recv = reinterpret_cast<uint4*>(smem);  // over the ring, once all of this CTA's MMAs are done
+    if (split > 1) {
+        cluster_sync_all();  // every CTA's ring is free
+        if (work && row0 - mb * BM < rows_in) {
+#pragma unroll 1
+            for (int c = 0; c < CH; ++c) {
+                const uint32_t owner = static_cast<uint32_t>(c % owners);
+                if (owner == rank) continue;
+                // slot: [chunk of the owner][sender][part][16-byte piece][row]
+                const int sender = static_cast<int>(rank > owner ? rank - 1 : rank);
+                const uint32_t slot = ((c / owners) * (split - 1) + sender) * PARTS;
+                const uint32_t dst = mapa_shared(smem_u32(recv), owner);
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(t_row + part * 64 + c * 32, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        st_cluster_v4(dst + (((slot + part) * 8 + j) * rows_in + ethread) * 16, r[4 * j], r[4 * j + 1],
+                                      r[4 * j + 2], r[4 * j + 3]);
+                }
+            }
+        }
+        cluster_sync_all();  // the partial sums have arrived
+    }
+    if (work) {
+        [[maybe_unused]] float* buf = reinterpret_cast<float*>(smem + S_RING) - (q + 1) * TURN_WORDS;
+#pragma unroll 1
+        for (int c = 0; c < CH; ++c) {
+            if (split > 1 && static_cast<uint32_t>(c % owners) != rank) continue;
+            float v[32];
+            [[maybe_unused]] float u[32];
+            load_acc32(t_row + c * 32, v);
+            if constexpr (GATED) load_acc32(t_row + 64 + c * 32, u);
+            if (split > 1 && row0 - mb * BM < rows_in) {
+#pragma unroll 1
+                for (uint32_t s = 0; s + 1 < split; ++s) {
+                    const uint32_t slot = ((c / owners) * (split - 1) + s) * PARTS;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 x = recv[(slot * 8 + j) * rows_in + ethread];
+                        v[4 * j] += __uint_as_float(x.x);
+                        v[4 * j + 1] += __uint_as_float(x.y);
+                        v[4 * j + 2] += __uint_as_float(x.z);
+                        v[4 * j + 3] += __uint_as_float(x.w);
+                        if constexpr (GATED) {
+                            const uint4 y = recv[((slot + 1) * 8 + j) * rows_in + ethread];
+                            u[4 * j] += __uint_as_float(y.x);
+                            u[4 * j + 1] += __uint_as_float(y.y);
+                            u[4 * j + 2] += __uint_as_float(y.z);
+                            u[4 * j + 3] += __uint_as_float(y.w);
+                        }
+                    }
+                }
+            }
+            if constexpr (GATED) swiglu_chunk(p, v, u, row0 + lane, f0 + c * 32);
+            else if constexpr (EPI == EPI_DSWIGLU) dswiglu_chunk(p, v, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, lane);
+            else store_chunk(p, v, row0 + lane, nb * S_BN + c * 32);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem_base, S_TMEM);
+    }
+}
+
+}  // namespace mx
+}  // namespace tpmlp

@@ -54,6 +54,12 @@ _SIGS = {
     "tpmlp_set_side_stream": [_vp, _vp, _vp],
     "tpmlp_set_gemm_raster": [_i32],
     "tpmlp_set_k_chunk": [_i32],
+    "tpmlp_mxfp4_quantize": [_vp] * 5 + [_i64] * 3 + [_i32, _i32, _vp],
+    "tpmlp_mxfp4_dequantize": [_vp] * 3 + [_i64] * 2 + [_i32, _vp],
+    "tpmlp_mxfp4_matmul": [_vp] * 6 + [_i64] * 3 + [_i32, _vp],
+    "tpmlp_mxfp4_swiglu_mlp_fwd": [_vp] * 10 + [_i64] * 4 + [_i32, _i32, _vp],
+    "tpmlp_mxfp4_swiglu_mlp_bwd": [_vp] * 13 + [_i64] * 4 + [_i32, _i32, _i32, _vp],
+    "tpmlp_set_mxfp4_mode": [_i32],
 
 }
 for _name, _args in _SIGS.items():
@@ -62,6 +68,13 @@ for _name, _args in _SIGS.items():
     _f.restype = ctypes.c_int
 lib.tpmlp_qkv_src_col.argtypes = [_i64, _i64, _i64]
 lib.tpmlp_qkv_src_col.restype = _i64
+for _name, _args in {"tpmlp_mxfp4_code_bytes": [_i64] * 2, "tpmlp_mxfp4_scale_bytes": [_i64] * 2,
+                     "tpmlp_mxfp4_swiglu_ws_bytes": [_i64] * 4 + [_i32, _i32]}.items():
+    _f = getattr(lib, _name)
+    _f.argtypes = _args
+    _f.restype = _i64
+lib.tpmlp_get_mxfp4_mode.argtypes = []
+lib.tpmlp_get_mxfp4_mode.restype = ctypes.c_int
 lib.tpmlp_status_string.argtypes = [ctypes.c_int]
 lib.tpmlp_status_string.restype = ctypes.c_char_p
 lib.tpmlp_last_error.argtypes = []
@@ -183,6 +196,69 @@ def tpmlp_swiglu_mlp_bwd(X, W_sh, B_sh, H_ws, Y_ws, dZ, dX, dW_sh, dB_sh, dbw_sh
 def tpmlp_swiglu_pack(G, U, W_sh, rows, ffn, p, dt=BF16, inverse=0, stream=None, check=True):
     st = lib.tpmlp_swiglu_pack(_ptr(G), _ptr(U), _ptr(W_sh), rows, ffn, p, dt, int(inverse), _stream(stream))
     return _done(st, check)
+
+
+def tpmlp_mxfp4_code_bytes(rows, k) -> int:
+    return int(lib.tpmlp_mxfp4_code_bytes(rows, k))
+
+
+def tpmlp_mxfp4_scale_bytes(rows, k) -> int:
+    return int(lib.tpmlp_mxfp4_scale_bytes(rows, k))
+
+
+def mxfp4_empty(rows, k, device="cuda"):
+    """Uninitialised (codes, scales) of an MXFP4 operand [rows, k]: bytes [rows, ceil(k/32) * 16] and scale
+    tiles [ceil(rows/128), ceil(k/128), 32, 4, 4]."""
+    import torch
+    return (torch.empty((rows, -(-k // 32) * 16), dtype=torch.uint8, device=device),
+            torch.empty((-(-rows // 128), -(-k // 128), 32, 4, 4), dtype=torch.uint8, device=device))
+
+
+def tpmlp_mxfp4_quantize(X, Q, S, Qt, St, rows, cols, ldx, p=1, dt=BF16, stream=None, check=True):
+    """X [p][rows][cols/p] -> (Q, S) in blocks of 32 columns and / or (Qt, St) in blocks of 32 rows."""
+    st = lib.tpmlp_mxfp4_quantize(_ptr(X), _ptr(Q), _ptr(S), _ptr(Qt), _ptr(St), rows, cols, ldx, p, dt,
+                                  _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_mxfp4_dequantize(Q, S, out, rows, k, dt=BF16, stream=None, check=True):
+    return _done(lib.tpmlp_mxfp4_dequantize(_ptr(Q), _ptr(S), _ptr(out), rows, k, dt, _stream(stream)), check)
+
+
+def tpmlp_mxfp4_matmul(Aq, As, Bq, Bs, bias, D, m, n, k, out_dt=BF16, stream=None, check=True):
+    """D[m, n] = sum_k A[m, k] B[n, k] + bias[n] on MXFP4 operands."""
+    st = lib.tpmlp_mxfp4_matmul(_ptr(Aq), _ptr(As), _ptr(Bq), _ptr(Bs), _ptr(bias), _ptr(D), m, n, k, out_dt,
+                                _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_mxfp4_swiglu_ws_bytes(s, b, h, ffn, p, backward=0) -> int:
+    return int(lib.tpmlp_mxfp4_swiglu_ws_bytes(s, b, h, ffn, p, int(backward)))
+
+
+def tpmlp_mxfp4_swiglu_mlp_fwd(X, Wq, Ws, bw_sh, Bq, Bs, b2, Z, H, ws, s, b, h, ffn, p, z_dt=BF16, stream=None,
+                               check=True):
+    """The SwiGLU block forward on MXFP4 operands; H (or None) saves the packed bf16 pre-activations."""
+    st = lib.tpmlp_mxfp4_swiglu_mlp_fwd(_ptr(X), _ptr(Wq), _ptr(Ws), _ptr(bw_sh), _ptr(Bq), _ptr(Bs), _ptr(b2), _ptr(Z),
+                                        _ptr(H), _ptr(ws), s, b, h, ffn, p, z_dt, _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_mxfp4_swiglu_mlp_bwd(X, Wq, Ws, Bq, Bs, H, dZ, dX, dW_sh, dB_sh, dbw_sh, db2, ws, s, b, h, ffn, p, dx_dt=BF16,
+                               grad_dt=F32, stream=None, check=True):
+    """Its backward; W and B quantised along their columns (the forward's are quantised along their rows)."""
+    st = lib.tpmlp_mxfp4_swiglu_mlp_bwd(_ptr(X), _ptr(Wq), _ptr(Ws), _ptr(Bq), _ptr(Bs), _ptr(H), _ptr(dZ), _ptr(dX),
+                                        _ptr(dW_sh), _ptr(dB_sh), _ptr(dbw_sh), _ptr(db2), _ptr(ws), s, b, h, ffn, p,
+                                        dx_dt, grad_dt, _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_set_mxfp4_mode(mode, check=True):
+    return _done(lib.tpmlp_set_mxfp4_mode(mode), check)
+
+
+def tpmlp_get_mxfp4_mode() -> int:
+    return int(lib.tpmlp_get_mxfp4_mode())
 
 
 def tpmlp_row_bwd(Y_sh, B_sh, dZ, H_sh, dY_sh, dB_sh, db2, s, b, h, ffn, p, dt=BF16, grad_dt=F32, act=ACT_NONE,
