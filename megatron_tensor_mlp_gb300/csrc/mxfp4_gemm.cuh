@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint64_t* drain = shared_free + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform for the compiler
     const int lane = threadIdx.x & 31;
     const uint32_t prank = cluster_ctarank();
     const bool leader = prank == 0;
@@ -318,38 +318,36 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------------------ producer (both CTAs)
-            int stage = 0;
-            uint32_t phase = 0, armed = 0, last_parity = 0;
-            bool ok = true;
-            const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-            for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters) {
-                int mb, nb;
-                decode_tile(p, t, mb, nb);
-                const int row_tile = mb * 2 + static_cast<int>(prank);
-                const int col0 = nb * P_BN + static_cast<int>(prank) * BM;
-                for (int it = 0; it < p.kb; ++it) {
-                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    if (leader) {
-                        mbar_arrive_expect_tx(full + stage, 2 * P_STAGE);
-                        armed |= 1u << stage;
-                        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-                    }
+        // ---------------------------------------------------------------- producer (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0, armed = 0, last_parity = 0;
+        bool ok = true;
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters) {
+            int mb, nb;
+            decode_tile(p, t, mb, nb);
+            const int row_tile = mb * 2 + static_cast<int>(prank);
+            const int col0 = nb * P_BN + static_cast<int>(prank) * BM;
+            for (int it = 0; it < p.kb; ++it) {
+                ok = mbar_wait_bounded_warp(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereProducer);
+                if (!ok) break;
+                if (elect_one()) {
+                    if (leader) mbar_arrive_expect_tx(full + stage, 2 * P_STAGE);
                     const uint32_t bar = full0 + stage * 8;
                     tma_load_3d_pair(sA + stage * OP_BYTES, &tmA, bar, it * 128, row_tile * BM, 0);
                     tma_load_3d_pair(sB + stage * OP_BYTES, &tmB, bar, it * 128, col0, 0);
                     tma_load_3d_pair(sSA + stage * P_SFA_BYTES, &tmSA, bar, 0, it * 2, row_tile);
                     tma_load_3d_pair(sSB + stage * P_SFB_BYTES, &tmSB, bar, 0, it * 2, nb * 2);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                armed |= 1u << stage;
+                last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
+        }
+        if (lane == 0) {
             if (ok) {
                 // every stage's last release has arrived before this CTA can exit
                 for (int i = 0; i < STAGES; ++i) {
@@ -359,39 +357,35 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                         phase ^= 1u;
                     }
                 }
+            } else if (leader) {
+                for (int s = 0; s < STAGES; ++s)
+                    if (armed & (1u << s))
+                        mbar_wait_bounded(full + s, (last_parity >> s) & 1u, p.status, p.timeout_ns, kWhereDrain, false);
             } else {
-                if (leader) {
-                    for (int s = 0; s < STAGES; ++s)
-                        if (armed & (1u << s))
-                            mbar_wait_bounded(full + s, (last_parity >> s) & 1u, p.status, p.timeout_ns, kWhereDrain, false);
-                } else {
-                    spin_ns(200000);  // this CTA's last copies, counted on the leader's barriers, land
-                }
+                spin_ns(200000);  // this CTA's last copies, counted on the leader's barriers, land
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            if (leader) {
-                // -------------------------------------------------------- MMA issuer (leader)
-                const uint64_t a0 = sdesc_sw128(smem_u32(sA), 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
-                const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
-                int stage = 0;
-                uint32_t phase = 0;
-                int lt = 0;
-                bool ok = true;
-                for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters, ++lt) {
-                    const int acc = lt & 1;
-                    ok = mbar_wait_bounded(tempty + acc, ((lt >> 1) & 1) ^ 1u, p.status, p.timeout_ns, kWhereMma);
-                    if (ok && lt > 0) ok = mbar_wait_bounded(shared_free, (lt - 1) & 1, p.status, p.timeout_ns, kWhereMma);
+        if (leader) {
+            // ------------------------------------------------------------ MMA issuer (leader)
+            const uint64_t a0 = sdesc_sw128(smem_u32(sA), 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+            const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
+            int stage = 0;
+            uint32_t phase = 0;
+            int lt = 0;
+            bool ok = true;
+            for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters, ++lt) {
+                const int acc = lt & 1;
+                ok = mbar_wait_bounded_warp(tempty + acc, ((lt >> 1) & 1) ^ 1u, p.status, p.timeout_ns, kWhereMma);
+                if (ok && lt > 0) ok = mbar_wait_bounded_warp(shared_free, (lt - 1) & 1, p.status, p.timeout_ns, kWhereMma);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + acc * P_ACC1;
+                for (int it = 0; it < p.kb; ++it) {
+                    ok = mbar_wait_bounded_warp(full + stage, phase, p.status, p.timeout_ns, kWhereMma);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem_base + acc * P_ACC1;
-                    for (int it = 0; it < p.kb; ++it) {
-                        if (!mbar_wait_bounded(full + stage, phase, p.status, p.timeout_ns, kWhereMma)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
+                    if (elect_one()) {
                         const uint64_t ad = a0 + static_cast<uint64_t>(stage * (OP_BYTES >> 4));
                         const uint64_t bd = b0 + static_cast<uint64_t>(stage * (OP_BYTES >> 4));
                         const uint64_t sad = sa0 + static_cast<uint64_t>(stage * (P_SFA_BYTES >> 4));
@@ -413,21 +407,23 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                                              (it | kk) != 0 ? 1u : 0u);
                         }
                         umma_commit_pair_mc(empty + stage, 0x3);
-                        if (++stage == STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                        if (it + 1 == p.kb) umma_commit_pair_mc(tfull + acc, 0x3);
                     }
-                    if (ok) umma_commit_pair_mc(tfull + acc, 0x3);
+                    __syncwarp();
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                umma_commit_pair_mc(drain, 0x3);
-                // the last releases of the epilogue warps, some from the peer SM, land before this CTA can exit
-                if (ok && lt > 0) ok = mbar_wait_bounded(shared_free, (lt - 1) & 1, p.status, p.timeout_ns, kWhereDrain);
-                for (int i = 0; ok && i < 2; ++i, ++lt)
-                    ok = mbar_wait_bounded(tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, p.status, p.timeout_ns, kWhereDrain);
             }
-            mbar_wait_bounded(drain, 0, p.status, p.timeout_ns, kWhereDrain, /*watch_status=*/false);
+            if (elect_one()) umma_commit_pair_mc(drain, 0x3);
+            __syncwarp();
+            // the last releases of the epilogue warps, some from the peer SM, land before this CTA can exit
+            if (ok && lt > 0) ok = mbar_wait_bounded_warp(shared_free, (lt - 1) & 1, p.status, p.timeout_ns, kWhereDrain);
+            for (int i = 0; ok && i < 2; ++i, ++lt)
+                ok = mbar_wait_bounded_warp(tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, p.status, p.timeout_ns, kWhereDrain);
         }
+        if (lane == 0) mbar_wait_bounded(drain, 0, p.status, p.timeout_ns, kWhereDrain, /*watch_status=*/false);
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3;
@@ -521,7 +517,7 @@ __global__ void __launch_bounds__(S_THREADS, 2)
     uint64_t* tfull = empty + S_MAX_STAGES;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform for the compiler
     const int lane = threadIdx.x & 31;
     uint32_t split, rank;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
@@ -559,18 +555,14 @@ __global__ void __launch_bounds__(S_THREADS, 2)
     const int f0 = nb * 64;
     const int gate_row = (f0 >> 7) * 256 + (f0 & 127);
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------------------ producer
-            int stage = 0;
-            uint32_t phase = 0, armed = 0, last_parity = 0;
-            bool ok = true;
-            const uint32_t bytes = static_cast<uint32_t>(a_bytes + OP_BYTES + 2 * SF_TILE + SFB);
-            for (int it = it0; it < it1; ++it) {
-                ok = mbar_wait_bounded(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereProducer);
-                if (!ok) break;
+        // ---------------------------------------------------------------- producer
+        int stage = 0;
+        uint32_t phase = 0, armed = 0, last_parity = 0;
+        const uint32_t bytes = static_cast<uint32_t>(a_bytes + OP_BYTES + 2 * SF_TILE + SFB);
+        for (int it = it0; it < it1; ++it) {
+            if (!mbar_wait_bounded_warp(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereProducer)) break;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(full + stage, bytes);
-                armed |= 1u << stage;
-                last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
                 uint8_t* b = sB + stage * OP_BYTES;
                 if constexpr (GATED) {
                     tma_load_3d(b, &tmB, full + stage, it * 128, gate_row, 0);
@@ -582,26 +574,30 @@ __global__ void __launch_bounds__(S_THREADS, 2)
                 }
                 tma_load_3d(sA + stage * a_bytes, &tmA, full + stage, it * 128, mb * BM, 0);
                 tma_load_3d(sSA + stage * 2 * SF_TILE, &tmSA, full + stage, 0, it * 2, mb);
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
             }
-            // all copies have landed before this CTA can reuse its ring or exit, also where a wait gave up
+            armed |= 1u << stage;
+            last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        // all copies have landed before this CTA can reuse its ring or exit, also where a wait gave up
+        if (lane == 0) {
             for (int s = 0; s < p.stages; ++s)
                 if (armed & (1u << s))
                     mbar_wait_bounded(full + s, (last_parity >> s) & 1u, p.status, p.timeout_ns, kWhereDrain, false);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------------------------------------ MMA issuer
-            const uint64_t a0 = sdesc_sw128(smem_u32(sA), 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
-            const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int it = it0; it < it1; ++it) {
-                if (!mbar_wait_bounded(full + stage, phase, p.status, p.timeout_ns, kWhereMma)) break;
-                tc_fence_after();
+        // ---------------------------------------------------------------- MMA issuer
+        const uint64_t a0 = sdesc_sw128(smem_u32(sA), 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+        const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int it = it0; it < it1; ++it) {
+            if (!mbar_wait_bounded_warp(full + stage, phase, p.status, p.timeout_ns, kWhereMma)) break;
+            tc_fence_after();
+            if (elect_one()) {
                 const uint64_t ad = a0 + static_cast<uint64_t>(stage * (a_bytes >> 4));
                 const uint64_t bd = b0 + static_cast<uint64_t>(stage * (OP_BYTES >> 4));
                 const uint64_t sad = sa0 + static_cast<uint64_t>(stage * (2 * SF_TILE >> 4));
@@ -632,13 +628,14 @@ __global__ void __launch_bounds__(S_THREADS, 2)
                     }
                 }
                 umma_commit(empty + stage);
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
             }
-            umma_commit(tfull);
+            __syncwarp();
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
         }
+        if (elect_one()) umma_commit(tfull);
     }
     __syncwarp();
     const int q = warp & 3;

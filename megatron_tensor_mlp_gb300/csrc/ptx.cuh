@@ -309,6 +309,24 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// True in one lane of a converged warp (the same one each time).  Where a whole warp walks a loop and
+// only this lane issues, the loop's values stay in uniform registers, which tcgen05 and TMA
+// instructions read; a loop that one lane walks alone has to move them there for every instruction.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+// mbar_wait_bounded by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t* bar, uint32_t parity, uint32_t* status, uint64_t timeout_ns,
+                                                       uint32_t where, bool watch_status = true) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, status, timeout_ns, where, watch_status)) != 0;
+}
+
 // Busy-wait for about `ns` nanoseconds.
 __device__ __forceinline__ void spin_ns(uint64_t ns) {
     const uint64_t t0 = globaltimer_ns();
