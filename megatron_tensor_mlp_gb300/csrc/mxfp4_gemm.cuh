@@ -126,6 +126,16 @@ __device__ __forceinline__ void store_chunk(const Args& p, float (&v)[32], int g
     else tc::store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + at, v, nvalid, p.st32 != 0);
 }
 
+// Two fp32 values in one register pair: sums and products of both in one instruction.
+using f2 = unsigned long long;
+// sigma(x) = 1 / (1 + 2^(-x log2 e)) with the hardware approximations.
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+    float a, b;
+    tc::f2_unpack(tc::f2_mul(x, tc::f2_pack(-1.4426950408889634f, -1.4426950408889634f)), a, b);
+    tc::f2_unpack(tc::f2_add(tc::f2_pack(tc::ex2_approx(a), tc::ex2_approx(b)), tc::f2_pack(1.0f, 1.0f)), a, b);
+    return tc::f2_pack(tc::rcp_approx(a), tc::rcp_approx(b));
+}
+
 // EPI_SWIGLU: y = silu(g) u for features f0..f0+31 of a row (one block), quantised from fp32.
 __device__ __forceinline__ void swiglu_chunk(const Args& p, float (&g)[32], float (&u)[32], int gm, int f0) {
     if (gm >= p.M || 2 * f0 >= p.N) return;
@@ -149,7 +159,10 @@ __device__ __forceinline__ void swiglu_chunk(const Args& p, float (&g)[32], floa
         tc::store_bf16x32(d + 128, u, 32, p.st32 != 0);
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) g[j] = g[j] * tc::sigmoid_approx(g[j]) * u[j];
+    for (int j = 0; j < 32; j += 2) {
+        const f2 x = tc::f2_pack(g[j], g[j + 1]);
+        tc::f2_unpack(tc::f2_mul(tc::f2_mul(x, sigmoid2(x)), tc::f2_pack(u[j], u[j + 1])), g[j], g[j + 1]);
+    }
     uint4 c;
     const uint32_t s = quantize32(g, c);
     *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + f0 / 2) = c;
@@ -178,42 +191,73 @@ __device__ __forceinline__ void put_token_block(const Args& p, uint8_t* q, uint8
     if (tb < p.t_tiles * 4) qs[scale_offset(col, tb, p.t_tiles)] = static_cast<uint8_t>(s);
 }
 
-// EPI_DSWIGLU: dY of features f0..f0+31 of this thread's row (token) and, from the saved bf16
-// pre-activations, dg = dY u silu'(g), du = dY silu(g) and y = silu(g) u, from fp32 quantised along the
-// columns (dg, du) and, turned through shared memory, along the tokens (dg, du, y).  tb: the warp's block of
-// 32 tokens.  Rows past M count as zero.
-__device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], int gm, int f0, int tb, float* buf, int lane) {
+// The saved bf16 pre-activations of features f0..f0+31 of row gm: 16 words of gate, 16 of up pairs;
+// zero past the last row.
+__device__ __forceinline__ void load_h(const Args& p, int gm, int f0, uint32_t (&h)[32]) {
+    if (gm < p.M && f0 < p.N) {
+        const __nv_bfloat16* hp = p.h_in + gm * p.h_ld + (long long)(f0 >> 7) * 256 + (f0 & 127);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            if (p.st32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t w[8];
+                    tc::ld_v8(hp + part * 128 + i * 16, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[part * 16 + i * 8 + j] = w[j];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(hp + part * 128 + i * 8);
+                    h[part * 16 + i * 4] = w.x;
+                    h[part * 16 + i * 4 + 1] = w.y;
+                    h[part * 16 + i * 4 + 2] = w.z;
+                    h[part * 16 + i * 4 + 3] = w.w;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) h[j] = 0;
+    }
+}
+
+// EPI_DSWIGLU: v = dY of features f0..f0+31 of this thread's row (token) and, from its pre-activations h,
+// dg = dY u silu'(g), du = dY silu(g) and y = silu(g) u, from fp32 quantised along the columns (dg, du) and,
+// turned through shared memory, along the tokens (dg, du, y).  tb: the warp's block of 32 tokens.  Rows past
+// M count as zero.  The next chunk's pre-activations (row gm_next) are loaded into h behind the quantisation.
+__device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], uint32_t (&h)[32], int gm, int f0, int tb, float* buf,
+                                              int lane, int f_next) {
     if (f0 >= p.N) return;  // (whole warp; features come in multiples of 128)
     const long long pg = (long long)(f0 >> 7) * 256 + (f0 & 127);
     const bool live = gm < p.M;
+    const f2 one = tc::f2_pack(1.0f, 1.0f);
     float g[32], u[32];
-    if (live) {
-        const __nv_bfloat16* hp = p.h_in + gm * p.h_ld + pg;
-        tc::load_bf16x32(hp, g, 32, p.st32 != 0);
-        tc::load_bf16x32(hp + 128, u, 32, p.st32 != 0);
-    }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float dy = v[j], gj = g[j], uj = u[j];
-        const float sg = tc::sigmoid_approx(gj), sl = gj * sg;
-        g[j] = live ? dy * uj * (sg * (1.0f + gj * (1.0f - sg))) : 0.0f;  // dg
-        u[j] = live ? dy * sl : 0.0f;                                     // du
-        v[j] = live ? sl * uj : 0.0f;                                     // y
+    for (int j = 0; j < 32; j += 2) {
+        const f2 g2 = tc::f2_pack(__uint_as_float(h[j / 2] << 16), __uint_as_float(h[j / 2] & 0xFFFF0000u));
+        const f2 u2 = tc::f2_pack(__uint_as_float(h[16 + j / 2] << 16), __uint_as_float(h[16 + j / 2] & 0xFFFF0000u));
+        // (a row past the last may hold a NaN from the scales beside it)
+        const f2 dy = tc::f2_pack(live ? v[j] : 0.0f, live ? v[j + 1] : 0.0f);
+        const f2 sg = sigmoid2(g2), sl = tc::f2_mul(g2, sg);
+        const f2 ds = tc::f2_mul(sg, tc::f2_fma(g2, tc::f2_fma(sg, tc::f2_pack(-1.0f, -1.0f), one), one));  // silu'
+        tc::f2_unpack(tc::f2_mul(tc::f2_mul(dy, u2), ds), g[j], g[j + 1]);
+        tc::f2_unpack(tc::f2_mul(sl, u2), v[j], v[j + 1]);
+        tc::f2_unpack(tc::f2_mul(dy, sl), u[j], u[j + 1]);
     }
-    if (live) {
-        uint4 c;
-        uint32_t s = quantize32(g, c);
-        *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + pg / 2) = c;
-        p.qs[scale_offset(gm, pg >> 5, p.q_tiles)] = static_cast<uint8_t>(s);
-        s = quantize32(u, c);
-        *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + pg / 2 + 64) = c;
-        p.qs[scale_offset(gm, (pg >> 5) + 4, p.q_tiles)] = static_cast<uint8_t>(s);
-    }
+    if (f_next >= 0) load_h(p, gm, f_next, h);
     float w[32];
     turn32(buf, v, w, lane);
     put_token_block(p, p.yt, p.yts, w, f0 + lane, tb);
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
+        if (live) {
+            uint4 c;
+            const uint32_t s = quantize32(part ? u : g, c);
+            *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + pg / 2 + part * 64) = c;
+            p.qs[scale_offset(gm, (pg >> 5) + part * 4, p.q_tiles)] = static_cast<uint8_t>(s);
+        }
         turn32(buf, part ? u : g, w, lane);
         put_token_block(p, p.ht, p.hts, w, pg + part * 128 + lane, tb);
         if (p.colsum != nullptr && (long long)tb * 16 < p.t_pitch) {
@@ -433,22 +477,25 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         int lt = 0;
         for (int t = cluster_id; t < p.num_tiles; t += n_clusters, ++lt) {
             const int acc = lt & 1;
+            int mb, nb;
+            decode_tile(p, t, mb, nb);  // before the wait: the next tile's MMAs wait for the first columns read here
+            const int row0 = mb * (2 * BM) + static_cast<int>(prank) * BM + q * 32;
+            constexpr int CH = EPI == EPI_SWIGLU ? 2 : 4;
+            const int col0 = half * (CH * 32);
+            // The first accumulator's shared columns are its last, the second's its first: walk the
+            // chunks so that they come first.  half 1 - acc holds them.
+            const int c_first = acc == 0 ? CH - 1 : 0, c_step = acc == 0 ? -1 : 1;
+            [[maybe_unused]] uint32_t h[32];
+            if constexpr (EPI == EPI_DSWIGLU) load_h(p, row0 + lane, nb * P_BN + col0 + c_first * 32, h);
             int okw = 0;
             if (lane == 0) okw = mbar_wait_bounded(tfull + acc, (lt >> 1) & 1, p.status, p.timeout_ns, kWhereEpilogue);
             okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
             if (!okw) break;
             tc_fence_after();
-            int mb, nb;
-            decode_tile(p, t, mb, nb);
-            const int row0 = mb * (2 * BM) + static_cast<int>(prank) * BM + q * 32;
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * P_ACC1;
-            // The first accumulator's shared columns are its last, the second's its first: walk the
-            // chunks so that they come first.  half 1 - acc holds them.
-            constexpr int CH = EPI == EPI_SWIGLU ? 2 : 4;
 #pragma unroll 1
             for (int i = 0; i < CH; ++i) {
-                const int c = acc == 0 ? CH - 1 - i : i;
-                const int col = half * (CH * 32) + c * 32;
+                const int col = col0 + (c_first + i * c_step) * 32;
                 float v[32];
                 [[maybe_unused]] float u[32];
                 load_acc32(t_row + col, v);
@@ -459,7 +506,9 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     if (lane == 0) mbar_arrive_cluster(shared0);
                 }
                 if constexpr (EPI == EPI_SWIGLU) swiglu_chunk(p, v, u, row0 + lane, nb * 128 + col);
-                else if constexpr (EPI == EPI_DSWIGLU) dswiglu_chunk(p, v, row0 + lane, nb * P_BN + col, row0 >> 5, buf, lane);
+                else if constexpr (EPI == EPI_DSWIGLU)
+                    dswiglu_chunk(p, v, h, row0 + lane, nb * P_BN + col, row0 >> 5, buf, lane,
+                                  i + 1 < CH ? nb * P_BN + col + c_step * 32 : -1);
                 else store_chunk(p, v, row0 + lane, nb * P_BN + col);
             }
             tc_fence_before();
@@ -712,8 +761,11 @@ __global__ void __launch_bounds__(S_THREADS, 2)
                 }
             }
             if constexpr (GATED) swiglu_chunk(p, v, u, row0 + lane, f0 + c * 32);
-            else if constexpr (EPI == EPI_DSWIGLU) dswiglu_chunk(p, v, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, lane);
-            else store_chunk(p, v, row0 + lane, nb * S_BN + c * 32);
+            else if constexpr (EPI == EPI_DSWIGLU) {
+                uint32_t h[32];
+                load_h(p, row0 + lane, nb * S_BN + c * 32, h);
+                dswiglu_chunk(p, v, h, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, lane, -1);
+            } else store_chunk(p, v, row0 + lane, nb * S_BN + c * 32);
         }
     }
     tc_fence_before();

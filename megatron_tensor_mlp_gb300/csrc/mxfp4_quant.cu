@@ -10,51 +10,54 @@
 namespace tpmlp {
 namespace {
 
-using mx::abs_bits;
-
-// 16 bytes of a row (8 bf16 or 4 fp32 values) widened to fp32; the first n of them, the rest zero.
+// 16 bytes of a row: 8 bf16 or 4 fp32 values.
 template <bool F32>
-struct Vec {
-    static constexpr int E = F32 ? 4 : 8;
-    float v[E];
-    uint4 raw;
-    __device__ __forceinline__ void load(const void* p, int n) {
-        if (n >= E) {
-            raw = *static_cast<const uint4*>(p);
-        } else {  // a row's ragged end: nothing past it is read
-            uint32_t w[4] = {0, 0, 0, 0};
-            for (int i = 0; i < n; ++i) {
-                if constexpr (F32) {
-                    w[i] = static_cast<const uint32_t*>(p)[i];
-                } else {
-                    w[i >> 1] |= static_cast<uint32_t>(static_cast<const unsigned short*>(p)[i]) << (16 * (i & 1));
-                }
+struct Piece {
+    static constexpr int E = F32 ? 4 : 8, ES = F32 ? 4 : 2;
+    static constexpr int LANES = 32 / E;  // lanes that share a block of 32
+
+    // The first n values at p, zeros behind them; nothing past them is read.
+    static __device__ __forceinline__ uint4 load(const uint8_t* p, int n) {
+        if (n >= E) return *reinterpret_cast<const uint4*>(p);
+        uint32_t w[4] = {0, 0, 0, 0};
+        for (int i = 0; i < n; ++i) {
+            if constexpr (F32) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+            else w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(p)[i]) << (16 * (i & 1));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // Scale byte of the block that this lane and its neighbours hold.
+    static __device__ __forceinline__ uint32_t scale(const uint4& r) {
+        uint32_t a;  // the bits of the largest magnitude as fp32
+        if constexpr (F32) {
+            a = __float_as_uint(mx::amax3(mx::amax3(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z)),
+                                          __uint_as_float(r.w), 0.0f));
+        } else {
+            const uint32_t m = mx::amax_bf16x2(mx::amax_bf16x2(r.x, r.y), mx::amax_bf16x2(r.z, r.w)) & 0x7FFF7FFFu;
+            a = max(m & 0xFFFF0000u, m << 16);
+        }
+#pragma unroll
+        for (int d = 1; d < LANES; d *= 2) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
+        return mx::scale_of(a);
+    }
+    // This lane's codes, E of them in the low E * 4 bits.
+    static __device__ __forceinline__ uint32_t codes(const uint4& r, uint32_t s) {
+        const float inv = mx::inverse_scale(s);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (F32) {
+                v[i] = __uint_as_float(w[i]);
+                v[4 + i] = 0.0f;
+            } else {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
             }
-            raw = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if constexpr (F32) v[i] = __uint_as_float(w[i]);
-            else v[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-        }
-    }
-    // Largest |v| over this thread's values and those of the other lanes of its block of 32.
-    __device__ __forceinline__ uint32_t block_amax() const {
-        uint32_t a = abs_bits(v[0]);
-#pragma unroll
-        for (int i = 1; i < E; ++i) a = max(a, abs_bits(v[i]));
-#pragma unroll
-        for (int d = 1; d < 32 / E; d *= 2) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
-        return a;
-    }
-    // This thread's codes (E of them in the low E * 4 bits).
-    __device__ __forceinline__ uint32_t codes(uint32_t s) const {
-        const float i = mx::inverse_scale(s);
-        if (s == 255u) return 0;
-        if constexpr (F32) return mx::encode8(v[0] * i, v[1] * i, v[2] * i, v[3] * i, 0.f, 0.f, 0.f, 0.f);
-        else
-            return mx::encode8(v[0] * i, v[1] * i, v[2] * i, v[3] * i, v[4] * i, v[5] * i, v[6] * i, v[7] * i);
+        for (int i = 0; i < E; i += 2) mx::mul2(v[i], v[i + 1], inv);
+        return s == 255u ? 0u : mx::encode8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
     }
 };
 
@@ -66,163 +69,197 @@ struct QuantArgs {
     uint8_t* s;
     uint8_t* qt;
     uint8_t* st;
+    long long spans;    // row kernel: warp spans a row; both kernel: column tiles
+    long long items;    // row kernel: spans of all rows; both kernel: tiles
 };
 
-// Along the columns only.  A group of 16 lanes takes 16 consecutive 16-byte pieces of one row (4
-// blocks of bf16 values, 2 of fp32), one piece a lane; a block's maximum takes 2 (bf16) or 3
-// (fp32) shuffles, its codes go out 4 (2) bytes a lane, its scales as one word (half word).  Bound
-// by memory; for one token by the launch.
+// Address and number of values of the piece at logical column c0 (row 0).
 template <bool F32>
+__device__ __forceinline__ const uint8_t* piece_at(const QuantArgs& a, long long c0, int& n) {
+    n = 0;
+    if (c0 >= static_cast<long long>(a.cols) * a.p) return a.x;
+    // shards are multiples of 32 columns wide (or there is one), so a piece lies in one shard
+    const long long sh = a.p == 1 ? 0 : c0 / a.cols;
+    const long long c = c0 - sh * a.cols;
+    n = static_cast<int>(a.cols - c < Piece<F32>::E ? a.cols - c : Piece<F32>::E);
+    return a.x + sh * a.ss + c * Piece<F32>::ES;
+}
+
+// Along the columns only: a warp takes U spans of 512 bytes of a row, a 16-byte piece a lane, all
+// loaded before the first is worked on.  A block's maximum takes 2 (bf16) or 3 (fp32) shuffles; its
+// codes go out 4 (2) bytes a lane.  Bound by memory; for one token by the launch.
+template <bool F32, int U>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
-    constexpr int E = Vec<F32>::E, SPAN = 16 * E, ES = F32 ? 4 : 2;
+    using P = Piece<F32>;
+    constexpr int SPAN = 32 * P::E;
+    const int lane = threadIdx.x & 31;
+    const long long total = static_cast<long long>(a.cols) * a.p;
+    const long long k_tiles = (total + 127) / 128, pitch = (total + 31) / 32 * 16;
+    const long long it0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * U;
+    long long row = it0 / a.spans, span = it0 - row * a.spans;
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    const int lane16 = threadIdx.x & 15;
-    const long long total_cols = static_cast<long long>(a.cols) * a.p;
-    // spans up to a multiple of 128 columns: the scales of padding blocks are written as zero
-    const long long spans = (total_cols + 127) / 128 * (128 / SPAN);
-    const long long k_tiles = (total_cols + 127) / 128;
-    const long long pitch = (total_cols + 31) / 32 * 16;
-    const long long items = spans * a.rows;
-    const long long step = static_cast<long long>(gridDim.x) * 16;
-    for (long long it = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 4); __any_sync(0xFFFFFFFFu, it < items);
-         it += step) {
-        const bool live = it < items;
-        const long long row = live ? it / spans : 0;
-        const long long c0 = live ? (it - row * spans) * SPAN + lane16 * E : total_cols;
-        Vec<F32> v;
-        int n = 0;
-        const uint8_t* src = a.x;
-        if (c0 < total_cols) {
-            // shards are at least 32 columns apart in multiples of 32, so a piece lies in one shard
-            const long long sh = a.p == 1 ? 0 : c0 / a.cols;
-            const long long c = c0 - sh * a.cols;
-            n = static_cast<int>(a.cols - c < E ? a.cols - c : E);
-            src = a.x + sh * a.ss + row * a.ldx + c * ES;
-        }
-        v.load(src, n);
-        const uint32_t s = mx::scale_of(v.block_amax());
-        const uint32_t code = v.codes(s);
-        if (c0 / 2 < pitch && live) {
-            if constexpr (F32) *reinterpret_cast<uint16_t*>(a.q + row * pitch + c0 / 2) = static_cast<uint16_t>(code);
-            else *reinterpret_cast<uint32_t*>(a.q + row * pitch + c0 / 2) = code;
-        }
-        // the group's scales in one word
-        constexpr int LB = 32 / E;  // lanes a block
-        const int lane = threadIdx.x & 31;
-        uint32_t w = 0;
+    uint4 r[U];
+    long long rows[U], c0[U];
 #pragma unroll
-        for (int j = 0; j < 16 / LB; ++j) w |= __shfl_sync(0xFFFFFFFFu, s, (lane & 16) + j * LB) << (8 * j);
-        if (lane16 == 0 && live) {
-            uint8_t* d = a.s + mx::scale_offset(row, c0 / 32, k_tiles);
-            if constexpr (F32) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(w);
-            else *reinterpret_cast<uint32_t*>(d) = w;
+    for (int i = 0; i < U; ++i) {
+        rows[i] = row;
+        c0[i] = span * SPAN + lane * P::E;
+        int n;
+        const uint8_t* src = piece_at<F32>(a, c0[i], n);
+        r[i] = P::load(src + row * a.ldx, row < a.rows ? n : 0);
+        if (++span == a.spans) {
+            span = 0;
+            ++row;
         }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const uint32_t s = P::scale(r[i]);
+        const uint32_t code = P::codes(r[i], s);
+        if (rows[i] >= a.rows) continue;
+        if (c0[i] / 2 < pitch) {
+            uint8_t* d = a.q + rows[i] * pitch + c0[i] / 2;
+            if constexpr (F32) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(code);
+            else *reinterpret_cast<uint32_t*>(d) = code;
+        }
+        // (padding blocks up to a whole scale tile: zero)
+        if (lane % P::LANES == 0 && c0[i] < k_tiles * 128)
+            a.s[mx::scale_offset(rows[i], c0[i] >> 5, k_tiles)] = static_cast<uint8_t>(s);
     }
 }
 
-// Along the rows, and along the columns too where q is given: a CTA takes 128 rows x 256 bytes of
-// columns (128 bf16, 64 fp32).  It reads the tile once, 16 lanes to a row, quantises the rows'
-// blocks on the way into shared memory, and then the columns' from there (a thread takes 32 rows of
-// one word: two bf16 columns or one fp32 column), whose codes it gathers in shared memory so that
-// each column leaves as one run of 64 bytes.
+// Along the rows, and along the columns too where q is given.  A CTA walks tiles of 128 rows x 256
+// bytes of columns (128 bf16, 64 fp32) through two shared-memory buffers, the next tile's
+// asynchronous copies running behind the work on this one: the tile's values are read from memory
+// once and its two quantisations work from shared memory.  Along the columns 16 lanes take a row;
+// along the rows a thread takes 32 rows of one word (two bf16 columns or one fp32 column), and the
+// codes are gathered in shared memory so that each column leaves as one run of 64 bytes.
+template <bool F32>
+struct BothSmem {
+    uint32_t tile[2][128 * 64];
+    uint8_t out[256 / Piece<F32>::ES * 80];  // 64 bytes of codes a column, pitch 80
+    uint32_t sc[256 / Piece<F32>::ES];
+};
+
 template <bool F32>
 __global__ void __launch_bounds__(256) quantize_both_kernel(const QuantArgs a) {
-    constexpr int E = Vec<F32>::E, ES = F32 ? 4 : 2, TC = 256 / ES, LB = 32 / E;
-    __shared__ __align__(16) uint32_t tile[128 * 64];
-    __shared__ __align__(16) uint8_t out[TC * 80];  // 64 bytes of codes a column, pitch 80
-    __shared__ uint32_t sc[TC];
-    griddep_wait();
-    if (threadIdx.x == 0) griddep_launch_dependents();
+    using P = Piece<F32>;
+    constexpr int TC = 256 / P::ES;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    BothSmem<F32>& sm = *reinterpret_cast<BothSmem<F32>*>(smem_raw);
     const int t = threadIdx.x, lane16 = t & 15;
-    const long long total_cols = static_cast<long long>(a.cols) * a.p;
-    // (up to a multiple of 128 columns: the scales of padding blocks are written as zero)
-    const unsigned col_tiles = static_cast<unsigned>((total_cols + 127) / 128 * (128 / TC));
-    const int row_tile = static_cast<int>(blockIdx.x / col_tiles);
-    const long long c_tile = static_cast<long long>(blockIdx.x - row_tile * col_tiles) * TC;
-    const int r_tile = row_tile * 128;
-    const long long k_tiles = (total_cols + 127) / 128;
-    const long long pitch = (total_cols + 31) / 32 * 16;
-    {
-        const long long c0 = c_tile + lane16 * E;
-        const uint8_t* src = a.x;
-        int n = 0;
-        if (c0 < total_cols) {
-            const long long sh = a.p == 1 ? 0 : c0 / a.cols;
-            const long long c = c0 - sh * a.cols;
-            n = static_cast<int>(a.cols - c < E ? a.cols - c : E);
-            src = a.x + sh * a.ss + c * ES;
-        }
-        Vec<F32> v[8];
+    const long long total = static_cast<long long>(a.cols) * a.p;
+    const long long k_tiles = (total + 127) / 128, pitch = (total + 31) / 32 * 16;
+    const long long t_pitch = (static_cast<long long>(a.rows) + 31) / 32 * 16, t_tiles = (static_cast<long long>(a.rows) + 127) / 128;
+    const unsigned col_tiles = static_cast<unsigned>(a.spans);
+    griddep_wait();
+    if (t == 0) griddep_launch_dependents();
+
+    auto fetch = [&](unsigned item, uint32_t* dst) {
+        const unsigned rt = item / col_tiles;
+        const long long c0 = static_cast<long long>(item - rt * col_tiles) * TC + lane16 * P::E;
+        int n;
+        const uint8_t* src = piece_at<F32>(a, c0, n);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int row = r_tile + (t >> 4) + i * 16;
-            v[i].load(src + row * a.ldx, row < a.rows ? n : 0);
+            const int r = (t >> 4) + i * 16;
+            const long long row = static_cast<long long>(rt) * 128 + r;
+            const uint32_t bytes = row < a.rows ? n * P::ES : 0;  // the rest of the 16 are zero-filled, not read
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * 64 + lane16 * 4)),
+                         "l"(bytes ? src + row * a.ldx : a.x), "r"(bytes)
+                         : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    unsigned item = blockIdx.x;
+    const unsigned items = static_cast<unsigned>(a.items);
+    int buf = 0;
+    if (item < items) fetch(item, sm.tile[0]);
+    for (; item < items; item += gridDim.x, buf ^= 1) {
+        if (item + gridDim.x < items) {
+            fetch(item + gridDim.x, sm.tile[buf ^ 1]);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncthreads();
+        const uint32_t* tile = sm.tile[buf];
+        const unsigned rt = item / col_tiles;
+        const long long c_tile = static_cast<long long>(item - rt * col_tiles) * TC, r_tile = static_cast<long long>(rt) * 128;
+        if (a.q != nullptr) {
+            const long long c0 = c_tile + lane16 * P::E;
+            uint8_t* qd = a.q + r_tile * pitch + c0 / 2;
+            uint8_t* sd = a.s + mx::scale_offset(r_tile, c0 >> 5, k_tiles);
+            const bool put = c0 / 2 < pitch;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = (t >> 4) + i * 16, row = r_tile + r;
-            *reinterpret_cast<uint4*>(tile + r * 64 + lane16 * 4) = v[i].raw;
-            if (a.q != nullptr) {
-                const uint32_t s = mx::scale_of(v[i].block_amax());
-                const uint32_t code = v[i].codes(s);
-                uint32_t w = 0;
-                const int lane = t & 31;
-#pragma unroll
-                for (int j = 0; j < 16 / LB; ++j) w |= __shfl_sync(0xFFFFFFFFu, s, (lane & 16) + j * LB) << (8 * j);
-                if (row < a.rows) {
-                    if (c0 / 2 < pitch) {
-                        if constexpr (F32)
-                            *reinterpret_cast<uint16_t*>(a.q + row * pitch + c0 / 2) = static_cast<uint16_t>(code);
-                        else *reinterpret_cast<uint32_t*>(a.q + row * pitch + c0 / 2) = code;
+            for (int i = 0; i < 8; ++i) {
+                const int r = (t >> 4) + i * 16;
+                const uint4 v = *reinterpret_cast<const uint4*>(tile + r * 64 + lane16 * 4);
+                const uint32_t s = P::scale(v);
+                const uint32_t code = P::codes(v, s);
+                if (r_tile + r < a.rows) {
+                    if (put) {
+                        if constexpr (F32) *reinterpret_cast<uint16_t*>(qd + r * pitch) = static_cast<uint16_t>(code);
+                        else *reinterpret_cast<uint32_t*>(qd + r * pitch) = code;
                     }
-                    if (lane16 == 0) {
-                        uint8_t* d = a.s + mx::scale_offset(row, c0 / 32, k_tiles);
-                        if constexpr (F32) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(w);
-                        else *reinterpret_cast<uint32_t*>(d) = w;
-                    }
+                    // (col_tiles cover whole scale tiles: padding blocks are written as zero)
+                    if (lane16 % P::LANES == 0) sd[(r & 31) * 16 + (r >> 5) * 4] = static_cast<uint8_t>(s);
                 }
             }
         }
-    }
-    __syncthreads();
-    {
-        const int word = t & 63, rb = t >> 6;
-        float lo[32], hi[32];
-#pragma unroll
-        for (int r = 0; r < 32; ++r) {
-            const uint32_t w = tile[(rb * 32 + r) * 64 + word];
+        {
+            const int word = t & 63, rb = t >> 6;
+            const uint32_t* col = tile + rb * 32 * 64 + word;
+            uint8_t* sb = reinterpret_cast<uint8_t*>(sm.sc);
             if constexpr (F32) {
-                lo[r] = __uint_as_float(w);
+                float v[32];
+#pragma unroll
+                for (int r = 0; r < 32; ++r) v[r] = __uint_as_float(col[r * 64]);
+                uint4 c;
+                sb[word * 4 + rb] = static_cast<uint8_t>(mx::quantize32(v, c));
+                *reinterpret_cast<uint4*>(sm.out + word * 80 + rb * 16) = c;
             } else {
-                lo[r] = __uint_as_float(w << 16);
-                hi[r] = __uint_as_float(w & 0xFFFF0000u);
+                uint32_t w[32];
+#pragma unroll
+                for (int r = 0; r < 32; ++r) w[r] = col[r * 64];
+                uint32_t m[4] = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+                for (int r = 4; r < 32; ++r) m[r & 3] = mx::amax_bf16x2(m[r & 3], w[r]);
+                const uint32_t mm = mx::amax_bf16x2(mx::amax_bf16x2(m[0], m[1]), mx::amax_bf16x2(m[2], m[3])) & 0x7FFF7FFFu;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t s = mx::scale_of(half ? (mm & 0xFFFF0000u) : (mm << 16));
+                    const float inv = mx::inverse_scale(s);
+                    uint32_t c[4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = __uint_as_float(half ? (w[g * 8 + i] & 0xFFFF0000u) : (w[g * 8 + i] << 16));
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) mx::mul2(v[i], v[i + 1], inv);
+                        c[g] = s == 255u ? 0u : mx::encode8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+                    }
+                    *reinterpret_cast<uint4*>(sm.out + (word * 2 + half) * 80 + rb * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+                    sb[(word * 2 + half) * 4 + rb] = static_cast<uint8_t>(s);
+                }
             }
         }
-        uint4 codes;
-        constexpr int PER = F32 ? 1 : 2;
-        uint8_t* sb = reinterpret_cast<uint8_t*>(sc);
-        uint32_t s = mx::quantize32(lo, codes);
-        *reinterpret_cast<uint4*>(out + word * PER * 80 + rb * 16) = codes;
-        sb[word * PER * 4 + rb] = static_cast<uint8_t>(s);
-        if constexpr (!F32) {
-            s = mx::quantize32(hi, codes);
-            *reinterpret_cast<uint4*>(out + (word * 2 + 1) * 80 + rb * 16) = codes;
-            sb[(word * 2 + 1) * 4 + rb] = static_cast<uint8_t>(s);
-        }
-    }
-    __syncthreads();
-    const long long t_pitch = (static_cast<long long>(a.rows) + 31) / 32 * 16;
-    const long long t_tiles = (static_cast<long long>(a.rows) + 127) / 128;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TC / 64; ++i) {
-        const int c = (t >> 2) + i * 64;
-        const long long col = c_tile + c, at = r_tile / 2 + (t & 3) * 16;
-        if (col < total_cols && at < t_pitch)
-            *reinterpret_cast<uint4*>(a.qt + col * t_pitch + at) = *reinterpret_cast<const uint4*>(out + c * 80 + (t & 3) * 16);
+        for (int i = 0; i < TC / 64; ++i) {
+            const int c = (t >> 2) + i * 64;
+            const long long col = c_tile + c, at = r_tile / 2 + (t & 3) * 16;
+            if (col < total && at < t_pitch)
+                *reinterpret_cast<uint4*>(a.qt + col * t_pitch + at) =
+                    *reinterpret_cast<const uint4*>(sm.out + c * 80 + (t & 3) * 16);
+        }
+        if (t < TC && c_tile + t < total)
+            *reinterpret_cast<uint32_t*>(a.st + mx::scale_offset(c_tile + t, rt * 4LL, t_tiles)) = sm.sc[t];
+        // (the next pass writes out and sc behind its first barrier, and this buffer's copies start there too)
     }
-    if (t < TC && c_tile + t < total_cols)
-        *reinterpret_cast<uint32_t*>(a.st + mx::scale_offset(c_tile + t, row_tile * 4LL, t_tiles)) = sc[t];
 }
 
 // Values of an operand: a thread takes 8 codes.
@@ -266,10 +303,11 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restri
 }
 
 template <typename... P, typename... A>
-tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, cudaStream_t st, A... args) {
+tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, int smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -286,26 +324,47 @@ tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, cudaStr
     return TPMLP_OK;
 }
 
+template <bool F32>
+tpmlp_status quantize(QuantArgs a, int64_t cols, const DeviceInfo& dev, cudaStream_t st) {
+    constexpr int E = Piece<F32>::E;
+    if (a.qt == nullptr) {
+        a.spans = (cols + 32 * E - 1) / (32 * E);
+        if constexpr (F32) a.spans = (cols + 127) / 128;  // one span is one scale tile wide
+        a.items = a.spans * a.rows;
+        // Four spans a warp keep 2 KB of loads in flight; while there are fewer warps than that fills
+        // the GPU with, one each.
+        const bool many = a.items >= static_cast<int64_t>(dev.sm_count) * 64 * 4;
+        const int64_t per = many ? 32 : 8;
+        const dim3 grid(static_cast<unsigned>((a.items + per - 1) / per));
+        return many ? launch_pdl("MXFP4 quantisation", quantize_rows_kernel<F32, 4>, grid, 0, st, a)
+                    : launch_pdl("MXFP4 quantisation", quantize_rows_kernel<F32, 1>, grid, 0, st, a);
+    }
+    constexpr int TC = 256 / Piece<F32>::ES;
+    a.spans = (cols + 127) / 128 * (128 / TC);
+    a.items = a.spans * ((a.rows + 127LL) / 128);
+    static bool attr_done[64];
+    constexpr int smem = sizeof(BothSmem<F32>);
+    if (dev.device >= 64 || !attr_done[dev.device]) {
+        const cudaError_t e = cudaFuncSetAttribute(quantize_both_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) {
+            set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            return TPMLP_ERR_CUDA;
+        }
+        if (dev.device < 64) attr_done[dev.device] = true;
+    }
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.items, dev.sm_count * 2)));
+    return launch_pdl("MXFP4 quantisation", quantize_both_kernel<F32>, grid, smem, st, a);
+}
+
 }  // namespace
 
 tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows,
                                    int64_t cols, int p, bool f32, const DeviceInfo& dev, cudaStream_t st) {
     const int64_t es = f32 ? 4 : 2;
-    QuantArgs a{static_cast<const uint8_t*>(X), ldx * es, rows * ldx * es, static_cast<int>(rows),
-                static_cast<int>(cols / p), p, static_cast<uint8_t*>(Q), static_cast<uint8_t*>(S),
-                static_cast<uint8_t*>(Qt), static_cast<uint8_t*>(St)};
-    if (Qt == nullptr) {
-        const int64_t span = f32 ? 64 : 128;
-        const int64_t items = (cols + 127) / 128 * (128 / span) * rows;
-        const int64_t most = static_cast<int64_t>(dev.sm_count) * 16;
-        const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + 15) / 16, most)));
-        return f32 ? launch_pdl("MXFP4 quantisation", quantize_rows_kernel<true>, grid, st, a)
-                   : launch_pdl("MXFP4 quantisation", quantize_rows_kernel<false>, grid, st, a);
-    }
-    const int64_t tc = f32 ? 64 : 128;
-    const dim3 grid(static_cast<unsigned>((cols + 127) / 128 * (128 / tc) * ((rows + 127) / 128)));
-    return f32 ? launch_pdl("MXFP4 quantisation", quantize_both_kernel<true>, grid, st, a)
-               : launch_pdl("MXFP4 quantisation", quantize_both_kernel<false>, grid, st, a);
+    const QuantArgs a{static_cast<const uint8_t*>(X), ldx * es, rows * ldx * es, static_cast<int>(rows),
+                      static_cast<int>(cols / p), p, static_cast<uint8_t*>(Q), static_cast<uint8_t*>(S),
+                      static_cast<uint8_t*>(Qt), static_cast<uint8_t*>(St), 0, 0};
+    return f32 ? quantize<true>(a, cols, dev, st) : quantize<false>(a, cols, dev, st);
 }
 
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
@@ -314,8 +373,8 @@ tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, in
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(dev.sm_count) * 32)));
     const auto* q = static_cast<const uint8_t*>(Q);
     const auto* s = static_cast<const uint8_t*>(S);
-    return f32 ? launch_pdl("MXFP4 dequantisation", dequantize_kernel<true>, grid, st, q, s, out, (long long)rows, (long long)k)
-               : launch_pdl("MXFP4 dequantisation", dequantize_kernel<false>, grid, st, q, s, out, (long long)rows, (long long)k);
+    return f32 ? launch_pdl("MXFP4 dequantisation", dequantize_kernel<true>, grid, 0, st, q, s, out, (long long)rows, (long long)k)
+               : launch_pdl("MXFP4 dequantisation", dequantize_kernel<false>, grid, 0, st, q, s, out, (long long)rows, (long long)k);
 }
 
 }  // namespace tpmlp
