@@ -182,12 +182,18 @@ __device__ __forceinline__ void turn32(float* buf, const float (&v)[32], float (
     __syncwarp();
 }
 
-// One block of 32 tokens of column `col` of an array quantised along the tokens.
-__device__ __forceinline__ void put_token_block(const Args& p, uint8_t* q, uint8_t* qs, const float (&w)[32], long long col,
-                                                int tb) {
+// The quantised blocks of a chunk (32 lanes x 16 bytes each: a row of 32 features, or a feature of 32
+// tokens, per lane) are laid out in shared memory and leave as TMA stores of 16 bytes x 32 rows: stores
+// from registers, every lane into another row, kept the load/store unit busy for longer than the arithmetic.
+enum { BOX_Y = 0, BOX_G = 1, BOX_U = 2, BOX_ROW_G = 3, BOX_ROW_U = 4, BOXES = 5 };
+constexpr int WARP_BUF = TURN_WORDS * 4 + BOXES * 512;  // one warp's shared memory: turn32's, then the boxes
+
+// This lane's block of 32 tokens of feature row `col` (from the warp's block tb) into its box.
+__device__ __forceinline__ void put_token_block(const Args& p, uint4* box, uint8_t* qs, const float (&w)[32], long long col, int tb,
+                                                int lane) {
     uint4 c;
     const uint32_t s = quantize32(w, c);
-    if ((long long)tb * 16 < p.t_pitch) *reinterpret_cast<uint4*>(q + col * p.t_pitch + tb * 16) = c;
+    box[lane] = c;
     if (tb < p.t_tiles * 4) qs[scale_offset(col, tb, p.t_tiles)] = static_cast<uint8_t>(s);
 }
 
@@ -226,9 +232,13 @@ __device__ __forceinline__ void load_h(const Args& p, int gm, int f0, uint32_t (
 // EPI_DSWIGLU: v = dY of features f0..f0+31 of this thread's row (token) and, from its pre-activations h,
 // dg = dY u silu'(g), du = dY silu(g) and y = silu(g) u, from fp32 quantised along the columns (dg, du) and,
 // turned through shared memory, along the tokens (dg, du, y).  tb: the warp's block of 32 tokens.  Rows past
-// M count as zero.  The next chunk's pre-activations (row gm_next) are loaded into h behind the quantisation.
-__device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], uint32_t (&h)[32], int gm, int f0, int tb, float* buf,
-                                              int lane, int f_next) {
+// M count as zero.  The next chunk's pre-activations (from feature f_next, none if negative) are loaded into
+// h behind the quantisation.  buf: WARP_BUF bytes of this warp's.
+struct StoreMaps {
+    const CUtensorMap *q, *h, *y;  // dH along the columns, dH and Y along the tokens: boxes of 16 bytes x 32 rows
+};
+__device__ __forceinline__ void dswiglu_chunk(const Args& p, const StoreMaps& tm, float (&v)[32], uint32_t (&h)[32], int gm, int f0,
+                                              int tb, float* buf, int lane, int f_next) {
     if (f0 >= p.N) return;  // (whole warp; features come in multiples of 128)
     const long long pg = (long long)(f0 >> 7) * 256 + (f0 & 127);
     const bool live = gm < p.M;
@@ -247,19 +257,19 @@ __device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], uin
         tc::f2_unpack(tc::f2_mul(dy, sl), u[j], u[j + 1]);
     }
     if (f_next >= 0) load_h(p, gm, f_next, h);
+    uint4* box = reinterpret_cast<uint4*>(buf + TURN_WORDS);
+    if (lane == 0) bulk_wait_group_read<0>();  // the last chunk's stores have read the boxes
     float w[32];
     turn32(buf, v, w, lane);
-    put_token_block(p, p.yt, p.yts, w, f0 + lane, tb);
+    put_token_block(p, box + BOX_Y * 32, p.yts, w, f0 + lane, tb, lane);
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
-        if (live) {
-            uint4 c;
-            const uint32_t s = quantize32(part ? u : g, c);
-            *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + pg / 2 + part * 64) = c;
-            p.qs[scale_offset(gm, (pg >> 5) + part * 4, p.q_tiles)] = static_cast<uint8_t>(s);
-        }
+        uint4 c;
+        const uint32_t s = quantize32(part ? u : g, c);
+        box[(BOX_ROW_G + part) * 32 + lane] = c;
+        if (live) p.qs[scale_offset(gm, (pg >> 5) + part * 4, p.q_tiles)] = static_cast<uint8_t>(s);
         turn32(buf, part ? u : g, w, lane);
-        put_token_block(p, p.ht, p.hts, w, pg + part * 128 + lane, tb);
+        put_token_block(p, box + (BOX_G + part) * 32, p.hts, w, pg + part * 128 + lane, tb, lane);
         if (p.colsum != nullptr && (long long)tb * 16 < p.t_pitch) {
             float s = 0.0f;
 #pragma unroll
@@ -267,6 +277,20 @@ __device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], uin
             p.colsum[(long long)tb * (2 * p.N) + pg + part * 128 + lane] = s;
         }
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (elect_one()) {
+        const int col = static_cast<int>(pg), row0 = tb * 32;
+        if (row0 < p.M) {  // rows past the last, and features past theirs, are clipped
+            tma_store_3d(tm.q, box + BOX_ROW_G * 32, col / 2, row0, 0);
+            tma_store_3d(tm.q, box + BOX_ROW_U * 32, col / 2 + 64, row0, 0);
+            tma_store_3d(tm.y, box + BOX_Y * 32, tb * 16, f0, 0);
+            tma_store_3d(tm.h, box + BOX_G * 32, tb * 16, col, 0);
+            tma_store_3d(tm.h, box + BOX_U * 32, tb * 16, col + 128, 0);
+        }
+        bulk_commit_group();
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ void load_acc32(uint32_t taddr, float (&v)[32]) {
@@ -286,8 +310,8 @@ constexpr int P_SFA_BYTES = 2 * SF_TILE, P_SFB_BYTES = 4 * SF_TILE;
 constexpr int P_STAGE = 2 * OP_BYTES + P_SFA_BYTES + P_SFB_BYTES;
 template <int EPI>
 struct PairGeom {
-    static constexpr int turn = EPI == EPI_DSWIGLU ? 8 * TURN_WORDS * 4 : 0;
-    static constexpr int stages = EPI == EPI_DSWIGLU ? 5 : 6;
+    static constexpr int turn = EPI == EPI_DSWIGLU ? 8 * WARP_BUF : 0;
+    static constexpr int stages = EPI == EPI_DSWIGLU ? 4 : 6;
     static constexpr int smem = 1024 + stages * P_STAGE + turn + 256;
     static_assert(smem <= 227 * 1024, "pair kernel shared memory");
 };
@@ -305,7 +329,9 @@ __device__ __forceinline__ void decode_tile(const Args& p, int t, int& mb, int& 
 template <int EPI>
 __global__ void __launch_bounds__(P_THREADS, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Args p) {
+                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                   const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmH,
+                   const __grid_constant__ CUtensorMap tmY, const Args p) {
     constexpr int STAGES = PairGeom<EPI>::stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -473,7 +499,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         const int q = warp & 3;
         const int half = (warp - 4) >> 2;
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0), shared0 = mapa_shared(smem_u32(shared_free), 0);
-        [[maybe_unused]] float* buf = turn + (warp - 4) * TURN_WORDS;
+        [[maybe_unused]] float* buf = turn + (warp - 4) * (WARP_BUF / 4);
+        [[maybe_unused]] const StoreMaps maps{&tmQ, &tmH, &tmY};
         int lt = 0;
         for (int t = cluster_id; t < p.num_tiles; t += n_clusters, ++lt) {
             const int acc = lt & 1;
@@ -507,13 +534,16 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 }
                 if constexpr (EPI == EPI_SWIGLU) swiglu_chunk(p, v, u, row0 + lane, nb * 128 + col);
                 else if constexpr (EPI == EPI_DSWIGLU)
-                    dswiglu_chunk(p, v, h, row0 + lane, nb * P_BN + col, row0 >> 5, buf, lane,
+                    dswiglu_chunk(p, maps, v, h, row0 + lane, nb * P_BN + col, row0 >> 5, buf, lane,
                                   i + 1 < CH ? nb * P_BN + col + c_step * 32 : -1);
                 else store_chunk(p, v, row0 + lane, nb * P_BN + col);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0 + acc * 8);
+        }
+        if constexpr (EPI == EPI_DSWIGLU) {
+            if (lane == 0) bulk_wait_group_all();  // this warp's stores are complete
         }
     }
 
@@ -535,7 +565,8 @@ constexpr int S_TMEM = 256;          // 128 accumulator columns, 24 of scales: t
 constexpr int S_SFA = 128, S_SFB = 136;
 constexpr int S_MAX_STAGES = 6;
 constexpr int S_SMEM = 113 * 1024;   // two CTAs an SM
-constexpr int S_RING = S_SMEM - 1024 - 256;
+constexpr int S_RING = S_SMEM - 1024 - 256;  // a multiple of 128
+static_assert(S_RING % 128 == 0 && WARP_BUF % 128 == 0 && (TURN_WORDS * 4) % 128 == 0, "TMA boxes");
 template <int EPI>
 struct SingleGeom {
     static constexpr int sfb = EPI == EPI_SWIGLU ? 4 * SF_TILE : 2 * SF_TILE;
@@ -551,7 +582,9 @@ static_assert(SingleGeom<EPI_STORE>::stages(128) >= 3 && SingleGeom<EPI_SWIGLU>:
 template <int EPI>
 __global__ void __launch_bounds__(S_THREADS, 2)
     mx_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Args p) {
+                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmH,
+                     const __grid_constant__ CUtensorMap tmY, const Args p) {
     constexpr bool GATED = EPI == EPI_SWIGLU;
     constexpr int SFB = SingleGeom<EPI>::sfb;
     extern __shared__ uint8_t smem_raw[];
@@ -731,7 +764,8 @@ __global__ void __launch_bounds__(S_THREADS, 2)
         cluster_sync_all();  // the partial sums have arrived
     }
     if (work) {
-        [[maybe_unused]] float* buf = reinterpret_cast<float*>(smem + S_RING) - (q + 1) * TURN_WORDS;
+        [[maybe_unused]] float* buf = reinterpret_cast<float*>(smem + S_RING - (q + 1) * WARP_BUF);
+        [[maybe_unused]] const StoreMaps maps{&tmQ, &tmH, &tmY};
 #pragma unroll 1
         for (int c = 0; c < CH; ++c) {
             if (split > 1 && static_cast<uint32_t>(c % owners) != rank) continue;
@@ -764,8 +798,11 @@ __global__ void __launch_bounds__(S_THREADS, 2)
             else if constexpr (EPI == EPI_DSWIGLU) {
                 uint32_t h[32];
                 load_h(p, row0 + lane, nb * S_BN + c * 32, h);
-                dswiglu_chunk(p, v, h, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, lane, -1);
+                dswiglu_chunk(p, maps, v, h, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, lane, -1);
             } else store_chunk(p, v, row0 + lane, nb * S_BN + c * 32);
+        }
+        if constexpr (EPI == EPI_DSWIGLU) {
+            if (lane == 0) bulk_wait_group_all();
         }
     }
     tc_fence_before();
