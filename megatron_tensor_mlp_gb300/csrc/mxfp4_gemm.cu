@@ -62,6 +62,12 @@ bool boxes_map(CUtensorMap* map, const void* ptr, int64_t pitch, int64_t rows) {
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, {w, r, 1}, {w, w * r}, {16, 32, 1}, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Saved pre-activations [rows][ld] bf16: boxes of 32 features x 32 rows.
+bool h_map(CUtensorMap* map, const void* ptr, int64_t ld, int64_t rows) {
+    const uint64_t w = static_cast<uint64_t>(ld), r = static_cast<uint64_t>(rows);
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, {w, r, 1}, {w * 2, w * r * 2}, {32, 32, 1}, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 // 0 auto, 1 single CTAs without a split, 2 CTA pairs, 3 / 4 / 5 single CTAs with the K loop split 2 / 4 / 8 ways
 // (where the exchange of that many partial sums fits)
 std::atomic<int> g_mode{0};
@@ -79,7 +85,7 @@ bool set_smem(Kern kern, int device, int bytes, bool (&done)[64]) {
 }
 
 template <typename Kern>
-tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const CUtensorMap (&m)[7],
+tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const CUtensorMap (&m)[8],
                     const mx::Args& k) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -95,7 +101,7 @@ tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluste
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], m[6], k);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], k);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("MXFP4 GEMM launch: %s", cudaGetErrorString(e));
@@ -154,9 +160,10 @@ tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec
     const int cap = pair_capacity<EPI>(dev);
     const int64_t m_pairs = (g.M + 255) / 256, n_pairs = (g.N + 255) / 256;
     const bool pair = cap > 0 && (mode == 2 || (mode == 0 && m_pairs * n_pairs >= cap));
-    CUtensorMap m[7];
+    CUtensorMap m[8];
     if constexpr (EPI == EPI_DSWIGLU) {
-        if (!boxes_map(&m[4], k.q, k.q_pitch, g.M) || !boxes_map(&m[5], k.ht, k.t_pitch, 2 * g.N) || !boxes_map(&m[6], k.yt, k.t_pitch, g.N))
+        if (!boxes_map(&m[4], k.q, k.q_pitch, g.M) || !boxes_map(&m[5], k.ht, k.t_pitch, 2 * g.N) || !boxes_map(&m[6], k.yt, k.t_pitch, g.N) ||
+            !h_map(&m[7], g.h_in, g.h_ld, g.M))
             return TPMLP_ERR_CUDA;
     }
     if (pair) {

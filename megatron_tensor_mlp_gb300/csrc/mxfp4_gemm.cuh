@@ -169,16 +169,18 @@ __device__ __forceinline__ void swiglu_chunk(const Args& p, float (&g)[32], floa
     p.qs[scale_offset(gm, f0 >> 5, p.q_tiles)] = static_cast<uint8_t>(s);
 }
 
-// A warp's 32 x 32 values, a row in each lane, turned so that each lane has a column.  buf: 32 rows
-// of 36 words of this warp's (both passes free of bank conflicts).
-constexpr int TURN_WORDS = 32 * 36;
+// A warp's 32 x 32 values, a row in each lane, turned so that each lane has a column.  buf: 4 KB of
+// this warp's; a row's eight 16-byte groups are permuted by the row's low bits, which keeps both passes
+// free of bank conflicts without padding.
+constexpr int TURN_WORDS = 32 * 32;
 __device__ __forceinline__ void turn32(float* buf, const float (&v)[32], float (&w)[32], int lane) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<float4*>(buf + lane * 36 + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        *reinterpret_cast<float4*>(buf + lane * 32 + 4 * (j ^ (lane & 7))) =
+            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     __syncwarp();
 #pragma unroll
-    for (int t = 0; t < 32; ++t) w[t] = buf[t * 36 + lane];
+    for (int t = 0; t < 32; ++t) w[t] = buf[t * 32 + 4 * ((lane >> 2) ^ (t & 7)) + (lane & 3)];
     __syncwarp();
 }
 
@@ -187,6 +189,7 @@ __device__ __forceinline__ void turn32(float* buf, const float (&v)[32], float (
 // from registers, every lane into another row, kept the load/store unit busy for longer than the arithmetic.
 enum { BOX_Y = 0, BOX_G = 1, BOX_U = 2, BOX_ROW_G = 3, BOX_ROW_U = 4, BOXES = 5 };
 constexpr int WARP_BUF = TURN_WORDS * 4 + BOXES * 512;  // one warp's shared memory: turn32's, then the boxes
+constexpr int H_BUF = 4096;                             // pair kernel: and 32 rows x 32 features of H, gate then up
 
 // This lane's block of 32 tokens of feature row `col` (from the warp's block tb) into its box.
 __device__ __forceinline__ void put_token_block(const Args& p, uint4* box, uint8_t* qs, const float (&w)[32], long long col, int tb,
@@ -229,16 +232,27 @@ __device__ __forceinline__ void load_h(const Args& p, int gm, int f0, uint32_t (
     }
 }
 
+// The same from a warp's 32 rows x 32 features of H in shared memory (gate, then up; 64-byte swizzle).
+__device__ __forceinline__ void read_h(const uint8_t* hb, int lane, uint32_t (&h)[32]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(hb + (i >> 2) * 2048 + lane * 64 + (((i & 3) ^ ((lane >> 1) & 3)) << 4));
+        h[i * 4] = w.x;
+        h[i * 4 + 1] = w.y;
+        h[i * 4 + 2] = w.z;
+        h[i * 4 + 3] = w.w;
+    }
+}
+
 // EPI_DSWIGLU: v = dY of features f0..f0+31 of this thread's row (token) and, from its pre-activations h,
 // dg = dY u silu'(g), du = dY silu(g) and y = silu(g) u, from fp32 quantised along the columns (dg, du) and,
 // turned through shared memory, along the tokens (dg, du, y).  tb: the warp's block of 32 tokens.  Rows past
-// M count as zero.  The next chunk's pre-activations (from feature f_next, none if negative) are loaded into
-// h behind the quantisation.  buf: WARP_BUF bytes of this warp's.
+// M count as zero.  buf: WARP_BUF bytes of this warp's.
 struct StoreMaps {
     const CUtensorMap *q, *h, *y;  // dH along the columns, dH and Y along the tokens: boxes of 16 bytes x 32 rows
 };
-__device__ __forceinline__ void dswiglu_chunk(const Args& p, const StoreMaps& tm, float (&v)[32], uint32_t (&h)[32], int gm, int f0,
-                                              int tb, float* buf, int lane, int f_next) {
+__device__ __forceinline__ void dswiglu_chunk(const Args& p, const StoreMaps& tm, float (&v)[32], const uint32_t (&h)[32], int gm, int f0,
+                                              int tb, float* buf, int lane) {
     if (f0 >= p.N) return;  // (whole warp; features come in multiples of 128)
     const long long pg = (long long)(f0 >> 7) * 256 + (f0 & 127);
     const bool live = gm < p.M;
@@ -256,7 +270,6 @@ __device__ __forceinline__ void dswiglu_chunk(const Args& p, const StoreMaps& tm
         tc::f2_unpack(tc::f2_mul(sl, u2), v[j], v[j + 1]);
         tc::f2_unpack(tc::f2_mul(dy, sl), u[j], u[j + 1]);
     }
-    if (f_next >= 0) load_h(p, gm, f_next, h);
     uint4* box = reinterpret_cast<uint4*>(buf + TURN_WORDS);
     if (lane == 0) bulk_wait_group_read<0>();  // the last chunk's stores have read the boxes
     float w[32];
@@ -310,7 +323,7 @@ constexpr int P_SFA_BYTES = 2 * SF_TILE, P_SFB_BYTES = 4 * SF_TILE;
 constexpr int P_STAGE = 2 * OP_BYTES + P_SFA_BYTES + P_SFB_BYTES;
 template <int EPI>
 struct PairGeom {
-    static constexpr int turn = EPI == EPI_DSWIGLU ? 8 * WARP_BUF : 0;
+    static constexpr int turn = EPI == EPI_DSWIGLU ? 8 * (H_BUF + WARP_BUF) : 0;
     static constexpr int stages = EPI == EPI_DSWIGLU ? 4 : 6;
     static constexpr int smem = 1024 + stages * P_STAGE + turn + 256;
     static_assert(smem <= 227 * 1024, "pair kernel shared memory");
@@ -331,7 +344,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmH,
-                   const __grid_constant__ CUtensorMap tmY, const Args p) {
+                   const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmHin,
+                   const Args p) {
     constexpr int STAGES = PairGeom<EPI>::stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -346,7 +360,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint64_t* tempty = tfull + 2;       // [2] accumulator read
     uint64_t* shared_free = tempty + 2; // the columns shared with the other accumulator read
     uint64_t* drain = shared_free + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* h_full = drain + 1;       // [8] EPI_DSWIGLU: an epilogue warp's piece of H has landed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(h_full + 8);
 
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform for the compiler
     const int lane = threadIdx.x & 31;
@@ -366,6 +381,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         }
         mbar_init(shared_free, 8);      // the 4 of either CTA that read the shared columns
         mbar_init(drain, 1);
+        for (int w = 0; w < 8; ++w) mbar_init(h_full + w, 1);
         fence_mbarrier_init();
         fence_proxy_async_smem();
     }
@@ -499,30 +515,51 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         const int q = warp & 3;
         const int half = (warp - 4) >> 2;
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0), shared0 = mapa_shared(smem_u32(shared_free), 0);
-        [[maybe_unused]] float* buf = turn + (warp - 4) * (WARP_BUF / 4);
+        [[maybe_unused]] uint8_t* hbuf = reinterpret_cast<uint8_t*>(turn) + (warp - 4) * H_BUF;
+        [[maybe_unused]] float* buf = turn + (8 * H_BUF + (warp - 4) * WARP_BUF) / 4;
         [[maybe_unused]] const StoreMaps maps{&tmQ, &tmH, &tmY};
+        constexpr int CH = EPI == EPI_SWIGLU ? 2 : 4;
+        const int col0 = half * (CH * 32);
+        // EPI_DSWIGLU: each warp copies its next 32 x 32 piece of H while it works on the present one.  (Loads
+        // into registers, a row a lane, were most of the epilogue's time.)
+        [[maybe_unused]] uint32_t h_phase = 0;
+        [[maybe_unused]] bool h_pending = false;
+        auto fetch_h = [&](int t, int lt, int i) {
+            int mb, nb;
+            decode_tile(p, t, mb, nb);
+            const int f = nb * P_BN + col0 + ((lt & 1) == 0 ? CH - 1 - i : i) * 32;
+            const int row = mb * (2 * BM) + static_cast<int>(prank) * BM + q * 32;
+            uint64_t* bar = h_full + (warp - 4);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar, H_BUF);
+                const int x = (f >> 7) * 256 + (f & 127);
+                tma_load_3d(hbuf, &tmHin, bar, x, row, 0);
+                tma_load_3d(hbuf + H_BUF / 2, &tmHin, bar, x + 128, row, 0);
+            }
+            __syncwarp();
+            h_pending = true;
+        };
+        if constexpr (EPI == EPI_DSWIGLU) {
+            if (cluster_id < p.num_tiles) fetch_h(cluster_id, 0, 0);
+        }
         int lt = 0;
-        for (int t = cluster_id; t < p.num_tiles; t += n_clusters, ++lt) {
+        bool ok = true;
+        for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters, ++lt) {
             const int acc = lt & 1;
             int mb, nb;
             decode_tile(p, t, mb, nb);  // before the wait: the next tile's MMAs wait for the first columns read here
             const int row0 = mb * (2 * BM) + static_cast<int>(prank) * BM + q * 32;
-            constexpr int CH = EPI == EPI_SWIGLU ? 2 : 4;
-            const int col0 = half * (CH * 32);
-            // The first accumulator's shared columns are its last, the second's its first: walk the
-            // chunks so that they come first.  half 1 - acc holds them.
-            const int c_first = acc == 0 ? CH - 1 : 0, c_step = acc == 0 ? -1 : 1;
-            [[maybe_unused]] uint32_t h[32];
-            if constexpr (EPI == EPI_DSWIGLU) load_h(p, row0 + lane, nb * P_BN + col0 + c_first * 32, h);
             int okw = 0;
             if (lane == 0) okw = mbar_wait_bounded(tfull + acc, (lt >> 1) & 1, p.status, p.timeout_ns, kWhereEpilogue);
             okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
             if (!okw) break;
             tc_fence_after();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * P_ACC1;
+            // The first accumulator's shared columns are its last, the second's its first: walk the
+            // chunks so that they come first.  half 1 - acc holds them.
 #pragma unroll 1
             for (int i = 0; i < CH; ++i) {
-                const int col = col0 + (c_first + i * c_step) * 32;
+                const int col = col0 + (acc == 0 ? CH - 1 - i : i) * 32;
                 float v[32];
                 [[maybe_unused]] float u[32];
                 load_acc32(t_row + col, v);
@@ -533,16 +570,26 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     if (lane == 0) mbar_arrive_cluster(shared0);
                 }
                 if constexpr (EPI == EPI_SWIGLU) swiglu_chunk(p, v, u, row0 + lane, nb * 128 + col);
-                else if constexpr (EPI == EPI_DSWIGLU)
-                    dswiglu_chunk(p, maps, v, h, row0 + lane, nb * P_BN + col, row0 >> 5, buf, lane,
-                                  i + 1 < CH ? nb * P_BN + col + c_step * 32 : -1);
-                else store_chunk(p, v, row0 + lane, nb * P_BN + col);
+                else if constexpr (EPI == EPI_DSWIGLU) {
+                    ok = mbar_wait_bounded_warp(h_full + (warp - 4), h_phase, p.status, p.timeout_ns, kWhereEpilogue);
+                    if (!ok) break;
+                    h_phase ^= 1u;
+                    h_pending = false;
+                    uint32_t h[32];
+                    read_h(hbuf, lane, h);
+                    __syncwarp();
+                    if (i + 1 < CH) fetch_h(t, lt, i + 1);
+                    else if (t + n_clusters < p.num_tiles) fetch_h(t + n_clusters, lt + 1, 0);
+                    dswiglu_chunk(p, maps, v, h, row0 + lane, nb * P_BN + col, row0 >> 5, buf, lane);
+                } else store_chunk(p, v, row0 + lane, nb * P_BN + col);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0 + acc * 8);
         }
         if constexpr (EPI == EPI_DSWIGLU) {
+            // (after a wait that gave up) no copy is in flight when this CTA exits
+            if (h_pending) mbar_wait_bounded_warp(h_full + (warp - 4), h_phase, p.status, p.timeout_ns, kWhereDrain, false);
             if (lane == 0) bulk_wait_group_all();  // this warp's stores are complete
         }
     }
@@ -584,7 +631,8 @@ __global__ void __launch_bounds__(S_THREADS, 2)
     mx_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                      const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmH,
-                     const __grid_constant__ CUtensorMap tmY, const Args p) {
+                     const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmHin,
+                   const Args p) {
     constexpr bool GATED = EPI == EPI_SWIGLU;
     constexpr int SFB = SingleGeom<EPI>::sfb;
     extern __shared__ uint8_t smem_raw[];
@@ -798,7 +846,7 @@ __global__ void __launch_bounds__(S_THREADS, 2)
             else if constexpr (EPI == EPI_DSWIGLU) {
                 uint32_t h[32];
                 load_h(p, row0 + lane, nb * S_BN + c * 32, h);
-                dswiglu_chunk(p, maps, v, h, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, lane, -1);
+                dswiglu_chunk(p, maps, v, h, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, lane);
             } else store_chunk(p, v, row0 + lane, nb * S_BN + c * 32);
         }
         if constexpr (EPI == EPI_DSWIGLU) {
