@@ -101,11 +101,13 @@ tpmlp_status launch_sum_finish(const float* S, const void* bias, void* out, int6
 tpmlp_status launch_swiglu_pack(void* G, void* U, void* W_sh, int64_t rows, int64_t ffn, int p, int esize,
                                 bool inverse, cudaStream_t st);
 
-// An MXFP4 operand [rows, K]: codes and tiled scales (mxfp4.cuh).
+// An MXFP4 operand [rows, K]: codes and tiled scales (mxfp4.cuh).  blocked: the codes are [ceil(K/32)][rows][16
+// bytes], as the GEMM's epilogues write them (between the block's kernels only; public operands are row-major).
 struct MxOperand {
     const void* codes;
     const void* scales;
     int64_t rows;
+    bool blocked = false;
 };
 // D[M,N] = sum_k A[M,k] B[N,k] on MXFP4 operands, and what its epilogue reads and writes.
 struct MxSpec {
@@ -115,8 +117,8 @@ struct MxSpec {
     void* out; int64_t out_ld, out_ss, shard_cols;  // shard_cols 0: the columns are not sharded
     const void* bias;                               // bf16, may be null
     const void* h_in; void* h_out; int64_t h_ld;    // packed bf16 pre-activations
-    void* q; void* qs; int64_t q_cols;              // quantised along the columns
-    void* ht; void* hts; void* yt; void* yts;       // quantised along the rows
+    void* q; void* qs; int64_t q_cols;              // quantised along the columns, codes blocked
+    void* ht; void* hts; void* yt; void* yts;       // quantised along the rows, codes blocked
     float* colsum;                                  // sums over blocks of 32 rows, may be null
 };
 tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev, cudaStream_t st);

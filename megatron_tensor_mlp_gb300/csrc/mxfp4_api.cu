@@ -30,7 +30,8 @@ struct Packed {
     uint8_t* codes;
     uint8_t* scales;
     int64_t rows;
-    MxOperand operand() const { return MxOperand{codes, scales, rows}; }
+    MxOperand operand() const { return MxOperand{codes, scales, rows, false}; }
+    MxOperand blocked() const { return MxOperand{codes, scales, rows, true}; }  // written by a GEMM's epilogue
 };
 
 // Carves a workspace into 256-byte aligned pieces; with a null base it only measures.
@@ -228,7 +229,7 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_fwd(const void* X, const void* Wq, const voi
     g.qs = w.y.scales;
     g.q_cols = ffn;
     TP_TRY(launch_mxfp4_gemm(w.x.operand(), {Wq, Ws, 2 * ffn}, g, *dev, st));
-    return product(w.y.operand(), {Bq, Bs, h}, b2, Z, ffn, z_dt == TPMLP_F32, 0, *dev, st);
+    return product(w.y.blocked(), {Bq, Bs, h}, b2, Z, ffn, z_dt == TPMLP_F32, 0, *dev, st);
 }
 
 tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const void* Ws, const void* Bq, const void* Bs, const void* H,
@@ -271,9 +272,9 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const voi
     TP_TRY(launch_mxfp4_gemm(w.dz.operand(), {Bq, Bs, ffn}, g, *dev, st));
     if (dbw_sh) TP_TRY(launch_colsum(w.colsum, true, 1, (M + 31) / 32, 2 * ffn, dbw_sh, gf32, st));
     if (db2) TP_TRY(launch_colsum(dZ, false, 1, M, h, db2, gf32, st));
-    TP_TRY(product(w.yt.operand(), w.dzt.operand(), nullptr, dB_sh, M, gf32, 0, *dev, st));
-    TP_TRY(product(w.xt.operand(), w.dht.operand(), nullptr, dW_sh, M, gf32, p > 1 ? 2 * ffn / p : 0, *dev, st));
-    return product(w.dh.operand(), {Wq, Ws, h}, nullptr, dX, 2 * ffn, dx_dt == TPMLP_F32, 0, *dev, st);
+    TP_TRY(product(w.yt.blocked(), w.dzt.operand(), nullptr, dB_sh, M, gf32, 0, *dev, st));
+    TP_TRY(product(w.xt.operand(), w.dht.blocked(), nullptr, dW_sh, M, gf32, p > 1 ? 2 * ffn / p : 0, *dev, st));
+    return product(w.dh.blocked(), {Wq, Ws, h}, nullptr, dX, 2 * ffn, dx_dt == TPMLP_F32, 0, *dev, st);
 }
 
 tpmlp_status tpmlp_set_mxfp4_mode(int mode) {

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "mxfp4_gemm.cuh"
 
@@ -44,7 +45,13 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, const c
 }
 
 // Codes [rows][pitch bytes]: boxes of 128 bytes (256 values of k) x box_rows.
+// Blocked codes [ceil(k/32)][rows][16 bytes]: boxes of box_rows rows (two 8-byte words each) x 8 blocks.
 bool codes_map(CUtensorMap* map, const MxOperand& o, int64_t k, uint32_t box_rows) {
+    if (o.blocked) {
+        const uint64_t words = static_cast<uint64_t>(o.rows) * 2, blocks = static_cast<uint64_t>((k + 31) / 32);
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, o.codes, {words, blocks, 1}, {words * 8, words * 8 * blocks},
+                      {box_rows * 2, 8, 1}, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
     const uint64_t pitch = static_cast<uint64_t>((k + 31) / 32 * 16), rows = static_cast<uint64_t>(o.rows);
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.codes, {pitch, rows, 1}, {pitch, pitch * rows}, {128, box_rows, 1},
                   CU_TENSOR_MAP_SWIZZLE_128B);
@@ -54,12 +61,6 @@ bool scales_map(CUtensorMap* map, const MxOperand& o, int64_t k, uint32_t box_ti
     const uint64_t kt = static_cast<uint64_t>((k + 127) / 128), rt = static_cast<uint64_t>((o.rows + 127) / 128);
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, o.scales, {128, kt, rt}, {512, 512 * kt}, {128, 2, box_tiles},
                   CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
-// Quantised output [rows][pitch bytes]: boxes of 16 bytes (one block) x 32 rows.
-bool boxes_map(CUtensorMap* map, const void* ptr, int64_t pitch, int64_t rows) {
-    const uint64_t w = static_cast<uint64_t>(pitch), r = static_cast<uint64_t>(rows);
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, {w, r, 1}, {w, w * r}, {16, 32, 1}, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // Saved pre-activations [rows][ld] bf16: boxes of 32 features x 32 rows.
@@ -85,7 +86,7 @@ bool set_smem(Kern kern, int device, int bytes, bool (&done)[64]) {
 }
 
 template <typename Kern>
-tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const CUtensorMap (&m)[8],
+tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const CUtensorMap (&m)[5],
                     const mx::Args& k) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -101,7 +102,10 @@ tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluste
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], k);
+    cudaError_t e;
+    if constexpr (std::is_invocable_v<Kern, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, mx::Args>)
+        e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], k);
+    else e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], k);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("MXFP4 GEMM launch: %s", cudaGetErrorString(e));
@@ -148,7 +152,7 @@ int exchange_bytes(int split, int rows) {
 }
 template <int EPI>
 bool split_fits(int split, int rows, int kb) {
-    const int room = mx::S_RING - (EPI == EPI_DSWIGLU ? 4 * mx::WARP_BUF : 0);
+    const int room = mx::S_RING - (EPI == EPI_DSWIGLU ? mx::S_EPI_BYTES : 0);
     return split <= kb && exchange_bytes<EPI>(split, std::min((rows + 31) / 32 * 32, mx::BM)) <= room;
 }
 
@@ -160,13 +164,11 @@ tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec
     const int cap = pair_capacity<EPI>(dev);
     const int64_t m_pairs = (g.M + 255) / 256, n_pairs = (g.N + 255) / 256;
     const bool pair = cap > 0 && (mode == 2 || (mode == 0 && m_pairs * n_pairs >= cap));
-    CUtensorMap m[8];
-    if constexpr (EPI == EPI_DSWIGLU) {
-        if (!boxes_map(&m[4], k.q, k.q_pitch, g.M) || !boxes_map(&m[5], k.ht, k.t_pitch, 2 * g.N) || !boxes_map(&m[6], k.yt, k.t_pitch, g.N) ||
-            !h_map(&m[7], g.h_in, g.h_ld, g.M))
-            return TPMLP_ERR_CUDA;
-    }
+    CUtensorMap m[5];
     if (pair) {
+        if constexpr (EPI == EPI_DSWIGLU) {
+            if (!h_map(&m[4], g.h_in, g.h_ld, g.M)) return TPMLP_ERR_CUDA;
+        }
         k.m_blocks = static_cast<int>(m_pairs);
         k.n_blocks = static_cast<int>(n_pairs);
         k.num_tiles = k.m_blocks * k.n_blocks;
@@ -222,15 +224,16 @@ tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxS
     k.h_in = static_cast<const __nv_bfloat16*>(g.h_in);
     k.h_out = static_cast<__nv_bfloat16*>(g.h_out);
     k.h_ld = g.h_ld;
-    k.q = static_cast<uint8_t*>(g.q);
+    k.a_blocked = a.blocked ? 1 : 0;
+    k.b_blocked = b.blocked ? 1 : 0;
+    k.q = static_cast<uint4*>(g.q);
     k.qs = static_cast<uint8_t*>(g.qs);
-    k.q_pitch = (g.q_cols + 31) / 32 * 16;
     k.q_tiles = (g.q_cols + 127) / 128;
-    k.ht = static_cast<uint8_t*>(g.ht);
+    k.ht = static_cast<uint4*>(g.ht);
     k.hts = static_cast<uint8_t*>(g.hts);
-    k.yt = static_cast<uint8_t*>(g.yt);
+    k.yt = static_cast<uint4*>(g.yt);
     k.yts = static_cast<uint8_t*>(g.yts);
-    k.t_pitch = (g.M + 31) / 32 * 16;
+    k.t_blocks = (g.M + 31) / 32;
     k.t_tiles = (g.M + 127) / 128;
     k.colsum = g.colsum;
     k.status = dev.status;

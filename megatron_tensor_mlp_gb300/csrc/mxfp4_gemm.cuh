@@ -46,16 +46,17 @@ struct Args {
     int m_blocks, n_blocks, num_tiles, group_m;  // pair kernel
     int a_box;       // single kernel: rows of A copied per stage (16, 32, 64 or 128)
     int stages;      // single kernel: ring stages
+    int a_blocked, b_blocked;  // operand's codes are [k / 32][rows][16 bytes] (written by an epilogue), not [rows][k / 2]
     int out_f32, st32;
     // EPI_STORE: D + bias; column n is at out + (n / shard_cols) * out_ss + m * out_ld + n % shard_cols
     void* out; long long out_ld, out_ss; int shard_cols;
     const __nv_bfloat16* bias;   // EPI_STORE [N], EPI_SWIGLU [N] packed
     // EPI_SWIGLU: h_out (optional) [M][2 ffn]; EPI_DSWIGLU: h_in
     const __nv_bfloat16* h_in; __nv_bfloat16* h_out; long long h_ld;
-    // quantised outputs along the columns: EPI_SWIGLU y [M][ffn], EPI_DSWIGLU dH [M][2 ffn]
-    uint8_t* q; uint8_t* qs; long long q_pitch, q_tiles;
+    // quantised outputs, codes blocked: along the columns EPI_SWIGLU y [M][ffn], EPI_DSWIGLU dH [M][2 ffn]
+    uint4* q; uint8_t* qs; long long q_tiles;
     // EPI_DSWIGLU: along the rows (tokens), dH^T [2 ffn][M] and Y^T [ffn][M]
-    uint8_t* ht; uint8_t* hts; uint8_t* yt; uint8_t* yts; long long t_pitch, t_tiles;
+    uint4* ht; uint8_t* hts; uint4* yt; uint8_t* yts; long long t_blocks, t_tiles;
     float* colsum;   // EPI_DSWIGLU, optional: sums of dH over blocks of 32 tokens [ceil(M/32)][2 ffn]
     uint32_t* status;
     unsigned long long timeout_ns;
@@ -69,6 +70,12 @@ struct Args {
 __host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t sf_id) {
     return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
            (static_cast<uint32_t>(m >> 4) << 24) | (sf_id << 29);
+}
+// Shared-memory descriptor of `rows` rows of blocked codes (K-major without swizzle): 8-row groups of 16
+// bytes a row 128 bytes apart, the next 16 bytes of k a block of all rows further.
+__device__ __forceinline__ uint64_t sdesc_blocked(uint32_t saddr, int rows) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(rows) << 16) |
+           (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 // Shared-memory descriptor of a scale tile for tcgen05.cp: no swizzle, 8-row groups 128 bytes apart.
 __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
@@ -137,8 +144,9 @@ __device__ __forceinline__ f2 sigmoid2(f2 x) {
 }
 
 // EPI_SWIGLU: y = silu(g) u for features f0..f0+31 of a row (one block), quantised from fp32.
-__device__ __forceinline__ void swiglu_chunk(const Args& p, float (&g)[32], float (&u)[32], int gm, int f0) {
-    if (gm >= p.M || 2 * f0 >= p.N) return;
+// Returns the block's scale byte.
+__device__ __forceinline__ uint32_t swiglu_chunk(const Args& p, float (&g)[32], float (&u)[32], int gm, int f0) {
+    if (gm >= p.M || 2 * f0 >= p.N) return 0;
     const long long pg = (long long)(f0 >> 7) * 256 + (f0 & 127);
     if (p.bias != nullptr) {
 #pragma unroll
@@ -165,8 +173,8 @@ __device__ __forceinline__ void swiglu_chunk(const Args& p, float (&g)[32], floa
     }
     uint4 c;
     const uint32_t s = quantize32(g, c);
-    *reinterpret_cast<uint4*>(p.q + gm * p.q_pitch + f0 / 2) = c;
-    p.qs[scale_offset(gm, f0 >> 5, p.q_tiles)] = static_cast<uint8_t>(s);
+    p.q[(long long)(f0 >> 5) * p.M + gm] = c;  // a warp's 32 rows: 512 bytes in a row
+    return s;
 }
 
 // A warp's 32 x 32 values, a row in each lane, turned so that each lane has a column.  buf: 4 KB of
@@ -184,20 +192,42 @@ __device__ __forceinline__ void turn32(float* buf, const float (&v)[32], float (
     __syncwarp();
 }
 
-// The quantised blocks of a chunk (32 lanes x 16 bytes each: a row of 32 features, or a feature of 32
-// tokens, per lane) are laid out in shared memory and leave as TMA stores of 16 bytes x 32 rows: stores
-// from registers, every lane into another row, kept the load/store unit busy for longer than the arithmetic.
-enum { BOX_Y = 0, BOX_G = 1, BOX_U = 2, BOX_ROW_G = 3, BOX_ROW_U = 4, BOXES = 5 };
-constexpr int WARP_BUF = TURN_WORDS * 4 + BOXES * 512;  // one warp's shared memory: turn32's, then the boxes
-constexpr int H_BUF = 4096;                             // pair kernel: and 32 rows x 32 features of H, gate then up
+// EPI_DSWIGLU leaves five quantised arrays.  Their codes go out blocked, a warp's 32 blocks of 16 bytes
+// as 512 bytes in a row.  (Row-major codes, 16 bytes a lane into 32 rows, kept the load/store unit busy for
+// longer than the arithmetic; as TMA stores of 16 bytes x 32 rows they still cost 25 us of 910 in the
+// backward of 4096 tokens, h5120, ffn20480.)  Their scales are gathered in shared memory: the 128 rows x
+// 128 features of four warps (a CTA's half of a pair tile) are one scale tile of each array.
+enum { SC_Y = 0, SC_G = 1, SC_U = 2, SC_ROW_G = 3, SC_ROW_U = 4, SC_ARRAYS = 5 };
+constexpr int SC_BYTES = SC_ARRAYS * SF_TILE;
+constexpr int H_BUF = 4096;  // pair kernel: a warp's 32 rows x 32 features of H, gate then up
 
-// This lane's block of 32 tokens of feature row `col` (from the warp's block tb) into its box.
-__device__ __forceinline__ void put_token_block(const Args& p, uint4* box, uint8_t* qs, const float (&w)[32], long long col, int tb,
-                                                int lane) {
-    uint4 c;
-    const uint32_t s = quantize32(w, c);
-    box[lane] = c;
-    if (tb < p.t_tiles * 4) qs[scale_offset(col, tb, p.t_tiles)] = static_cast<uint8_t>(s);
+// Writes the five tiles of a half (128 threads, all its chunks done): features f0..f0+127 of rows row0..row0+127.
+// chunks: bit c set where this CTA did features 32 c.. (a split tile's CTAs share them).
+__device__ __forceinline__ void put_scales(const Args& p, const uint8_t* sc, int row0, int f0, int thread, uint32_t chunks) {
+    const long long k_tile = row0 >> 7, f_tile = f0 >> 7;
+    if (f0 >= p.N || k_tile >= p.t_tiles) return;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(sc) + thread;
+    // along the tokens: word i of a 16-byte group is features 32 i.., bytes the token blocks
+    if (chunks >> (thread & 3) & 1u) {
+        uint32_t* y = reinterpret_cast<uint32_t*>(p.yts + (f_tile * p.t_tiles + k_tile) * SF_TILE);
+        uint32_t* h = reinterpret_cast<uint32_t*>(p.hts + (2 * f_tile * p.t_tiles + k_tile) * SF_TILE);
+        y[thread] = w[SC_Y * 128];
+        h[thread] = w[SC_G * 128];
+        h[thread + p.t_tiles * 128] = w[SC_U * 128];
+    }
+    // along the features: word = row, byte c = features 32 c..
+    uint32_t* r = reinterpret_cast<uint32_t*>(p.qs + (k_tile * p.q_tiles + 2 * f_tile) * SF_TILE);
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        const uint32_t v = w[(SC_ROW_G + part) * 128];
+        if (chunks == 15u) {
+            r[thread + part * 128] = v;
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (chunks >> c & 1u) reinterpret_cast<uint8_t*>(r + thread + part * 128)[c] = static_cast<uint8_t>(v >> (8 * c));
+        }
+    }
 }
 
 // The saved bf16 pre-activations of features f0..f0+31 of row gm: 16 words of gate, 16 of up pairs;
@@ -247,12 +277,9 @@ __device__ __forceinline__ void read_h(const uint8_t* hb, int lane, uint32_t (&h
 // EPI_DSWIGLU: v = dY of features f0..f0+31 of this thread's row (token) and, from its pre-activations h,
 // dg = dY u silu'(g), du = dY silu(g) and y = silu(g) u, from fp32 quantised along the columns (dg, du) and,
 // turned through shared memory, along the tokens (dg, du, y).  tb: the warp's block of 32 tokens.  Rows past
-// M count as zero.  buf: WARP_BUF bytes of this warp's.
-struct StoreMaps {
-    const CUtensorMap *q, *h, *y;  // dH along the columns, dH and Y along the tokens: boxes of 16 bytes x 32 rows
-};
-__device__ __forceinline__ void dswiglu_chunk(const Args& p, const StoreMaps& tm, float (&v)[32], const uint32_t (&h)[32], int gm, int f0,
-                                              int tb, float* buf, int lane) {
+// M count as zero.  buf: turn32's; sc: the five scale tiles.
+__device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], const uint32_t (&h)[32], int gm, int f0, int tb,
+                                              float* buf, uint8_t* sc, int lane) {
     if (f0 >= p.N) return;  // (whole warp; features come in multiples of 128)
     const long long pg = (long long)(f0 >> 7) * 256 + (f0 & 127);
     const bool live = gm < p.M;
@@ -270,40 +297,39 @@ __device__ __forceinline__ void dswiglu_chunk(const Args& p, const StoreMaps& tm
         tc::f2_unpack(tc::f2_mul(sl, u2), v[j], v[j + 1]);
         tc::f2_unpack(tc::f2_mul(dy, sl), u[j], u[j + 1]);
     }
-    uint4* box = reinterpret_cast<uint4*>(buf + TURN_WORDS);
-    if (lane == 0) bulk_wait_group_read<0>();  // the last chunk's stores have read the boxes
+    const bool blk = tb < p.t_blocks;     // the warp's block of tokens holds a row
+    const int c = (f0 >> 5) & 3, q = tb & 3;
+    uint8_t* by_token = sc + lane * 16 + c * 4 + q;  // scale of feature f0 + lane, token block q
+    uint8_t* by_row = sc + SC_ROW_G * SF_TILE + lane * 16 + q * 4 + c;  // of this row, feature block c
     float w[32];
+    uint4 code;
     turn32(buf, v, w, lane);
-    put_token_block(p, box + BOX_Y * 32, p.yts, w, f0 + lane, tb, lane);
+    by_token[SC_Y * SF_TILE] = static_cast<uint8_t>(quantize32(w, code));
+    if (blk) p.yt[(long long)tb * p.N + f0 + lane] = code;
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
-        uint4 c;
-        const uint32_t s = quantize32(part ? u : g, c);
-        box[(BOX_ROW_G + part) * 32 + lane] = c;
-        if (live) p.qs[scale_offset(gm, (pg >> 5) + part * 4, p.q_tiles)] = static_cast<uint8_t>(s);
+        by_row[part * SF_TILE] = static_cast<uint8_t>(quantize32(part ? u : g, code));
+        if (live) p.q[((pg >> 5) + part * 4) * p.M + gm] = code;
         turn32(buf, part ? u : g, w, lane);
-        put_token_block(p, box + (BOX_G + part) * 32, p.hts, w, pg + part * 128 + lane, tb, lane);
-        if (p.colsum != nullptr && (long long)tb * 16 < p.t_pitch) {
+        by_token[(SC_G + part) * SF_TILE] = static_cast<uint8_t>(quantize32(w, code));
+        const long long col = pg + part * 128 + lane;
+        if (blk) p.ht[(long long)tb * (2 * p.N) + col] = code;
+        if (p.colsum != nullptr && blk) {
             float s = 0.0f;
 #pragma unroll
             for (int t = 0; t < 32; ++t) s += w[t];
-            p.colsum[(long long)tb * (2 * p.N) + pg + part * 128 + lane] = s;
+            p.colsum[(long long)tb * (2 * p.N) + col] = s;
         }
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (elect_one()) {
-        const int col = static_cast<int>(pg), row0 = tb * 32;
-        if (row0 < p.M) {  // rows past the last, and features past theirs, are clipped
-            tma_store_3d(tm.q, box + BOX_ROW_G * 32, col / 2, row0, 0);
-            tma_store_3d(tm.q, box + BOX_ROW_U * 32, col / 2 + 64, row0, 0);
-            tma_store_3d(tm.y, box + BOX_Y * 32, tb * 16, f0, 0);
-            tma_store_3d(tm.h, box + BOX_G * 32, tb * 16, col, 0);
-            tma_store_3d(tm.h, box + BOX_U * 32, tb * 16, col + 128, 0);
-        }
-        bulk_commit_group();
-    }
-    __syncwarp();
+}
+
+// One stage's codes of an operand, rows from `row`: 128 bytes of k of each (row-major) or 8 blocks of
+// all of them (blocked; x counts 8-byte words).
+template <bool PAIR>
+__device__ __forceinline__ void load_codes(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int it, int row, int blocked) {
+    const int x = blocked ? row * 2 : it * 128, y = blocked ? it * 8 : row;
+    if constexpr (PAIR) tma_load_3d_pair(dst, map, bar, x, y, 0);
+    else tma_load_3d_bar(dst, map, bar, x, y, 0);
 }
 
 __device__ __forceinline__ void load_acc32(uint32_t taddr, float (&v)[32]) {
@@ -323,7 +349,7 @@ constexpr int P_SFA_BYTES = 2 * SF_TILE, P_SFB_BYTES = 4 * SF_TILE;
 constexpr int P_STAGE = 2 * OP_BYTES + P_SFA_BYTES + P_SFB_BYTES;
 template <int EPI>
 struct PairGeom {
-    static constexpr int turn = EPI == EPI_DSWIGLU ? 8 * (H_BUF + WARP_BUF) : 0;
+    static constexpr int turn = EPI == EPI_DSWIGLU ? 8 * (H_BUF + TURN_WORDS * 4) + 4 * SC_BYTES : 0;
     static constexpr int stages = EPI == EPI_DSWIGLU ? 4 : 6;
     static constexpr int smem = 1024 + stages * P_STAGE + turn + 256;
     static_assert(smem <= 227 * 1024, "pair kernel shared memory");
@@ -343,9 +369,7 @@ template <int EPI>
 __global__ void __launch_bounds__(P_THREADS, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                   const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmH,
-                   const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmHin,
-                   const Args p) {
+                   const __grid_constant__ CUtensorMap tmH, const Args p) {
     constexpr int STAGES = PairGeom<EPI>::stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -361,7 +385,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     uint64_t* shared_free = tempty + 2; // the columns shared with the other accumulator read
     uint64_t* drain = shared_free + 1;
     uint64_t* h_full = drain + 1;       // [8] EPI_DSWIGLU: an epilogue warp's piece of H has landed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(h_full + 8);
+    uint64_t* sc_full = h_full + 8;     // [2] EPI_DSWIGLU: the four warps of a half have left a tile's scales
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + 2);
 
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform for the compiler
     const int lane = threadIdx.x & 31;
@@ -382,6 +407,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         mbar_init(shared_free, 8);      // the 4 of either CTA that read the shared columns
         mbar_init(drain, 1);
         for (int w = 0; w < 8; ++w) mbar_init(h_full + w, 1);
+        for (int w = 0; w < 2; ++w) mbar_init(sc_full + w, 4);
         fence_mbarrier_init();
         fence_proxy_async_smem();
     }
@@ -420,8 +446,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(full + stage, 2 * P_STAGE);
                     const uint32_t bar = full0 + stage * 8;
-                    tma_load_3d_pair(sA + stage * OP_BYTES, &tmA, bar, it * 128, row_tile * BM, 0);
-                    tma_load_3d_pair(sB + stage * OP_BYTES, &tmB, bar, it * 128, col0, 0);
+                    load_codes<true>(sA + stage * OP_BYTES, &tmA, bar, it, row_tile * BM, p.a_blocked);
+                    load_codes<true>(sB + stage * OP_BYTES, &tmB, bar, it, col0, p.b_blocked);
                     tma_load_3d_pair(sSA + stage * P_SFA_BYTES, &tmSA, bar, 0, it * 2, row_tile);
                     tma_load_3d_pair(sSB + stage * P_SFB_BYTES, &tmSB, bar, 0, it * 2, nb * 2);
                 }
@@ -454,7 +480,10 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     } else if (warp == 1) {
         if (leader) {
             // ------------------------------------------------------------ MMA issuer (leader)
-            const uint64_t a0 = sdesc_sw128(smem_u32(sA), 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+            const uint64_t a0 = p.a_blocked ? sdesc_blocked(smem_u32(sA), BM) : sdesc_sw128(smem_u32(sA), 16, 1024);
+            const uint64_t b0 = p.b_blocked ? sdesc_blocked(smem_u32(sB), BM) : sdesc_sw128(smem_u32(sB), 16, 1024);
+            // descriptor step of 64 k: 32 bytes of a swizzled row, or two blocks of all rows
+            const uint64_t a_step = p.a_blocked ? 2 * BM : 2, b_step = p.b_blocked ? 2 * BM : 2;
             const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
             int stage = 0;
             uint32_t phase = 0;
@@ -488,7 +517,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             if (kk < steps)
-                                umma_mxf4<2>(d, ad + kk * 2, bd + kk * 2, idesc_mxf4(2 * BM, P_BN, (kk & 1) * 2),
+                                umma_mxf4<2>(d, ad + kk * a_step, bd + kk * b_step, idesc_mxf4(2 * BM, P_BN, (kk & 1) * 2),
                                              tmem_base + P_SFA + (kk >> 1) * 4, tmem_base + P_SFB + (kk >> 1) * 8,
                                              (it | kk) != 0 ? 1u : 0u);
                         }
@@ -516,8 +545,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         const int half = (warp - 4) >> 2;
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0), shared0 = mapa_shared(smem_u32(shared_free), 0);
         [[maybe_unused]] uint8_t* hbuf = reinterpret_cast<uint8_t*>(turn) + (warp - 4) * H_BUF;
-        [[maybe_unused]] float* buf = turn + (8 * H_BUF + (warp - 4) * WARP_BUF) / 4;
-        [[maybe_unused]] const StoreMaps maps{&tmQ, &tmH, &tmY};
+        [[maybe_unused]] float* buf = turn + 8 * H_BUF / 4 + (warp - 4) * TURN_WORDS;
+        [[maybe_unused]] uint8_t* sc0 = reinterpret_cast<uint8_t*>(turn + 8 * (H_BUF / 4 + TURN_WORDS)) + half * 2 * SC_BYTES;
         constexpr int CH = EPI == EPI_SWIGLU ? 2 : 4;
         const int col0 = half * (CH * 32);
         // EPI_DSWIGLU: each warp copies its next 32 x 32 piece of H while it works on the present one.  (Loads
@@ -533,8 +562,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar, H_BUF);
                 const int x = (f >> 7) * 256 + (f & 127);
-                tma_load_3d(hbuf, &tmHin, bar, x, row, 0);
-                tma_load_3d(hbuf + H_BUF / 2, &tmHin, bar, x + 128, row, 0);
+                tma_load_3d(hbuf, &tmH, bar, x, row, 0);
+                tma_load_3d(hbuf + H_BUF / 2, &tmH, bar, x + 128, row, 0);
             }
             __syncwarp();
             h_pending = true;
@@ -555,6 +584,8 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             if (!okw) break;
             tc_fence_after();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * P_ACC1;
+            [[maybe_unused]] uint32_t ys = 0;                         // EPI_SWIGLU: the row's two scale bytes
+            [[maybe_unused]] uint8_t* sc = sc0 + acc * SC_BYTES;      // EPI_DSWIGLU: alternating, see below
             // The first accumulator's shared columns are its last, the second's its first: walk the
             // chunks so that they come first.  half 1 - acc holds them.
 #pragma unroll 1
@@ -569,7 +600,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(shared0);
                 }
-                if constexpr (EPI == EPI_SWIGLU) swiglu_chunk(p, v, u, row0 + lane, nb * 128 + col);
+                if constexpr (EPI == EPI_SWIGLU) ys |= swiglu_chunk(p, v, u, row0 + lane, nb * 128 + col) << (col & 32 ? 8 : 0);
                 else if constexpr (EPI == EPI_DSWIGLU) {
                     ok = mbar_wait_bounded_warp(h_full + (warp - 4), h_phase, p.status, p.timeout_ns, kWhereEpilogue);
                     if (!ok) break;
@@ -580,17 +611,28 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     __syncwarp();
                     if (i + 1 < CH) fetch_h(t, lt, i + 1);
                     else if (t + n_clusters < p.num_tiles) fetch_h(t + n_clusters, lt + 1, 0);
-                    dswiglu_chunk(p, maps, v, h, row0 + lane, nb * P_BN + col, row0 >> 5, buf, lane);
+                    dswiglu_chunk(p, v, h, row0 + lane, nb * P_BN + col, row0 >> 5, buf, sc, lane);
                 } else store_chunk(p, v, row0 + lane, nb * P_BN + col);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty0 + acc * 8);
+            if constexpr (EPI == EPI_SWIGLU) {
+                const int f0 = nb * 128 + col0;
+                if (row0 + lane < p.M && 2 * f0 < p.N)
+                    *reinterpret_cast<uint16_t*>(p.qs + scale_offset(row0 + lane, f0 >> 5, p.q_tiles)) = static_cast<uint16_t>(ys);
+            }
+            if constexpr (EPI == EPI_DSWIGLU) {
+                // The half's four warps have written this tile's scales.  The next tile's go to the other buffer,
+                // and nobody writes this one again before all have passed the next tile's wait.
+                if (lane == 0) mbar_arrive(sc_full + half);
+                ok = ok && mbar_wait_bounded_warp(sc_full + half, lt & 1, p.status, p.timeout_ns, kWhereEpilogue);
+                if (ok) put_scales(p, sc, row0 - q * 32, nb * P_BN + col0, q * 32 + lane, 15u);
+            }
         }
         if constexpr (EPI == EPI_DSWIGLU) {
             // (after a wait that gave up) no copy is in flight when this CTA exits
             if (h_pending) mbar_wait_bounded_warp(h_full + (warp - 4), h_phase, p.status, p.timeout_ns, kWhereDrain, false);
-            if (lane == 0) bulk_wait_group_all();  // this warp's stores are complete
         }
     }
 
@@ -612,8 +654,8 @@ constexpr int S_TMEM = 256;          // 128 accumulator columns, 24 of scales: t
 constexpr int S_SFA = 128, S_SFB = 136;
 constexpr int S_MAX_STAGES = 6;
 constexpr int S_SMEM = 113 * 1024;   // two CTAs an SM
-constexpr int S_RING = S_SMEM - 1024 - 256;  // a multiple of 128
-static_assert(S_RING % 128 == 0 && WARP_BUF % 128 == 0 && (TURN_WORDS * 4) % 128 == 0, "TMA boxes");
+constexpr int S_RING = S_SMEM - 1024 - 256;
+constexpr int S_EPI_BYTES = 4 * TURN_WORDS * 4 + SC_BYTES;  // EPI_DSWIGLU: the end of the ring
 template <int EPI>
 struct SingleGeom {
     static constexpr int sfb = EPI == EPI_SWIGLU ? 4 * SF_TILE : 2 * SF_TILE;
@@ -630,9 +672,7 @@ template <int EPI>
 __global__ void __launch_bounds__(S_THREADS, 2)
     mx_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmH,
-                     const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmHin,
-                   const Args p) {
+                     const Args p) {
     constexpr bool GATED = EPI == EPI_SWIGLU;
     constexpr int SFB = SingleGeom<EPI>::sfb;
     extern __shared__ uint8_t smem_raw[];
@@ -694,15 +734,16 @@ __global__ void __launch_bounds__(S_THREADS, 2)
             if (elect_one()) {
                 mbar_arrive_expect_tx(full + stage, bytes);
                 uint8_t* b = sB + stage * OP_BYTES;
+                const uint32_t bar = smem_u32(full + stage);
                 if constexpr (GATED) {
                     tma_load_3d(b, &tmB, full + stage, it * 128, gate_row, 0);
                     tma_load_3d(b + OP_BYTES / 2, &tmB, full + stage, it * 128, gate_row + 128, 0);
                     tma_load_3d(sSB + stage * SFB, &tmSB, full + stage, 0, it * 2, (f0 >> 7) * 2);
                 } else {
-                    tma_load_3d(b, &tmB, full + stage, it * 128, nb * S_BN, 0);
+                    load_codes<false>(b, &tmB, bar, it, nb * S_BN, p.b_blocked);
                     tma_load_3d(sSB + stage * SFB, &tmSB, full + stage, 0, it * 2, nb);
                 }
-                tma_load_3d(sA + stage * a_bytes, &tmA, full + stage, it * 128, mb * BM, 0);
+                load_codes<false>(sA + stage * a_bytes, &tmA, bar, it, mb * BM, p.a_blocked);
                 tma_load_3d(sSA + stage * 2 * SF_TILE, &tmSA, full + stage, 0, it * 2, mb);
             }
             armed |= 1u << stage;
@@ -720,7 +761,9 @@ __global__ void __launch_bounds__(S_THREADS, 2)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        const uint64_t a0 = sdesc_sw128(smem_u32(sA), 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+        const uint64_t a0 = p.a_blocked ? sdesc_blocked(smem_u32(sA), p.a_box) : sdesc_sw128(smem_u32(sA), 16, 1024);
+        const uint64_t b0 = p.b_blocked ? sdesc_blocked(smem_u32(sB), BM) : sdesc_sw128(smem_u32(sB), 16, 1024);
+        const uint64_t a_step = p.a_blocked ? 2 * p.a_box : 2, b_step = p.b_blocked ? 2 * BM : 2;
         const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
         int stage = 0;
         uint32_t phase = 0;
@@ -749,11 +792,11 @@ __global__ void __launch_bounds__(S_THREADS, 2)
                         if constexpr (GATED) {
                             // 64 rows of a scale tile are two of its four columns
                             const uint32_t id = idesc_mxf4(BM, 64, (kk & 1) * 2), odd = (f0 & 64) ? 2u : 0u;
-                            umma_mxf4<1>(tmem_base, ad + kk * 2, bd + kk * 2, id, sfa, sfb + odd, add);
-                            umma_mxf4<1>(tmem_base + 64, ad + kk * 2, bd + (OP_BYTES / 2 >> 4) + kk * 2, id, sfa, sfb + 8 + odd,
+                            umma_mxf4<1>(tmem_base, ad + kk * a_step, bd + kk * 2, id, sfa, sfb + odd, add);
+                            umma_mxf4<1>(tmem_base + 64, ad + kk * a_step, bd + (OP_BYTES / 2 >> 4) + kk * 2, id, sfa, sfb + 8 + odd,
                                          add);
                         } else {
-                            umma_mxf4<1>(tmem_base, ad + kk * 2, bd + kk * 2, idesc_mxf4(BM, S_BN, (kk & 1) * 2), sfa, sfb, add);
+                            umma_mxf4<1>(tmem_base, ad + kk * a_step, bd + kk * b_step, idesc_mxf4(BM, S_BN, (kk & 1) * 2), sfa, sfb, add);
                         }
                     }
                 }
@@ -812,8 +855,10 @@ __global__ void __launch_bounds__(S_THREADS, 2)
         cluster_sync_all();  // the partial sums have arrived
     }
     if (work) {
-        [[maybe_unused]] float* buf = reinterpret_cast<float*>(smem + S_RING - (q + 1) * WARP_BUF);
-        [[maybe_unused]] const StoreMaps maps{&tmQ, &tmH, &tmY};
+        // (at the ring's end, behind the received partial sums)
+        [[maybe_unused]] uint8_t* sc = smem + S_RING - SC_BYTES;
+        [[maybe_unused]] float* buf = reinterpret_cast<float*>(sc) - (q + 1) * TURN_WORDS;
+        [[maybe_unused]] uint32_t done = 0;
 #pragma unroll 1
         for (int c = 0; c < CH; ++c) {
             if (split > 1 && static_cast<uint32_t>(c % owners) != rank) continue;
@@ -842,15 +887,19 @@ __global__ void __launch_bounds__(S_THREADS, 2)
                     }
                 }
             }
-            if constexpr (GATED) swiglu_chunk(p, v, u, row0 + lane, f0 + c * 32);
-            else if constexpr (EPI == EPI_DSWIGLU) {
+            if constexpr (GATED) {
+                const uint32_t s = swiglu_chunk(p, v, u, row0 + lane, f0 + c * 32);
+                if (row0 + lane < p.M) p.qs[scale_offset(row0 + lane, (f0 >> 5) + c, p.q_tiles)] = static_cast<uint8_t>(s);
+            } else if constexpr (EPI == EPI_DSWIGLU) {
                 uint32_t h[32];
                 load_h(p, row0 + lane, nb * S_BN + c * 32, h);
-                dswiglu_chunk(p, maps, v, h, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, lane);
+                dswiglu_chunk(p, v, h, row0 + lane, nb * S_BN + c * 32, row0 >> 5, buf, sc, lane);
+                done |= 1u << c;
             } else store_chunk(p, v, row0 + lane, nb * S_BN + c * 32);
         }
         if constexpr (EPI == EPI_DSWIGLU) {
-            if (lane == 0) bulk_wait_group_all();
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps' scales are there
+            put_scales(p, sc, mb * BM, nb * S_BN, q * 32 + lane, done);
         }
     }
     tc_fence_before();

@@ -110,6 +110,16 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
+// The same with the mbarrier given by its shared-memory address.
+__device__ __forceinline__ void tma_load_3d_bar(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                                int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 // 4-D tiled load (used for MN-major operands viewed as [shard][chunk][K][64]).
 __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
                                             int32_t y, int32_t z, int32_t w) {
