@@ -111,10 +111,21 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = _device = None  # torch's raw-handle lookups, once CUDA is up
+
+
 def _stream(s):
     if s is None:
+        global _raw_stream, _device
+        if _raw_stream is not None:  # (a Stream object costs several microseconds a call)
+            return _raw_stream(_device())
         import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if not torch.cuda.is_available():
+            return None
+        handle = torch.cuda.current_stream().cuda_stream  # initialises CUDA
+        _device = getattr(torch._C, "_cuda_getDevice", None)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if _device is not None else None
+        return handle
     if isinstance(s, int):
         return s
     return s.cuda_stream
