@@ -150,20 +150,85 @@ int exchange_bytes(int split, int rows) {
     const int owners = std::min(split, CH);
     return (CH + owners - 1) / owners * (split - 1) * PARTS * 128 * rows;
 }
-template <int EPI>
+template <int EPI, int CTAS>
 bool split_fits(int split, int rows, int kb) {
-    const int room = mx::S_RING - (EPI == EPI_DSWIGLU ? mx::S_EPI_BYTES : 0);
+    const int room = mx::SingleGeom<EPI, CTAS>::ring - (EPI == EPI_DSWIGLU ? mx::S_EPI_BYTES : 0);
     return split <= kb && exchange_bytes<EPI>(split, std::min((rows + 31) / 32 * 32, mx::BM)) <= room;
+}
+
+template <int EPI, int CTAS>
+tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec& g, mx::Args k, int mode, int split, CUtensorMap (&m)[5],
+                           const DeviceInfo& dev, cudaStream_t st) {
+    using Geom = mx::SingleGeom<EPI, CTAS>;
+    constexpr bool GATED = EPI == EPI_SWIGLU;
+    static bool attr_done[64];
+    auto kern = mx::mx_single_kernel<EPI, CTAS>;
+    if (!set_smem(kern, dev.device, Geom::smem, attr_done)) return TPMLP_ERR_CUDA;
+    k.a_box = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+    k.stages = Geom::stages(k.a_box);
+    const int64_t n_blocks = GATED ? g.N / 128 : (g.N + 127) / 128, m_blocks = (g.M + 127) / 128;
+    const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
+    if (mode >= 3) {
+        split = 2 << (mode - 3);
+        while (split > 1 && !split_fits<EPI, CTAS>(split, rows, k.kb)) split /= 2;
+    }
+    k.m_blocks = static_cast<int>(m_blocks);
+    if (!codes_map(&m[0], a, g.K, static_cast<uint32_t>(k.a_box)) || !codes_map(&m[1], b, g.K, GATED ? 64 : 128) ||
+        !scales_map(&m[2], a, g.K, 1) || !scales_map(&m[3], b, g.K, GATED ? 2 : 1))
+        return TPMLP_ERR_CUDA;
+    return launch(kern, dim3(static_cast<unsigned>(n_blocks * m_blocks * split)), mx::S_THREADS, Geom::smem,
+                  static_cast<unsigned>(split), st, m, k);
+}
+
+// Which kernel takes a product, by its expected time in microseconds.  Fitted to one GB300's times of 30
+// products (N x K of 40960x5120, 5120x20480, 8192x1024, 4096x4096, 2048x8192, 128 to 2048 rows; most within 15 %):
+//   pairs    4 + waves (0.265 kb + 1.6)       256x256 tiles over the CTA pairs, kb stages of 256 k each
+//   single   2.8 + 0.35 kb                     at most one CTA an SM,
+//            2.8 + 0.40 kb                     at most two, else
+//            2.8 + waves (0.40 kb + 3)
+//   split    2.8 + 0.35 kb / split + 3         at most one CTA an SM: the partial sums cross in about 3 us,
+//            2.8 + 0.40 kb / split + 5.5       at most two
+// For example 512 x 5120 x 20480: pairs 27.3 measured, single 32.6, split two ways 39; 800 rows: single 34.8,
+// pairs 49.8 (80 tiles, two waves); 48 x 5120 x 20480: split four ways 15.3, single 25.7, pairs 26.0;
+// 333 x 4096 x 16384: split two ways 19.4, pairs 22.1, single 25.1.
+// At most 128 rows: single CTAs, which copy no more rows of A than there are (4 x 40960 x 5120: 26 against 31).
+struct Choice {
+    bool pair;
+    int split;
+};
+template <int EPI>
+Choice choose(const MxSpec& g, int kb, int cap, int sms) {
+    const int64_t n1 = EPI == EPI_SWIGLU ? g.N / 128 : (g.N + 127) / 128, tiles1 = n1 * ((g.M + 127) / 128);
+    const int64_t tiles2 = ((g.M + 255) / 256) * ((g.N + 255) / 256);
+    const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
+    const int64_t waves1 = (tiles1 + 2 * sms - 1) / (2 * sms);
+    Choice c{false, 1};
+    double best = 2.8 + (tiles1 <= sms ? 0.35 * kb : waves1 == 1 ? 0.40 * kb : waves1 * (0.40 * kb + 3.0));
+    for (int s = 2; s <= 8; s *= 2) {
+        // (40 tiles split four ways are 160 CTAs on 152 SMs: a few SMs with two cost little)
+        const bool one = tiles1 * s <= sms + sms / 16;
+        if (tiles1 * s > 2 * sms || !split_fits<EPI, 2>(s, rows, kb)) break;
+        const double t = one ? 2.8 + 0.35 * kb / s + 3.0 : 2.8 + 0.40 * kb / s + 5.5;
+        if (t < best) {
+            best = t;
+            c.split = s;
+        }
+    }
+    if (cap > 0 && g.M > mx::BM) {
+        const int64_t waves2 = (tiles2 + cap - 1) / cap;
+        if (4.0 + waves2 * (0.265 * kb + 1.6) < best) c.pair = true;
+    }
+    return c;
 }
 
 template <int EPI>
 tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec& g, mx::Args k, const DeviceInfo& dev,
                             cudaStream_t st) {
-    constexpr bool GATED = EPI == EPI_SWIGLU;
     const int mode = g_mode.load(std::memory_order_relaxed);
     const int cap = pair_capacity<EPI>(dev);
     const int64_t m_pairs = (g.M + 255) / 256, n_pairs = (g.N + 255) / 256;
-    const bool pair = cap > 0 && (mode == 2 || (mode == 0 && m_pairs * n_pairs >= cap));
+    const Choice choice = mode == 0 ? choose<EPI>(g, k.kb, cap, dev.sm_count) : Choice{mode == 2 && cap > 0, 1};
+    const bool pair = choice.pair;
     CUtensorMap m[5];
     if (pair) {
         if constexpr (EPI == EPI_DSWIGLU) {
@@ -178,29 +243,15 @@ tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec
         const int clusters = std::min(k.num_tiles, cap);
         return launch(mx::mx_pair_kernel<EPI>, dim3(2 * clusters), mx::P_THREADS, mx::PairGeom<EPI>::smem, 2, st, m, k);
     }
-    static bool attr_done[64];
-    auto kern = mx::mx_single_kernel<EPI>;
-    if (!set_smem(kern, dev.device, mx::S_SMEM, attr_done)) return TPMLP_ERR_CUDA;
-    k.a_box = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
-    k.stages = mx::SingleGeom<EPI>::stages(k.a_box);
-    const int64_t n_blocks = GATED ? g.N / 128 : (g.N + 127) / 128, m_blocks = (g.M + 127) / 128;
-    const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
-    int split = 1;
-    if (mode >= 3) {
-        split = 2 << (mode - 3);
-        while (split > 1 && !split_fits<EPI>(split, rows, k.kb)) split /= 2;
-    } else if (mode == 0) {
-        while (split < 8 && split_fits<EPI>(split * 2, rows, k.kb) && n_blocks * m_blocks * split * 2 <= 2 * dev.sm_count) split *= 2;
+    if constexpr (EPI != EPI_DSWIGLU) {
+        // Three CTAs an SM (three ring stages each, at most 32 rows of A) where two would need another wave for the
+        // rest of the tiles: 4 x 40960 x 5120, 320 tiles: 22.8 us against 26.1.  Where two are enough their longer
+        // rings are better: 1 x 32768 x 4096, 256 tiles: 14.4 against 15.3.
+        const int64_t tiles = EPI == EPI_SWIGLU ? g.N / 128 : (g.N + 127) / 128;
+        if (mode == 0 && g.M <= 32 && tiles > 2 * dev.sm_count)
+            return launch_single<EPI, 3>(a, b, g, k, mode, 1, m, dev, st);
     }
-    if (m_blocks > 65535 || n_blocks * split > 0x7FFFFFFF) {
-        set_error("MXFP4 GEMM: %lld x %lld tiles", (long long)m_blocks, (long long)n_blocks);
-        return TPMLP_ERR_SHAPE;
-    }
-    if (!codes_map(&m[0], a, g.K, static_cast<uint32_t>(k.a_box)) || !codes_map(&m[1], b, g.K, GATED ? 64 : 128) ||
-        !scales_map(&m[2], a, g.K, 1) || !scales_map(&m[3], b, g.K, GATED ? 2 : 1))
-        return TPMLP_ERR_CUDA;
-    return launch(kern, dim3(static_cast<unsigned>(n_blocks * split), static_cast<unsigned>(m_blocks)), mx::S_THREADS, mx::S_SMEM,
-                  static_cast<unsigned>(split), st, m, k);
+    return launch_single<EPI, 2>(a, b, g, k, mode, choice.split, m, dev, st);
 }
 
 }  // namespace

@@ -650,31 +650,34 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 // ---------------------------------------------------------------- single kernel
 constexpr int S_BN = 128;
 constexpr int S_THREADS = 192;       // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
-constexpr int S_TMEM = 256;          // 128 accumulator columns, 24 of scales: two CTAs an SM
-constexpr int S_SFA = 128, S_SFB = 136;
+// Tensor memory: 128 accumulator columns and 32 for the scales, two allocations, so that three CTAs
+// fit an SM's 512 columns.
+constexpr int S_ACC_COLS = 128, S_SF_COLS = 32;
+constexpr int S_SFA = 0, S_SFB = 8;
 constexpr int S_MAX_STAGES = 6;
-constexpr int S_SMEM = 113 * 1024;   // two CTAs an SM
-constexpr int S_RING = S_SMEM - 1024 - 256;
 constexpr int S_EPI_BYTES = 4 * TURN_WORDS * 4 + SC_BYTES;  // EPI_DSWIGLU: the end of the ring
-template <int EPI>
+template <int EPI, int CTAS>
 struct SingleGeom {
+    static constexpr int smem = CTAS == 3 ? 75 * 1024 : 113 * 1024;
+    static constexpr int ring = smem - 1024 - 256;
     static constexpr int sfb = EPI == EPI_SWIGLU ? 4 * SF_TILE : 2 * SF_TILE;
     static __host__ __device__ constexpr int stage(int a_box) { return a_box * 128 + OP_BYTES + 2 * SF_TILE + sfb; }
-    // stages that fit with the MMA's reads past a narrow A box kept inside the ring
+    // (the MMA's reads past a narrow A box stay inside the ring: the B stages follow)
     static __host__ __device__ constexpr int stages(int a_box) {
-        const int n = S_RING / stage(a_box);
+        const int n = ring / stage(a_box);
         return n < S_MAX_STAGES ? n : S_MAX_STAGES;
     }
 };
-static_assert(SingleGeom<EPI_STORE>::stages(128) >= 3 && SingleGeom<EPI_SWIGLU>::stages(128) >= 3, "ring depth");
+static_assert(SingleGeom<EPI_STORE, 2>::stages(128) >= 3 && SingleGeom<EPI_SWIGLU, 2>::stages(128) >= 3, "ring depth");
+static_assert(SingleGeom<EPI_SWIGLU, 3>::stages(32) >= 3, "ring depth");
 
-template <int EPI>
-__global__ void __launch_bounds__(S_THREADS, 2)
+template <int EPI, int CTAS>
+__global__ void __launch_bounds__(S_THREADS, CTAS)
     mx_single_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                      const Args p) {
     constexpr bool GATED = EPI == EPI_SWIGLU;
-    constexpr int SFB = SingleGeom<EPI>::sfb;
+    constexpr int SFB = SingleGeom<EPI, CTAS>::sfb, S_RING = SingleGeom<EPI, CTAS>::ring;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int a_bytes = p.a_box * 128;
@@ -685,14 +688,15 @@ __global__ void __launch_bounds__(S_THREADS, 2)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S_RING);
     uint64_t* empty = full + S_MAX_STAGES;
     uint64_t* tfull = empty + S_MAX_STAGES;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);  // [2]
 
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);  // warp-uniform for the compiler
     const int lane = threadIdx.x & 31;
     uint32_t split, rank;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
     rank = cluster_ctarank();
-    const int nb = blockIdx.x / split, mb = blockIdx.y;
+    // all row tiles of a column tile first: B's codes are read from memory once
+    const int tile = blockIdx.x / split, nb = tile / p.m_blocks, mb = tile - nb * p.m_blocks;
     const int it0 = static_cast<int>((long long)p.kb * rank / split), it1 = static_cast<int>((long long)p.kb * (rank + 1) / split);
 
     if (threadIdx.x == 0) {
@@ -711,13 +715,14 @@ __global__ void __launch_bounds__(S_THREADS, 2)
         tma_prefetch_desc(&tmSB);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, S_TMEM);
+        tmem_alloc(tmem_slot, S_ACC_COLS);
+        tmem_alloc(tmem_slot + 1, S_SF_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem_base = tmem_slot[0], sf_base = tmem_slot[1];
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
 
@@ -779,16 +784,16 @@ __global__ void __launch_bounds__(S_THREADS, 2)
 #pragma unroll
                 for (int kt = 0; kt < 2; ++kt) {
                     if (kt * 2 < steps) {
-                        copy_scales<1>(tmem_base + S_SFA + kt * 4, sad + kt * (SF_TILE >> 4));
-                        copy_scales<1>(tmem_base + S_SFB + kt * 4, sbd + kt * (SF_TILE >> 4));
-                        if constexpr (GATED) copy_scales<1>(tmem_base + S_SFB + 8 + kt * 4, sbd + (2 + kt) * (SF_TILE >> 4));
+                        copy_scales<1>(sf_base + S_SFA + kt * 4, sad + kt * (SF_TILE >> 4));
+                        copy_scales<1>(sf_base + S_SFB + kt * 4, sbd + kt * (SF_TILE >> 4));
+                        if constexpr (GATED) copy_scales<1>(sf_base + S_SFB + 8 + kt * 4, sbd + (2 + kt) * (SF_TILE >> 4));
                     }
                 }
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     if (kk < steps) {
                         const uint32_t add = (it != it0 || kk != 0) ? 1u : 0u;
-                        const uint32_t sfa = tmem_base + S_SFA + (kk >> 1) * 4, sfb = tmem_base + S_SFB + (kk >> 1) * 4;
+                        const uint32_t sfa = sf_base + S_SFA + (kk >> 1) * 4, sfb = sf_base + S_SFB + (kk >> 1) * 4;
                         if constexpr (GATED) {
                             // 64 rows of a scale tile are two of its four columns
                             const uint32_t id = idesc_mxf4(BM, 64, (kk & 1) * 2), odd = (f0 & 64) ? 2u : 0u;
@@ -907,7 +912,8 @@ __global__ void __launch_bounds__(S_THREADS, 2)
     tc_fence_after();
     if (warp == 1) {
         __syncwarp();
-        tmem_dealloc(tmem_base, S_TMEM);
+        tmem_dealloc(tmem_base, S_ACC_COLS);
+        tmem_dealloc(sf_base, S_SF_COLS);
     }
 }
 
