@@ -86,7 +86,7 @@ bool set_smem(Kern kern, int device, int bytes, bool (&done)[64]) {
 }
 
 template <typename Kern>
-tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const CUtensorMap (&m)[5],
+tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const CUtensorMap (&m)[6],
                     const mx::Args& k) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -105,7 +105,7 @@ tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluste
     cudaError_t e;
     if constexpr (std::is_invocable_v<Kern, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, mx::Args>)
         e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], k);
-    else e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], k);
+    else e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], k);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("MXFP4 GEMM launch: %s", cudaGetErrorString(e));
@@ -157,7 +157,7 @@ bool split_fits(int split, int rows, int kb) {
 }
 
 template <int EPI, int CTAS>
-tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec& g, mx::Args k, int mode, int split, CUtensorMap (&m)[5],
+tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec& g, mx::Args k, int mode, int split, CUtensorMap (&m)[6],
                            const DeviceInfo& dev, cudaStream_t st) {
     using Geom = mx::SingleGeom<EPI, CTAS>;
     constexpr bool GATED = EPI == EPI_SWIGLU;
@@ -229,16 +229,16 @@ tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec
     const int64_t m_pairs = (g.M + 255) / 256, n_pairs = (g.N + 255) / 256;
     const Choice choice = mode == 0 ? choose<EPI>(g, k.kb, cap, dev.sm_count) : Choice{mode == 2 && cap > 0, 1};
     const bool pair = choice.pair;
-    CUtensorMap m[5];
+    CUtensorMap m[6];
     if (pair) {
         if constexpr (EPI == EPI_DSWIGLU) {
-            if (!h_map(&m[4], g.h_in, g.h_ld, g.M)) return TPMLP_ERR_CUDA;
+            if (!h_map(&m[5], g.h_in, g.h_ld, g.M)) return TPMLP_ERR_CUDA;
         }
         k.m_blocks = static_cast<int>(m_pairs);
         k.n_blocks = static_cast<int>(n_pairs);
         k.num_tiles = k.m_blocks * k.n_blocks;
         if (!codes_map(&m[0], a, g.K, mx::BM) || !codes_map(&m[1], b, g.K, mx::BM) || !scales_map(&m[2], a, g.K, 1) ||
-            !scales_map(&m[3], b, g.K, 2))
+            !scales_map(&m[3], b, g.K, 2) || !codes_map(&m[4], b, g.K, mx::BM / 2))
             return TPMLP_ERR_CUDA;
         const int clusters = std::min(k.num_tiles, cap);
         return launch(mx::mx_pair_kernel<EPI>, dim3(2 * clusters), mx::P_THREADS, mx::PairGeom<EPI>::smem, 2, st, m, k);
