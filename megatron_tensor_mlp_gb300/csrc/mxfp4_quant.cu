@@ -129,185 +129,190 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
     }
 }
 
-// Along the rows, and along the columns too where q is given.  A CTA walks tiles of 128 rows x 256
-// bytes of columns (128 bf16, 64 fp32) through two shared-memory buffers, the next tile's
-// asynchronous copies running behind the work on this one: the tile's values are read from memory
-// once and its two quantisations work from shared memory.  Along the columns 16 lanes take a row;
-// along the rows a thread takes 32 rows of one word (two bf16 columns or one fp32 column), and the
-// codes are gathered in shared memory so that each column leaves as one run of 64 bytes.
+// Along the rows, and along the columns too where q is given.  A CTA takes a tile of 128 rows x 256
+// bytes of columns (128 bf16, 64 fp32): asynchronous copies bring it to shared memory, both
+// quantisations work from there, and the other four CTAs of the SM cover its latency.  Along the
+// columns 16 lanes take a row; along the rows a thread takes 32 rows of one word (two bf16 columns or
+// one fp32 column), and the codes are gathered in shared memory so that each column leaves as one run
+// of 64 bytes.  The values are read from memory once.
 template <bool F32>
 struct BothSmem {
-    uint32_t tile[2][128 * 64];
+    uint32_t tile[128 * 64];
     uint8_t out[256 / Piece<F32>::ES * 80];  // 64 bytes of codes a column, pitch 80
     uint32_t sc[256 / Piece<F32>::ES];
 };
 
 template <bool F32>
-__global__ void __launch_bounds__(256) quantize_both_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(256, 5) quantize_both_kernel(const QuantArgs a) {
     using P = Piece<F32>;
     constexpr int TC = 256 / P::ES;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    BothSmem<F32>& sm = *reinterpret_cast<BothSmem<F32>*>(smem_raw);
-    const int t = threadIdx.x, lane16 = t & 15;
+    __shared__ __align__(16) BothSmem<F32> sm;
+    const int t = threadIdx.x, lane16 = t & 15, r0 = t >> 4;
     const long long total = static_cast<long long>(a.cols) * a.p;
-    const long long k_tiles = (total + 127) / 128, pitch = (total + 31) / 32 * 16;
-    const long long t_pitch = (static_cast<long long>(a.rows) + 31) / 32 * 16, t_tiles = (static_cast<long long>(a.rows) + 127) / 128;
     const unsigned col_tiles = static_cast<unsigned>(a.spans);
+    const unsigned rt = blockIdx.x / col_tiles;
+    const long long c_tile = static_cast<long long>(blockIdx.x - rt * col_tiles) * TC, r_tile = static_cast<long long>(rt) * 128;
+    const long long c0 = c_tile + lane16 * P::E;
+    const int rows = static_cast<int>(a.rows - r_tile < 128 ? a.rows - r_tile : 128);  // of this tile
     griddep_wait();
     if (t == 0) griddep_launch_dependents();
-
-    auto fetch = [&](unsigned item, uint32_t* dst) {
-        const unsigned rt = item / col_tiles;
-        const long long c0 = static_cast<long long>(item - rt * col_tiles) * TC + lane16 * P::E;
+    {
         int n;
-        const uint8_t* src = piece_at<F32>(a, c0, n);
+        const uint8_t* src = piece_at<F32>(a, c0, n) + (r_tile + r0) * a.ldx;
+        uint32_t dst = smem_u32(sm.tile + r0 * 64 + lane16 * 4);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int r = (t >> 4) + i * 16;
-            const long long row = static_cast<long long>(rt) * 128 + r;
-            const uint32_t bytes = row < a.rows ? n * P::ES : 0;  // the rest of the 16 are zero-filled, not read
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + r * 64 + lane16 * 4)),
-                         "l"(bytes ? src + row * a.ldx : a.x), "r"(bytes)
+            const uint32_t bytes = r0 + i * 16 < rows ? n * P::ES : 0;  // the rest of the 16 are zero-filled, not read
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 4096), "l"(bytes ? src : a.x), "r"(bytes)
                          : "memory");
+            src += 16 * a.ldx;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    unsigned item = blockIdx.x;
-    const unsigned items = static_cast<unsigned>(a.items);
-    int buf = 0;
-    if (item < items) fetch(item, sm.tile[0]);
-    for (; item < items; item += gridDim.x, buf ^= 1) {
-        if (item + gridDim.x < items) {
-            fetch(item + gridDim.x, sm.tile[buf ^ 1]);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        __syncthreads();
-        const uint32_t* tile = sm.tile[buf];
-        const unsigned rt = item / col_tiles;
-        const long long c_tile = static_cast<long long>(item - rt * col_tiles) * TC, r_tile = static_cast<long long>(rt) * 128;
-        if (a.q != nullptr) {
-            const long long c0 = c_tile + lane16 * P::E;
-            uint8_t* qd = a.q + r_tile * pitch + c0 / 2;
-            uint8_t* sd = a.s + mx::scale_offset(r_tile, c0 >> 5, k_tiles);
-            const bool put = c0 / 2 < pitch;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = (t >> 4) + i * 16;
-                const uint4 v = *reinterpret_cast<const uint4*>(tile + r * 64 + lane16 * 4);
-                const uint32_t s = P::scale(v);
-                const uint32_t code = P::codes(v, s);
-                if (r_tile + r < a.rows) {
-                    if (put) {
-                        if constexpr (F32) *reinterpret_cast<uint16_t*>(qd + r * pitch) = static_cast<uint16_t>(code);
-                        else *reinterpret_cast<uint32_t*>(qd + r * pitch) = code;
-                    }
-                    // (col_tiles cover whole scale tiles: padding blocks are written as zero)
-                    if (lane16 % P::LANES == 0) sd[(r & 31) * 16 + (r >> 5) * 4] = static_cast<uint8_t>(s);
-                }
-            }
-        }
-        {
-            const int word = t & 63, rb = t >> 6;
-            const uint32_t* col = tile + rb * 32 * 64 + word;
-            uint8_t* sb = reinterpret_cast<uint8_t*>(sm.sc);
-            if constexpr (F32) {
-                float v[32];
-#pragma unroll
-                for (int r = 0; r < 32; ++r) v[r] = __uint_as_float(col[r * 64]);
-                uint4 c;
-                sb[word * 4 + rb] = static_cast<uint8_t>(mx::quantize32(v, c));
-                *reinterpret_cast<uint4*>(sm.out + word * 80 + rb * 16) = c;
-            } else {
-                uint32_t w[32];
-#pragma unroll
-                for (int r = 0; r < 32; ++r) w[r] = col[r * 64];
-                uint32_t m[4] = {w[0], w[1], w[2], w[3]};
-#pragma unroll
-                for (int r = 4; r < 32; ++r) m[r & 3] = mx::amax_bf16x2(m[r & 3], w[r]);
-                const uint32_t mm = mx::amax_bf16x2(mx::amax_bf16x2(m[0], m[1]), mx::amax_bf16x2(m[2], m[3])) & 0x7FFF7FFFu;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t s = mx::scale_of(half ? (mm & 0xFFFF0000u) : (mm << 16));
-                    const float inv = mx::inverse_scale(s);
-                    uint32_t c[4];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            v[i] = __uint_as_float(half ? (w[g * 8 + i] & 0xFFFF0000u) : (w[g * 8 + i] << 16));
-#pragma unroll
-                        for (int i = 0; i < 8; i += 2) mx::mul2(v[i], v[i + 1], inv);
-                        c[g] = s == 255u ? 0u : mx::encode8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
-                    }
-                    *reinterpret_cast<uint4*>(sm.out + (word * 2 + half) * 80 + rb * 16) = make_uint4(c[0], c[1], c[2], c[3]);
-                    sb[(word * 2 + half) * 4 + rb] = static_cast<uint8_t>(s);
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < TC / 64; ++i) {
-            const int c = (t >> 2) + i * 64;
-            const long long col = c_tile + c, at = r_tile / 2 + (t & 3) * 16;
-            if (col < total && at < t_pitch)
-                *reinterpret_cast<uint4*>(a.qt + col * t_pitch + at) =
-                    *reinterpret_cast<const uint4*>(sm.out + c * 80 + (t & 3) * 16);
-        }
-        if (t < TC && c_tile + t < total)
-            *reinterpret_cast<uint32_t*>(a.st + mx::scale_offset(c_tile + t, rt * 4LL, t_tiles)) = sm.sc[t];
-        // (the next pass writes out and sc behind its first barrier, and this buffer's copies start there too)
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    __syncthreads();
+    if (a.q != nullptr) {
+        const long long k_tiles = (total + 127) / 128, pitch = (total + 31) / 32 * 16;
+        uint8_t* qd = a.q + (r_tile + r0) * pitch + c0 / 2;
+        // (r0 < 16: rows r0 + 16 i of a scale tile are constant distances apart)
+        uint8_t* sd = a.s + mx::scale_offset(r_tile + r0, c0 >> 5, k_tiles);
+        const bool put = c0 / 2 < pitch;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(sm.tile + (r0 + i * 16) * 64 + lane16 * 4);
+            const uint32_t s = P::scale(v);
+            const uint32_t code = P::codes(v, s);
+            if (r0 + i * 16 < rows) {
+                if (put) {
+                    if constexpr (F32) *reinterpret_cast<uint16_t*>(qd) = static_cast<uint16_t>(code);
+                    else *reinterpret_cast<uint32_t*>(qd) = code;
+                }
+                // (col_tiles cover whole scale tiles: padding blocks are written as zero)
+                if (lane16 % P::LANES == 0) sd[(i & 1) * 256 + (i >> 1) * 4] = static_cast<uint8_t>(s);
+            }
+            qd += 16 * pitch;
+        }
+    }
+    {
+        const int word = t & 63, rb = t >> 6;
+        const uint32_t* col = sm.tile + rb * 32 * 64 + word;
+        uint8_t* sb = reinterpret_cast<uint8_t*>(sm.sc);
+        if constexpr (F32) {
+            float v[32];
+#pragma unroll
+            for (int r = 0; r < 32; ++r) v[r] = __uint_as_float(col[r * 64]);
+            uint4 c;
+            sb[word * 4 + rb] = static_cast<uint8_t>(mx::quantize32(v, c));
+            *reinterpret_cast<uint4*>(sm.out + word * 80 + rb * 16) = c;
+        } else {
+            // (the values are read twice, so that a CTA's registers leave room for five)
+            uint32_t m[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) m[r] = mx::amax_bf16x2(col[r * 64], col[(r + 4) * 64]);
+#pragma unroll
+            for (int r = 8; r < 32; ++r) m[r & 3] = mx::amax_bf16x2(m[r & 3], col[r * 64]);
+            const uint32_t mm = mx::amax_bf16x2(mx::amax_bf16x2(m[0], m[1]), mx::amax_bf16x2(m[2], m[3])) & 0x7FFF7FFFu;
+            const uint32_t s0 = mx::scale_of(mm << 16), s1 = mx::scale_of(mm & 0xFFFF0000u);
+            const float inv0 = mx::inverse_scale(s0), inv1 = mx::inverse_scale(s1);
+            uint32_t c0w[4], c1w[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float lo[8], hi[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t w = col[(g * 8 + i) * 64];
+                    lo[i] = __uint_as_float(w << 16);
+                    hi[i] = __uint_as_float(w & 0xFFFF0000u);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    mx::mul2(lo[i], lo[i + 1], inv0);
+                    mx::mul2(hi[i], hi[i + 1], inv1);
+                }
+                c0w[g] = s0 == 255u ? 0u : mx::encode8(lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]);
+                c1w[g] = s1 == 255u ? 0u : mx::encode8(hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]);
+            }
+            uint8_t* o = sm.out + word * 160 + rb * 16;
+            *reinterpret_cast<uint4*>(o) = make_uint4(c0w[0], c0w[1], c0w[2], c0w[3]);
+            *reinterpret_cast<uint4*>(o + 80) = make_uint4(c1w[0], c1w[1], c1w[2], c1w[3]);
+            sb[word * 8 + rb] = static_cast<uint8_t>(s0);
+            sb[word * 8 + 4 + rb] = static_cast<uint8_t>(s1);
+        }
+    }
+    __syncthreads();
+    const long long t_pitch = (static_cast<long long>(a.rows) + 31) / 32 * 16, t_tiles = (static_cast<long long>(a.rows) + 127) / 128;
+#pragma unroll
+    for (int i = 0; i < TC / 64; ++i) {
+        const int c = (t >> 2) + i * 64;
+        const long long col = c_tile + c, at = r_tile / 2 + (t & 3) * 16;
+        if (col < total && at < t_pitch)
+            *reinterpret_cast<uint4*>(a.qt + col * t_pitch + at) = *reinterpret_cast<const uint4*>(sm.out + c * 80 + (t & 3) * 16);
+    }
+    if (t < TC && c_tile + t < total)
+        *reinterpret_cast<uint32_t*>(a.st + mx::scale_offset(c_tile + t, rt * 4LL, t_tiles)) = sm.sc[t];
 }
 
-// Values of an operand: a thread takes 8 codes.
-template <bool F32>
+// Values of an operand: a warp takes U spans of 32 words (256 values) of a row, a word of eight codes a
+// lane, all loaded before the first is worked on.
+template <bool F32, int U>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s, void* out,
-                                                         long long rows, long long k) {
+                                                         long long rows, long long k, long long spans) {
+    const int lane = threadIdx.x & 31;
+    const long long pitch = (k + 31) / 32 * 16, k_tiles = (k + 127) / 128, words = (k + 7) / 8;
+    const long long it0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * U;
+    long long row = it0 / spans, span = it0 - row * spans;
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    const long long pitch = (k + 31) / 32 * 16, k_tiles = (k + 127) / 128, words = (k + 7) / 8;
-    const long long items = rows * words;
-    for (long long it = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; it < items;
-         it += static_cast<long long>(gridDim.x) * 256) {
-        const long long row = it / words, w = it - row * words;
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(q + row * pitch + w * 4);
-        const float sv = mx::scale_value(s[mx::scale_offset(row, w / 4, k_tiles)]);
-        float v[8];
-        mx::decode8(c, v);
+    uint32_t c[U], sb[U];
+    long long rw[U], w[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= sv;
-        const long long at = row * k + w * 8;
+    for (int i = 0; i < U; ++i) {
+        rw[i] = row;
+        w[i] = row < rows ? span * 32 + lane : words;
+        if (w[i] < words) {
+            c[i] = __ldg(reinterpret_cast<const uint32_t*>(q + row * pitch) + w[i]);
+            sb[i] = __ldg(s + mx::scale_offset(row, w[i] >> 2, k_tiles));
+        }
+        if (++span == spans) {
+            span = 0;
+            ++row;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        if (w[i] >= words) continue;
+        const float sv = mx::scale_value(sb[i]);
+        float v[8];
+        mx::decode8(c[i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= sv;
+        const long long at = rw[i] * k + w[i] * 8;
         if constexpr (F32) {
             float* d = static_cast<float*>(out) + at;
-            if (k % 4 == 0 && w * 8 + 8 <= k) {
+            if (k % 4 == 0 && w[i] * 8 + 8 <= k) {
                 *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
                 *reinterpret_cast<float4*>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
             } else {
-                for (int i = 0; i < 8 && w * 8 + i < k; ++i) d[i] = v[i];
+                for (int j = 0; j < 8 && w[i] * 8 + j < k; ++j) d[j] = v[j];
             }
         } else {
             __nv_bfloat16* d = static_cast<__nv_bfloat16*>(out) + at;
             if (k % 8 == 0) {
                 __nv_bfloat162 b[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
                 *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(b);
             } else {
-                for (int i = 0; i < 8 && w * 8 + i < k; ++i) d[i] = __float2bfloat16_rn(v[i]);
+                for (int j = 0; j < 8 && w[i] * 8 + j < k; ++j) d[j] = __float2bfloat16_rn(v[j]);
             }
         }
     }
 }
 
 template <typename... P, typename... A>
-tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, int smem, cudaStream_t st, A... args) {
+tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -336,24 +341,13 @@ tpmlp_status quantize(QuantArgs a, int64_t cols, const DeviceInfo& dev, cudaStre
         const bool many = a.items >= static_cast<int64_t>(dev.sm_count) * 64 * 4;
         const int64_t per = many ? 32 : 8;
         const dim3 grid(static_cast<unsigned>((a.items + per - 1) / per));
-        return many ? launch_pdl("MXFP4 quantisation", quantize_rows_kernel<F32, 4>, grid, 0, st, a)
-                    : launch_pdl("MXFP4 quantisation", quantize_rows_kernel<F32, 1>, grid, 0, st, a);
+        return many ? launch_pdl("MXFP4 quantisation", quantize_rows_kernel<F32, 4>, grid, st, a)
+                    : launch_pdl("MXFP4 quantisation", quantize_rows_kernel<F32, 1>, grid, st, a);
     }
     constexpr int TC = 256 / Piece<F32>::ES;
     a.spans = (cols + 127) / 128 * (128 / TC);
     a.items = a.spans * ((a.rows + 127LL) / 128);
-    static bool attr_done[64];
-    constexpr int smem = sizeof(BothSmem<F32>);
-    if (dev.device >= 64 || !attr_done[dev.device]) {
-        const cudaError_t e = cudaFuncSetAttribute(quantize_both_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) {
-            set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-            return TPMLP_ERR_CUDA;
-        }
-        if (dev.device < 64) attr_done[dev.device] = true;
-    }
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.items, dev.sm_count * 2)));
-    return launch_pdl("MXFP4 quantisation", quantize_both_kernel<F32>, grid, smem, st, a);
+    return launch_pdl("MXFP4 quantisation", quantize_both_kernel<F32>, dim3(static_cast<unsigned>(a.items)), st, a);
 }
 
 }  // namespace
@@ -369,12 +363,19 @@ tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S,
 
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
                                      const DeviceInfo& dev, cudaStream_t st) {
-    const int64_t items = rows * ((k + 7) / 8);
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + 255) / 256, static_cast<int64_t>(dev.sm_count) * 32)));
+    const int64_t spans = (k + 255) / 256, items = rows * spans;
+    const bool many = items >= static_cast<int64_t>(dev.sm_count) * 64 * 4;  // as in the quantisation
+    const int64_t per = many ? 32 : 8;
+    const dim3 grid(static_cast<unsigned>((items + per - 1) / per));
     const auto* q = static_cast<const uint8_t*>(Q);
     const auto* s = static_cast<const uint8_t*>(S);
-    return f32 ? launch_pdl("MXFP4 dequantisation", dequantize_kernel<true>, grid, 0, st, q, s, out, (long long)rows, (long long)k)
-               : launch_pdl("MXFP4 dequantisation", dequantize_kernel<false>, grid, 0, st, q, s, out, (long long)rows, (long long)k);
+    const long long r = rows, kk = k, sp = spans;
+    const char* what = "MXFP4 dequantisation";
+    if (f32)
+        return many ? launch_pdl(what, dequantize_kernel<true, 4>, grid, st, q, s, out, r, kk, sp)
+                    : launch_pdl(what, dequantize_kernel<true, 1>, grid, st, q, s, out, r, kk, sp);
+    return many ? launch_pdl(what, dequantize_kernel<false, 4>, grid, st, q, s, out, r, kk, sp)
+                : launch_pdl(what, dequantize_kernel<false, 1>, grid, st, q, s, out, r, kk, sp);
 }
 
 }  // namespace tpmlp
