@@ -124,7 +124,7 @@ struct MxSpec {
 tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev, cudaStream_t st);
 // X [p][rows][cols / p] (row pitch ldx) -> (Q, S) along the columns and / or (Qt, St) along the rows
 tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows,
-                                   int64_t cols, int p, bool f32, const DeviceInfo& dev, cudaStream_t st);
+                                   int64_t cols, int p, bool f32, cudaStream_t st);
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
                                      const DeviceInfo& dev, cudaStream_t st);
 // Process-wide kernel choice of the MXFP4 GEMM (see tpmlp_set_mxfp4_mode).

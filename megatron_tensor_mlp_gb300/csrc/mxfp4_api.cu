@@ -162,7 +162,7 @@ tpmlp_status tpmlp_mxfp4_quantize(const void* X, void* Q, void* S, void* Qt, voi
     const DeviceInfo* dev;
     TP_TRY(get_device(&dev));
     if (rows == 0) return TPMLP_OK;
-    return launch_mxfp4_quantize(X, ldx, Q, S, Qt, St, rows, cols, p, dt == TPMLP_F32, *dev, static_cast<cudaStream_t>(stream));
+    return launch_mxfp4_quantize(X, ldx, Q, S, Qt, St, rows, cols, p, dt == TPMLP_F32, static_cast<cudaStream_t>(stream));
 }
 
 tpmlp_status tpmlp_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, tpmlp_dtype dt, void* stream) {
@@ -220,7 +220,7 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_fwd(const void* X, const void* Wq, const voi
     TP_TRY(get_device(&dev));
     if (M == 0) return TPMLP_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    TP_TRY(launch_mxfp4_quantize(X, h, w.x.codes, w.x.scales, nullptr, nullptr, M, h, 1, false, *dev, st));
+    TP_TRY(launch_mxfp4_quantize(X, h, w.x.codes, w.x.scales, nullptr, nullptr, M, h, 1, false, st));
     MxSpec g = mx_spec(M, 2 * ffn, h, EPI_SWIGLU);
     g.bias = bw_sh;
     g.h_out = H;
@@ -255,8 +255,8 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const voi
     if (M == 0) return TPMLP_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool gf32 = grad_dt == TPMLP_F32;
-    TP_TRY(launch_mxfp4_quantize(dZ, h, w.dz.codes, w.dz.scales, w.dzt.codes, w.dzt.scales, M, h, 1, false, *dev, st));
-    TP_TRY(launch_mxfp4_quantize(X, h, nullptr, nullptr, w.xt.codes, w.xt.scales, M, h, 1, false, *dev, st));
+    TP_TRY(launch_mxfp4_quantize(dZ, h, w.dz.codes, w.dz.scales, w.dzt.codes, w.dzt.scales, M, h, 1, false, st));
+    TP_TRY(launch_mxfp4_quantize(X, h, nullptr, nullptr, w.xt.codes, w.xt.scales, M, h, 1, false, st));
     // dY = dZ B^T; its epilogue leaves dH = [dg | du] quantised along both axes and Y along the tokens
     MxSpec g = mx_spec(M, ffn, h, EPI_DSWIGLU);
     g.h_in = H;

@@ -1,7 +1,7 @@
 // MXFP4 quantisation along either axis, or both from one read, and its inverse.
 #include <cuda_runtime.h>
 
-#include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "mxfp4.cuh"
@@ -69,8 +69,7 @@ struct QuantArgs {
     uint8_t* s;
     uint8_t* qt;
     uint8_t* st;
-    long long spans;    // row kernel: warp spans a row; both kernel: column tiles
-    long long items;    // row kernel: spans of all rows; both kernel: tiles
+    long long spans;    // row kernel: warp spans of a row; tile kernel: column tiles
 };
 
 // Address and number of values of the piece at logical column c0 (row 0).
@@ -85,56 +84,42 @@ __device__ __forceinline__ const uint8_t* piece_at(const QuantArgs& a, long long
     return a.x + sh * a.ss + c * Piece<F32>::ES;
 }
 
-// Along the columns only: a warp takes U spans of 512 bytes of a row, a 16-byte piece a lane, all
-// loaded before the first is worked on.  A block's maximum takes 2 (bf16) or 3 (fp32) shuffles; its
-// codes go out 4 (2) bytes a lane.  Bound by memory; for one token by the launch.
-template <bool F32, int U>
+// Along the columns of a few rows: a warp takes a span of 512 bytes of a row, a 16-byte piece a lane.  A
+// block's maximum takes 2 (bf16) or 3 (fp32) shuffles; its codes go out 4 (2) bytes a lane.  Bound by the
+// launch (one token of 5120: 1.2 us in a graph).
+template <bool F32>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const QuantArgs a) {
     using P = Piece<F32>;
     constexpr int SPAN = 32 * P::E;
     const int lane = threadIdx.x & 31;
     const long long total = static_cast<long long>(a.cols) * a.p;
     const long long k_tiles = (total + 127) / 128, pitch = (total + 31) / 32 * 16;
-    const long long it0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * U;
-    long long row = it0 / a.spans, span = it0 - row * a.spans;
+    const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const long long row = item / a.spans, c0 = (item - row * a.spans) * SPAN + lane * P::E;
+    int n;
+    const uint8_t* src = piece_at<F32>(a, c0, n);
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    uint4 r[U];
-    long long rows[U], c0[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        rows[i] = row;
-        c0[i] = span * SPAN + lane * P::E;
-        int n;
-        const uint8_t* src = piece_at<F32>(a, c0[i], n);
-        r[i] = P::load(src + row * a.ldx, row < a.rows ? n : 0);
-        if (++span == a.spans) {
-            span = 0;
-            ++row;
-        }
+    if (row >= a.rows) return;
+    const uint4 v = P::load(src + row * a.ldx, n);
+    const uint32_t s = P::scale(v);
+    const uint32_t code = P::codes(v, s);
+    if (c0 / 2 < pitch) {
+        uint8_t* d = a.q + row * pitch + c0 / 2;
+        if constexpr (F32) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(code);
+        else *reinterpret_cast<uint32_t*>(d) = code;
     }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const uint32_t s = P::scale(r[i]);
-        const uint32_t code = P::codes(r[i], s);
-        if (rows[i] >= a.rows) continue;
-        if (c0[i] / 2 < pitch) {
-            uint8_t* d = a.q + rows[i] * pitch + c0[i] / 2;
-            if constexpr (F32) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(code);
-            else *reinterpret_cast<uint32_t*>(d) = code;
-        }
-        // (padding blocks up to a whole scale tile: zero)
-        if (lane % P::LANES == 0 && c0[i] < k_tiles * 128)
-            a.s[mx::scale_offset(rows[i], c0[i] >> 5, k_tiles)] = static_cast<uint8_t>(s);
-    }
+    // (padding blocks up to a whole scale tile: zero)
+    if (lane % P::LANES == 0 && c0 < k_tiles * 128) a.s[mx::scale_offset(row, c0 >> 5, k_tiles)] = static_cast<uint8_t>(s);
 }
 
-// Along the rows, and along the columns too where q is given.  A CTA takes a tile of 128 rows x 256
-// bytes of columns (128 bf16, 64 fp32): asynchronous copies bring it to shared memory, both
-// quantisations work from there, and the other four CTAs of the SM cover its latency.  Along the
-// columns 16 lanes take a row; along the rows a thread takes 32 rows of one word (two bf16 columns or
-// one fp32 column), and the codes are gathered in shared memory so that each column leaves as one run
-// of 64 bytes.  The values are read from memory once.
+// Along the columns, the rows (ACROSS) or both.  A CTA takes a tile of 128 rows x 256 bytes of columns (128
+// bf16, 64 fp32), 16 lanes to a row.  ACROSS: asynchronous copies bring it to shared memory, both
+// quantisations work from there, and the other four CTAs of the SM cover its latency; along the rows a
+// thread takes 32 rows of one word (two bf16 columns or one fp32 column), and the codes are gathered in
+// shared memory so that each column leaves as one run of 64 bytes.  The values are read from memory once.
+// 8192 x 5120 bf16: along the columns 18.3 us (5.8 TB/s, 85 % of a copy's), along the rows 17.3, both 25.0
+// (5.1 TB/s; there issue slots and memory bind about equally).
 template <bool F32>
 struct BothSmem {
     uint32_t tile[128 * 64];
@@ -142,11 +127,11 @@ struct BothSmem {
     uint32_t sc[256 / Piece<F32>::ES];
 };
 
-template <bool F32>
-__global__ void __launch_bounds__(256, 5) quantize_both_kernel(const QuantArgs a) {
+template <bool F32, bool ACROSS>
+__global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(const QuantArgs a) {
     using P = Piece<F32>;
     constexpr int TC = 256 / P::ES;
-    __shared__ __align__(16) BothSmem<F32> sm;
+    __shared__ __align__(16) std::conditional_t<ACROSS, BothSmem<F32>, uint4> sm;
     const int t = threadIdx.x, lane16 = t & 15, r0 = t >> 4;
     const long long total = static_cast<long long>(a.cols) * a.p;
     const unsigned col_tiles = static_cast<unsigned>(a.spans);
@@ -156,7 +141,21 @@ __global__ void __launch_bounds__(256, 5) quantize_both_kernel(const QuantArgs a
     const int rows = static_cast<int>(a.rows - r_tile < 128 ? a.rows - r_tile : 128);  // of this tile
     griddep_wait();
     if (t == 0) griddep_launch_dependents();
-    {
+    [[maybe_unused]] uint4 piece[8];
+    if constexpr (!ACROSS) {
+        int n;
+        const uint8_t* src = piece_at<F32>(a, c0, n) + (r_tile + r0) * a.ldx;
+        if (n == P::E) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                piece[i] = make_uint4(0, 0, 0, 0);
+                if (r0 + i * 16 < rows) piece[i] = *reinterpret_cast<const uint4*>(src + i * 16 * a.ldx);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) piece[i] = P::load(src + i * 16 * a.ldx, r0 + i * 16 < rows ? n : 0);
+        }
+    } else {
         int n;
         const uint8_t* src = piece_at<F32>(a, c0, n) + (r_tile + r0) * a.ldx;
         uint32_t dst = smem_u32(sm.tile + r0 * 64 + lane16 * 4);
@@ -168,8 +167,8 @@ __global__ void __launch_bounds__(256, 5) quantize_both_kernel(const QuantArgs a
             src += 16 * a.ldx;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
     }
-    __syncthreads();
     if (a.q != nullptr) {
         const long long k_tiles = (total + 127) / 128, pitch = (total + 31) / 32 * 16;
         uint8_t* qd = a.q + (r_tile + r0) * pitch + c0 / 2;
@@ -178,7 +177,9 @@ __global__ void __launch_bounds__(256, 5) quantize_both_kernel(const QuantArgs a
         const bool put = c0 / 2 < pitch;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(sm.tile + (r0 + i * 16) * 64 + lane16 * 4);
+            uint4 v;
+            if constexpr (ACROSS) v = *reinterpret_cast<const uint4*>(sm.tile + (r0 + i * 16) * 64 + lane16 * 4);
+            else v = piece[i];
             const uint32_t s = P::scale(v);
             const uint32_t code = P::codes(v, s);
             if (r0 + i * 16 < rows) {
@@ -192,63 +193,65 @@ __global__ void __launch_bounds__(256, 5) quantize_both_kernel(const QuantArgs a
             qd += 16 * pitch;
         }
     }
-    {
-        const int word = t & 63, rb = t >> 6;
-        const uint32_t* col = sm.tile + rb * 32 * 64 + word;
-        uint8_t* sb = reinterpret_cast<uint8_t*>(sm.sc);
-        if constexpr (F32) {
-            float v[32];
+    if constexpr (ACROSS) {
+        {
+            const int word = t & 63, rb = t >> 6;
+            const uint32_t* col = sm.tile + rb * 32 * 64 + word;
+            uint8_t* sb = reinterpret_cast<uint8_t*>(sm.sc);
+            if constexpr (F32) {
+                float v[32];
 #pragma unroll
-            for (int r = 0; r < 32; ++r) v[r] = __uint_as_float(col[r * 64]);
-            uint4 c;
-            sb[word * 4 + rb] = static_cast<uint8_t>(mx::quantize32(v, c));
-            *reinterpret_cast<uint4*>(sm.out + word * 80 + rb * 16) = c;
-        } else {
-            // (the values are read twice, so that a CTA's registers leave room for five)
-            uint32_t m[4];
+                for (int r = 0; r < 32; ++r) v[r] = __uint_as_float(col[r * 64]);
+                uint4 c;
+                sb[word * 4 + rb] = static_cast<uint8_t>(mx::quantize32(v, c));
+                *reinterpret_cast<uint4*>(sm.out + word * 80 + rb * 16) = c;
+            } else {
+                // (the values are read twice, so that a CTA's registers leave room for five)
+                uint32_t m[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) m[r] = mx::amax_bf16x2(col[r * 64], col[(r + 4) * 64]);
+                for (int r = 0; r < 4; ++r) m[r] = mx::amax_bf16x2(col[r * 64], col[(r + 4) * 64]);
 #pragma unroll
-            for (int r = 8; r < 32; ++r) m[r & 3] = mx::amax_bf16x2(m[r & 3], col[r * 64]);
-            const uint32_t mm = mx::amax_bf16x2(mx::amax_bf16x2(m[0], m[1]), mx::amax_bf16x2(m[2], m[3])) & 0x7FFF7FFFu;
-            const uint32_t s0 = mx::scale_of(mm << 16), s1 = mx::scale_of(mm & 0xFFFF0000u);
-            const float inv0 = mx::inverse_scale(s0), inv1 = mx::inverse_scale(s1);
-            uint32_t c0w[4], c1w[4];
+                for (int r = 8; r < 32; ++r) m[r & 3] = mx::amax_bf16x2(m[r & 3], col[r * 64]);
+                const uint32_t mm = mx::amax_bf16x2(mx::amax_bf16x2(m[0], m[1]), mx::amax_bf16x2(m[2], m[3])) & 0x7FFF7FFFu;
+                const uint32_t s0 = mx::scale_of(mm << 16), s1 = mx::scale_of(mm & 0xFFFF0000u);
+                const float inv0 = mx::inverse_scale(s0), inv1 = mx::inverse_scale(s1);
+                uint32_t c0w[4], c1w[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float lo[8], hi[8];
+                for (int g = 0; g < 4; ++g) {
+                    float lo[8], hi[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t w = col[(g * 8 + i) * 64];
-                    lo[i] = __uint_as_float(w << 16);
-                    hi[i] = __uint_as_float(w & 0xFFFF0000u);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t w = col[(g * 8 + i) * 64];
+                        lo[i] = __uint_as_float(w << 16);
+                        hi[i] = __uint_as_float(w & 0xFFFF0000u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        mx::mul2(lo[i], lo[i + 1], inv0);
+                        mx::mul2(hi[i], hi[i + 1], inv1);
+                    }
+                    c0w[g] = s0 == 255u ? 0u : mx::encode8(lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]);
+                    c1w[g] = s1 == 255u ? 0u : mx::encode8(hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    mx::mul2(lo[i], lo[i + 1], inv0);
-                    mx::mul2(hi[i], hi[i + 1], inv1);
-                }
-                c0w[g] = s0 == 255u ? 0u : mx::encode8(lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]);
-                c1w[g] = s1 == 255u ? 0u : mx::encode8(hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]);
+                uint8_t* o = sm.out + word * 160 + rb * 16;
+                *reinterpret_cast<uint4*>(o) = make_uint4(c0w[0], c0w[1], c0w[2], c0w[3]);
+                *reinterpret_cast<uint4*>(o + 80) = make_uint4(c1w[0], c1w[1], c1w[2], c1w[3]);
+                sb[word * 8 + rb] = static_cast<uint8_t>(s0);
+                sb[word * 8 + 4 + rb] = static_cast<uint8_t>(s1);
             }
-            uint8_t* o = sm.out + word * 160 + rb * 16;
-            *reinterpret_cast<uint4*>(o) = make_uint4(c0w[0], c0w[1], c0w[2], c0w[3]);
-            *reinterpret_cast<uint4*>(o + 80) = make_uint4(c1w[0], c1w[1], c1w[2], c1w[3]);
-            sb[word * 8 + rb] = static_cast<uint8_t>(s0);
-            sb[word * 8 + 4 + rb] = static_cast<uint8_t>(s1);
         }
-    }
-    __syncthreads();
-    const long long t_pitch = (static_cast<long long>(a.rows) + 31) / 32 * 16, t_tiles = (static_cast<long long>(a.rows) + 127) / 128;
+        __syncthreads();
+        const long long t_pitch = (static_cast<long long>(a.rows) + 31) / 32 * 16, t_tiles = (static_cast<long long>(a.rows) + 127) / 128;
 #pragma unroll
-    for (int i = 0; i < TC / 64; ++i) {
-        const int c = (t >> 2) + i * 64;
-        const long long col = c_tile + c, at = r_tile / 2 + (t & 3) * 16;
-        if (col < total && at < t_pitch)
-            *reinterpret_cast<uint4*>(a.qt + col * t_pitch + at) = *reinterpret_cast<const uint4*>(sm.out + c * 80 + (t & 3) * 16);
+        for (int i = 0; i < TC / 64; ++i) {
+            const int c = (t >> 2) + i * 64;
+            const long long col = c_tile + c, at = r_tile / 2 + (t & 3) * 16;
+            if (col < total && at < t_pitch)
+                *reinterpret_cast<uint4*>(a.qt + col * t_pitch + at) = *reinterpret_cast<const uint4*>(sm.out + c * 80 + (t & 3) * 16);
+        }
+        if (t < TC && c_tile + t < total)
+            *reinterpret_cast<uint32_t*>(a.st + mx::scale_offset(c_tile + t, rt * 4LL, t_tiles)) = sm.sc[t];
     }
-    if (t < TC && c_tile + t < total)
-        *reinterpret_cast<uint32_t*>(a.st + mx::scale_offset(c_tile + t, rt * 4LL, t_tiles)) = sm.sc[t];
 }
 
 // Values of an operand: a warp takes U spans of 32 words (256 values) of a row, a word of eight codes a
@@ -330,35 +333,30 @@ tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, cudaStr
 }
 
 template <bool F32>
-tpmlp_status quantize(QuantArgs a, int64_t cols, const DeviceInfo& dev, cudaStream_t st) {
-    constexpr int E = Piece<F32>::E;
-    if (a.qt == nullptr) {
-        a.spans = (cols + 32 * E - 1) / (32 * E);
-        if constexpr (F32) a.spans = (cols + 127) / 128;  // one span is one scale tile wide
-        a.items = a.spans * a.rows;
-        // Four spans a warp keep 2 KB of loads in flight; while there are fewer warps than that fills
-        // the GPU with, one each.
-        const bool many = a.items >= static_cast<int64_t>(dev.sm_count) * 64 * 4;
-        const int64_t per = many ? 32 : 8;
-        const dim3 grid(static_cast<unsigned>((a.items + per - 1) / per));
-        return many ? launch_pdl("MXFP4 quantisation", quantize_rows_kernel<F32, 4>, grid, st, a)
-                    : launch_pdl("MXFP4 quantisation", quantize_rows_kernel<F32, 1>, grid, st, a);
+tpmlp_status quantize(QuantArgs a, int64_t cols, cudaStream_t st) {
+    const char* what = "MXFP4 quantisation";
+    // Along the columns, few values: a span a warp spreads them over more warps than tiles of 128 rows do (bf16, 1 x
+    // 5120 1.2 us against 1.6, 128 x 5120 1.6 against 2.2, 2048 x 1024 2.3 both, 8192 x 5120 32 against 18).
+    if (a.qt == nullptr && a.rows * cols < (1 << 21)) {
+        a.spans = F32 ? (cols + 127) / 128 : (cols + 255) / 256;  // of 512 bytes, whole scale tiles
+        return launch_pdl(what, quantize_rows_kernel<F32>, dim3(static_cast<unsigned>((a.spans * a.rows + 7) / 8)), st, a);
     }
     constexpr int TC = 256 / Piece<F32>::ES;
     a.spans = (cols + 127) / 128 * (128 / TC);
-    a.items = a.spans * ((a.rows + 127LL) / 128);
-    return launch_pdl("MXFP4 quantisation", quantize_both_kernel<F32>, dim3(static_cast<unsigned>(a.items)), st, a);
+    const dim3 grid(static_cast<unsigned>(a.spans * ((a.rows + 127LL) / 128)));
+    return a.qt == nullptr ? launch_pdl(what, quantize_tile_kernel<F32, false>, grid, st, a)
+                           : launch_pdl(what, quantize_tile_kernel<F32, true>, grid, st, a);
 }
 
 }  // namespace
 
 tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows,
-                                   int64_t cols, int p, bool f32, const DeviceInfo& dev, cudaStream_t st) {
+                                   int64_t cols, int p, bool f32, cudaStream_t st) {
     const int64_t es = f32 ? 4 : 2;
     const QuantArgs a{static_cast<const uint8_t*>(X), ldx * es, rows * ldx * es, static_cast<int>(rows),
                       static_cast<int>(cols / p), p, static_cast<uint8_t*>(Q), static_cast<uint8_t*>(S),
-                      static_cast<uint8_t*>(Qt), static_cast<uint8_t*>(St), 0, 0};
-    return f32 ? quantize<true>(a, cols, dev, st) : quantize<false>(a, cols, dev, st);
+                      static_cast<uint8_t*>(Qt), static_cast<uint8_t*>(St), 0};
+    return f32 ? quantize<true>(a, cols, st) : quantize<false>(a, cols, st);
 }
 
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
