@@ -122,9 +122,19 @@ struct MxSpec {
     float* colsum;                                  // sums over blocks of 32 rows, may be null
 };
 tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev, cudaStream_t st);
-// X [p][rows][cols / p] (row pitch ldx) -> (Q, S) along the columns and / or (Qt, St) along the rows
+// One product of a group of independent ones (EPI_STORE).
+struct MxProduct {
+    MxOperand a, b;
+    MxSpec g;
+};
+tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const DeviceInfo& dev, cudaStream_t st);
+// X [p][rows][cols / p] (row pitch ldx) -> (Q, S) along the columns and / or (Qt, St) along the rows; sums (bf16 with Qt,
+// or null): fp32 column sums over blocks of 32 rows [ceil(rows/32)][cols]
 tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows,
-                                   int64_t cols, int p, bool f32, cudaStream_t st);
+                                   int64_t cols, int p, bool f32, cudaStream_t st, float* sums = nullptr);
+// out0[c] = sum over r of in0[r][c], and out1 from in1 (an output may be null, not both); fp32 or bf16 outputs
+tpmlp_status launch_mxfp4_sums(const float* in0, void* out0, int64_t cols0, const float* in1, void* out1, int64_t cols1, int64_t rows,
+                               bool f32, cudaStream_t st);
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
                                      const DeviceInfo& dev, cudaStream_t st);
 // Process-wide kernel choice of the MXFP4 GEMM (see tpmlp_set_mxfp4_mode).

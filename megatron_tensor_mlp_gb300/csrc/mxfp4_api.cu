@@ -64,7 +64,7 @@ struct FwdWs {
 };
 struct BwdWs {
     Packed dz, dzt, xt, dh, dht, yt;
-    float* colsum;
+    float *dh_sums, *dz_sums;  // column sums over blocks of 32 tokens
     int64_t bytes;
     BwdWs(void* base, int64_t M, int64_t h, int64_t ffn) {
         Carver c{static_cast<uint8_t*>(base)};
@@ -74,7 +74,8 @@ struct BwdWs {
         dh = c.packed(M, 2 * ffn);
         dht = c.packed(2 * ffn, M);
         yt = c.packed(ffn, M);
-        colsum = reinterpret_cast<float*>(c.take((M + 31) / 32 * 2 * ffn * 4));
+        dh_sums = reinterpret_cast<float*>(c.take((M + 31) / 32 * 2 * ffn * 4));
+        dz_sums = reinterpret_cast<float*>(c.take((M + 31) / 32 * h * 4));
         bytes = c.at;
     }
 };
@@ -90,17 +91,17 @@ MxSpec mx_spec(int64_t M, int64_t N, int64_t K, int epi) {
 }
 
 // D = A B^T (+ bias): a plain product, its columns in shards of shard_cols (0: not sharded).
-tpmlp_status product(const MxOperand& a, const MxOperand& b, const void* bias, void* D, int64_t K, bool f32, int64_t shard_cols,
-                     const DeviceInfo& dev, cudaStream_t st) {
-    MxSpec g = mx_spec(a.rows, b.rows, K, EPI_STORE);
-    g.out = D;
-    g.out_f32 = f32;
-    g.shard_cols = shard_cols;
-    g.out_ld = shard_cols > 0 ? shard_cols : b.rows;
-    g.out_ss = shard_cols > 0 ? a.rows * shard_cols : 0;
-    g.bias = bias;
-    return launch_mxfp4_gemm(a, b, g, dev, st);
+MxProduct product(const MxOperand& a, const MxOperand& b, const void* bias, void* D, int64_t K, bool f32, int64_t shard_cols) {
+    MxProduct c{a, b, mx_spec(a.rows, b.rows, K, EPI_STORE)};
+    c.g.out = D;
+    c.g.out_f32 = f32;
+    c.g.shard_cols = shard_cols;
+    c.g.out_ld = shard_cols > 0 ? shard_cols : b.rows;
+    c.g.out_ss = shard_cols > 0 ? a.rows * shard_cols : 0;
+    c.g.bias = bias;
+    return c;
 }
+tpmlp_status run(const MxProduct& c, const DeviceInfo& dev, cudaStream_t st) { return launch_mxfp4_gemm(c.a, c.b, c.g, dev, st); }
 
 tpmlp_status check_gated(int64_t s, int64_t b, int64_t h, int64_t ffn, int p) {
     TP_TRY(check_mlp_shape(s, b, h, ffn, p, true));
@@ -197,7 +198,7 @@ tpmlp_status tpmlp_mxfp4_matmul(const void* Aq, const void* As, const void* Bq, 
     const DeviceInfo* dev;
     TP_TRY(get_device(&dev));
     if (m == 0) return TPMLP_OK;
-    return product({Aq, As, m}, {Bq, Bs, n}, bias, D, k, out_dt == TPMLP_F32, 0, *dev, static_cast<cudaStream_t>(stream));
+    return run(product({Aq, As, m}, {Bq, Bs, n}, bias, D, k, out_dt == TPMLP_F32, 0), *dev, static_cast<cudaStream_t>(stream));
 }
 
 tpmlp_status tpmlp_mxfp4_swiglu_mlp_fwd(const void* X, const void* Wq, const void* Ws, const void* bw_sh, const void* Bq, const void* Bs,
@@ -229,7 +230,7 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_fwd(const void* X, const void* Wq, const voi
     g.qs = w.y.scales;
     g.q_cols = ffn;
     TP_TRY(launch_mxfp4_gemm(w.x.operand(), {Wq, Ws, 2 * ffn}, g, *dev, st));
-    return product(w.y.blocked(), {Bq, Bs, h}, b2, Z, ffn, z_dt == TPMLP_F32, 0, *dev, st);
+    return run(product(w.y.blocked(), {Bq, Bs, h}, b2, Z, ffn, z_dt == TPMLP_F32, 0), *dev, st);
 }
 
 tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const void* Ws, const void* Bq, const void* Bs, const void* H,
@@ -255,7 +256,8 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const voi
     if (M == 0) return TPMLP_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool gf32 = grad_dt == TPMLP_F32;
-    TP_TRY(launch_mxfp4_quantize(dZ, h, w.dz.codes, w.dz.scales, w.dzt.codes, w.dzt.scales, M, h, 1, false, st));
+    TP_TRY(launch_mxfp4_quantize(dZ, h, w.dz.codes, w.dz.scales, w.dzt.codes, w.dzt.scales, M, h, 1, false, st,
+                                 db2 ? w.dz_sums : nullptr));
     TP_TRY(launch_mxfp4_quantize(X, h, nullptr, nullptr, w.xt.codes, w.xt.scales, M, h, 1, false, st));
     // dY = dZ B^T; its epilogue leaves dH = [dg | du] quantised along both axes and Y along the tokens
     MxSpec g = mx_spec(M, ffn, h, EPI_DSWIGLU);
@@ -268,13 +270,13 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const voi
     g.hts = w.dht.scales;
     g.yt = w.yt.codes;
     g.yts = w.yt.scales;
-    g.colsum = dbw_sh ? w.colsum : nullptr;
+    g.colsum = dbw_sh ? w.dh_sums : nullptr;
     TP_TRY(launch_mxfp4_gemm(w.dz.operand(), {Bq, Bs, ffn}, g, *dev, st));
-    if (dbw_sh) TP_TRY(launch_colsum(w.colsum, true, 1, (M + 31) / 32, 2 * ffn, dbw_sh, gf32, st));
-    if (db2) TP_TRY(launch_colsum(dZ, false, 1, M, h, db2, gf32, st));
-    TP_TRY(product(w.yt.blocked(), w.dzt.operand(), nullptr, dB_sh, M, gf32, 0, *dev, st));
-    TP_TRY(product(w.xt.operand(), w.dht.blocked(), nullptr, dW_sh, M, gf32, p > 1 ? 2 * ffn / p : 0, *dev, st));
-    return product(w.dh.blocked(), {Wq, Ws, h}, nullptr, dX, 2 * ffn, dx_dt == TPMLP_F32, 0, *dev, st);
+    if (dbw_sh || db2) TP_TRY(launch_mxfp4_sums(w.dh_sums, dbw_sh, 2 * ffn, w.dz_sums, db2, h, (M + 31) / 32, gf32, st));
+    const MxProduct dB = product(w.yt.blocked(), w.dzt.operand(), nullptr, dB_sh, M, gf32, 0);
+    const MxProduct dW = product(w.xt.operand(), w.dht.blocked(), nullptr, dW_sh, M, gf32, p > 1 ? 2 * ffn / p : 0);
+    const MxProduct dx = product(w.dh.blocked(), {Wq, Ws, h}, nullptr, dX, 2 * ffn, dx_dt == TPMLP_F32, 0);
+    return launch_mxfp4_gemms({dB, dW, dx}, *dev, st);
 }
 
 tpmlp_status tpmlp_set_mxfp4_mode(int mode) {

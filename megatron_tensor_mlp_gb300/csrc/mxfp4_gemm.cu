@@ -6,7 +6,6 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
-#include <type_traits>
 
 #include "mxfp4_gemm.cuh"
 
@@ -85,11 +84,10 @@ bool set_smem(Kern kern, int device, int bytes, bool (&done)[64]) {
     return true;
 }
 
-template <typename Kern>
-tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const CUtensorMap (&m)[6],
-                    const mx::Args& k) {
+template <typename Kern, typename... A>
+tpmlp_status launch(Kern kern, unsigned grid, int threads, int smem, unsigned cluster, cudaStream_t st, const A&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -102,10 +100,7 @@ tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluste
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e;
-    if constexpr (std::is_invocable_v<Kern, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, mx::Args>)
-        e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], k);
-    else e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], k);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("MXFP4 GEMM launch: %s", cudaGetErrorString(e));
@@ -115,13 +110,13 @@ tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluste
     return TPMLP_OK;
 }
 
-template <int EPI>
+template <int EPI, int N = 1>
 int pair_capacity(const DeviceInfo& dev) {
     static int cap[64];
     static bool done[64], attr_done[64];
     if (dev.device >= 64) return 0;
     if (done[dev.device]) return cap[dev.device];
-    auto kern = mx::mx_pair_kernel<EPI>;
+    auto kern = mx::mx_pair_kernel<EPI, N>;
     int n = 0;
     if (set_smem(kern, dev.device, mx::PairGeom<EPI>::smem, attr_done)) {
         cudaLaunchConfig_t cfg = {};
@@ -157,8 +152,8 @@ bool split_fits(int split, int rows, int kb) {
 }
 
 template <int EPI, int CTAS>
-tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec& g, mx::Args k, int mode, int split, CUtensorMap (&m)[6],
-                           const DeviceInfo& dev, cudaStream_t st) {
+tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec& g, mx::Args k, int mode, int split, const DeviceInfo& dev,
+                           cudaStream_t st) {
     using Geom = mx::SingleGeom<EPI, CTAS>;
     constexpr bool GATED = EPI == EPI_SWIGLU;
     static bool attr_done[64];
@@ -173,11 +168,12 @@ tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec&
         while (split > 1 && !split_fits<EPI, CTAS>(split, rows, k.kb)) split /= 2;
     }
     k.m_blocks = static_cast<int>(m_blocks);
+    CUtensorMap m[4];
     if (!codes_map(&m[0], a, g.K, static_cast<uint32_t>(k.a_box)) || !codes_map(&m[1], b, g.K, GATED ? 64 : 128) ||
         !scales_map(&m[2], a, g.K, 1) || !scales_map(&m[3], b, g.K, GATED ? 2 : 1))
         return TPMLP_ERR_CUDA;
-    return launch(kern, dim3(static_cast<unsigned>(n_blocks * m_blocks * split)), mx::S_THREADS, Geom::smem,
-                  static_cast<unsigned>(split), st, m, k);
+    return launch(kern, static_cast<unsigned>(n_blocks * m_blocks * split), mx::S_THREADS, Geom::smem,
+                  static_cast<unsigned>(split), st, m[0], m[1], m[2], m[3], k);
 }
 
 // Which kernel takes a product, by its expected time in microseconds.  Fitted to one GB300's times of 30
@@ -195,14 +191,17 @@ tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec&
 struct Choice {
     bool pair;
     int split;
+    double us;
 };
+constexpr double kPairStart = 4.0;
+double pair_tile_us(int kb) { return 0.265 * kb + 1.6; }
 template <int EPI>
 Choice choose(const MxSpec& g, int kb, int cap, int sms) {
     const int64_t n1 = EPI == EPI_SWIGLU ? g.N / 128 : (g.N + 127) / 128, tiles1 = n1 * ((g.M + 127) / 128);
     const int64_t tiles2 = ((g.M + 255) / 256) * ((g.N + 255) / 256);
     const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
     const int64_t waves1 = (tiles1 + 2 * sms - 1) / (2 * sms);
-    Choice c{false, 1};
+    Choice c{false, 1, 0.0};
     double best = 2.8 + (tiles1 <= sms ? 0.35 * kb : waves1 == 1 ? 0.40 * kb : waves1 * (0.40 * kb + 3.0));
     for (int s = 2; s <= 8; s *= 2) {
         // (40 tiles split four ways are 160 CTAs on 152 SMs: a few SMs with two cost little)
@@ -216,32 +215,39 @@ Choice choose(const MxSpec& g, int kb, int cap, int sms) {
     }
     if (cap > 0 && g.M > mx::BM) {
         const int64_t waves2 = (tiles2 + cap - 1) / cap;
-        if (4.0 + waves2 * (0.265 * kb + 1.6) < best) c.pair = true;
+        const double t = kPairStart + waves2 * pair_tile_us(kb);
+        if (t < best) {
+            best = t;
+            c.pair = true;
+        }
     }
+    c.us = best;
     return c;
 }
+
+// The pair kernel's view of a product.
+bool pair_problem(mx::Problem* pr, const MxOperand& a, const MxOperand& b, const MxSpec& g, const mx::Args& k) {
+    pr->p = k;
+    pr->p.m_blocks = static_cast<int>((g.M + 255) / 256);
+    pr->p.n_blocks = static_cast<int>((g.N + 255) / 256);
+    return codes_map(&pr->a, a, g.K, mx::BM) && codes_map(&pr->b, b, g.K, mx::BM) && scales_map(&pr->sa, a, g.K, 1) &&
+           scales_map(&pr->sb, b, g.K, 2) && codes_map(&pr->b2, b, g.K, mx::BM / 2) &&
+           (g.epi != EPI_DSWIGLU || h_map(&pr->h, g.h_in, g.h_ld, g.M));
+}
+int pair_tiles(const mx::Problem& pr) { return pr.p.m_blocks * pr.p.n_blocks; }
 
 template <int EPI>
 tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec& g, mx::Args k, const DeviceInfo& dev,
                             cudaStream_t st) {
     const int mode = g_mode.load(std::memory_order_relaxed);
     const int cap = pair_capacity<EPI>(dev);
-    const int64_t m_pairs = (g.M + 255) / 256, n_pairs = (g.N + 255) / 256;
-    const Choice choice = mode == 0 ? choose<EPI>(g, k.kb, cap, dev.sm_count) : Choice{mode == 2 && cap > 0, 1};
-    const bool pair = choice.pair;
-    CUtensorMap m[6];
-    if (pair) {
-        if constexpr (EPI == EPI_DSWIGLU) {
-            if (!h_map(&m[5], g.h_in, g.h_ld, g.M)) return TPMLP_ERR_CUDA;
-        }
-        k.m_blocks = static_cast<int>(m_pairs);
-        k.n_blocks = static_cast<int>(n_pairs);
-        k.num_tiles = k.m_blocks * k.n_blocks;
-        if (!codes_map(&m[0], a, g.K, mx::BM) || !codes_map(&m[1], b, g.K, mx::BM) || !scales_map(&m[2], a, g.K, 1) ||
-            !scales_map(&m[3], b, g.K, 2) || !codes_map(&m[4], b, g.K, mx::BM / 2))
-            return TPMLP_ERR_CUDA;
-        const int clusters = std::min(k.num_tiles, cap);
-        return launch(mx::mx_pair_kernel<EPI>, dim3(2 * clusters), mx::P_THREADS, mx::PairGeom<EPI>::smem, 2, st, m, k);
+    const Choice choice = mode == 0 ? choose<EPI>(g, k.kb, cap, dev.sm_count) : Choice{mode == 2 && cap > 0, 1, 0.0};
+    if (choice.pair) {
+        mx::Problems<1> all{};
+        if (!pair_problem(&all.of[0], a, b, g, k)) return TPMLP_ERR_CUDA;
+        all.n_long = 1;
+        all.long_tiles = pair_tiles(all.of[0]);
+        return launch(mx::mx_pair_kernel<EPI, 1>, 2 * std::min(all.long_tiles, cap), mx::P_THREADS, mx::PairGeom<EPI>::smem, 2, st, all);
     }
     if constexpr (EPI != EPI_DSWIGLU) {
         // Three CTAs an SM (three ring stages each, at most 32 rows of A) where two would need another wave for the
@@ -249,17 +255,12 @@ tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec
         // rings are better: 1 x 32768 x 4096, 256 tiles: 14.4 against 15.3.
         const int64_t tiles = EPI == EPI_SWIGLU ? g.N / 128 : (g.N + 127) / 128;
         if (mode == 0 && g.M <= 32 && tiles > 2 * dev.sm_count)
-            return launch_single<EPI, 3>(a, b, g, k, mode, 1, m, dev, st);
+            return launch_single<EPI, 3>(a, b, g, k, mode, 1, dev, st);
     }
-    return launch_single<EPI, 2>(a, b, g, k, mode, choice.split, m, dev, st);
+    return launch_single<EPI, 2>(a, b, g, k, mode, choice.split, dev, st);
 }
 
-}  // namespace
-
-void set_mxfp4_mode(int mode) { g_mode.store(mode, std::memory_order_relaxed); }
-int get_mxfp4_mode() { return g_mode.load(std::memory_order_relaxed); }
-
-tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev, cudaStream_t st) {
+mx::Args make_args(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev) {
     mx::Args k{};
     k.M = static_cast<int>(g.M);
     k.N = static_cast<int>(g.N);
@@ -297,6 +298,16 @@ tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxS
         const int64_t es = g.out_f32 ? 4 : 2;
         k.st32 = rows32(g.out, g.out_ld * es, g.out_ss * es) && rows32(g.h_in, g.h_ld * 2, 0) && rows32(g.h_out, g.h_ld * 2, 0);
     }
+    return k;
+}
+
+}  // namespace
+
+void set_mxfp4_mode(int mode) { g_mode.store(mode, std::memory_order_relaxed); }
+int get_mxfp4_mode() { return g_mode.load(std::memory_order_relaxed); }
+
+tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev, cudaStream_t st) {
+    const mx::Args k = make_args(a, b, g, dev);
     switch (g.epi) {
         case EPI_STORE: return launch_variant<EPI_STORE>(a, b, g, k, dev, st);
         case EPI_SWIGLU: return launch_variant<EPI_SWIGLU>(a, b, g, k, dev, st);
@@ -304,6 +315,43 @@ tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxS
     }
     set_error("internal: no MXFP4 GEMM for epilogue %d", g.epi);
     return TPMLP_ERR_CUDA;
+}
+
+// Independent plain products, in one launch of CTA pairs where that is expected to be faster than one after the
+// other: it saves their launches and their last waves.  (s=499 b=4 h1024 ffn4096, the backward's three products: 35 us
+// one by one; 4096 tokens, h5120, ffn20480: dX alone ends in a wave of 16 of 76 pairs that lasts 42 us.)
+tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const DeviceInfo& dev, cudaStream_t st) {
+    const int cap = pair_capacity<EPI_STORE, 3>(dev);
+    mx::Args k[3];
+    int order[3] = {0, 1, 2};
+    double apart = 0.0, together = 0.0;
+    for (int i = 0; i < 3; ++i) {
+        k[i] = make_args(c[i].a, c[i].b, c[i].g, dev);
+        apart += choose<EPI_STORE>(c[i].g, k[i].kb, cap, dev.sm_count).us;
+        together += static_cast<double>((c[i].g.M + 255) / 256 * ((c[i].g.N + 255) / 256)) * pair_tile_us(k[i].kb);
+    }
+    const int mode = g_mode.load(std::memory_order_relaxed);
+    if (cap <= 0 || (mode != 0 && mode != 2) || (mode == 0 && kPairStart + together / cap + pair_tile_us(1) >= apart)) {
+        for (const MxProduct& x : c) {
+            const tpmlp_status r = launch_mxfp4_gemm(x.a, x.b, x.g, dev, st);
+            if (r != TPMLP_OK) return r;
+        }
+        return TPMLP_OK;
+    }
+    std::sort(order, order + 3, [&](int x, int y) { return k[x].kb > k[y].kb; });
+    mx::Problems<3> all{};
+    for (int i = 0; i < 3; ++i) {
+        const MxProduct& x = c[order[i]];
+        if (!pair_problem(&all.of[i], x.a, x.b, x.g, k[order[i]])) return TPMLP_ERR_CUDA;
+        const bool longest = k[order[i]].kb == k[order[0]].kb;
+        int& tiles = longest ? all.long_tiles : all.short_tiles;
+        all.first[i] = tiles;
+        tiles += pair_tiles(all.of[i]);
+        if (longest) all.n_long = i + 1;
+        else if (all.skip == 0) all.skip = static_cast<int>(pair_tile_us(k[order[0]].kb) / pair_tile_us(k[order[i]].kb) + 0.5);
+    }
+    const int clusters = std::min(all.long_tiles + all.short_tiles, cap);
+    return launch(mx::mx_pair_kernel<EPI_STORE, 3>, 2 * clusters, mx::P_THREADS, mx::PairGeom<EPI_STORE>::smem, 2, st, all);
 }
 
 }  // namespace tpmlp

@@ -43,7 +43,7 @@ struct Args {
     int M, N;
     int kb;          // ring stages of K: ceil(K / 256)
     int last_steps;  // MMAs (64 k each) of the last one: 1..4
-    int m_blocks, n_blocks, num_tiles, group_m;  // pair kernel
+    int m_blocks, n_blocks, group_m;  // tiles
     int a_box;       // single kernel: rows of A copied per stage (16, 32, 64 or 128)
     int stages;      // single kernel: ring stages
     int a_blocked, b_blocked;  // operand's codes are [k / 32][rows][16 bytes] (written by an epilogue), not [rows][k / 2]
@@ -366,11 +366,52 @@ __device__ __forceinline__ void decode_tile(const Args& p, int t, int& mb, int& 
     nb = r / gm;
 }
 
-template <int EPI>
-__global__ void __launch_bounds__(P_THREADS, 1)
-    mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                   const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmH, const Args p) {
+// One product: its operands' maps (b2: B in boxes of 64 rows; h: EPI_DSWIGLU's pre-activations) and the rest.
+struct Problem {
+    CUtensorMap a, b, sa, sb, b2, h;
+    Args p;
+};
+// Up to N independent products in one launch, the longest K loops first.  Every pair takes its share of the long
+// tiles; where these do not come out even, the pairs that had one less start on the short ones `skip` tiles
+// earlier, which is what a long tile costs.  So no product ends in a wave of its own with most of the GPU idle.
+template <int N>
+struct Problems {
+    Problem of[N];
+    int first[N];     // first tile of each product in its class
+    int n_long;       // products of the long class
+    int long_tiles, short_tiles, skip;
+
+    // Tile i of pair `c` of `n`: the product, its tile in t; -1 past the last.
+    __device__ __forceinline__ int tile(int c, int n, int i, int& t) const {
+        if constexpr (N == 1) {
+            t = c + i * n;
+            return t < long_tiles ? 0 : -1;
+        } else {
+            const int r = long_tiles % n, mine = long_tiles / n + (c < r ? 1 : 0);
+            int lo = 0, hi = n_long;
+            if (i < mine) {
+                t = c + i * n;
+            } else {
+                const int round = i - mine + (c < r ? skip : 0), early = r > 0 ? skip : 0;
+                t = round < early ? round * (n - r) + c - r : early * (n - r) + (round - early) * n + c;
+                if (t >= short_tiles) return -1;
+                lo = n_long;
+                hi = N;
+            }
+            int g = lo;
+#pragma unroll
+            for (int k = 1; k < N; ++k)
+                if (k > lo && k < hi && t >= first[k]) g = k;
+            t -= first[g];
+            return g;
+        }
+    }
+};
+
+template <int EPI, int N>
+__global__ void __launch_bounds__(P_THREADS, 1) mx_pair_kernel(const __grid_constant__ Problems<N> all) {
+    uint32_t* const status = all.of[0].p.status;
+    const unsigned long long timeout_ns = all.of[0].p.timeout_ns;
     constexpr int LAST = PairGeom<EPI>::last;
     constexpr int STAGES = PairGeom<EPI>::stages;
     extern __shared__ uint8_t smem_raw[];
@@ -416,10 +457,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         fence_proxy_async_smem();
     }
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
-        tma_prefetch_desc(&tmSA);
-        tma_prefetch_desc(&tmSB);
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+            tma_prefetch_desc(&all.of[g].a);
+            tma_prefetch_desc(&all.of[g].b);
+            tma_prefetch_desc(&all.of[g].sa);
+            tma_prefetch_desc(&all.of[g].sb);
+        }
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -439,28 +483,32 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         uint32_t phase = 0, armed = 0, last_parity = 0;
         bool ok = true;
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-        for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters) {
-            int mb, nb;
+        for (int i = 0; ok; ++i) {
+            int t, mb, nb;
+            const int g = all.tile(cluster_id, n_clusters, i, t);
+            if (g < 0) break;
+            const Problem& pr = all.of[g];
+            const Args& p = pr.p;
             decode_tile(p, t, mb, nb);
             const int row_tile = mb * 2 + static_cast<int>(prank);
             const int col0 = nb * P_BN + static_cast<int>(prank) * BM;
             for (int it = 0; it < p.kb; ++it) {
-                ok = mbar_wait_bounded_warp(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereProducer);
+                ok = mbar_wait_bounded_warp(empty + stage, phase ^ 1u, status, timeout_ns, kWhereProducer);
                 if (!ok) break;
                 if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(full + stage, 2 * P_STAGE);
                     const uint32_t bar = full0 + stage * 8;
-                    load_codes<true>(sA + stage * OP_BYTES, &tmA, bar, it, row_tile * BM, p.a_blocked);
+                    load_codes<true>(sA + stage * OP_BYTES, &pr.a, bar, it, row_tile * BM, p.a_blocked);
                     if (it < p.kb - LAST) {
-                        load_codes<true>(sB + stage * OP_BYTES, &tmB, bar, it, col0, p.b_blocked);
+                        load_codes<true>(sB + stage * OP_BYTES, &pr.b, bar, it, col0, p.b_blocked);
                     } else {
                         // each half of the tile's columns as a product of its own: 64 of its columns in each CTA
                         const int c = nb * P_BN + static_cast<int>(prank) * 64;
-                        load_codes<true>(sB + stage * OP_BYTES, &tmB2, bar, it, c, p.b_blocked);
-                        load_codes<true>(sB + stage * OP_BYTES + OP_BYTES / 2, &tmB2, bar, it, c + 128, p.b_blocked);
+                        load_codes<true>(sB + stage * OP_BYTES, &pr.b2, bar, it, c, p.b_blocked);
+                        load_codes<true>(sB + stage * OP_BYTES + OP_BYTES / 2, &pr.b2, bar, it, c + 128, p.b_blocked);
                     }
-                    tma_load_3d_pair(sSA + stage * P_SFA_BYTES, &tmSA, bar, 0, it * 2, row_tile);
-                    tma_load_3d_pair(sSB + stage * P_SFB_BYTES, &tmSB, bar, 0, it * 2, nb * 2);
+                    tma_load_3d_pair(sSA + stage * P_SFA_BYTES, &pr.sa, bar, 0, it * 2, row_tile);
+                    tma_load_3d_pair(sSB + stage * P_SFB_BYTES, &pr.sb, bar, 0, it * 2, nb * 2);
                 }
                 armed |= 1u << stage;
                 last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
@@ -474,7 +522,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             if (ok) {
                 // every stage's last release has arrived before this CTA can exit
                 for (int i = 0; i < STAGES; ++i) {
-                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, p.status, p.timeout_ns, kWhereDrain)) break;
+                    if (!mbar_wait_bounded(empty + stage, phase ^ 1u, status, timeout_ns, kWhereDrain)) break;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -483,7 +531,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             } else if (leader) {
                 for (int s = 0; s < STAGES; ++s)
                     if (armed & (1u << s))
-                        mbar_wait_bounded(full + s, (last_parity >> s) & 1u, p.status, p.timeout_ns, kWhereDrain, false);
+                        mbar_wait_bounded(full + s, (last_parity >> s) & 1u, status, timeout_ns, kWhereDrain, false);
             } else {
                 spin_ns(200000);  // this CTA's last copies, counted on the leader's barriers, land
             }
@@ -491,26 +539,30 @@ __global__ void __launch_bounds__(P_THREADS, 1)
     } else if (warp == 1) {
         if (leader) {
             // ------------------------------------------------------------ MMA issuer (leader)
-            const uint64_t a0 = p.a_blocked ? sdesc_blocked(smem_u32(sA), BM) : sdesc_sw128(smem_u32(sA), 16, 1024);
-            const uint64_t b0 = p.b_blocked ? sdesc_blocked(smem_u32(sB), BM) : sdesc_sw128(smem_u32(sB), 16, 1024);
-            // descriptor step of 64 k: 32 bytes of a swizzled row, or two blocks of all rows
-            const uint64_t a_step = p.a_blocked ? 2 * BM : 2, b_step = p.b_blocked ? 2 * BM : 2;
-            const uint64_t b0h = p.b_blocked ? sdesc_blocked(smem_u32(sB), 64) : b0, bh_step = p.b_blocked ? 128 : 2;
             const uint64_t sa0 = sdesc_scales(smem_u32(sSA)), sb0 = sdesc_scales(smem_u32(sSB));
             int stage = 0;
             uint32_t phase = 0;
             int lt = 0;
             bool ok = true;
-            for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters, ++lt) {
+            for (; ok; ++lt) {
+                int t;
+                const int g = all.tile(cluster_id, n_clusters, lt, t);
+                if (g < 0) break;
+                const Args& p = all.of[g].p;
+                const uint64_t a0 = p.a_blocked ? sdesc_blocked(smem_u32(sA), BM) : sdesc_sw128(smem_u32(sA), 16, 1024);
+                const uint64_t b0 = p.b_blocked ? sdesc_blocked(smem_u32(sB), BM) : sdesc_sw128(smem_u32(sB), 16, 1024);
+                // descriptor step of 64 k: 32 bytes of a swizzled row, or two blocks of all rows
+                const uint64_t a_step = p.a_blocked ? 2 * BM : 2, b_step = p.b_blocked ? 2 * BM : 2;
+                const uint64_t b0h = p.b_blocked ? sdesc_blocked(smem_u32(sB), 64) : b0, bh_step = p.b_blocked ? 128 : 2;
                 const int acc = lt & 1;
-                ok = mbar_wait_bounded_warp(tempty + acc, ((lt >> 1) & 1) ^ 1u, p.status, p.timeout_ns, kWhereMma);
-                if (ok && lt > 0) ok = mbar_wait_bounded_warp(shared_free, (lt - 1) & 1, p.status, p.timeout_ns, kWhereMma);
+                ok = mbar_wait_bounded_warp(tempty + acc, ((lt >> 1) & 1) ^ 1u, status, timeout_ns, kWhereMma);
+                if (ok && lt > 0) ok = mbar_wait_bounded_warp(shared_free, (lt - 1) & 1, status, timeout_ns, kWhereMma);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * P_ACC1;
                 const int it_last = max(p.kb - LAST, 0);
                 for (int it = 0; it < it_last; ++it) {
-                    ok = mbar_wait_bounded_warp(full + stage, phase, p.status, p.timeout_ns, kWhereMma);
+                    ok = mbar_wait_bounded_warp(full + stage, phase, status, timeout_ns, kWhereMma);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -547,7 +599,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     uint32_t ph = phase;
                     for (int it = it_last; it < p.kb; ++it) {
                         if (pass == 0) {
-                            ok = mbar_wait_bounded_warp(full + st, ph, p.status, p.timeout_ns, kWhereMma);
+                            ok = mbar_wait_bounded_warp(full + st, ph, status, timeout_ns, kWhereMma);
                             if (!ok) break;
                             tc_fence_after();
                         }
@@ -589,11 +641,11 @@ __global__ void __launch_bounds__(P_THREADS, 1)
             if (elect_one()) umma_commit_pair_mc(drain, 0x3);
             __syncwarp();
             // the last releases of the epilogue warps, some from the peer SM, land before this CTA can exit
-            if (ok && lt > 0) ok = mbar_wait_bounded_warp(shared_free, (lt - 1) & 1, p.status, p.timeout_ns, kWhereDrain);
+            if (ok && lt > 0) ok = mbar_wait_bounded_warp(shared_free, (lt - 1) & 1, status, timeout_ns, kWhereDrain);
             for (int i = 0; ok && i < 2; ++i, ++lt)
-                ok = mbar_wait_bounded_warp(tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, p.status, p.timeout_ns, kWhereDrain);
+                ok = mbar_wait_bounded_warp(tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, status, timeout_ns, kWhereDrain);
         }
-        if (lane == 0) mbar_wait_bounded(drain, 0, p.status, p.timeout_ns, kWhereDrain, /*watch_status=*/false);
+        if (lane == 0) mbar_wait_bounded(drain, 0, status, timeout_ns, kWhereDrain, /*watch_status=*/false);
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3;
@@ -608,36 +660,42 @@ __global__ void __launch_bounds__(P_THREADS, 1)
         // into registers, a row a lane, were most of the epilogue's time.)
         [[maybe_unused]] uint32_t h_phase = 0;
         [[maybe_unused]] bool h_pending = false;
-        auto fetch_h = [&](int t, int lt, int i) {
-            int mb, nb;
-            decode_tile(p, t, mb, nb);
+        auto fetch_h = [&](int lt, int i) {
+            int t, mb, nb;
+            const int g = all.tile(cluster_id, n_clusters, lt, t);
+            if (g < 0) return;
+            const Problem& pr = all.of[g];
+            decode_tile(pr.p, t, mb, nb);
             const int f = nb * P_BN + col0 + ((lt & 1) == 0 ? CH - 1 - i : i) * 32;
             const int row = mb * (2 * BM) + static_cast<int>(prank) * BM + q * 32;
             uint64_t* bar = h_full + (warp - 4);
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar, H_BUF);
                 const int x = (f >> 7) * 256 + (f & 127);
-                tma_load_3d(hbuf, &tmH, bar, x, row, 0);
-                tma_load_3d(hbuf + H_BUF / 2, &tmH, bar, x + 128, row, 0);
+                tma_load_3d(hbuf, &pr.h, bar, x, row, 0);
+                tma_load_3d(hbuf + H_BUF / 2, &pr.h, bar, x + 128, row, 0);
             }
             __syncwarp();
             h_pending = true;
         };
         if constexpr (EPI == EPI_DSWIGLU) {
-            if (cluster_id < p.num_tiles) fetch_h(cluster_id, 0, 0);
+            fetch_h(0, 0);
         }
         int lt = 0;
         bool ok = true;
-        for (int t = cluster_id; t < p.num_tiles && ok; t += n_clusters, ++lt) {
+        for (; ok; ++lt) {
             const int acc = lt & 1;
-            int mb, nb;
+            int t, mb, nb;
+            const int g = all.tile(cluster_id, n_clusters, lt, t);
+            if (g < 0) break;
+            const Args& p = all.of[g].p;
             decode_tile(p, t, mb, nb);  // before the wait: the next tile's MMAs wait for the first columns read here
             const int row0 = mb * (2 * BM) + static_cast<int>(prank) * BM + q * 32;
             // The half with the shared columns: its 128 accumulator columns are complete first.
             const bool first = half == 1 - acc;
             int okw = 0;
             if (lane == 0)
-                okw = mbar_wait_bounded((first ? hfull : tfull) + acc, (lt >> 1) & 1, p.status, p.timeout_ns, kWhereEpilogue);
+                okw = mbar_wait_bounded((first ? hfull : tfull) + acc, (lt >> 1) & 1, status, timeout_ns, kWhereEpilogue);
             okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
             if (!okw) break;
             tc_fence_after();
@@ -663,7 +721,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(shared0);
                     if constexpr (EPI == EPI_SWIGLU) {
-                        ok = mbar_wait_bounded_warp(tfull + acc, (lt >> 1) & 1, p.status, p.timeout_ns, kWhereEpilogue);
+                        ok = mbar_wait_bounded_warp(tfull + acc, (lt >> 1) & 1, status, timeout_ns, kWhereEpilogue);
                         if (!ok) break;
                         tc_fence_after();
                         if (acc == 0) load_acc32(t_row + col, v);
@@ -672,15 +730,18 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 }
                 if constexpr (EPI == EPI_SWIGLU) ys |= swiglu_chunk(p, v, u, row0 + lane, nb * 128 + col) << (col & 32 ? 8 : 0);
                 else if constexpr (EPI == EPI_DSWIGLU) {
-                    ok = mbar_wait_bounded_warp(h_full + (warp - 4), h_phase, p.status, p.timeout_ns, kWhereEpilogue);
+                    ok = mbar_wait_bounded_warp(h_full + (warp - 4), h_phase, status, timeout_ns, kWhereEpilogue);
                     if (!ok) break;
                     h_phase ^= 1u;
                     h_pending = false;
                     uint32_t h[32];
                     read_h(hbuf, lane, h);
+                    // Every lane's reads are done before the next copy may write here: a warp barrier alone does not
+                    // order them before the async proxy's writes (now and then a row came out of the next piece).
+                    fence_proxy_async_smem();
                     __syncwarp();
-                    if (i + 1 < CH) fetch_h(t, lt, i + 1);
-                    else if (t + n_clusters < p.num_tiles) fetch_h(t + n_clusters, lt + 1, 0);
+                    if (i + 1 < CH) fetch_h(lt, i + 1);
+                    else fetch_h(lt + 1, 0);
                     dswiglu_chunk(p, v, h, row0 + lane, nb * P_BN + col, row0 >> 5, buf, sc, lane);
                 } else store_chunk(p, v, row0 + lane, nb * P_BN + col);
             }
@@ -696,13 +757,13 @@ __global__ void __launch_bounds__(P_THREADS, 1)
                 // The half's four warps have written this tile's scales.  The next tile's go to the other buffer,
                 // and nobody writes this one again before all have passed the next tile's wait.
                 if (lane == 0) mbar_arrive(sc_full + half);
-                ok = ok && mbar_wait_bounded_warp(sc_full + half, lt & 1, p.status, p.timeout_ns, kWhereEpilogue);
+                ok = ok && mbar_wait_bounded_warp(sc_full + half, lt & 1, status, timeout_ns, kWhereEpilogue);
                 if (ok) put_scales(p, sc, row0 - q * 32, nb * P_BN + col0, q * 32 + lane, 15u);
             }
         }
         if constexpr (EPI == EPI_DSWIGLU) {
             // (after a wait that gave up) no copy is in flight when this CTA exits
-            if (h_pending) mbar_wait_bounded_warp(h_full + (warp - 4), h_phase, p.status, p.timeout_ns, kWhereDrain, false);
+            if (h_pending) mbar_wait_bounded_warp(h_full + (warp - 4), h_phase, status, timeout_ns, kWhereDrain, false);
         }
     }
 
@@ -898,6 +959,7 @@ __global__ void __launch_bounds__(S_THREADS, CTAS)
     if (lane == 0) mbar_wait_bounded(tfull, 0, p.status, p.timeout_ns, kWhereEpilogue, /*watch_status=*/false);
     __syncwarp();
     tc_fence_after();
+    fence_proxy_async_all();  // the ring becomes this kernel's own memory: after the copies' writes and the MMAs' reads
     constexpr int CH = GATED ? 2 : 4;        // 32-column chunks (gated: of features)
     constexpr int PARTS = GATED ? 2 : 1;     // accumulator chunks of one of them
     const int owners = min(static_cast<int>(split), CH);

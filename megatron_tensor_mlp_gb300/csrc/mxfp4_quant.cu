@@ -69,6 +69,7 @@ struct QuantArgs {
     uint8_t* s;
     uint8_t* qt;
     uint8_t* st;
+    float* sums;        // sums over blocks of 32 rows [ceil(rows/32)][p * cols]
     long long spans;    // row kernel: warp spans of a row; tile kernel: column tiles
 };
 
@@ -127,7 +128,8 @@ struct BothSmem {
     uint32_t sc[256 / Piece<F32>::ES];
 };
 
-template <bool F32, bool ACROSS>
+// SUMS (bf16 ACROSS): also a.sums.
+template <bool F32, bool ACROSS, bool SUMS = false>
 __global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(const QuantArgs a) {
     using P = Piece<F32>;
     constexpr int TC = 256 / P::ES;
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(cons
                 const uint32_t s0 = mx::scale_of(mm << 16), s1 = mx::scale_of(mm & 0xFFFF0000u);
                 const float inv0 = mx::inverse_scale(s0), inv1 = mx::inverse_scale(s1);
                 uint32_t c0w[4], c1w[4];
+                [[maybe_unused]] float x0 = 0.0f, x1 = 0.0f;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     float lo[8], hi[8];
@@ -224,6 +227,10 @@ __global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(cons
                         const uint32_t w = col[(g * 8 + i) * 64];
                         lo[i] = __uint_as_float(w << 16);
                         hi[i] = __uint_as_float(w & 0xFFFF0000u);
+                        if constexpr (SUMS) {
+                            x0 += lo[i];
+                            x1 += hi[i];
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
@@ -238,6 +245,11 @@ __global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(cons
                 *reinterpret_cast<uint4*>(o + 80) = make_uint4(c1w[0], c1w[1], c1w[2], c1w[3]);
                 sb[word * 8 + rb] = static_cast<uint8_t>(s0);
                 sb[word * 8 + 4 + rb] = static_cast<uint8_t>(s1);
+                if (SUMS && rb * 32 < rows) {
+                    float* d = a.sums + (rt * 4LL + rb) * total + c_tile + word * 2;
+                    if (c_tile + word * 2 < total) d[0] = x0;
+                    if (c_tile + word * 2 + 1 < total) d[1] = x1;
+                }
             }
         }
         __syncthreads();
@@ -251,6 +263,34 @@ __global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(cons
         }
         if (t < TC && c_tile + t < total)
             *reinterpret_cast<uint32_t*>(a.st + mx::scale_offset(c_tile + t, rt * 4LL, t_tiles)) = sm.sc[t];
+    }
+}
+
+// Column sums of up to two fp32 arrays [rows][cols] of partial sums, in a fixed order, rounded to the
+// output's type: a CTA takes 32 columns, 32 warps every 32nd row each.
+struct SumsArgs {
+    const float* in[2];
+    void* out[2];
+    int cols[2];
+    int rows, blocks0;  // CTAs of the first array
+    int f32;
+};
+__global__ void __launch_bounds__(1024) finish_sums_kernel(const SumsArgs a) {
+    __shared__ float part[32][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int k = static_cast<int>(blockIdx.x) >= a.blocks0;
+    const int c = (blockIdx.x - (k ? a.blocks0 : 0)) * 32 + x;
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    float v = 0.0f;
+    if (c < a.cols[k])
+        for (int r = y; r < a.rows; r += 32) v += a.in[k][static_cast<long long>(r) * a.cols[k] + c];
+    part[y][x] = v;
+    __syncthreads();
+    if (y == 0 && c < a.cols[k]) {
+        for (int i = 1; i < 32; ++i) v += part[i][x];
+        if (a.f32) static_cast<float*>(a.out[k])[c] = v;
+        else static_cast<__nv_bfloat16*>(a.out[k])[c] = __float2bfloat16_rn(v);
     }
 }
 
@@ -311,11 +351,11 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restri
     }
 }
 
-template <typename... P, typename... A>
+template <int THREADS = 256, typename... P, typename... A>
 tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -344,6 +384,9 @@ tpmlp_status quantize(QuantArgs a, int64_t cols, cudaStream_t st) {
     constexpr int TC = 256 / Piece<F32>::ES;
     a.spans = (cols + 127) / 128 * (128 / TC);
     const dim3 grid(static_cast<unsigned>(a.spans * ((a.rows + 127LL) / 128)));
+    if constexpr (!F32) {
+        if (a.sums != nullptr) return launch_pdl(what, quantize_tile_kernel<false, true, true>, grid, st, a);
+    }
     return a.qt == nullptr ? launch_pdl(what, quantize_tile_kernel<F32, false>, grid, st, a)
                            : launch_pdl(what, quantize_tile_kernel<F32, true>, grid, st, a);
 }
@@ -351,12 +394,33 @@ tpmlp_status quantize(QuantArgs a, int64_t cols, cudaStream_t st) {
 }  // namespace
 
 tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows,
-                                   int64_t cols, int p, bool f32, cudaStream_t st) {
+                                   int64_t cols, int p, bool f32, cudaStream_t st, float* sums) {
     const int64_t es = f32 ? 4 : 2;
     const QuantArgs a{static_cast<const uint8_t*>(X), ldx * es, rows * ldx * es, static_cast<int>(rows),
                       static_cast<int>(cols / p), p, static_cast<uint8_t*>(Q), static_cast<uint8_t*>(S),
-                      static_cast<uint8_t*>(Qt), static_cast<uint8_t*>(St), 0};
+                      static_cast<uint8_t*>(Qt), static_cast<uint8_t*>(St), sums, 0};
     return f32 ? quantize<true>(a, cols, st) : quantize<false>(a, cols, st);
+}
+
+tpmlp_status launch_mxfp4_sums(const float* in0, void* out0, int64_t cols0, const float* in1, void* out1, int64_t cols1, int64_t rows,
+                               bool f32, cudaStream_t st) {
+    SumsArgs a{};
+    int n = 0;
+    const int64_t blocks[2] = {out0 ? (cols0 + 31) / 32 : 0, out1 ? (cols1 + 31) / 32 : 0};
+    if (out0) {
+        a.in[n] = in0;
+        a.out[n] = out0;
+        a.cols[n++] = static_cast<int>(cols0);
+    }
+    if (out1) {
+        a.in[n] = in1;
+        a.out[n] = out1;
+        a.cols[n++] = static_cast<int>(cols1);
+    }
+    a.rows = static_cast<int>(rows);
+    a.blocks0 = static_cast<int>(out0 ? blocks[0] : blocks[1]);
+    a.f32 = f32;
+    return launch_pdl<1024>("column sums", finish_sums_kernel, dim3(static_cast<unsigned>(blocks[0] + blocks[1])), st, a);
 }
 
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,

@@ -279,7 +279,7 @@ def test_block_forward(T, shape, mode):
         assert torch.equal(Z32.to(torch.bfloat16), Z[:M])
 
 
-@pytest.mark.parametrize("shape", BLOCKS + [(1, 31, 256, 256, 2), (32, 1, 256, 256, 2), (256, 1, 264, 256, 1)],
+@pytest.mark.parametrize("shape", BLOCKS + [(1, 31, 256, 256, 2), (32, 1, 256, 256, 2), (256, 1, 264, 256, 1), (512, 1, 256, 256, 1), (170, 5, 256, 128, 1)],
                          ids=lambda s: "s{}b{}h{}f{}p{}".format(*s))
 def test_block_backward(T, shape, mode):
     import torch
@@ -308,6 +308,58 @@ def test_block_backward(T, shape, mode):
                                  grad_dt=T.BF16)
     T.tpmlp_device_status()
     assert torch.equal(dX32.to(torch.bfloat16), dX) and torch.equal(dW2, dW) and torch.equal(dB2, dB)
+
+
+def test_block_backward_of_many_tiles(T):
+    """Weight gradients and dX of more tiles than CTA pairs, dX's K loop the longest: the three products in one
+    launch against one after the other (single CTAs), and against the reference."""
+    import torch
+    s, b, h, f, p = 201, 5, 1024, 4096, 4
+    M = s * b
+    d = make_block(T, s, b, h, f, p, seed=8)
+    H = bf16(np.random.default_rng(2).standard_normal((M, 2 * f)))
+    outs = []
+    for md in (2, 0, 1):
+        dX, dW, dB = torch.empty((M, h), device="cuda"), torch.empty((p, h, 2 * f // p), device="cuda"), torch.empty((f, h), device="cuda")
+        ws, _ = workspace(T, s, b, h, f, p, 1)
+        T.tpmlp_set_mxfp4_mode(md)
+        try:
+            T.tpmlp_mxfp4_swiglu_mlp_bwd(d["X"], *d["Wn"], *d["Bn"], H, d["dZ"], dX, dW, dB, None, None, ws, s, b, h, f, p, dx_dt=T.F32)
+            T.tpmlp_device_status()
+        finally:
+            T.tpmlp_set_mxfp4_mode(0)
+        outs.append((dX, dW, dB))
+    ref = R.block_bwd(host(d["X"]), R.q(host(d["W"])), R.q(host(d["B"])), host(H), host(d["dZ"]))
+    for dX, dW, dB in outs:
+        U.assert_close(host(dX), ref[0], "bf16", "dX")
+        U.assert_close(host(dW.transpose(0, 1).reshape(h, 2 * f)), ref[1], "bf16", "dW")
+        U.assert_close(host(dB), ref[2], "bf16", "dB")
+
+
+def test_block_backward_same_bits_in_every_tiling(T):
+    """Both tilings walk K in the same order without a split, so the backward's outputs are the same bits, run after
+    run.  Large enough that every epilogue warp turns its buffers over many times (a copy that overtakes a read of
+    the buffer it fills shows as a few wrong rows here)."""
+    import torch
+    s, b, h, f, p = 1024, 3, 512, 20480, 1
+    M = s * b
+    d = make_block(T, s, b, h, f, p, seed=4)
+    H = torch.randn((M, 2 * f), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(torch.bfloat16)
+    want = None
+    for md in (1, 2, 2, 2, 2, 0, 0):
+        dX, dW, dB = torch.empty((M, h), device="cuda"), torch.empty((h, 2 * f), device="cuda"), torch.empty((f, h), device="cuda")
+        dbw, db2 = torch.empty(2 * f, device="cuda"), torch.empty(h, device="cuda")
+        ws, _ = workspace(T, s, b, h, f, p, 1)
+        T.tpmlp_set_mxfp4_mode(md)
+        try:
+            T.tpmlp_mxfp4_swiglu_mlp_bwd(d["X"], *d["Wn"], *d["Bn"], H, d["dZ"], dX, dW, dB, dbw, db2, ws, s, b, h, f, p, dx_dt=T.F32)
+            T.tpmlp_device_status()
+        finally:
+            T.tpmlp_set_mxfp4_mode(0)
+        got = (dX, dW, dB, dbw, db2)
+        want = want or got
+        for name, x, y in zip(("dX", "dW", "dB", "dbw", "db2"), want, got):
+            assert torch.equal(x, y), (md, name, int((x != y).sum()))
 
 
 def test_block_results_do_not_depend_on_p(T):
