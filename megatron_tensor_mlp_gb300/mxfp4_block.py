@@ -1,0 +1,106 @@
+"""The gated feed-forward block with 4-bit operands, trained and served: an example of the MXFP4 entry points.
+
+``GatedMLP`` keeps bf16 weights in the tensor-parallel shard layout (``tpmlp_swiglu_pack``), lays them out as
+MXFP4 operands once for each direction they are used in (``tpmlp_mxfp4_quantize``: one read gives both), and runs
+the block's forward and backward on them.  Everything is computed by the library; PyTorch holds the memory.
+
+    python -m megatron_tensor_mlp_gb300.mxfp4_block
+
+trains a block towards another one's outputs for a few steps of gradient descent on fp32 master weights, then
+serves single tokens with the trained 4-bit weights and compares them with the batch's rows.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import tpmlp as T
+
+
+class GatedMLP:
+    """Z = (silu(X G + bg) * (X U + bu)) B + b2 with X, the activation and all weights rounded to MXFP4."""
+
+    def __init__(self, gate, up, down, bias_gate=None, bias_up=None, bias_down=None, p: int = 1):
+        """gate, up [h, ffn], down [ffn, h] and the biases: bf16 on the GPU.  p: tensor-parallel shards."""
+        self.h, self.ffn, self.p = gate.shape[0], gate.shape[1], p
+        h, f = self.h, self.ffn
+        self.W = torch.empty((p, h, 2 * f // p), dtype=torch.bfloat16, device=gate.device)
+        self.B = torch.empty((f, h), dtype=torch.bfloat16, device=gate.device)
+        self.bw = None
+        if bias_gate is not None:
+            self.bw = torch.empty(2 * f, dtype=torch.bfloat16, device=gate.device)
+            T.tpmlp_swiglu_pack(bias_gate, bias_up, self.bw, 1, f, p)
+        self.b2 = bias_down
+        # W as the operand of X W and of dH W^T, B as that of Y B and of dZ B^T
+        self.Wt, self.Wn = T.mxfp4_empty(2 * f, h), T.mxfp4_empty(h, 2 * f)
+        self.Bt, self.Bn = T.mxfp4_empty(h, f), T.mxfp4_empty(f, h)
+        self._work = {}
+        self.load(gate, up, down)
+
+    def load(self, gate, up, down):
+        """Takes new weights (bf16) and lays out their MXFP4 operands for both directions."""
+        h, f, p = self.h, self.ffn, self.p
+        T.tpmlp_swiglu_pack(gate, up, self.W, h, f, p)
+        self.B.copy_(down)
+        T.tpmlp_mxfp4_quantize(self.W, *self.Wn, *self.Wt, h, 2 * f, 2 * f // p, p)
+        T.tpmlp_mxfp4_quantize(self.B, *self.Bn, *self.Bt, f, h, h)
+
+    def _workspace(self, tokens, backward):
+        n = T.tpmlp_mxfp4_swiglu_ws_bytes(tokens, 1, self.h, self.ffn, self.p, backward)
+        if n > self._work.get(backward, torch.empty(0)).numel():
+            self._work[backward] = torch.empty(n, dtype=torch.uint8, device=self.B.device)
+        return self._work[backward]
+
+    def forward(self, X, save: bool = False):
+        """X [tokens, h] bf16 -> Z; with save also the pre-activations that backward needs."""
+        m = X.shape[0]
+        Z = torch.empty_like(X)
+        H = torch.empty((m, 2 * self.ffn), dtype=torch.bfloat16, device=X.device) if save else None
+        T.tpmlp_mxfp4_swiglu_mlp_fwd(X, *self.Wt, self.bw, *self.Bt, self.b2, Z, H, self._workspace(m, 0), m, 1, self.h,
+                                     self.ffn, self.p)
+        return (Z, H) if save else Z
+
+    def backward(self, X, H, dZ):
+        """The gradients of X (bf16) and of gate, up and down (fp32)."""
+        m, h, f, p = X.shape[0], self.h, self.ffn, self.p
+        dX = torch.empty_like(X)
+        dW = torch.empty((p, h, 2 * f // p), device=X.device)
+        dB = torch.empty((f, h), device=X.device)
+        T.tpmlp_mxfp4_swiglu_mlp_bwd(X, *self.Wn, *self.Bn, H, dZ, dX, dW, dB, None, None, self._workspace(m, 1), m, 1, h, f, p)
+        dG, dU = torch.empty((h, f), device=X.device), torch.empty((h, f), device=X.device)
+        T.tpmlp_swiglu_pack(dG, dU, dW, h, f, p, T.F32, inverse=1)
+        return dX, dG, dU, dB
+
+
+def train_and_serve(tokens=512, h=256, ffn=1024, p=2, steps=40, lr=0.5, seed=0, log=None):
+    """Trains a block towards another one's outputs; returns the losses, and the outputs of the first tokens served
+    one by one beside the batch's."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    normal = lambda *shape: torch.randn(*shape, generator=g, device="cuda")  # noqa: E731
+    bf = torch.bfloat16
+    teacher = GatedMLP(*(normal(*s).mul_(s[0] ** -0.5).to(bf) for s in ((h, ffn), (h, ffn), (ffn, h))), p=p)
+    masters = [normal(*s).mul_(s[0] ** -0.5) for s in ((h, ffn), (h, ffn), (ffn, h))]
+    block = GatedMLP(*(w.to(bf) for w in masters), p=p)
+    X = normal(tokens, h).to(bf)
+    target = teacher.forward(X).float()
+    losses = []
+    for step in range(steps):
+        Z, H = block.forward(X, save=True)
+        err = Z.float() - target
+        losses.append(float(err.square().mean()))
+        if log and step % 10 == 0:
+            log(f"step {step:3d}  loss {losses[-1]:.4f}")
+        _, *grads = block.backward(X, H, (err / tokens).to(bf))
+        for w, d in zip(masters, grads):
+            w.add_(d, alpha=-lr)
+        block.load(*(w.to(bf) for w in masters))
+    batch = block.forward(X)
+    served = torch.cat([block.forward(X[i:i + 1]) for i in range(8)])
+    T.tpmlp_device_status()
+    if log:
+        log(f"loss {losses[0]:.4f} -> {losses[-1]:.4f}; served tokens differ from the batch's by "
+            f"{float((served.float() - batch[:8].float()).abs().max()):.2e} at most")
+    return losses, served, batch[:8]
+
+
+if __name__ == "__main__":
+    train_and_serve(log=print)

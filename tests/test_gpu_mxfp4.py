@@ -451,3 +451,14 @@ def test_empty_batch_writes_nothing(T):
     T.tpmlp_mxfp4_dequantize(t, t[512:], o, 0, 32, T.F32)
     torch.cuda.synchronize()
     assert T.tpmlp_launch_count() == n0 and bool((o == 5.0).all())
+
+
+def test_example_trains_and_serves(T):
+    """The example's block learns, and single tokens give the batch's rows: to the bf16 store (a row is quantised by
+    itself, the kernels for one token and for many differ in fp32 summation order only) up to a rounding of Y that
+    falls the other way, 2e-2 of the outputs' size."""
+    from megatron_tensor_mlp_gb300 import mxfp4_block
+    losses, served, batch = mxfp4_block.train_and_serve()
+    assert losses[-1] < 0.5 * losses[0], losses
+    a, b = host(served), host(batch)
+    assert np.max(np.abs(a - b)) <= 2e-2 * np.sqrt(np.mean(b * b)) + R.half_spacing(np.max(np.abs(b)), 8) * 2
