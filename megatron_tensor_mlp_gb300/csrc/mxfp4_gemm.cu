@@ -176,52 +176,51 @@ tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec&
                   static_cast<unsigned>(split), st, m[0], m[1], m[2], m[3], k);
 }
 
-// Which kernel takes a product, by its expected time in microseconds.  Fitted to one GB300's times of 30
-// products (N x K of 40960x5120, 5120x20480, 8192x1024, 4096x4096, 2048x8192, 128 to 2048 rows; most within 15 %):
-//   pairs    4 + waves (0.265 kb + 1.6)       256x256 tiles over the CTA pairs, kb stages of 256 k each
-//   single   2.8 + 0.35 kb                     at most one CTA an SM,
-//            2.8 + 0.40 kb                     at most two, else
-//            2.8 + waves (0.40 kb + 3)
-//   split    2.8 + 0.35 kb / split + 3         at most one CTA an SM: the partial sums cross in about 3 us,
-//            2.8 + 0.40 kb / split + 5.5       at most two
-// For example 512 x 5120 x 20480: pairs 27.3 measured, single 32.6, split two ways 39; 800 rows: single 34.8,
-// pairs 49.8 (80 tiles, two waves); 48 x 5120 x 20480: split four ways 15.3, single 25.7, pairs 26.0;
-// 333 x 4096 x 16384: split two ways 19.4, pairs 22.1, single 25.1.
-// At most 128 rows: single CTAs, which copy no more rows of A than there are (4 x 40960 x 5120: 26 against 31).
+// Which kernel takes a product, by its expected time in microseconds.  Fitted to one GB300's times of 63
+// products (N x K of 40960x5120, 5120x20480, 8192x1024, 4096x4096, 2048x8192, 20480x2048, 1024x1024, 64 to 2048
+// rows, weights out of L2); kb = stages of 256 k:
+//   pairs    4 + waves (0.265 kb + 1.05)      256x256 tiles over the CTA pairs
+//   single   4 + 0.34 kb                       at most one CTA an SM,
+//            5.3 + 0.38 kb                     at most two, else
+//            2.5 + waves (0.38 kb + 3)
+//   split    the same of kb / split, and 1.5 (one CTA an SM) or 2.3 (two) log2(split) for the exchange
+// The choice costs at most 10 % against the best of them.  For example 512 x 5120 x 20480: pairs 26.7, single 33.7,
+// split two ways 41.6; 800 rows: single 35.9, pairs 48.2 (80 tiles, two waves); 64 x 5120 x 20480: split four ways
+// 15.7, single 25.8, pairs 25.3; 333 x 4096 x 16384: split two ways 19.5, pairs 22.1, single 25.1.
+// At most 32 rows: single CTAs, which copy no more rows of A than there are (4 x 40960 x 5120: 23 against 31).
 struct Choice {
     bool pair;
     int split;
     double us;
 };
 constexpr double kPairStart = 4.0;
-double pair_tile_us(int kb) { return 0.265 * kb + 1.6; }
+double pair_tile_us(int kb) { return 0.265 * kb + 1.05; }
 template <int EPI>
 Choice choose(const MxSpec& g, int kb, int cap, int sms) {
     const int64_t n1 = EPI == EPI_SWIGLU ? g.N / 128 : (g.N + 127) / 128, tiles1 = n1 * ((g.M + 127) / 128);
     const int64_t tiles2 = ((g.M + 255) / 256) * ((g.N + 255) / 256);
     const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
-    const int64_t waves1 = (tiles1 + 2 * sms - 1) / (2 * sms);
     Choice c{false, 1, 0.0};
-    double best = 2.8 + (tiles1 <= sms ? 0.35 * kb : waves1 == 1 ? 0.40 * kb : waves1 * (0.40 * kb + 3.0));
-    for (int s = 2; s <= 8; s *= 2) {
+    for (int s = 1, log = 0; s <= 8; s *= 2, ++log) {
         // (40 tiles split four ways are 160 CTAs on 152 SMs: a few SMs with two cost little)
         const bool one = tiles1 * s <= sms + sms / 16;
-        if (tiles1 * s > 2 * sms || !split_fits<EPI, 2>(s, rows, kb)) break;
-        const double t = one ? 2.8 + 0.35 * kb / s + 3.0 : 2.8 + 0.40 * kb / s + 5.5;
-        if (t < best) {
-            best = t;
+        if (s > 1 && (tiles1 * s > 2 * sms || !split_fits<EPI, 2>(s, rows, kb))) break;
+        const int64_t waves = (tiles1 * s + 2 * sms - 1) / (2 * sms);
+        const double k = static_cast<double>(kb) / s;
+        const double t = one ? 4.0 + 0.34 * k + 1.5 * log : waves <= 1 ? 5.3 + 0.38 * k + 2.3 * log : 2.5 + waves * (0.38 * k + 3.0);
+        if (s == 1 || t < c.us) {
+            c.us = t;
             c.split = s;
         }
     }
-    if (cap > 0 && g.M > mx::BM) {
+    if (cap > 0 && g.M > 32) {
         const int64_t waves2 = (tiles2 + cap - 1) / cap;
         const double t = kPairStart + waves2 * pair_tile_us(kb);
-        if (t < best) {
-            best = t;
+        if (t < c.us) {
+            c.us = t;
             c.pair = true;
         }
     }
-    c.us = best;
     return c;
 }
 
