@@ -277,7 +277,8 @@ __device__ __forceinline__ void read_h(const uint8_t* hb, int lane, uint32_t (&h
 // EPI_DSWIGLU: v = dY of features f0..f0+31 of this thread's row (token) and, from its pre-activations h,
 // dg = dY u silu'(g), du = dY silu(g) and y = silu(g) u, from fp32 quantised along the columns (dg, du) and,
 // turned through shared memory, along the tokens (dg, du, y).  tb: the warp's block of 32 tokens.  Rows past
-// M count as zero.  buf: turn32's; sc: the five scale tiles.
+// M are zero: their h is, and their dY is finite (the quantiser writes zero scales for dZ's rows up to a whole
+// tile; a NaN there would need a select for every value, which cost 15 us of 770).  buf: turn32's; sc: the five scale tiles.
 __device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], const uint32_t (&h)[32], int gm, int f0, int tb,
                                               float* buf, uint8_t* sc, int lane) {
     if (f0 >= p.N) return;  // (whole warp; features come in multiples of 128)
@@ -289,8 +290,7 @@ __device__ __forceinline__ void dswiglu_chunk(const Args& p, float (&v)[32], con
     for (int j = 0; j < 32; j += 2) {
         const f2 g2 = tc::f2_pack(__uint_as_float(h[j / 2] << 16), __uint_as_float(h[j / 2] & 0xFFFF0000u));
         const f2 u2 = tc::f2_pack(__uint_as_float(h[16 + j / 2] << 16), __uint_as_float(h[16 + j / 2] & 0xFFFF0000u));
-        // (a row past the last may hold a NaN from the scales beside it)
-        const f2 dy = tc::f2_pack(live ? v[j] : 0.0f, live ? v[j + 1] : 0.0f);
+        const f2 dy = tc::f2_pack(v[j], v[j + 1]);
         const f2 sg = sigmoid2(g2), sl = tc::f2_mul(g2, sg);
         const f2 ds = tc::f2_mul(sg, tc::f2_fma(g2, tc::f2_fma(sg, tc::f2_pack(-1.0f, -1.0f), one), one));  // silu'
         tc::f2_unpack(tc::f2_mul(tc::f2_mul(dy, u2), ds), g[j], g[j + 1]);

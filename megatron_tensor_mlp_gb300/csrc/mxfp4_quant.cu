@@ -189,9 +189,10 @@ __global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(cons
                     if constexpr (F32) *reinterpret_cast<uint16_t*>(qd) = static_cast<uint16_t>(code);
                     else *reinterpret_cast<uint32_t*>(qd) = code;
                 }
-                // (col_tiles cover whole scale tiles: padding blocks are written as zero)
-                if (lane16 % P::LANES == 0) sd[(i & 1) * 256 + (i >> 1) * 4] = static_cast<uint8_t>(s);
             }
+            // (whole scale tiles: the scales of padding blocks and rows are written as zero; no product reads those of
+            // padding rows but the gated backward's dY, whose epilogue wants them finite)
+            if (lane16 % P::LANES == 0) sd[(i & 1) * 256 + (i >> 1) * 4] = static_cast<uint8_t>(s);
             qd += 16 * pitch;
         }
     }
