@@ -265,7 +265,6 @@ mx::Args make_args(const MxOperand& a, const MxOperand& b, const MxSpec& g, cons
     k.N = static_cast<int>(g.N);
     k.kb = static_cast<int>((g.K + mx::KC - 1) / mx::KC);
     k.last_steps = static_cast<int>((g.K - static_cast<int64_t>(k.kb - 1) * mx::KC + 63) / 64);
-    k.group_m = 16;
     k.out_f32 = g.out_f32 ? 1 : 0;
     k.out = g.out;
     k.out_ld = g.out_ld;

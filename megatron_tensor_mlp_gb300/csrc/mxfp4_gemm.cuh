@@ -38,12 +38,13 @@ constexpr int BM = 128;           // rows of A (and of B) in one CTA's stage
 constexpr int KC = 256;           // k per ring stage: 128 bytes of codes a row
 constexpr int OP_BYTES = BM * 128;
 constexpr int SF_TILE = 512;      // scales of 128 rows x 128 k
+constexpr int GROUP_M = 16;       // pair kernel: row blocks walked together (4 to 32 within 1 % of one another)
 
 struct Args {
     int M, N;
     int kb;          // ring stages of K: ceil(K / 256)
     int last_steps;  // MMAs (64 k each) of the last one: 1..4
-    int m_blocks, n_blocks, group_m;  // tiles
+    int m_blocks, n_blocks;  // tiles
     int a_box;       // single kernel: rows of A copied per stage (16, 32, 64 or 128)
     int stages;      // single kernel: ring stages
     int a_blocked, b_blocked;  // operand's codes are [k / 32][rows][16 bytes] (written by an epilogue), not [rows][k / 2]
@@ -357,10 +358,10 @@ struct PairGeom {
 };
 
 __device__ __forceinline__ void decode_tile(const Args& p, int t, int& mb, int& nb) {
-    const int per_group = p.group_m * p.n_blocks;
+    const int per_group = GROUP_M * p.n_blocks;
     const int g = t / per_group;
-    const int first_m = g * p.group_m;
-    const int gm = min(p.m_blocks - first_m, p.group_m);
+    const int first_m = g * GROUP_M;
+    const int gm = min(p.m_blocks - first_m, GROUP_M);
     const int r = t - g * per_group;
     mb = first_m + r % gm;
     nb = r / gm;

@@ -441,6 +441,85 @@ def test_block_on_another_stream_and_in_a_graph(T):
     assert torch.equal(Z0, Z1) and torch.equal(Z0, Z2)
 
 
+def test_bases_aligned_to_16_bytes_only(T, mode):
+    """Every tensor 16 bytes into an allocation: 32-byte accesses must give way."""
+    import torch
+    s, b, h, f, p = 37, 4, 256, 512, 2
+    M = s * b
+
+    def at16(t):
+        n = t.numel() * t.element_size()
+        raw = torch.zeros(n + 16, dtype=torch.uint8, device="cuda")
+        v = raw[16:].view(t.dtype).view(t.shape)
+        v.copy_(t)
+        return v
+
+    d = make_block(T, s, b, h, f, p, seed=12)
+    e = {k: tuple(at16(x) for x in v) if isinstance(v, tuple) else at16(v) for k, v in d.items()}
+    outs = []
+    for x, put in ((d, lambda t: t), (e, at16)):
+        Z, H = put(torch.zeros_like(x["X"])), put(torch.zeros((M, 2 * f), dtype=torch.bfloat16, device="cuda"))
+        ws = put(workspace(T, s, b, h, f, p, 0)[0])
+        T.tpmlp_mxfp4_swiglu_mlp_fwd(x["X"], *x["Wt"], x["bw"], *x["Bt"], x["b2"], Z, H, ws, s, b, h, f, p)
+        dX, dW, dB = put(torch.zeros_like(x["X"])), put(torch.zeros((p, h, 2 * f // p), device="cuda")), put(torch.zeros((f, h), device="cuda"))
+        dbw, db2 = put(torch.zeros(2 * f, device="cuda")), put(torch.zeros(h, device="cuda"))
+        ws = put(workspace(T, s, b, h, f, p, 1)[0])
+        T.tpmlp_mxfp4_swiglu_mlp_bwd(x["X"], *x["Wn"], *x["Bn"], H, x["dZ"], dX, dW, dB, dbw, db2, ws, s, b, h, f, p)
+        T.tpmlp_device_status()
+        outs.append((Z, H, dX, dW, dB, dbw, db2))
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
+def test_offsets_past_32_bits(T):
+    """Tensors of more than 2^31 values: what lies at their far end is right."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    n = 24  # rows looked at
+    rows, cols = 270_001, 8192
+    X = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    X.normal_(generator=gen)
+    a, t = T.mxfp4_empty(rows, cols), T.mxfp4_empty(cols, rows)
+    T.tpmlp_mxfp4_quantize(X, *a, *t, rows, cols, cols)
+    codes, sc = R.quantize(host(X[-n:]))
+    assert np.array_equal(a[0][-n:].cpu().numpy(), codes)
+    got = R.untile_scales(a[1][-1:].cpu().numpy(), rows - (rows - 1) // 128 * 128, cols)
+    assert np.array_equal(got[-min(n, got.shape[0]):], sc[-min(n, got.shape[0]):])
+    codes, _ = R.quantize(host(X[:, -n:]).T)
+    assert np.array_equal(t[0][-n:].cpu().numpy(), codes)
+    out = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    T.tpmlp_mxfp4_dequantize(*a, out, rows, cols)
+    assert np.array_equal(host(out[-n:]), R.q(host(X[-n:])))
+    del X, a, t, out
+    # product: D of 2.2e9 values
+    m, k = 540_000, 64
+    A = torch.randn((m, k), generator=gen, device="cuda").to(torch.bfloat16)
+    B = torch.randn((4096, k), generator=gen, device="cuda").to(torch.bfloat16)
+    aq, bq = T.mxfp4_empty(m, k), T.mxfp4_empty(4096, k)
+    T.tpmlp_mxfp4_quantize(A, *aq, None, None, m, k, k)
+    T.tpmlp_mxfp4_quantize(B, *bq, None, None, 4096, k, k)
+    D = torch.empty((m, 4096), dtype=torch.bfloat16, device="cuda")
+    T.tpmlp_mxfp4_matmul(*aq, *bq, None, D, m, 4096, k)
+    R.assert_product(host(D[-n:]), R.q(host(A[-n:])), R.q(host(B)))
+    del A, D
+    # block: pre-activations of 2.3e9 values
+    s, b, h, f, p = 55_001, 1, 256, 20480, 2
+    d = make_block(T, s, b, h, f, p, seed=30)
+    Z, H = torch.empty((s, h), dtype=torch.bfloat16, device="cuda"), torch.empty((s, 2 * f), dtype=torch.bfloat16, device="cuda")
+    ws, _ = workspace(T, s, b, h, f, p, 0)
+    T.tpmlp_mxfp4_swiglu_mlp_fwd(d["X"], *d["Wt"], d["bw"], *d["Bt"], d["b2"], Z, H, ws, s, b, h, f, p)
+    Zr, Hr = R.block_fwd(host(d["X"][-n:]), R.q(host(d["W"]).T), R.q(host(d["B"]).T), host(d["bw"]), host(d["b2"]))
+    U.assert_close(host(H[-n:]), Hr, "bf16", "H")
+    U.assert_close(host(Z[-n:]), Zr, "bf16", "Z")
+    dX, dW, dB = torch.empty_like(Z), torch.empty((p, h, 2 * f // p), device="cuda"), torch.empty((f, h), device="cuda")
+    dbw, db2 = torch.empty(2 * f, device="cuda"), torch.empty(h, device="cuda")
+    ws, _ = workspace(T, s, b, h, f, p, 1)
+    T.tpmlp_mxfp4_swiglu_mlp_bwd(d["X"], *d["Wn"], *d["Bn"], H, d["dZ"], dX, dW, dB, dbw, db2, ws, s, b, h, f, p)
+    T.tpmlp_device_status()
+    dXr = R.block_bwd(host(d["X"][-n:]), R.q(host(d["W"])), R.q(host(d["B"])), host(H[-n:]), host(d["dZ"][-n:]))[0]
+    U.assert_close(host(dX[-n:]), dXr, "bf16", "dX")
+    U.assert_close(host(db2), d["dZ"].double().sum(0).cpu().numpy(), "bf16", "db2")
+
+
 def test_empty_batch_writes_nothing(T):
     import torch
     n0 = T.tpmlp_launch_count()
