@@ -14,14 +14,22 @@
 //                     accumulators and 24 columns of scales do not fit 512 tensor-memory columns,
 //                     so the accumulators share 32: [0,256) and [224,480), scales from 480.  Each
 //                     epilogue reads the shared columns first and reports them free; the next
-//                     tile's MMAs start then, beside the rest of the epilogue.
+//                     tile's MMAs start then, beside the rest of the epilogue.  Several independent
+//                     products can share a launch (Problems).
+//                     A pair reads 70 KB a stage from L2 for 512 tensor cycles, about the 64 bytes a
+//                     cycle that an SM gets, so L2 binds first and, over milliseconds, the power cap:
+//                     8192 x 20480 x 5120 takes 218 us (7.9 PFLOP/s) cold and 248 us (6.9) at the cap's
+//                     1.6 GHz; tensor pipe 83 % of active cycles.  (The instruction's 96-deep form would
+//                     only move the limit further to L2.)
 //   mx_single_kernel  one CTA per 128x128 tile (128 rows of A, 128 of B; for the gated forward 64
 //                     gate and 64 up columns), two CTAs an SM, not persistent: for few rows, where
 //                     reading B's codes bounds the time, and for GEMMs of few tiles.  Clusters of
 //                     up to 8 CTAs split the K loop and add their partial sums through distributed
 //                     shared memory in a fixed order.  With at most 64 rows of A only those rows
 //                     are copied: the MMA's other rows read whatever lies behind them in shared
-//                     memory, and their results are not stored.
+//                     memory, and their results are not stored.  1 x 5120 x 20480, weights from
+//                     memory: 14 us, of which 8.2 us are its 56 MB at a copy's rate and 5 us a launch's
+//                     chain of latencies; 4 x 40960 x 5120 23 us (16.4).
 //
 // Every wait on an mbarrier is bounded (a status word records a timeout); no TMA load uses
 // cluster multicast.
@@ -193,6 +201,11 @@ __device__ __forceinline__ void turn32(float* buf, const float (&v)[32], float (
     __syncwarp();
 }
 
+// EPI_DSWIGLU, 4096 tokens, h5120, ffn20480: 195 us against 130 for the product alone (before the power cap); the
+// epilogue binds, a tile's arithmetic and its shared-memory traffic taking twice the MMAs' time.  Turning the three
+// arrays costs 48 us of it, the row-wise blocks 25, the activation 19, the stores 10.  Twelve epilogue warps
+// that turn half blocks took 266 us.
+//
 // EPI_DSWIGLU leaves five quantised arrays.  Their codes go out blocked, a warp's 32 blocks of 16 bytes
 // as 512 bytes in a row.  (Row-major codes, 16 bytes a lane into 32 rows, kept the load/store unit busy for
 // longer than the arithmetic; as TMA stores of 16 bytes x 32 rows they still cost 25 us of 910 in the
