@@ -25,6 +25,15 @@ tpmlp_status check_matrix(int64_t rows, int64_t cols, const char* what) {
     return TPMLP_OK;
 }
 
+// Rows and columns of a product: the kernels' 32-bit indexes run up to a tile past them.
+tpmlp_status check_product(int64_t m, int64_t n) {
+    if (m > kMaxDim - 1024 || n > kMaxDim - 1024) {
+        set_error("shape too large: %lld rows, %lld columns", (long long)m, (long long)n);
+        return TPMLP_ERR_SHAPE;
+    }
+    return TPMLP_OK;
+}
+
 // An MXFP4 operand inside a workspace.
 struct Packed {
     uint8_t* codes;
@@ -105,6 +114,12 @@ tpmlp_status run(const MxProduct& c, const DeviceInfo& dev, cudaStream_t st) { r
 
 tpmlp_status check_gated(int64_t s, int64_t b, int64_t h, int64_t ffn, int p) {
     TP_TRY(check_mlp_shape(s, b, h, ffn, p, true));
+    // (blocked operands count a row as two 8-byte words, in 32 bits)
+    if (ffn > (int64_t(1) << 28) || s * b > (int64_t(1) << 29)) {
+        set_error("shape too large: the gated block takes at most 2^29 tokens and 2^28 features");
+        return TPMLP_ERR_SHAPE;
+    }
+    TP_TRY(check_product(h, h));
     if ((ffn / p) % 128 != 0) {
         set_error("the gated block needs ffn/p to be a multiple of 128 (ffn=%lld, p=%d)", (long long)ffn, p);
         return TPMLP_ERR_DIVISIBILITY;
@@ -190,6 +205,7 @@ tpmlp_status tpmlp_mxfp4_matmul(const void* Aq, const void* As, const void* Bq, 
     TP_TRY(check_matrix(m, k, "A"));
     TP_TRY(check_matrix(n, k, "B"));
     TP_TRY(check_matrix(m, n, "D"));
+    TP_TRY(check_product(m, n));
     TP_TRY(check_dtype(out_dt));
     TP_TRY(check_aligned({Aq, As, Bq, Bs, bias, D}));
     TP_TRY(check_pitch(n, out_dt, "n"));

@@ -33,7 +33,7 @@ class GatedMLP:
         # W as the operand of X W and of dH W^T, B as that of Y B and of dZ B^T
         self.Wt, self.Wn = T.mxfp4_empty(2 * f, h), T.mxfp4_empty(h, 2 * f)
         self.Bt, self.Bn = T.mxfp4_empty(h, f), T.mxfp4_empty(f, h)
-        self._work = {}
+        self._spaces = {}
         self.load(gate, up, down)
 
     def load(self, gate, up, down):
@@ -46,9 +46,9 @@ class GatedMLP:
 
     def _workspace(self, tokens, backward):
         n = T.tpmlp_mxfp4_swiglu_ws_bytes(tokens, 1, self.h, self.ffn, self.p, backward)
-        if n > self._work.get(backward, torch.empty(0)).numel():
-            self._work[backward] = torch.empty(n, dtype=torch.uint8, device=self.B.device)
-        return self._work[backward]
+        if n > self._spaces.get(backward, torch.empty(0)).numel():
+            self._spaces[backward] = torch.empty(n, dtype=torch.uint8, device=self.B.device)
+        return self._spaces[backward]
 
     def forward(self, X, save: bool = False):
         """X [tokens, h] bf16 -> Z; with save also the pre-activations that backward needs."""

@@ -191,6 +191,54 @@ def test_product(T, m, n, k, mode):
         R.assert_product(host(D[:m]), a, b, host(bias_d) if with_bias else None, out_dt == T.BF16, f"{m}x{n}x{k}")
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 4, 1), (7, 16, 1), (20, 24, 33), (5, 12, 40), (130, 260, 31)])
+def test_product_smallest_and_odd(T, m, n, k, mode):
+    """One value of k, K that ends inside a block, rows of fp32 D that are no multiple of 8 long."""
+    import torch
+    rng = np.random.default_rng(m * n + k)
+    aq, as_, a = operand(T, rng.standard_normal((m, k)))
+    bq, bs, b = operand(T, rng.standard_normal((n, k)))
+    bias = bf16(rng.standard_normal(n))
+    for out_dt, tdt in ((T.F32, torch.float32),) + (((T.BF16, torch.bfloat16),) if n % 8 == 0 else ()):
+        D = torch.full((m + 1, n), 7.0, dtype=tdt, device="cuda")
+        T.tpmlp_mxfp4_matmul(aq, as_, bq, bs, bias, D, m, n, k, out_dt)
+        T.tpmlp_device_status()
+        assert bool((D[m] == 7.0).all())
+        R.assert_product(host(D[:m]), a, b, host(bias), out_dt == T.BF16, f"{m}x{n}x{k}")
+
+
+def test_block_not_finite_rows(T):
+    """A NaN in one token's input makes that token's output NaN and no other's; extreme gates (the sigmoid at 0 and 1)
+    stay finite."""
+    import torch
+    s, b, h, f, p = 70, 1, 256, 512, 1
+    d = make_block(T, s, b, h, f, p, seed=40)
+    X = d["X"].clone()
+    X[5, 17] = float("nan")
+    bw = d["bw"].clone()
+    bw[:64], bw[64:128] = 3e4, -3e4
+    Z, H = torch.empty_like(X), torch.empty((s, 2 * f), dtype=torch.bfloat16, device="cuda")
+    ws, _ = workspace(T, s, b, h, f, p, 0)
+    T.tpmlp_mxfp4_swiglu_mlp_fwd(X, *d["Wt"], bw, *d["Bt"], None, Z, H, ws, s, b, h, f, p)
+    T.tpmlp_device_status()
+    z = host(Z)
+    rest = np.arange(s) != 5
+    assert np.isnan(z[5]).all()
+    Zr, Hr = R.block_fwd(host(X[torch.from_numpy(rest).cuda()]), R.q(host(d["W"]).T), R.q(host(d["B"]).T), host(bw))
+    U.assert_close(z[rest], Zr, "bf16", "Z")
+    U.assert_close(host(H)[rest], Hr, "bf16", "H")
+    dX, dW, dB = torch.empty_like(X), torch.empty((p, h, 2 * f), device="cuda"), torch.empty((f, h), device="cuda")
+    Hc = torch.where(H.isnan(), torch.zeros_like(H), H)
+    ws, _ = workspace(T, s, b, h, f, p, 1)
+    T.tpmlp_mxfp4_swiglu_mlp_bwd(d["X"], *d["Wn"], *d["Bn"], Hc, d["dZ"], dX, dW, dB, None, None, ws, s, b, h, f, p)
+    T.tpmlp_device_status()
+    with np.errstate(over="ignore"):
+        ref = R.block_bwd(host(d["X"]), R.q(host(d["W"])), R.q(host(d["B"])), host(Hc), host(d["dZ"]))
+    U.assert_close(host(dX), ref[0], "bf16", "dX")
+    U.assert_close(host(dW[0]), ref[1], "bf16", "dW")
+    U.assert_close(host(dB), ref[2], "bf16", "dB")
+
+
 def test_product_many_tiles_and_repeats(T):
     """Several waves of pair tiles, and the same bits twice in every tiling."""
     import torch

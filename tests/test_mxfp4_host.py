@@ -60,6 +60,7 @@ def test_matmul_and_dequantize_refusals():
     assert matmul(D=None) == T.ERR_NULL and matmul(As=None) == T.ERR_NULL
     assert matmul(m=-1) == T.ERR_SHAPE and matmul(k=0) == T.ERR_SHAPE and matmul(n=0) == T.ERR_SHAPE
     assert matmul(m=1 << 30, n=1 << 20) == T.ERR_SHAPE
+    assert matmul(m=(1 << 31) - 100, n=8) == T.ERR_SHAPE and matmul(m=1, n=(1 << 31) - 8) == T.ERR_SHAPE  # within a tile of 2^31
     assert matmul(out_dt=3) == T.ERR_DTYPE
     assert matmul(Bq=addr(2) + 4) == T.ERR_ALIGNMENT
     assert matmul(n=68) == T.ERR_ALIGNMENT and matmul(n=66, out_dt=T.F32) == T.ERR_ALIGNMENT
@@ -93,6 +94,7 @@ def test_block_refusals(call):
     assert call(X=None) == T.ERR_NULL and call(ws=None) == T.ERR_NULL and call(Ws=None) == T.ERR_NULL
     assert call(h=0) == T.ERR_SHAPE and call(s=-1) == T.ERR_SHAPE and call(p=0) == T.ERR_SHAPE
     assert call(s=1 << 20, b=1 << 12) == T.ERR_SHAPE
+    assert call(s=1, b=1, h=8, ffn=1 << 29, p=1) == T.ERR_SHAPE
     assert call(ffn=510, p=4) == T.ERR_DIVISIBILITY and call(ffn=512, p=8, h=64) == T.ERR_DIVISIBILITY  # shards of 64 features
     assert call(h=66, p=4) == T.ERR_DIVISIBILITY
     assert call(**{"z_dt" if call is fwd else "dx_dt": 4}) == T.ERR_DTYPE
