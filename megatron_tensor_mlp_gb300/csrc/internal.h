@@ -120,6 +120,7 @@ struct MxSpec {
     void* q; void* qs; int64_t q_cols;              // quantised along the columns, codes blocked
     void* ht; void* hts; void* yt; void* yts;       // quantised along the rows, codes blocked
     float* colsum;                                  // sums over blocks of 32 rows, may be null
+    bool prefetch_b;                                // B towards L2 while the kernel ahead in the stream ends
 };
 tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxSpec& g, const DeviceInfo& dev, cudaStream_t st);
 // One product of a group of independent ones (EPI_STORE).

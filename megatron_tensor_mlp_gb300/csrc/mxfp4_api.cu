@@ -245,8 +245,11 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_fwd(const void* X, const void* Wq, const voi
     g.q = w.y.codes;
     g.qs = w.y.scales;
     g.q_cols = ffn;
+    g.prefetch_b = true;
     TP_TRY(launch_mxfp4_gemm(w.x.operand(), {Wq, Ws, 2 * ffn}, g, *dev, st));
-    return run(product(w.y.blocked(), {Bq, Bs, h}, b2, Z, ffn, z_dt == TPMLP_F32, 0), *dev, st);
+    MxProduct row = product(w.y.blocked(), {Bq, Bs, h}, b2, Z, ffn, z_dt == TPMLP_F32, 0);
+    row.g.prefetch_b = true;
+    return run(row, *dev, st);
 }
 
 tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const void* Ws, const void* Bq, const void* Bs, const void* H,

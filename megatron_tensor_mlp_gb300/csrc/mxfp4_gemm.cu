@@ -286,6 +286,7 @@ mx::Args make_args(const MxOperand& a, const MxOperand& b, const MxSpec& g, cons
     k.t_blocks = (g.M + 31) / 32;
     k.t_tiles = (g.M + 127) / 128;
     k.colsum = g.colsum;
+    k.prefetch_b = g.prefetch_b ? 1 : 0;
     k.status = dev.status;
     k.timeout_ns = 2000000000ull;  // 2 s per wait
     {

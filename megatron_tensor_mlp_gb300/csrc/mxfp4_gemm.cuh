@@ -55,6 +55,7 @@ struct Args {
     int m_blocks, n_blocks;  // tiles
     int a_box;       // single kernel: rows of A copied per stage (16, 32, 64 or 128)
     int stages;      // single kernel: ring stages
+    int prefetch_b;  // single kernel: B's first stages into L2 while the kernel ahead in the stream ends (B not blocked)
     int a_blocked, b_blocked;  // operand's codes are [k / 32][rows][16 bytes] (written by an epilogue), not [rows][k / 2]
     int out_f32, st32;
     // EPI_STORE: D + bias; column n is at out + (n / shard_cols) * out_ss + m * out_ld + n % shard_cols
@@ -853,11 +854,34 @@ __global__ void __launch_bounds__(S_THREADS, CTAS)
         fence_mbarrier_init();
         fence_proxy_async_smem();
     }
+    // the tile's columns: gated, 64 gate rows of B and the 64 up rows of the same features
+    const int f0 = nb * 64;
+    const int gate_row = (f0 >> 7) * 256 + (f0 & 127);
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
         tma_prefetch_desc(&tmSA);
         tma_prefetch_desc(&tmSB);
+    }
+    if (warp == 2 && lane == 0) {
+        // Within the block's forward, the ring's worth of B goes on its way into L2 while the kernel ahead ends:
+        // 4 tokens at h5120 f20480 39.3 -> 38.6 us, 100 at h4096 f16384 34.1 -> 33.4.  Twice the ring gained nothing
+        // over none and four times lost 4 %.  Products called one after another lose by it (1x20480x5120 12.6 -> 14.0):
+        // their kernel ahead still reads memory at full rate.  Nothing is read before the wait, so the order of the
+        // stream holds whoever writes B: L2 is where writes arrive.
+        if (p.prefetch_b && mb == 0) {
+            const int end = min(it0 + p.stages, it1);
+            for (int it = it0; it < end; ++it) {
+                if constexpr (GATED) {
+                    tma_prefetch_3d(&tmB, it * 128, gate_row, 0);
+                    tma_prefetch_3d(&tmB, it * 128, gate_row + 128, 0);
+                    tma_prefetch_3d(&tmSB, 0, it * 2, (f0 >> 7) * 2);
+                } else {
+                    tma_prefetch_3d(&tmB, it * 128, nb * S_BN, 0);
+                    tma_prefetch_3d(&tmSB, 0, it * 2, nb);
+                }
+            }
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, S_ACC_COLS);
@@ -871,9 +895,6 @@ __global__ void __launch_bounds__(S_THREADS, CTAS)
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
 
-    // the tile's columns: gated, 64 gate rows of B and the 64 up rows of the same features
-    const int f0 = nb * 64;
-    const int gate_row = (f0 >> 7) * 256 + (f0 & 127);
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
         int stage = 0;

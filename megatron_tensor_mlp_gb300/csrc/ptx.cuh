@@ -110,6 +110,13 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // The same with the mbarrier given by its shared-memory address.
 __device__ __forceinline__ void tma_load_3d_bar(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
                                                 int32_t z) {

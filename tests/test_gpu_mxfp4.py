@@ -489,6 +489,37 @@ def test_block_on_another_stream_and_in_a_graph(T):
     assert torch.equal(Z0, Z1) and torch.equal(Z0, Z2)
 
 
+def test_block_forward_right_after_its_weights_are_written(T):
+    """The forward's kernels may start while the one ahead ends; weights written just before a call are the ones it uses."""
+    import torch
+    s, b, h, f, p = 4, 1, 512, 1024, 1
+    two = [make_block(T, s, b, h, f, p, seed=31 + i) for i in range(2)]
+    ws, _ = workspace(T, s, b, h, f, p, 0)
+    X = two[0]["X"]
+    want = []
+    for d in two:
+        Z = torch.empty((s, h), dtype=torch.bfloat16, device="cuda")
+        T.tpmlp_mxfp4_swiglu_mlp_fwd(X, *d["Wt"], None, *d["Bt"], None, Z, None, ws, s, b, h, f, p)
+        torch.cuda.synchronize()
+        want.append(Z)
+    assert not torch.equal(*want)
+    W, Wt, Bt = torch.empty_like(two[0]["W"]), T.mxfp4_empty(2 * f, h), T.mxfp4_empty(h, f)
+    Z = torch.empty((40, s, h), dtype=torch.bfloat16, device="cuda")
+    for i in range(40):
+        d = two[i % 2]
+        if i % 4 < 2:  # by copies, or by the quantiser with a copy ahead of it
+            for dst, src in zip(Wt + Bt, d["Wt"] + d["Bt"]):
+                dst.copy_(src)
+        else:
+            W.copy_(d["W"])
+            T.tpmlp_mxfp4_quantize(d["B"], None, None, *Bt, f, h, h)
+            T.tpmlp_mxfp4_quantize(W, None, None, *Wt, h, 2 * f, 2 * f)
+        T.tpmlp_mxfp4_swiglu_mlp_fwd(X, *Wt, None, *Bt, None, Z[i], None, ws, s, b, h, f, p)
+    T.tpmlp_device_status()
+    for i in range(40):
+        assert torch.equal(Z[i], want[i % 2]), i
+
+
 def test_bases_aligned_to_16_bytes_only(T, mode):
     """Every tensor 16 bytes into an allocation: 32-byte accesses must give way."""
     import torch
