@@ -128,14 +128,24 @@ struct MxProduct {
     MxOperand a, b;
     MxSpec g;
 };
-tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const DeviceInfo& dev, cudaStream_t st);
-// X [p][rows][cols / p] (row pitch ldx) -> (Q, S) along the columns and / or (Qt, St) along the rows; sums (bf16 with Qt,
-// or null): fp32 column sums over blocks of 32 rows [ceil(rows/32)][cols]
-tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows,
-                                   int64_t cols, int p, bool f32, cudaStream_t st, float* sums = nullptr);
-// out0[c] = sum over r of in0[r][c], and out1 from in1 (an output may be null, not both); fp32 or bf16 outputs
-tpmlp_status launch_mxfp4_sums(const float* in0, void* out0, int64_t cols0, const float* in1, void* out1, int64_t cols1, int64_t rows,
-                               bool f32, cudaStream_t st);
+// Column sums along with them: out[c] = sum over r of in[r][c], fp32 or bf16 outputs (either may be null).
+struct MxSums {
+    const float* in[2];
+    void* out[2];
+    int64_t cols[2];
+    int64_t rows;
+    bool f32;
+};
+tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const MxSums& sums, const DeviceInfo& dev, cudaStream_t st);
+namespace mx { struct SumsArgs; }
+tpmlp_status launch_mxfp4_sums(const mx::SumsArgs& a, cudaStream_t st);
+// X [p][rows][cols / p] (row pitch ldx) -> (Q, S) along the columns and / or (Qt, St) along the rows
+tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows, int64_t cols,
+                                   int p, bool f32, cudaStream_t st);
+// The gated backward's, bf16 [rows][cols]: dZ along both, with (or null) fp32 column sums over blocks of 32 rows
+// [ceil(rows/32)][cols], and X along the rows
+tpmlp_status launch_mxfp4_quantize_bwd(const void* dZ, void* Q, void* S, void* Qt, void* St, float* sums, const void* X, void* Xt,
+                                       void* XSt, int64_t rows, int64_t cols, cudaStream_t st);
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
                                      const DeviceInfo& dev, cudaStream_t st);
 // Process-wide kernel choice of the MXFP4 GEMM (see tpmlp_set_mxfp4_mode).

@@ -130,5 +130,32 @@ __device__ __forceinline__ uint32_t quantize32(const float (&v)[32], uint4& code
     return s;
 }
 
+// Column sums of up to two fp32 arrays [rows][cols] of partial sums, rounded to the output's type.
+struct SumsArgs {
+    const float* in[2];
+    void* out[2];
+    int cols[2];
+    int rows, f32;
+    int items0, items;  // items of 8 columns of the first array, of both
+};
+// One item, a warp: four lanes share a column, each takes every fourth row.  The order is fixed and does not depend
+// on who takes the item.
+__device__ __forceinline__ void sum_columns(const SumsArgs& a, int item, int lane) {
+    const int k = item >= a.items0, cols = a.cols[k];
+    const int c = (item - (k ? a.items0 : 0)) * 8 + (lane & 7);
+    float v = 0.0f;
+    if (c < cols) {
+        const float* src = a.in[k] + c;
+#pragma unroll 8
+        for (int r = lane >> 3; r < a.rows; r += 4) v += src[static_cast<long long>(r) * cols];
+    }
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+    if (lane < 8 && c < cols) {
+        if (a.f32) static_cast<float*>(a.out[k])[c] = v;
+        else static_cast<__nv_bfloat16*>(a.out[k])[c] = __float2bfloat16_rn(v);
+    }
+}
+
 }  // namespace mx
 }  // namespace tpmlp

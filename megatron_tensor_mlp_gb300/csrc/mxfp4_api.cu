@@ -275,9 +275,8 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const voi
     if (M == 0) return TPMLP_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool gf32 = grad_dt == TPMLP_F32;
-    TP_TRY(launch_mxfp4_quantize(dZ, h, w.dz.codes, w.dz.scales, w.dzt.codes, w.dzt.scales, M, h, 1, false, st,
-                                 db2 ? w.dz_sums : nullptr));
-    TP_TRY(launch_mxfp4_quantize(X, h, nullptr, nullptr, w.xt.codes, w.xt.scales, M, h, 1, false, st));
+    TP_TRY(launch_mxfp4_quantize_bwd(dZ, w.dz.codes, w.dz.scales, w.dzt.codes, w.dzt.scales, db2 ? w.dz_sums : nullptr, X, w.xt.codes,
+                                     w.xt.scales, M, h, st));
     // dY = dZ B^T; its epilogue leaves dH = [dg | du] quantised along both axes and Y along the tokens
     MxSpec g = mx_spec(M, ffn, h, EPI_DSWIGLU);
     g.h_in = H;
@@ -291,11 +290,11 @@ tpmlp_status tpmlp_mxfp4_swiglu_mlp_bwd(const void* X, const void* Wq, const voi
     g.yts = w.yt.scales;
     g.colsum = dbw_sh ? w.dh_sums : nullptr;
     TP_TRY(launch_mxfp4_gemm(w.dz.operand(), {Bq, Bs, ffn}, g, *dev, st));
-    if (dbw_sh || db2) TP_TRY(launch_mxfp4_sums(w.dh_sums, dbw_sh, 2 * ffn, w.dz_sums, db2, h, (M + 31) / 32, gf32, st));
     const MxProduct dB = product(w.yt.blocked(), w.dzt.operand(), nullptr, dB_sh, M, gf32, 0);
     const MxProduct dW = product(w.xt.operand(), w.dht.blocked(), nullptr, dW_sh, M, gf32, p > 1 ? 2 * ffn / p : 0);
     const MxProduct dx = product(w.dh.blocked(), {Wq, Ws, h}, nullptr, dX, 2 * ffn, dx_dt == TPMLP_F32, 0);
-    return launch_mxfp4_gemms({dB, dW, dx}, *dev, st);
+    const MxSums sums{{w.dh_sums, w.dz_sums}, {dbw_sh, db2}, {2 * ffn, h}, (M + 31) / 32, gf32};
+    return launch_mxfp4_gemms({dB, dW, dx}, sums, *dev, st);
 }
 
 tpmlp_status tpmlp_set_mxfp4_mode(int mode) {

@@ -319,7 +319,19 @@ tpmlp_status launch_mxfp4_gemm(const MxOperand& a, const MxOperand& b, const MxS
 // Independent plain products, in one launch of CTA pairs where that is expected to be faster than one after the
 // other: it saves their launches and their last waves.  (s=499 b=4 h1024 ffn4096, the backward's three products: 35 us
 // one by one; 4096 tokens, h5120, ffn20480: dX alone ends in a wave of 16 of 76 pairs that lasts 42 us.)
-tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const DeviceInfo& dev, cudaStream_t st) {
+// The column sums go with the pairs' launch (see the kernel) or into one ahead of the products.
+tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const MxSums& sums, const DeviceInfo& dev, cudaStream_t st) {
+    mx::SumsArgs sa{};
+    sa.rows = static_cast<int>(sums.rows);
+    sa.f32 = sums.f32;
+    for (int i = 0, n = 0; i < 2; ++i) {
+        if (sums.out[i] == nullptr) continue;
+        sa.in[n] = sums.in[i];
+        sa.out[n] = sums.out[i];
+        sa.cols[n++] = static_cast<int>(sums.cols[i]);
+        if (n == 1) sa.items0 = static_cast<int>((sums.cols[i] + 7) / 8);
+        sa.items += static_cast<int>((sums.cols[i] + 7) / 8);
+    }
     const int cap = pair_capacity<EPI_STORE, 3>(dev);
     mx::Args k[3];
     int order[3] = {0, 1, 2};
@@ -331,6 +343,10 @@ tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const DeviceInfo& dev, 
     }
     const int mode = g_mode.load(std::memory_order_relaxed);
     if (cap <= 0 || (mode != 0 && mode != 2) || (mode == 0 && kPairStart + together / cap + pair_tile_us(1) >= apart)) {
+        if (sa.items > 0) {
+            const tpmlp_status r = launch_mxfp4_sums(sa, st);
+            if (r != TPMLP_OK) return r;
+        }
         for (const MxProduct& x : c) {
             const tpmlp_status r = launch_mxfp4_gemm(x.a, x.b, x.g, dev, st);
             if (r != TPMLP_OK) return r;
@@ -349,6 +365,7 @@ tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const DeviceInfo& dev, 
         if (longest) all.n_long = i + 1;
         else if (all.skip == 0) all.skip = static_cast<int>(pair_tile_us(k[order[0]].kb) / pair_tile_us(k[order[i]].kb) + 0.5);
     }
+    all.sums = sa;
     const int clusters = std::min(all.long_tiles + all.short_tiles, cap);
     return launch(mx::mx_pair_kernel<EPI_STORE, 3>, 2 * clusters, mx::P_THREADS, mx::PairGeom<EPI_STORE>::smem, 2, st, all);
 }

@@ -395,6 +395,7 @@ struct Problems {
     int first[N];     // first tile of each product in its class
     int n_long;       // products of the long class
     int long_tiles, short_tiles, skip;
+    SumsArgs sums;    // N > 1: the block's bias gradients
 
     // Tile i of pair `c` of `n`: the product, its tile in t; -1 past the last.
     __device__ __forceinline__ int tile(int c, int n, int i, int& t) const {
@@ -695,6 +696,12 @@ __global__ void __launch_bounds__(P_THREADS, 1) mx_pair_kernel(const __grid_cons
         };
         if constexpr (EPI == EPI_DSWIGLU) {
             fetch_h(0, 0);
+        }
+        if constexpr (N > 1) {
+            // While the first tile's products run, these warps have nothing to do but the column sums, which would
+            // otherwise be a launch of their own between the kernels before and after.
+            for (int item = static_cast<int>(blockIdx.x) * 8 + warp - 4; item < all.sums.items; item += static_cast<int>(gridDim.x) * 8)
+                sum_columns(all.sums, item, lane);
         }
         int lt = 0;
         bool ok = true;

@@ -129,11 +129,10 @@ struct BothSmem {
 };
 
 // SUMS (bf16 ACROSS): also a.sums.
-template <bool F32, bool ACROSS, bool SUMS = false>
-__global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(const QuantArgs a) {
+template <bool F32, bool ACROSS, bool SUMS>
+__device__ __forceinline__ void quantize_tile(const QuantArgs& a, std::conditional_t<ACROSS, BothSmem<F32>, uint4>& sm) {
     using P = Piece<F32>;
     constexpr int TC = 256 / P::ES;
-    __shared__ __align__(16) std::conditional_t<ACROSS, BothSmem<F32>, uint4> sm;
     const int t = threadIdx.x, lane16 = t & 15, r0 = t >> 4;
     const long long total = static_cast<long long>(a.cols) * a.p;
     const unsigned col_tiles = static_cast<unsigned>(a.spans);
@@ -267,32 +266,29 @@ __global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(cons
     }
 }
 
-// Column sums of up to two fp32 arrays [rows][cols] of partial sums, in a fixed order, rounded to the
-// output's type: a CTA takes 32 columns, 32 warps every 32nd row each.
-struct SumsArgs {
-    const float* in[2];
-    void* out[2];
-    int cols[2];
-    int rows, blocks0;  // CTAs of the first array
-    int f32;
+template <bool F32, bool ACROSS>
+__global__ void __launch_bounds__(256, ACROSS ? 5 : 4) quantize_tile_kernel(const QuantArgs a) {
+    __shared__ __align__(16) std::conditional_t<ACROSS, BothSmem<F32>, uint4> sm;
+    quantize_tile<F32, ACROSS, false>(a, sm);
+}
+
+// Two bf16 matrices of one shape, along the rows and where wanted the columns, the first with sums where wanted.
+struct QuantPair {
+    QuantArgs of[2];
 };
-__global__ void __launch_bounds__(1024) finish_sums_kernel(const SumsArgs a) {
-    __shared__ float part[32][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int k = static_cast<int>(blockIdx.x) >= a.blocks0;
-    const int c = (blockIdx.x - (k ? a.blocks0 : 0)) * 32 + x;
+__global__ void __launch_bounds__(256, 5) quantize_pair_kernel(const __grid_constant__ QuantPair a) {
+    __shared__ __align__(16) BothSmem<false> sm;
+    const QuantArgs& m = a.of[blockIdx.y];
+    if (m.sums != nullptr) quantize_tile<false, true, true>(m, sm);
+    else quantize_tile<false, true, false>(m, sm);
+}
+
+// The column sums where no kernel of CTA pairs takes them along.
+__global__ void __launch_bounds__(256) finish_sums_kernel(const mx::SumsArgs a) {
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    float v = 0.0f;
-    if (c < a.cols[k])
-        for (int r = y; r < a.rows; r += 32) v += a.in[k][static_cast<long long>(r) * a.cols[k] + c];
-    part[y][x] = v;
-    __syncthreads();
-    if (y == 0 && c < a.cols[k]) {
-        for (int i = 1; i < 32; ++i) v += part[i][x];
-        if (a.f32) static_cast<float*>(a.out[k])[c] = v;
-        else static_cast<__nv_bfloat16*>(a.out[k])[c] = __float2bfloat16_rn(v);
-    }
+    const int item = static_cast<int>(blockIdx.x * 8 + (threadIdx.x >> 5));
+    if (item < a.items) mx::sum_columns(a, item, threadIdx.x & 31);
 }
 
 // Values of an operand: a warp takes U spans of 32 words (256 values) of a row, a word of eight codes a
@@ -352,11 +348,11 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restri
     }
 }
 
-template <int THREADS = 256, typename... P, typename... A>
+template <typename... P, typename... A>
 tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -374,6 +370,13 @@ tpmlp_status launch_pdl(const char* what, void (*kern)(P...), dim3 grid, cudaStr
 }
 
 template <bool F32>
+dim3 tile_grid(QuantArgs& a, int64_t cols) {
+    constexpr int TC = 256 / Piece<F32>::ES;
+    a.spans = (cols + 127) / 128 * (128 / TC);
+    return dim3(static_cast<unsigned>(a.spans * ((a.rows + 127LL) / 128)));
+}
+
+template <bool F32>
 tpmlp_status quantize(QuantArgs a, int64_t cols, cudaStream_t st) {
     const char* what = "MXFP4 quantisation";
     // Along the columns, few values: a span a warp spreads them over more warps than tiles of 128 rows do (bf16, 1 x
@@ -382,46 +385,37 @@ tpmlp_status quantize(QuantArgs a, int64_t cols, cudaStream_t st) {
         a.spans = F32 ? (cols + 127) / 128 : (cols + 255) / 256;  // of 512 bytes, whole scale tiles
         return launch_pdl(what, quantize_rows_kernel<F32>, dim3(static_cast<unsigned>((a.spans * a.rows + 7) / 8)), st, a);
     }
-    constexpr int TC = 256 / Piece<F32>::ES;
-    a.spans = (cols + 127) / 128 * (128 / TC);
-    const dim3 grid(static_cast<unsigned>(a.spans * ((a.rows + 127LL) / 128)));
-    if constexpr (!F32) {
-        if (a.sums != nullptr) return launch_pdl(what, quantize_tile_kernel<false, true, true>, grid, st, a);
-    }
+    const dim3 grid = tile_grid<F32>(a, cols);
     return a.qt == nullptr ? launch_pdl(what, quantize_tile_kernel<F32, false>, grid, st, a)
                            : launch_pdl(what, quantize_tile_kernel<F32, true>, grid, st, a);
 }
 
+QuantArgs quant_args(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows, int64_t cols, int p, int64_t es,
+                     float* sums) {
+    return {static_cast<const uint8_t*>(X), ldx * es, rows * ldx * es, static_cast<int>(rows), static_cast<int>(cols / p), p,
+            static_cast<uint8_t*>(Q), static_cast<uint8_t*>(S), static_cast<uint8_t*>(Qt), static_cast<uint8_t*>(St), sums, 0};
+}
+
 }  // namespace
 
-tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows,
-                                   int64_t cols, int p, bool f32, cudaStream_t st, float* sums) {
-    const int64_t es = f32 ? 4 : 2;
-    const QuantArgs a{static_cast<const uint8_t*>(X), ldx * es, rows * ldx * es, static_cast<int>(rows),
-                      static_cast<int>(cols / p), p, static_cast<uint8_t*>(Q), static_cast<uint8_t*>(S),
-                      static_cast<uint8_t*>(Qt), static_cast<uint8_t*>(St), sums, 0};
+tpmlp_status launch_mxfp4_quantize(const void* X, int64_t ldx, void* Q, void* S, void* Qt, void* St, int64_t rows, int64_t cols,
+                                   int p, bool f32, cudaStream_t st) {
+    const QuantArgs a = quant_args(X, ldx, Q, S, Qt, St, rows, cols, p, f32 ? 4 : 2, nullptr);
     return f32 ? quantize<true>(a, cols, st) : quantize<false>(a, cols, st);
 }
 
-tpmlp_status launch_mxfp4_sums(const float* in0, void* out0, int64_t cols0, const float* in1, void* out1, int64_t cols1, int64_t rows,
-                               bool f32, cudaStream_t st) {
-    SumsArgs a{};
-    int n = 0;
-    const int64_t blocks[2] = {out0 ? (cols0 + 31) / 32 : 0, out1 ? (cols1 + 31) / 32 : 0};
-    if (out0) {
-        a.in[n] = in0;
-        a.out[n] = out0;
-        a.cols[n++] = static_cast<int>(cols0);
-    }
-    if (out1) {
-        a.in[n] = in1;
-        a.out[n] = out1;
-        a.cols[n++] = static_cast<int>(cols1);
-    }
-    a.rows = static_cast<int>(rows);
-    a.blocks0 = static_cast<int>(out0 ? blocks[0] : blocks[1]);
-    a.f32 = f32;
-    return launch_pdl<1024>("column sums", finish_sums_kernel, dim3(static_cast<unsigned>(blocks[0] + blocks[1])), st, a);
+tpmlp_status launch_mxfp4_quantize_bwd(const void* dZ, void* Q, void* S, void* Qt, void* St, float* sums, const void* X, void* Xt,
+                                       void* XSt, int64_t rows, int64_t cols, cudaStream_t st) {
+    QuantPair a{{quant_args(dZ, cols, Q, S, Qt, St, rows, cols, 1, 2, sums),
+                 quant_args(X, cols, nullptr, nullptr, Xt, XSt, rows, cols, 1, 2, nullptr)}};
+    dim3 grid = tile_grid<false>(a.of[0], cols);
+    a.of[1].spans = a.of[0].spans;
+    grid.y = 2;
+    return launch_pdl("MXFP4 quantisation", quantize_pair_kernel, grid, st, a);
+}
+
+tpmlp_status launch_mxfp4_sums(const mx::SumsArgs& a, cudaStream_t st) {
+    return launch_pdl("column sums", finish_sums_kernel, dim3(static_cast<unsigned>((a.items + 7) / 8)), st, a);
 }
 
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
