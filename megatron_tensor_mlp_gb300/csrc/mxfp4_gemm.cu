@@ -186,7 +186,8 @@ tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec&
 //   split    the same of kb / split, and 1.5 (one CTA an SM) or 2.3 (two) log2(split) for the exchange
 // The choice costs at most 10 % against the best of them.  For example 512 x 5120 x 20480: pairs 26.7, single 33.7,
 // split two ways 41.6; 800 rows: single 35.9, pairs 48.2 (80 tiles, two waves); 64 x 5120 x 20480: split four ways
-// 15.7, single 25.8, pairs 25.3; 333 x 4096 x 16384: split two ways 19.5, pairs 22.1, single 25.1.
+// 15.7, single 25.8, pairs 25.3; 333 x 4096 x 16384: split two ways 19.5, pairs 22.1, single 25.1.  Split three ways:
+// 200 x 5120 x 20480 20.4 (two ways 22.6, pairs 26.2), 640 x 1024 x 8192 10.3 (two 11.0, four 13.2).
 // At most 32 rows: single CTAs, which copy no more rows of A than there are (4 x 40960 x 5120: 23 against 31).
 struct Choice {
     bool pair;
@@ -201,12 +202,18 @@ Choice choose(const MxSpec& g, int kb, int cap, int sms) {
     const int64_t tiles2 = ((g.M + 255) / 256) * ((g.N + 255) / 256);
     const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
     Choice c{false, 1, 0.0};
-    for (int s = 1, log = 0; s <= 8; s *= 2, ++log) {
-        // (40 tiles split four ways are 160 CTAs on 152 SMs: a few SMs with two cost little)
-        const bool one = tiles1 * s <= sms + sms / 16;
-        if (s > 1 && (tiles1 * s > 2 * sms || !split_fits<EPI, 2>(s, rows, kb))) break;
-        const int64_t waves = (tiles1 * s + 2 * sms - 1) / (2 * sms);
-        const double k = static_cast<double>(kb) / s;
+    for (int s : {1, 2, 3, 4, 8}) {
+        const int64_t ctas = tiles1 * s;
+        if (s > 1 && (ctas > 2 * sms || !split_fits<EPI, 2>(s, rows, kb))) break;
+        // (40 tiles split four ways are 160 CTAs on 152 SMs: with few rows a few SMs with two cost little)
+        bool one = ctas <= sms + (g.M <= 64 ? sms / 16 : 0);
+        if (s == 3) {
+            // clusters of three leave SMs of a GPC over, and a third of the columns' owners get twice the exchange
+            one = ctas <= sms * 4 / 5;
+            if (ctas > sms * 8 / 5) continue;
+        }
+        const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
+        const double k = static_cast<double>(kb) / s, log = s == 3 ? 1.6 : s == 8 ? 3.0 : s / 2;
         const double t = one ? 4.0 + 0.34 * k + 1.5 * log : waves <= 1 ? 5.3 + 0.38 * k + 2.3 * log : 2.5 + waves * (0.38 * k + 3.0);
         if (s == 1 || t < c.us) {
             c.us = t;

@@ -261,6 +261,54 @@ def test_product_many_tiles_and_repeats(T):
         R.assert_product(host(outs[0]), a, b, None, False, f"mode {md}")
 
 
+@pytest.mark.parametrize("m,n,k", [(640, 1024, 8192), (150, 2500, 8000)])
+def test_product_of_long_rows_and_few_tiles(T, m, n, k):
+    """K split over the CTAs of a cluster, also three ways."""
+    import torch
+    rng = np.random.default_rng(m)
+    aq, as_, a = operand(T, rng.standard_normal((m, k)))
+    bq, bs, b = operand(T, rng.standard_normal((n, k)))
+    outs = []
+    for _ in range(2):
+        D = torch.full((m + 1, n), 7.0, device="cuda")
+        T.tpmlp_mxfp4_matmul(aq, as_, bq, bs, None, D, m, n, k, T.F32)
+        T.tpmlp_device_status()
+        assert bool((D[m] == 7.0).all())
+        outs.append(D[:m])
+    assert torch.equal(outs[0], outs[1])
+    R.assert_product(host(outs[0]), a, b, None, False, "auto")
+
+
+@pytest.mark.parametrize("shape", [(128, 1, 4096, 2560, 1), (100, 1, 4096, 5120, 2)], ids=lambda s: "s{}b{}h{}f{}p{}".format(*s))
+def test_block_of_long_rows_and_few_tiles(T, shape):
+    """The gated epilogues behind a K loop split over a cluster, also three ways, against the same without a split.
+    Sums in another order move a value by some 2^-20 of its size; one in 10^5 then falls on the other side of a
+    rounding boundary of the 4-bit grid, a third of its size away: norms agree to sqrt(1e-5) / 3, 0.1 %; three times that."""
+    import torch
+    s, b, h, f, p = shape
+    M = s * b
+    d = make_block(T, *shape, seed=f)
+    H = torch.randn((M, 2 * f), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(torch.bfloat16)
+    new = lambda *shp: torch.full(shp, float("nan"), device="cuda")  # noqa: E731
+    outs = []
+    for md in (1, 0):
+        Z, dX, dW, dB = new(M, h), new(M, h), new(p, h, 2 * f // p), new(f, h)
+        Hs, dbw, db2 = torch.empty((M, 2 * f), dtype=torch.bfloat16, device="cuda"), new(2 * f), new(h)
+        T.tpmlp_set_mxfp4_mode(md)
+        try:
+            ws, _ = workspace(T, *shape, 0)
+            T.tpmlp_mxfp4_swiglu_mlp_fwd(d["X"], *d["Wt"], d["bw"], *d["Bt"], d["b2"], Z, Hs, ws, *shape, z_dt=T.F32)
+            ws, _ = workspace(T, *shape, 1)
+            T.tpmlp_mxfp4_swiglu_mlp_bwd(d["X"], *d["Wn"], *d["Bn"], H, d["dZ"], dX, dW, dB, dbw, db2, ws, *shape, dx_dt=T.F32)
+            T.tpmlp_device_status()
+        finally:
+            T.tpmlp_set_mxfp4_mode(0)
+        outs.append((Z, Hs, dX, dW, dB, dbw, db2))
+    for name, x, y in zip(("Z", "H", "dX", "dW", "dB", "dbw", "db2"), *outs):
+        off = float((x.double() - y.double()).norm() / x.double().norm())
+        assert off <= 3e-3, (name, off)
+
+
 def test_product_nan_block_reaches_its_row_only(T, mode):
     import torch
     m, n, k = 40, 128, 512
