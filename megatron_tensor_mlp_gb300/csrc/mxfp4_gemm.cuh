@@ -118,6 +118,8 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
 }
 
 // ---------------------------------------------------------------- epilogues
+// (Biases are read by ordinary loads: the kernel ahead in the stream may write them while this one is resident, which
+// a non-coherent load does not allow.)
 // EPI_STORE: 32 consecutive columns of a row.
 __device__ __forceinline__ void store_chunk(const Args& p, float (&v)[32], int gm, int gn0) {
     const int nvalid = p.N - gn0;
@@ -128,7 +130,7 @@ __device__ __forceinline__ void store_chunk(const Args& p, float (&v)[32], int g
             const __nv_bfloat16* bp = p.bias + gn0 + g * 8;
             if ((g + 1) * 8 <= nvalid) {
                 float b[8];
-                tc::unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(bp)), b);
+                tc::unpack_bf16x8(*reinterpret_cast<const uint4*>(bp), b);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[g * 8 + i] += b[i];
             } else if (g * 8 < nvalid) {  // fp32 rows may end on a multiple of 4
@@ -162,8 +164,8 @@ __device__ __forceinline__ uint32_t swiglu_chunk(const Args& p, float (&g)[32], 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float bg[8], bu[8];
-            tc::unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.bias + pg + j * 8)), bg);
-            tc::unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.bias + pg + 128 + j * 8)), bu);
+            tc::unpack_bf16x8(*reinterpret_cast<const uint4*>(p.bias + pg + j * 8), bg);
+            tc::unpack_bf16x8(*reinterpret_cast<const uint4*>(p.bias + pg + 128 + j * 8), bu);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 g[j * 8 + i] += bg[i];

@@ -292,10 +292,11 @@ __global__ void __launch_bounds__(256) finish_sums_kernel(const mx::SumsArgs a) 
 }
 
 // Values of an operand: a warp takes U spans of 32 words (256 values) of a row, a word of eight codes a
-// lane, all loaded before the first is worked on.
+// lane, all loaded before the first is worked on.  Ordinary loads: the quantiser ahead may still be writing q and s when
+// this kernel becomes resident, which a non-coherent load does not allow.
 template <bool F32, int U>
-__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s, void* out,
-                                                         long long rows, long long k, long long spans) {
+__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* q, const uint8_t* s, void* out, long long rows,
+                                                         long long k, long long spans) {
     const int lane = threadIdx.x & 31;
     const long long pitch = (k + 31) / 32 * 16, k_tiles = (k + 127) / 128, words = (k + 7) / 8;
     const long long it0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * U;
@@ -309,8 +310,8 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* __restri
         rw[i] = row;
         w[i] = row < rows ? span * 32 + lane : words;
         if (w[i] < words) {
-            c[i] = __ldg(reinterpret_cast<const uint32_t*>(q + row * pitch) + w[i]);
-            sb[i] = __ldg(s + mx::scale_offset(row, w[i] >> 2, k_tiles));
+            c[i] = reinterpret_cast<const uint32_t*>(q + row * pitch)[w[i]];
+            sb[i] = s[mx::scale_offset(row, w[i] >> 2, k_tiles)];
         }
         if (++span == spans) {
             span = 0;
