@@ -33,7 +33,6 @@ class GatedMLP:
         # W as the operand of X W and of dH W^T, B as that of Y B and of dZ B^T
         self.Wt, self.Wn = T.mxfp4_empty(2 * f, h), T.mxfp4_empty(h, 2 * f)
         self.Bt, self.Bn = T.mxfp4_empty(h, f), T.mxfp4_empty(f, h)
-        self._spaces = {}
         self.load(gate, up, down)
 
     def load(self, gate, up, down):
@@ -45,10 +44,10 @@ class GatedMLP:
         T.tpmlp_mxfp4_quantize(self.B, *self.Bn, *self.Bt, f, h, h)
 
     def _workspace(self, tokens, backward):
+        """Scratch of one call.  Each call has its own: two calls on different streams, or from different threads, may run
+        at the same time.  (The allocator reuses the memory behind this stream's work only, and costs about a microsecond.)"""
         n = T.tpmlp_mxfp4_swiglu_ws_bytes(tokens, 1, self.h, self.ffn, self.p, backward)
-        if n > self._spaces.get(backward, torch.empty(0)).numel():
-            self._spaces[backward] = torch.empty(n, dtype=torch.uint8, device=self.B.device)
-        return self._spaces[backward]
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.B.device)  # (a shape that is refused gives -1)
 
     def forward(self, X, save: bool = False):
         """X [tokens, h] bf16 -> Z; with save also the pre-activations that backward needs."""

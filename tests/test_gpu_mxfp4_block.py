@@ -1,0 +1,56 @@
+"""The example block (mxfp4_block.GatedMLP) on the GPU."""
+import numpy as np
+import pytest
+
+import gpu_util as U
+import mxfp4_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def Block():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from megatron_tensor_mlp_gb300 import mxfp4_block
+    return mxfp4_block.GatedMLP
+
+
+def normal(seed, *shape, scale=1.0):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(torch.bfloat16)
+
+
+def make(Block, h, f, seed=0, **kw):
+    return Block(normal(seed, h, f, scale=h ** -0.5), normal(seed + 1, h, f, scale=h ** -0.5), normal(seed + 2, f, h, scale=f ** -0.5), **kw)
+
+
+def host(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def test_two_streams_use_one_block(Block):
+    """Forwards and backwards of one object on two streams at a time give what each gives alone."""
+    import torch
+    m = make(Block, 512, 2048)
+    X = [normal(10 + i, 700 + 400 * i, 512) for i in range(2)]
+    dZ = [normal(20 + i, 700 + 400 * i, 512) for i in range(2)]
+
+    def both(i):
+        Z, H = m.forward(X[i], save=True)
+        return [Z, H, *m.backward(X[i], H, dZ[i])]
+
+    want = [both(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(both(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(outs, want[i]))
