@@ -54,13 +54,16 @@ class GatedMLP:
         m = X.shape[0]
         Z = torch.empty_like(X)
         H = torch.empty((m, 2 * self.ffn), dtype=torch.bfloat16, device=X.device) if save else None
-        T.tpmlp_mxfp4_swiglu_mlp_fwd(X, *self.Wt, self.bw, *self.Bt, self.b2, Z, H, self._workspace(m, 0), m, 1, self.h,
-                                     self.ffn, self.p)
+        if m > 0:  # (an empty tensor has no address to pass)
+            T.tpmlp_mxfp4_swiglu_mlp_fwd(X, *self.Wt, self.bw, *self.Bt, self.b2, Z, H, self._workspace(m, 0), m, 1, self.h,
+                                         self.ffn, self.p)
         return (Z, H) if save else Z
 
     def backward(self, X, H, dZ):
         """The gradients of X (bf16) and of gate, up and down (fp32)."""
         m, h, f, p = X.shape[0], self.h, self.ffn, self.p
+        if m == 0:
+            return torch.empty_like(X), *(torch.zeros(s, device=X.device) for s in ((h, f), (h, f), (f, h)))
         dX = torch.empty_like(X)
         dW = torch.empty((p, h, 2 * f // p), device=X.device)
         dB = torch.empty((f, h), device=X.device)

@@ -54,3 +54,12 @@ def test_two_streams_use_one_block(Block):
     for i in range(2):
         for outs in got[i]:
             assert all(torch.equal(x, y) for x, y in zip(outs, want[i]))
+
+
+def test_no_tokens(Block):
+    m = make(Block, 256, 512)
+    X = normal(3, 4, 256)[:0]
+    Z, H = m.forward(X, save=True)
+    grads = m.backward(X, H, X)
+    assert Z.shape == (0, 256) and H.shape == (0, 1024) and grads[0].shape == (0, 256)
+    assert all(not bool(g.any()) for g in grads[1:])

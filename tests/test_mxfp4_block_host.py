@@ -47,3 +47,18 @@ def test_every_call_has_a_workspace_of_its_own(calls):
     assert [s.numel() for s in spaces] == ([T.tpmlp_mxfp4_swiglu_ws_bytes(5, 1, H, F, 1, 0)] * 3
                                            + [T.tpmlp_mxfp4_swiglu_ws_bytes(5, 1, H, F, 1, 1)] * 3)
     assert len({s.data_ptr() for s in spaces}) == 6
+
+
+def test_no_tokens(calls):
+    """An empty batch is a batch: no output rows, gradients of zero, nothing launched (an empty tensor's address is NULL,
+    which the entry points refuse)."""
+    m = block()
+    del calls[:]
+    X = bf16(0, H)
+    Z, Hs = m.forward(X, save=True)
+    assert Z.shape == (0, H) and Hs.shape == (0, 2 * F) and m.forward(X).shape == (0, H)
+    dX, dG, dU, dB = m.backward(X, Hs, X)
+    assert not calls
+    assert dX.shape == (0, H) and dX.dtype == torch.bfloat16
+    for d, shape in ((dG, (H, F)), (dU, (H, F)), (dB, (F, H))):
+        assert d.shape == shape and d.dtype == torch.float32 and not d.any()
