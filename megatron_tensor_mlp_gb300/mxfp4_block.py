@@ -25,23 +25,24 @@ class GatedMLP:
         h, f = self.h, self.ffn
         self.W = torch.empty((p, h, 2 * f // p), dtype=torch.bfloat16, device=gate.device)
         self.B = torch.empty((f, h), dtype=torch.bfloat16, device=gate.device)
-        self.bw = None
-        if bias_gate is not None:
-            self.bw = torch.empty(2 * f, dtype=torch.bfloat16, device=gate.device)
-            T.tpmlp_swiglu_pack(bias_gate, bias_up, self.bw, 1, f, p)
-        self.b2 = bias_down
+        self.bw = self.b2 = None
         # W as the operand of X W and of dH W^T, B as that of Y B and of dZ B^T
         self.Wt, self.Wn = T.mxfp4_empty(2 * f, h), T.mxfp4_empty(h, 2 * f)
         self.Bt, self.Bn = T.mxfp4_empty(h, f), T.mxfp4_empty(f, h)
-        self.load(gate, up, down)
+        self.load(gate, up, down, bias_gate, bias_up, bias_down)
 
-    def load(self, gate, up, down):
-        """Takes new weights (bf16) and lays out their MXFP4 operands for both directions."""
+    def load(self, gate, up, down, bias_gate=None, bias_up=None, bias_down=None):
+        """Takes new weights (bf16) and lays out their MXFP4 operands for both directions; biases where given."""
         h, f, p = self.h, self.ffn, self.p
         T.tpmlp_swiglu_pack(gate, up, self.W, h, f, p)
         self.B.copy_(down)
         T.tpmlp_mxfp4_quantize(self.W, *self.Wn, *self.Wt, h, 2 * f, 2 * f // p, p)
         T.tpmlp_mxfp4_quantize(self.B, *self.Bn, *self.Bt, f, h, h)
+        if bias_gate is not None:
+            self.bw = torch.empty(2 * f, dtype=torch.bfloat16, device=gate.device)
+            T.tpmlp_swiglu_pack(bias_gate, bias_up, self.bw, 1, f, p)
+        if bias_down is not None:
+            self.b2 = bias_down
 
     def _workspace(self, tokens, backward):
         """Scratch of one call.  Each call has its own: two calls on different streams, or from different threads, may run
@@ -60,17 +61,26 @@ class GatedMLP:
         return (Z, H) if save else Z
 
     def backward(self, X, H, dZ):
-        """The gradients of X (bf16) and of gate, up and down (fp32)."""
+        """The gradients of X (bf16) and, fp32, of gate, up, down and, in this order, of the biases that the block has."""
         m, h, f, p = X.shape[0], self.h, self.ffn, self.p
-        if m == 0:
-            return torch.empty_like(X), *(torch.zeros(s, device=X.device) for s in ((h, f), (h, f), (f, h)))
+        if m == 0:  # (an empty tensor has no address to pass)
+            shapes = [(h, f), (h, f), (f, h)] + ([] if self.bw is None else [(f,), (f,)]) + ([] if self.b2 is None else [(h,)])
+            return torch.empty_like(X), *(torch.zeros(s, device=X.device) for s in shapes)
         dX = torch.empty_like(X)
-        dW = torch.empty((p, h, 2 * f // p), device=X.device)
-        dB = torch.empty((f, h), device=X.device)
-        T.tpmlp_mxfp4_swiglu_mlp_bwd(X, *self.Wn, *self.Bn, H, dZ, dX, dW, dB, None, None, self._workspace(m, 1), m, 1, h, f, p)
-        dG, dU = torch.empty((h, f), device=X.device), torch.empty((h, f), device=X.device)
-        T.tpmlp_swiglu_pack(dG, dU, dW, h, f, p, T.F32, inverse=1)
-        return dX, dG, dU, dB
+        dW, dB = torch.empty((p, h, 2 * f // p), device=X.device), torch.empty((f, h), device=X.device)
+        dbw = None if self.bw is None else torch.empty(2 * f, device=X.device)
+        db2 = None if self.b2 is None else torch.empty(h, device=X.device)
+        T.tpmlp_mxfp4_swiglu_mlp_bwd(X, *self.Wn, *self.Bn, H, dZ, dX, dW, dB, dbw, db2, self._workspace(m, 1), m, 1, h, f, p)
+        grads = (dX, *self._unpack(dW, h), dB)
+        if dbw is not None:
+            grads += tuple(v.view(f) for v in self._unpack(dbw, 1))
+        return grads if db2 is None else (*grads, db2)
+
+    def _unpack(self, packed, rows):
+        """The gate and up halves [rows, ffn] of an fp32 tensor in the shard layout."""
+        G, U = (torch.empty((rows, self.ffn), device=packed.device) for _ in range(2))
+        T.tpmlp_swiglu_pack(G, U, packed, rows, self.ffn, self.p, T.F32, inverse=1)
+        return G, U
 
 
 def train_and_serve(tokens=512, h=256, ffn=1024, p=2, steps=40, lr=0.5, seed=0, log=None):

@@ -63,3 +63,32 @@ def test_no_tokens(Block):
     grads = m.backward(X, H, X)
     assert Z.shape == (0, 256) and H.shape == (0, 1024) and grads[0].shape == (0, 256)
     assert all(not bool(g.any()) for g in grads[1:])
+
+
+@pytest.mark.parametrize("p", [1, 2])
+def test_gradients_with_biases(Block, p):
+    """All gradients of a block with biases against the 64-bit reference; the biases' are used in a step of descent."""
+    import torch
+    h, f, m = 256, 512, 150
+    bias = dict(bias_gate=normal(6, f, scale=0.3), bias_up=normal(7, f, scale=0.3), bias_down=normal(8, h, scale=0.3))
+    blk = make(Block, h, f, p=p, **bias)
+    X, dZ = normal(4, m, h), normal(5, m, h)
+    Z, H = blk.forward(X, save=True)
+    dX, dG, dU, dB, dbg, dbu, db2 = blk.backward(X, H, dZ)
+    w = host(blk.W.transpose(0, 1).reshape(h, 2 * f))
+    packed = R.join(host(bias["bias_gate"])[None], host(bias["bias_up"])[None])[0]
+    Zr, Hr = R.block_fwd(host(X), R.q(w.T), R.q(host(blk.B).T), packed, host(bias["bias_down"]))
+    U.assert_close(host(Z), Zr, "bf16", "Z")
+    ref = R.block_bwd(host(X), R.q(w), R.q(host(blk.B)), host(H), host(dZ))
+    for name, got, want in (("dX", dX, ref[0]), ("dB", dB, ref[2]), ("db2", db2, ref[4])):
+        U.assert_close(host(got), want, "bf16", name)
+    for name, got, want in zip(("dG", "dU"), (dG, dU), R.split(ref[1])):
+        U.assert_close(host(got), want, "bf16", name)
+    for name, got, want in zip(("dbg", "dbu"), (dbg, dbu), R.split(ref[3][None])):
+        U.assert_close(host(got)[None], want, "bf16", name)
+    weights = (normal(0, h, f, scale=h ** -0.5), normal(1, h, f, scale=h ** -0.5), normal(2, f, h, scale=f ** -0.5))
+    loss = lambda: float((blk.forward(X).double() * dZ.double()).sum())  # noqa: E731
+    before = loss()
+    step = {k: (v.float() - 0.01 * g).to(torch.bfloat16) for (k, v), g in zip(bias.items(), (dbg, dbu, db2))}
+    blk.load(*weights, **step)
+    assert loss() < before

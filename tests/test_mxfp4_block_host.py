@@ -62,3 +62,37 @@ def test_no_tokens(calls):
     assert dX.shape == (0, H) and dX.dtype == torch.bfloat16
     for d, shape in ((dG, (H, F)), (dU, (H, F)), (dB, (F, H))):
         assert d.shape == shape and d.dtype == torch.float32 and not d.any()
+
+
+def biases():
+    return dict(bias_gate=bf16(F), bias_up=bf16(F), bias_down=bf16(H))
+
+
+def test_gradients_of_the_biases(calls):
+    """A block with biases asks for their gradients and returns them, in the constructor's order."""
+    X = bf16(5, H)
+    m = block(**biases(), p=2)
+    Z, Hs = m.forward(X, save=True)
+    grads = m.backward(X, Hs, X)
+    dbw, db2 = of(calls, "tpmlp_mxfp4_swiglu_mlp_bwd")[0][10:12]
+    assert dbw.numel() == 2 * F and db2.numel() == H and dbw.dtype == db2.dtype == torch.float32
+    assert [tuple(g.shape) for g in grads] == [(5, H), (H, F), (H, F), (F, H), (F,), (F,), (H,)]
+    assert grads[6].data_ptr() == db2.data_ptr()
+    unpack = of(calls, "tpmlp_swiglu_pack")[-1]  # (G, U, packed, rows, ffn, p, ...)
+    assert [t.data_ptr() for t in unpack[:3]] == [grads[4].data_ptr(), grads[5].data_ptr(), dbw.data_ptr()] and unpack[3:6] == (1, F, 2)
+    assert [tuple(g.shape) for g in m.backward(X[:0], Hs[:0], X[:0])] == [(0, H)] + [tuple(g.shape) for g in grads[1:]]
+    # only some of them
+    assert len(block(bias_down=bf16(H)).backward(X, Hs, X)) == 5
+    assert len(block(bias_gate=bf16(F), bias_up=bf16(F)).backward(X, Hs, X)) == 6
+    assert len(block().backward(X, Hs, X)) == 4
+
+
+def test_new_biases_are_taken(calls):
+    m = block(**biases())
+    new = biases()
+    m.load(bf16(H, F), bf16(H, F), bf16(F, H), **new)
+    X = bf16(5, H)
+    m.forward(X)
+    pack = of(calls, "tpmlp_swiglu_pack")[-1]
+    args = of(calls, "tpmlp_mxfp4_swiglu_mlp_fwd")[-1]
+    assert pack[0] is new["bias_gate"] and pack[1] is new["bias_up"] and args[3] is pack[2] and args[6] is new["bias_down"]
