@@ -21,8 +21,10 @@ class GatedMLP:
 
     def __init__(self, gate, up, down, bias_gate=None, bias_up=None, bias_down=None, p: int = 1):
         """gate, up [h, ffn], down [ffn, h] and the biases: bf16 on the GPU.  p: tensor-parallel shards."""
-        self.h, self.ffn, self.p = gate.shape[0], gate.shape[1], p
+        self.h, self.ffn, self.p = gate.shape[0], gate.shape[-1], p
         h, f = self.h, self.ffn
+        self.device = gate.device
+        self._check_weights(gate, up, down, bias_gate, bias_up, bias_down)
         self.W = torch.empty((p, h, 2 * f // p), dtype=torch.bfloat16, device=gate.device)
         self.B = torch.empty((f, h), dtype=torch.bfloat16, device=gate.device)
         self.bw = self.b2 = None
@@ -34,6 +36,7 @@ class GatedMLP:
     def load(self, gate, up, down, bias_gate=None, bias_up=None, bias_down=None):
         """Takes new weights (bf16) and lays out their MXFP4 operands for both directions; biases where given."""
         h, f, p = self.h, self.ffn, self.p
+        self._check_weights(gate, up, down, bias_gate, bias_up, bias_down)
         T.tpmlp_swiglu_pack(gate, up, self.W, h, f, p)
         self.B.copy_(down)
         T.tpmlp_mxfp4_quantize(self.W, *self.Wn, *self.Wt, h, 2 * f, 2 * f // p, p)
@@ -44,15 +47,34 @@ class GatedMLP:
         if bias_down is not None:
             self.b2 = bias_down
 
+    def _check(self, name, t, *shape):
+        """The entry points take addresses: a tensor of another form would be read as if it were this one."""
+        if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 tensor {list(shape)} on {self.device}, not {t.dtype} {list(t.shape)} "
+                             f"with strides {list(t.stride())} on {t.device}")
+
+    def _check_weights(self, gate, up, down, bias_gate, bias_up, bias_down):
+        h, f = self.h, self.ffn
+        self._check("gate", gate, h, f)
+        self._check("up", up, h, f)
+        if tuple(down.shape) != (f, h):  # (copied, whatever its type and strides)
+            raise ValueError(f"down must be [{f}, {h}], not {list(down.shape)}")
+        if (bias_gate is None) != (bias_up is None):
+            raise ValueError("bias_gate and bias_up come together")
+        for name, b, n in (("bias_gate", bias_gate, f), ("bias_up", bias_up, f), ("bias_down", bias_down, h)):
+            if b is not None:
+                self._check(name, b, n)
+
     def _workspace(self, tokens, backward):
         """Scratch of one call.  Each call has its own: two calls on different streams, or from different threads, may run
         at the same time.  (The allocator reuses the memory behind this stream's work only, and costs about a microsecond.)"""
         n = T.tpmlp_mxfp4_swiglu_ws_bytes(tokens, 1, self.h, self.ffn, self.p, backward)
-        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.B.device)  # (a shape that is refused gives -1)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)  # (a shape that is refused gives -1)
 
     def forward(self, X, save: bool = False):
         """X [tokens, h] bf16 -> Z; with save also the pre-activations that backward needs."""
         m = X.shape[0]
+        self._check("X", X, m, self.h)
         Z = torch.empty_like(X)
         H = torch.empty((m, 2 * self.ffn), dtype=torch.bfloat16, device=X.device) if save else None
         if m > 0:  # (an empty tensor has no address to pass)
@@ -63,6 +85,9 @@ class GatedMLP:
     def backward(self, X, H, dZ):
         """The gradients of X (bf16) and, fp32, of gate, up, down and, in this order, of the biases that the block has."""
         m, h, f, p = X.shape[0], self.h, self.ffn, self.p
+        self._check("X", X, m, h)
+        self._check("H", H, m, 2 * f)
+        self._check("dZ", dZ, m, h)
         if m == 0:  # (an empty tensor has no address to pass)
             shapes = [(h, f), (h, f), (f, h)] + ([] if self.bw is None else [(f,), (f,)]) + ([] if self.b2 is None else [(h,)])
             return torch.empty_like(X), *(torch.zeros(s, device=X.device) for s in shapes)

@@ -96,3 +96,37 @@ def test_new_biases_are_taken(calls):
     pack = of(calls, "tpmlp_swiglu_pack")[-1]
     args = of(calls, "tpmlp_mxfp4_swiglu_mlp_fwd")[-1]
     assert pack[0] is new["bias_gate"] and pack[1] is new["bias_up"] and args[3] is pack[2] and args[6] is new["bias_down"]
+
+
+def test_tensors_of_another_form_are_refused(calls):
+    """The entry points take addresses: a tensor of another type, shape or stride would be read as if it were the right
+    one, past its end at worst.  Nothing is called with one."""
+    m = block(**biases())
+    X = bf16(5, H)
+    Z, Hs = m.forward(X, save=True)
+    good = dict(X=X, H=Hs, dZ=X)
+    del calls[:]
+    wrong = [X.float(), X.half(), bf16(5, 2 * H)[:, :H], bf16(1, H).expand(5, H), bf16(H, 5).t(), bf16(5, H + 8), bf16(5 * H), bf16(5, 1, H),
+             torch.zeros(5, H, dtype=torch.bfloat16, device="meta")]
+    for bad in wrong:
+        with pytest.raises(ValueError):
+            m.forward(bad)
+        for name in ("X", "dZ"):
+            with pytest.raises(ValueError):
+                m.backward(**{**good, name: bad})
+    for bad in (bf16(4, 2 * F), Hs.float(), bf16(5, F), bf16(1, 2 * F).expand(5, 2 * F)):
+        with pytest.raises(ValueError):
+            m.backward(X, bad, X)
+    with pytest.raises(ValueError):
+        m.backward(X, Hs, bf16(4, H))
+    weights = dict(gate=bf16(H, F), up=bf16(H, F), down=bf16(F, H), **biases())
+    for name, bad in (("gate", bf16(H, F).float()), ("gate", bf16(F, H).t()), ("up", bf16(H, F + 8)), ("up", bf16(F, H)), ("down", bf16(1, H)),
+                      ("bias_gate", torch.zeros(F)), ("bias_up", bf16(F - 8)), ("bias_up", None), ("bias_gate", None),
+                      ("bias_down", bf16(2 * H)[::2])):
+        with pytest.raises(ValueError):
+            m.load(**{**weights, name: bad})
+        with pytest.raises(ValueError):
+            mxfp4_block.GatedMLP(**{**weights, name: bad})
+    assert not calls
+    m.forward(X), m.backward(**good), m.load(**weights)
+    assert len(of(calls, "tpmlp_mxfp4_swiglu_mlp_fwd")) == len(of(calls, "tpmlp_mxfp4_swiglu_mlp_bwd")) == 1
