@@ -9,6 +9,7 @@
 
 #include "gemm_tc.cuh"
 #include "internal.h"
+#include "per_device.h"
 
 namespace tpmlp {
 namespace {
@@ -100,16 +101,14 @@ std::atomic<int> g_group_m{16};  // M-blocks per raster group
 constexpr int kDefaultKChunkBlocks = 4096;
 std::atomic<int> g_k_chunk_blocks{kDefaultKChunkBlocks};
 
+// Allows the kernel its dynamic shared memory, once per device.
 template <typename Kern>
-bool set_smem_attr(Kern kern, int device, int bytes, bool* done) {
-    if (device < 64 && done[device]) return true;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) {
-        set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        return false;
-    }
-    if (device < 64) done[device] = true;
-    return true;
+bool set_smem_attr(Kern kern, int device, int bytes, PerDevice<bool>& done) {
+    return done.get(device, [&](bool& ok) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        return ok = e == cudaSuccess;
+    });
 }
 
 // 4-D bf16 tensor map of an MN-major operand whose MN extent is a multiple of 64:
@@ -144,7 +143,7 @@ tpmlp_status launch_single(const CUtensorMap& ma, const CUtensorMap& mb, const t
                            int max_grid, cudaStream_t st) {
     auto kern = tc::gemm_kernel<A_MN, B_MN, EPI, SBN>;
     constexpr int smem = tc::SingleGeom<SBN>::smem_bytes;
-    static bool attr_done[64] = {};
+    static PerDevice<bool> attr_done;
     if (!set_smem_attr(kern, dev.device, smem, attr_done)) return TPMLP_ERR_CUDA;
     int grid = k.num_tiles < dev.sm_count ? k.num_tiles : dev.sm_count;
     if (max_grid > 0 && grid > max_grid) grid = max_grid;
@@ -171,32 +170,29 @@ tpmlp_status launch_single(const CUtensorMap& ma, const CUtensorMap& mb, const t
 // Co-resident CTA pairs (clusters of two) of the pair kernel on this device (0 if it cannot run).
 template <bool A_MN, bool B_MN, int EPI, bool STAGED>
 int pair_capacity(const DeviceInfo& dev) {
-    static int cap[64];
-    static bool done[64];
-    static bool attr_done[64] = {};
-    if (dev.device >= 64) return 0;
-    if (done[dev.device]) return cap[dev.device];
-    auto kern = tc::gemm_pair_kernel<A_MN, B_MN, EPI, STAGED>;
-    constexpr int smem = tc::PairGeom<STAGED>::smem_bytes;
-    int n = 0;
-    if (set_smem_attr(kern, dev.device, smem, attr_done)) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * (dev.sm_count / 2));
-        cfg.blockDim = dim3(tc::PairGeom<STAGED>::threads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
-        cudaGetLastError();
-    }
-    cap[dev.device] = n;
-    done[dev.device] = true;
-    return n;
+    static PerDevice<int> cap;
+    static PerDevice<bool> attr_done;
+    if (dev.device >= PerDevice<int>::kDevices) return 0;
+    return cap.get(dev.device, [&](int& n) {
+        auto kern = tc::gemm_pair_kernel<A_MN, B_MN, EPI, STAGED>;
+        constexpr int smem = tc::PairGeom<STAGED>::smem_bytes;
+        if (set_smem_attr(kern, dev.device, smem, attr_done)) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 * (dev.sm_count / 2));
+            cfg.blockDim = dim3(tc::PairGeom<STAGED>::threads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+            cudaGetLastError();
+        }
+        return true;
+    });
 }
 
 template <bool A_MN, bool B_MN, int EPI, bool STAGED>
@@ -230,31 +226,28 @@ tpmlp_status launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, const CUt
 // Co-resident clusters of the split-K kernel (two CTA pairs each) on this device.
 template <bool A_MN, bool B_MN, int EPI>
 int splitk_capacity(const DeviceInfo& dev) {
-    static int cap[64];
-    static bool done[64];
-    static bool attr_done[64] = {};
-    if (dev.device >= 64) return 0;
-    if (done[dev.device]) return cap[dev.device];
-    auto kern = tc::gemm_splitk_kernel<A_MN, B_MN, EPI>;
-    int n = 0;
-    if (set_smem_attr(kern, dev.device, tc::SK_SMEM, attr_done)) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(4 * (dev.sm_count / 4));
-        cfg.blockDim = dim3(tc::SK_THREADS);
-        cfg.dynamicSmemBytes = tc::SK_SMEM;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 4;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
-        cudaGetLastError();
-    }
-    cap[dev.device] = n;
-    done[dev.device] = true;
-    return n;
+    static PerDevice<int> cap;
+    static PerDevice<bool> attr_done;
+    if (dev.device >= PerDevice<int>::kDevices) return 0;
+    return cap.get(dev.device, [&](int& n) {
+        auto kern = tc::gemm_splitk_kernel<A_MN, B_MN, EPI>;
+        if (set_smem_attr(kern, dev.device, tc::SK_SMEM, attr_done)) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(4 * (dev.sm_count / 4));
+            cfg.blockDim = dim3(tc::SK_THREADS);
+            cfg.dynamicSmemBytes = tc::SK_SMEM;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 4;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+            cudaGetLastError();
+        }
+        return true;
+    });
 }
 
 template <bool A_MN, bool B_MN, int EPI>

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "mxfp4_gemm.cuh"
+#include "per_device.h"
 
 namespace tpmlp {
 namespace {
@@ -72,16 +73,14 @@ bool h_map(CUtensorMap* map, const void* ptr, int64_t ld, int64_t rows) {
 // (where the exchange of that many partial sums fits)
 std::atomic<int> g_mode{0};
 
+// Allows the kernel its dynamic shared memory, once per device.
 template <typename Kern>
-bool set_smem(Kern kern, int device, int bytes, bool (&done)[64]) {
-    if (device < 64 && done[device]) return true;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) {
-        set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        return false;
-    }
-    if (device < 64) done[device] = true;
-    return true;
+bool set_smem(Kern kern, int device, int bytes, PerDevice<bool>& done) {
+    return done.get(device, [&](bool& ok) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        return ok = e == cudaSuccess;
+    });
 }
 
 template <typename Kern, typename... A>
@@ -112,30 +111,28 @@ tpmlp_status launch(Kern kern, unsigned grid, int threads, int smem, unsigned cl
 
 template <int EPI, int N = 1>
 int pair_capacity(const DeviceInfo& dev) {
-    static int cap[64];
-    static bool done[64], attr_done[64];
-    if (dev.device >= 64) return 0;
-    if (done[dev.device]) return cap[dev.device];
-    auto kern = mx::mx_pair_kernel<EPI, N>;
-    int n = 0;
-    if (set_smem(kern, dev.device, mx::PairGeom<EPI>::smem, attr_done)) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * (dev.sm_count / 2));
-        cfg.blockDim = dim3(mx::P_THREADS);
-        cfg.dynamicSmemBytes = mx::PairGeom<EPI>::smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
-        cudaGetLastError();
-    }
-    cap[dev.device] = n;
-    done[dev.device] = true;
-    return n;
+    static PerDevice<int> cap;
+    static PerDevice<bool> attr_done;
+    if (dev.device >= PerDevice<int>::kDevices) return 0;
+    return cap.get(dev.device, [&](int& n) {
+        auto kern = mx::mx_pair_kernel<EPI, N>;
+        if (set_smem(kern, dev.device, mx::PairGeom<EPI>::smem, attr_done)) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 * (dev.sm_count / 2));
+            cfg.blockDim = dim3(mx::P_THREADS);
+            cfg.dynamicSmemBytes = mx::PairGeom<EPI>::smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+            cudaGetLastError();
+        }
+        return true;
+    });
 }
 
 // Bytes that one CTA of a split tile receives: the chunks it finishes, from every other CTA.
@@ -156,7 +153,7 @@ tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec&
                            cudaStream_t st) {
     using Geom = mx::SingleGeom<EPI, CTAS>;
     constexpr bool GATED = EPI == EPI_SWIGLU;
-    static bool attr_done[64];
+    static PerDevice<bool> attr_done;
     auto kern = mx::mx_single_kernel<EPI, CTAS>;
     if (!set_smem(kern, dev.device, Geom::smem, attr_done)) return TPMLP_ERR_CUDA;
     k.a_box = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
