@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtpmlp.so")
 SOURCES = ["tpmlp_api.cu", "gemm_tc.cu", "kernels_misc.cu", "noalloc.cu",
            "mxfp4_quant.cu", "mxfp4_gemm.cu", "mxfp4_api.cu"]
-HEADERS = ["ptx.cuh", "gemm_tc.cuh", "internal.h", "api_common.h", "per_device.h", "mxfp4.cuh", "mxfp4_gemm.cuh"]
+HEADERS = ["ptx.cuh", "gemm_tc.cuh", "internal.h", "api_common.h", "per_device.h", "mxfp4.cuh", "mxfp4_choice.h",
+           "mxfp4_gemm.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr"]

@@ -7,6 +7,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "mxfp4_choice.h"
 #include "mxfp4_gemm.cuh"
 #include "per_device.h"
 
@@ -135,17 +136,43 @@ int pair_capacity(const DeviceInfo& dev) {
     });
 }
 
-// Bytes that one CTA of a split tile receives: the chunks it finishes, from every other CTA.
-template <int EPI>
-int exchange_bytes(int split, int rows) {
-    constexpr int CH = EPI == EPI_SWIGLU ? 2 : 4, PARTS = EPI == EPI_SWIGLU ? 2 : 1;
-    const int owners = std::min(split, CH);
-    return (CH + owners - 1) / owners * (split - 1) * PARTS * 128 * rows;
-}
 template <int EPI, int CTAS>
-bool split_fits(int split, int rows, int kb) {
-    const int room = mx::SingleGeom<EPI, CTAS>::ring - (EPI == EPI_DSWIGLU ? mx::S_EPI_BYTES : 0);
-    return split <= kb && exchange_bytes<EPI>(split, std::min((rows + 31) / 32 * 32, mx::BM)) <= room;
+constexpr mx::Exchange kExchange{EPI == EPI_SWIGLU ? 2 : 4, EPI == EPI_SWIGLU ? 2 : 1,
+                                 mx::SingleGeom<EPI, CTAS>::ring - (EPI == EPI_DSWIGLU ? mx::S_EPI_BYTES : 0)};
+
+// The single kernel is allowed more dynamic shared memory than it takes, so that the occupancy of clusters can be asked
+// for one CTA an SM.
+constexpr int kOneCtaSmem = 120 * 1024;
+static_assert(2 * kOneCtaSmem > 227 * 1024 && kOneCtaSmem >= mx::SingleGeom<EPI_STORE, 2>::smem, "one CTA an SM");
+
+template <int EPI>
+mx::Machine machine(const DeviceInfo& dev, int pairs) {
+    static PerDevice<mx::Machine> kept;
+    mx::Machine on = kept.get(dev.device, [&](mx::Machine& m) {
+        auto kern = mx::mx_single_kernel<EPI, 2>;
+        m.clusters[1] = dev.sm_count;
+        bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneCtaSmem) == cudaSuccess;
+        for (int s : {2, 3, 4, 8}) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(s * (dev.sm_count / s));
+            cfg.blockDim = dim3(mx::S_THREADS);
+            cfg.dynamicSmemBytes = kOneCtaSmem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = s;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (!ok || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) ok = false;
+            m.clusters[s] = ok ? n : 0;
+        }
+        cudaGetLastError();
+        return ok;
+    });
+    on.pairs = pairs;
+    return on;
 }
 
 template <int EPI, int CTAS>
@@ -155,14 +182,14 @@ tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec&
     constexpr bool GATED = EPI == EPI_SWIGLU;
     static PerDevice<bool> attr_done;
     auto kern = mx::mx_single_kernel<EPI, CTAS>;
-    if (!set_smem(kern, dev.device, Geom::smem, attr_done)) return TPMLP_ERR_CUDA;
+    if (!set_smem(kern, dev.device, CTAS == 2 ? kOneCtaSmem : Geom::smem, attr_done)) return TPMLP_ERR_CUDA;
     k.a_box = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
     k.stages = Geom::stages(k.a_box);
     const int64_t n_blocks = GATED ? g.N / 128 : (g.N + 127) / 128, m_blocks = (g.M + 127) / 128;
     const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
     if (mode >= 3) {
         split = 2 << (mode - 3);
-        while (split > 1 && !split_fits<EPI, CTAS>(split, rows, k.kb)) split /= 2;
+        while (split > 1 && !kExchange<EPI, CTAS>.fits(split, rows, k.kb)) split /= 2;
     }
     k.m_blocks = static_cast<int>(m_blocks);
     CUtensorMap m[4];
@@ -173,59 +200,11 @@ tpmlp_status launch_single(const MxOperand& a, const MxOperand& b, const MxSpec&
                   static_cast<unsigned>(split), st, m[0], m[1], m[2], m[3], k);
 }
 
-// Which kernel takes a product, by its expected time in microseconds.  Fitted to one GB300's times of 63
-// products (N x K of 40960x5120, 5120x20480, 8192x1024, 4096x4096, 2048x8192, 20480x2048, 1024x1024, 64 to 2048
-// rows, weights out of L2); kb = stages of 256 k:
-//   pairs    4 + waves (0.265 kb + 1.05)      256x256 tiles over the CTA pairs
-//   single   4 + 0.34 kb                       at most one CTA an SM,
-//            5.3 + 0.38 kb                     at most two, else
-//            2.5 + waves (0.38 kb + 3)
-//   split    the same of kb / split, and 1.5 (one CTA an SM) or 2.3 (two) log2(split) for the exchange
-// The choice costs at most 10 % against the best of them.  For example 512 x 5120 x 20480: pairs 26.7, single 33.7,
-// split two ways 41.6; 800 rows: single 35.9, pairs 48.2 (80 tiles, two waves); 64 x 5120 x 20480: split four ways
-// 15.7, single 25.8, pairs 25.3; 333 x 4096 x 16384: split two ways 19.5, pairs 22.1, single 25.1.  Split three ways:
-// 200 x 5120 x 20480 20.4 (two ways 22.6, pairs 26.2), 640 x 1024 x 8192 10.3 (two 11.0, four 13.2).
-// At most 32 rows: single CTAs, which copy no more rows of A than there are (4 x 40960 x 5120: 23 against 31).
-struct Choice {
-    bool pair;
-    int split;
-    double us;
-};
-constexpr double kPairStart = 4.0;
-double pair_tile_us(int kb) { return 0.265 * kb + 1.05; }
 template <int EPI>
-Choice choose(const MxSpec& g, int kb, int cap, int sms) {
-    const int64_t n1 = EPI == EPI_SWIGLU ? g.N / 128 : (g.N + 127) / 128, tiles1 = n1 * ((g.M + 127) / 128);
-    const int64_t tiles2 = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-    const int rows = static_cast<int>(std::min<int64_t>(g.M, mx::BM));
-    Choice c{false, 1, 0.0};
-    for (int s : {1, 2, 3, 4, 8}) {
-        const int64_t ctas = tiles1 * s;
-        if (s > 1 && (ctas > 2 * sms || !split_fits<EPI, 2>(s, rows, kb))) break;
-        // (40 tiles split four ways are 160 CTAs on 152 SMs: with few rows a few SMs with two cost little)
-        bool one = ctas <= sms + (g.M <= 64 ? sms / 16 : 0);
-        if (s == 3) {
-            // clusters of three leave SMs of a GPC over, and a third of the columns' owners get twice the exchange
-            one = ctas <= sms * 4 / 5;
-            if (ctas > sms * 8 / 5) continue;
-        }
-        const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
-        const double k = static_cast<double>(kb) / s, log = s == 3 ? 1.6 : s == 8 ? 3.0 : s / 2;
-        const double t = one ? 4.0 + 0.34 * k + 1.5 * log : waves <= 1 ? 5.3 + 0.38 * k + 2.3 * log : 2.5 + waves * (0.38 * k + 3.0);
-        if (s == 1 || t < c.us) {
-            c.us = t;
-            c.split = s;
-        }
-    }
-    if (cap > 0 && g.M > 32) {
-        const int64_t waves2 = (tiles2 + cap - 1) / cap;
-        const double t = kPairStart + waves2 * pair_tile_us(kb);
-        if (t < c.us) {
-            c.us = t;
-            c.pair = true;
-        }
-    }
-    return c;
+mx::Choice choose(const MxSpec& g, int kb, int pairs, const DeviceInfo& dev) {
+    const int64_t n = EPI == EPI_SWIGLU ? g.N / 128 : (g.N + 127) / 128;
+    return mx::choose(machine<EPI>(dev, pairs), kExchange<EPI, 2>,
+                      {g.M, n * ((g.M + 127) / 128), ((g.M + 255) / 256) * ((g.N + 255) / 256), kb});
 }
 
 // The pair kernel's view of a product.
@@ -244,7 +223,7 @@ tpmlp_status launch_variant(const MxOperand& a, const MxOperand& b, const MxSpec
                             cudaStream_t st) {
     const int mode = g_mode.load(std::memory_order_relaxed);
     const int cap = pair_capacity<EPI>(dev);
-    const Choice choice = mode == 0 ? choose<EPI>(g, k.kb, cap, dev.sm_count) : Choice{mode == 2 && cap > 0, 1, 0.0};
+    const mx::Choice choice = mode == 0 ? choose<EPI>(g, k.kb, cap, dev) : mx::Choice{mode == 2 && cap > 0, 1, 0.0};
     if (choice.pair) {
         mx::Problems<1> all{};
         if (!pair_problem(&all.of[0], a, b, g, k)) return TPMLP_ERR_CUDA;
@@ -342,11 +321,11 @@ tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const MxSums& sums, con
     double apart = 0.0, together = 0.0;
     for (int i = 0; i < 3; ++i) {
         k[i] = make_args(c[i].a, c[i].b, c[i].g, dev);
-        apart += choose<EPI_STORE>(c[i].g, k[i].kb, cap, dev.sm_count).us;
-        together += static_cast<double>((c[i].g.M + 255) / 256 * ((c[i].g.N + 255) / 256)) * pair_tile_us(k[i].kb);
+        apart += choose<EPI_STORE>(c[i].g, k[i].kb, cap, dev).us;
+        together += static_cast<double>((c[i].g.M + 255) / 256 * ((c[i].g.N + 255) / 256)) * mx::pair_tile_us(k[i].kb);
     }
     const int mode = g_mode.load(std::memory_order_relaxed);
-    if (cap <= 0 || (mode != 0 && mode != 2) || (mode == 0 && kPairStart + together / cap + pair_tile_us(1) >= apart)) {
+    if (cap <= 0 || (mode != 0 && mode != 2) || (mode == 0 && mx::kPairStart + together / cap + mx::pair_tile_us(1) >= apart)) {
         if (sa.items > 0) {
             const tpmlp_status r = launch_mxfp4_sums(sa, st);
             if (r != TPMLP_OK) return r;
@@ -367,7 +346,7 @@ tpmlp_status launch_mxfp4_gemms(const MxProduct (&c)[3], const MxSums& sums, con
         all.first[i] = tiles;
         tiles += pair_tiles(all.of[i]);
         if (longest) all.n_long = i + 1;
-        else if (all.skip == 0) all.skip = static_cast<int>(pair_tile_us(k[order[0]].kb) / pair_tile_us(k[order[i]].kb) + 0.5);
+        else if (all.skip == 0) all.skip = static_cast<int>(mx::pair_tile_us(k[order[0]].kb) / mx::pair_tile_us(k[order[i]].kb) + 0.5);
     }
     all.sums = sa;
     const int clusters = std::min(all.long_tiles + all.short_tiles, cap);
