@@ -160,3 +160,31 @@ def test_weight_gradients_over_many_tokens(T):
     t = slice(m - 40, m)
     ref = R.block_bwd(x[t], R.q(host(W)), R.q(host(B)), host(H[t]), dz[t])[0]
     U.assert_close(host(dX[t]), ref, "bf16", "dX")
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2, 4], ids=["auto", "single", "pair", "split4"])
+@pytest.mark.parametrize("k", [5120, 20480, 262144 + 96])
+@pytest.mark.parametrize("one_sign", [False, True], ids=["signs", "one-sign"])
+def test_products_of_blocks_of_many_sizes(T, set_mode, mode, k, one_sign):
+    """Blocks of 2^-16 to 1 times the same values: with blocks of one size nearly every partial sum is a number of 24 bits,
+    here they have to be rounded.  The bounds are those above."""
+    import torch
+    set_mode(mode)
+    m, n = 40, 136
+
+    def blocks(seed, rows):
+        x = normal(seed, rows, k)
+        g = torch.Generator(device="cuda").manual_seed(seed + 100)
+        e = torch.randint(-16, 1, (rows, -(-k // 32)), generator=g, device="cuda").repeat_interleave(32, dim=1)[:, :k]
+        x = torch.ldexp(x.float(), e).to(torch.bfloat16)
+        return x.abs() if one_sign else x
+
+    (aq, as_), a = operand(T, blocks(1, m))
+    (bq, bs), b = operand(T, blocks(2, n))
+    D = torch.empty((m, n), device="cuda")
+    T.tpmlp_mxfp4_matmul(aq, as_, bq, bs, None, D, m, n, k, T.F32)
+    T.tpmlp_device_status()
+    ref = a @ b.T
+    off = np.linalg.norm(host(D) - ref) / np.linalg.norm(ref)
+    assert off <= (-(-k // 64) + 16) * 2.0 ** -23, off
+    R.assert_product(host(D), a, b, None, False)
