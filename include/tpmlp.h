@@ -32,8 +32,12 @@
  *     the kernels are enqueued on `stream` (a cudaStream_t; NULL = legacy
  *     default stream).  The GEMM kernels are launched with programmatic
  *     dependent launch: their set-up may overlap the end of the preceding
- *     kernel in the stream, but they touch no global memory before that
- *     kernel has completed, so stream order holds as for any launch.
+ *     kernel in the stream, but they read and write no global memory before
+ *     that kernel has completed, so stream order holds as for any launch.
+ *     (Inside tpmlp_mxfp4_swiglu_mlp_fwd the second and third kernel ask for
+ *     weights to be brought into L2 while the call's own kernel ahead of them
+ *     ends.  That kernel writes no weights and itself starts after all earlier
+ *     work; the weights are read after the wait, as stated.)
  *   Validation.  Arguments are checked on the host before anything is
  *     enqueued, in this order: NULL pointers (TPMLP_ERR_NULL), shapes
  *     (TPMLP_ERR_SHAPE: s, b >= 0; h, ffn, p >= 1; sizes below 2^31 rows),
@@ -50,7 +54,9 @@
  *     and returns; tpmlp_device_status() reports it as TPMLP_ERR_TIMEOUT.
  *     tpmlp_last_error() gives a thread-local message for the last failure.
  *   Numerics.  bf16 inputs, fp32 accumulation in tensor memory, bf16 outputs
- *     (rounded to nearest even); fp32 inputs run on fp32 FMA (no TF32).
+ *     (rounded to nearest even); fp32 inputs run on fp32 FMA (no TF32).  MXFP4
+ *     operands: exact products of the 4-bit values and their scales, fp32
+ *     accumulation in tensor memory, bf16 or fp32 outputs.
  */
 #ifndef TPMLP_H
 #define TPMLP_H
@@ -348,8 +354,10 @@ int64_t tpmlp_mxfp4_swiglu_ws_bytes(int64_t s, int64_t b, int64_t h, int64_t ffn
 /*
  * Tiling of the MXFP4 products, process wide, for tuning and tests: 0 = automatic (default), 1 = single
  * CTAs (128x128 tiles), 2 = CTA pairs (256x256), 3, 4, 5 = single CTAs with the K loop split 2, 4, 8 ways
- * (fewer where K is too short or the exchange of the partial sums does not fit).  Results agree within
- * fp32 rounding.  TPMLP_ERR_SHAPE for other values.
+ * (fewer where K is too short or the exchange of the partial sums does not fit).  Results of tpmlp_mxfp4_matmul
+ * agree within the fp32 rounding of their sums, single CTAs and pairs to the bit.  Those of the gated block do so too
+ * without a split; with one, a value of Y or dH in 10^5 may fall on the other side of a 4-bit rounding boundary, and
+ * outputs agree within 3e-3 in the Frobenius norm.  TPMLP_ERR_SHAPE for other values.
  */
 tpmlp_status tpmlp_set_mxfp4_mode(int mode);
 int tpmlp_get_mxfp4_mode(void);

@@ -28,11 +28,7 @@ __host__ __device__ __forceinline__ long long scale_offset(long long row, long l
     return ((row >> 7) * k_tiles + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
 }
 
-// |x| as ordered bits: finite < 0x7F800000 <= infinity and NaN, so that an integer maximum keeps a
-// NaN where a floating one would drop it.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
-// Scale byte of a block whose largest |x| has the bits amax.
+// Scale byte of a block whose largest |x| has the bits amax (ordered: finite < 0x7F800000 <= infinity and NaN).
 __device__ __forceinline__ uint32_t scale_of(uint32_t amax) {
     const uint32_t ex = amax >> 23;
     return amax >= 0x7F800000u ? 255u : (ex > 2u ? ex - 2u : 0u);

@@ -16,11 +16,12 @@
 //                     epilogue reads the shared columns first and reports them free; the next
 //                     tile's MMAs start then, beside the rest of the epilogue.  Several independent
 //                     products can share a launch (Problems).
-//                     A pair reads 70 KB a stage from L2 for 512 tensor cycles, about the 64 bytes a
-//                     cycle that an SM gets, so L2 binds first and, over milliseconds, the power cap:
-//                     8192 x 20480 x 5120 takes 218 us (7.9 PFLOP/s) cold and 248 us (6.9) at the cap's
-//                     1.6 GHz; tensor pipe 83 % of active cycles.  (The instruction's 96-deep form would
-//                     only move the limit further to L2.)
+//                     The tensor pipe binds first and, over milliseconds, the power cap: 8192 x 20480 x
+//                     5120 takes 218 us (7.9 PFLOP/s) cold and 248 us (6.9) at the cap's 1.6 GHz.  At
+//                     4096 x 8192 x 5120 the pipe is busy for 83 % of active cycles, L2 for 47 % and the way
+//                     from it to the SMs for 40 % (70 KB a stage and pair in 512 tensor cycles).  The
+//                     instruction's 96-deep form, half as fast again, has not been tried: a stage's 256 k
+//                     and blocks of 32 do not divide into it, and at the cap it is power that binds.
 //   mx_single_kernel  one CTA per 128x128 tile (128 rows of A, 128 of B; for the gated forward 64
 //                     gate and 64 up columns), two CTAs an SM, not persistent: for few rows, where
 //                     reading B's codes bounds the time, and for GEMMs of few tiles.  Clusters of

@@ -422,7 +422,8 @@ tpmlp_status launch_mxfp4_sums(const mx::SumsArgs& a, cudaStream_t st) {
 tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, int64_t rows, int64_t k, bool f32,
                                      const DeviceInfo& dev, cudaStream_t st) {
     const int64_t spans = (k + 255) / 256, items = rows * spans;
-    const bool many = items >= static_cast<int64_t>(dev.sm_count) * 64 * 4;  // as in the quantisation
+    // four spans a warp where every SM then has its 64 warps full
+    const bool many = items >= static_cast<int64_t>(dev.sm_count) * 64 * 4;
     const int64_t per = many ? 32 : 8;
     const dim3 grid(static_cast<unsigned>((items + per - 1) / per));
     const auto* q = static_cast<const uint8_t*>(Q);
