@@ -83,7 +83,8 @@ typedef enum {
 
 typedef enum { TPMLP_BF16 = 0, TPMLP_F32 = 1 } tpmlp_dtype;
 
-typedef enum { TPMLP_ACT_NONE = 0, TPMLP_ACT_GELU_ERF = 1 } tpmlp_act;
+/* TPMLP_ACT_SWIGLU: the products grouped by expert only. */
+typedef enum { TPMLP_ACT_NONE = 0, TPMLP_ACT_GELU_ERF = 1, TPMLP_ACT_SWIGLU = 2 } tpmlp_act;
 
 /*
  * Column-parallel layer for all p shards in one launch
@@ -361,6 +362,116 @@ int64_t tpmlp_mxfp4_swiglu_ws_bytes(int64_t s, int64_t b, int64_t h, int64_t ffn
  */
 tpmlp_status tpmlp_set_mxfp4_mode(int mode);
 int tpmlp_get_mxfp4_mode(void);
+
+/*
+ * Layer norm over rows (Level 2, M034: between the tensor-parallel regions, local to a rank's tokens):
+ *   Y[r] = (X[r] - mean[r]) rstd[r] gamma + beta,   rstd = 1 / sqrt(mean of (X - mean)^2 + eps)
+ *   X [rows][h] dt, row pitch ldx >= h (elements); gamma, beta [h] dt, each may be NULL (1, 0);
+ *   Y [rows][h] dt, row pitch ldy; mean, rstd [rows] fp32, both or neither, for the backward.
+ * Statistics in fp32.  h at most 16384.  Pointers and pitches need the alignment of their elements only; rows are
+ * read 16 bytes at a time where all of h, the pitches and the addresses of X, Y, gamma and beta are multiples of 16 bytes.
+ */
+tpmlp_status tpmlp_layernorm_fwd(const void* X, const void* gamma, const void* beta, void* Y, void* mean, void* rstd,
+                                 int64_t rows, int64_t h, int64_t ldx, int64_t ldy, float eps, tpmlp_dtype dt, void* stream);
+
+/*
+ * Its backward:
+ *   dX = rstd (g - mean(g) - xhat mean(g xhat)),  g = dY gamma,  xhat = (X - mean) rstd
+ *   dgamma = sum over rows of dY xhat,  dbeta = sum over rows of dY     (each may be NULL; grad_dt)
+ *   X, gamma, mean, rstd as in the forward; dY [rows][h] dt, pitch lddy; dX [rows][h] dt, pitch lddx.
+ *   ws: tpmlp_layernorm_ws_bytes(rows, h) bytes (NULL where neither dgamma nor dbeta is wanted).
+ * The sums over rows are added in a fixed order: the same call gives the same bits.  Without rows dgamma and dbeta are
+ * set to zero.
+ */
+tpmlp_status tpmlp_layernorm_bwd(const void* X, const void* gamma, const void* mean, const void* rstd, const void* dY, void* dX,
+                                 void* dgamma, void* dbeta, void* ws, int64_t rows, int64_t h, int64_t ldx, int64_t lddy,
+                                 int64_t lddx, tpmlp_dtype dt, tpmlp_dtype grad_dt, void* stream);
+
+/* Workspace of the call above, in bytes (-1 for a bad shape). */
+int64_t tpmlp_layernorm_ws_bytes(int64_t rows, int64_t h);
+
+/*
+ * Mixture of experts: routing.  Each token's k experts are those with its largest logits, in falling order; a tie goes
+ * to the lower index, a NaN counts as the largest, and an expert of -inf is never chosen (a token of -inf alone, padding
+ * for instance, has no rows).  Their weights are the softmax over all experts' logits (chosen = 0) or over the chosen
+ * ones' (chosen = 1).  Rows are the chosen (token, slot) pairs sorted by expert, then token.
+ *   logits    [tokens][experts] dt
+ *   ids       [tokens][k] int32, the slots' experts (-1: none)
+ *   weights   [tokens][k] fp32 (0 where there is none)
+ *   offsets   [experts + 1] int32: expert e has rows offsets[e] .. offsets[e + 1] - 1
+ *   row_token [tokens * k] int32: the token of each row, -1 past the last row
+ *   slot_row  [tokens][k] int32: the row of each slot (-1: none)
+ *   ws        tpmlp_moe_route_ws_bytes(tokens, experts, k) bytes
+ * experts at most 1024, k at most 32 and at most experts.  Pointers need the alignment of their elements only.  Without
+ * tokens the offsets are set to zero.  The plan stays on the device: nothing has to be read back before the products.
+ */
+tpmlp_status tpmlp_moe_route(const void* logits, void* ids, void* weights, void* offsets, void* row_token, void* slot_row, void* ws,
+                             int64_t tokens, int64_t experts, int k, int chosen, tpmlp_dtype dt, void* stream);
+
+/* Workspace of the call above, in bytes (-1 for a bad shape). */
+int64_t tpmlp_moe_route_ws_bytes(int64_t tokens, int64_t experts, int k);
+
+/*
+ * The gradient of the logits from that of the weights (ids and weights as tpmlp_moe_route gave them):
+ *   dlogits[t][i] = p_i ([i chosen] dw_i - sum_j w_j dw_j),  p the softmax over all experts, or over the chosen
+ *   dweights [tokens][k] fp32 (not read where no expert was chosen);  dlogits [tokens][experts] dt
+ */
+tpmlp_status tpmlp_moe_route_bwd(const void* logits, const void* ids, const void* weights, const void* dweights, void* dlogits,
+                                 int64_t tokens, int64_t experts, int k, int chosen, tpmlp_dtype dt, void* stream);
+
+/*
+ * Products grouped by expert: row r, of expert e (offsets[e] <= r < offsets[e + 1]),
+ *   Y[r] = act(X[row_token[r]] W[e] + bias[e])
+ *   X         [tokens][K] bf16; row_token [rows] int32, or NULL: X has the rows themselves (tokens == rows)
+ *   offsets   [experts + 1] int32, rising, at most rows
+ *   W         [experts][K][N] bf16; bias [experts][N] bf16 or NULL
+ *   act       TPMLP_ACT_NONE: Y [rows][N] out_dt, H NULL
+ *             TPMLP_ACT_SWIGLU: N = 2 f packed in blocks of 256 columns, 128 gate features and then their up features
+ *             (tpmlp_swiglu_pack with p = 1), Y = silu(gate) up [rows][f] bf16, from fp32; H [rows][N] bf16, the packed
+ *             pre-activations for the backward, or NULL.  f a multiple of 128.
+ * experts at most 1024; K and N multiples of 8.  row_token and offsets are read on the device.  Rows that no expert has
+ * are left as they were.  Row ranges past `rows`, or tokens past `tokens`, are cut to what there is, and
+ * tpmlp_device_status reports TPMLP_ERR_DEVICE.
+ */
+tpmlp_status tpmlp_moe_matmul(const void* X, const void* row_token, const void* offsets, const void* W, const void* bias, void* Y,
+                              void* H, int64_t tokens, int64_t rows, int64_t experts, int64_t K, int64_t N, tpmlp_act act,
+                              tpmlp_dtype out_dt, void* stream);
+
+/*
+ * The gradient of their inputs, row by row:
+ *   act TPMLP_ACT_NONE:   dX[r] = dY[r] W[e]^T,  dX [rows][K] dx_dt, H NULL
+ *   act TPMLP_ACT_SWIGLU: W is the layer behind the gated activation: with D = dY[r] W[e]^T (f = K values) and the packed
+ *   pre-activations H [rows][2 K] bf16, dX [rows][2 K] bf16 is their packed gradient (D up silu'(gate), D silu(gate)).
+ *   dY [rows][N] bf16, W [experts][K][N] bf16, offsets as above.
+ * (For rows that were read through row_token, tpmlp_moe_combine without weights adds dX up into the tokens.)
+ */
+tpmlp_status tpmlp_moe_matmul_dx(const void* dY, const void* offsets, const void* W, const void* H, void* dX, int64_t rows,
+                                 int64_t experts, int64_t K, int64_t N, tpmlp_act act, tpmlp_dtype dx_dt, void* stream);
+
+/*
+ * The gradients of their weights: over the rows r of expert e
+ *   dW[e] = sum X[row_token[r]]^T dY[r]  [experts][K][N],   dbias[e] = sum dY[r]  [experts][N] or NULL      (grad_dt)
+ * X, row_token, offsets as in tpmlp_moe_matmul.  An expert without rows has zero gradients.
+ */
+tpmlp_status tpmlp_moe_matmul_dw(const void* X, const void* row_token, const void* offsets, const void* dY, void* dW, void* dbias,
+                                 int64_t tokens, int64_t rows, int64_t experts, int64_t K, int64_t N, tpmlp_dtype grad_dt,
+                                 void* stream);
+
+/*
+ * The experts' rows back into tokens, slots in order, added in fp32:
+ *   Z[t] = sum_j weights[t][j] O[slot_row[t][j]]      (slots without a row are left out; a token without any gives zeros)
+ *   O [rows][h] bf16; slot_row [tokens][k] int32; weights [tokens][k] fp32 or NULL (1); Z [tokens][h] bf16
+ * h a multiple of 8, k at most 32.
+ */
+tpmlp_status tpmlp_moe_combine(const void* O, const void* slot_row, const void* weights, void* Z, int64_t tokens, int64_t rows, int k,
+                               int64_t h, void* stream);
+
+/*
+ * Its backward: for each slot with a row, dO[row] = weights[t][j] dZ[t] and dweights[t][j] = dZ[t] . O[row] (0 without a
+ * row).  dO [rows][h] bf16 (rows of no slot are left as they were); dweights [tokens][k] fp32 or NULL (O may then be NULL).
+ */
+tpmlp_status tpmlp_moe_combine_bwd(const void* O, const void* slot_row, const void* weights, const void* dZ, void* dO, void* dweights,
+                                   int64_t tokens, int64_t rows, int k, int64_t h, void* stream);
 
 /*
  * The MLP block forward without a caller workspace.  The pages have no

@@ -108,6 +108,16 @@ inline tpmlp_status check_dtype(tpmlp_dtype dt) {
         if (_st != TPMLP_OK) return _st;      \
     } while (0)
 
+// Zeros to an output that is a sum over nothing.
+inline tpmlp_status clear_memory(void* p, int64_t bytes, cudaStream_t st) {
+    const cudaError_t e = cudaMemsetAsync(p, 0, static_cast<size_t>(bytes), st);
+    if (e != cudaSuccess) {
+        set_error("cudaMemsetAsync: %s", cudaGetErrorString(e));
+        return TPMLP_ERR_CUDA;
+    }
+    return TPMLP_OK;
+}
+
 inline tpmlp_status get_device(const DeviceInfo** out) {
     const DeviceInfo* d = device_info();
     if (!d) return TPMLP_ERR_CUDA;

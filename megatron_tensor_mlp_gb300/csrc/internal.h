@@ -152,6 +152,43 @@ tpmlp_status launch_mxfp4_dequantize(const void* Q, const void* S, void* out, in
 void set_mxfp4_mode(int mode);
 int get_mxfp4_mode();
 
+// A product grouped by expert (see tpmlp_moe_matmul, _dx, _dw): rows [offsets[e], offsets[e + 1]) are expert e's.
+struct MoeSpec {
+    int64_t rows, tokens, K, N;
+    int experts;
+    const int* offsets;
+    const int* src;    // token of each row (null: x has the rows themselves)
+    const void* x;     // forward and dw: X; dx: dY
+    const void* dy;    // dw: dY
+    const void* w;     // [experts][K][N]
+    const void* bias;  // [experts][N], may be null
+    void* out;         // Y, dX or dW
+    bool out_f32;
+    bool gated;        // the gated activation (forward) or its derivative (dx)
+    void* h;           // packed pre-activations: forward saves them here (may be null), dx reads them
+    void* dbias;       // dw: [experts][N], may be null
+};
+tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st);
+tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st);
+tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st);
+// Routing: top-k, weights and the plan of rows; workspace: MoeRouteWs (moe_route.cu).
+int64_t moe_route_ws_bytes(int64_t tokens, int experts);
+tpmlp_status launch_moe_route(const void* logits, int* ids, float* weights, int* offsets, int* row_token, int* slot_row, void* ws,
+                              int64_t tokens, int experts, int k, bool chosen, bool f32, cudaStream_t st);
+tpmlp_status launch_moe_route_bwd(const void* logits, const int* ids, const float* weights, const float* dweights, void* dlogits,
+                                  int64_t tokens, int experts, int k, bool chosen, bool f32, cudaStream_t st);
+tpmlp_status launch_moe_combine(const void* O, const int* slot_row, const float* weights, void* Z, int64_t tokens, int64_t rows, int k,
+                                int64_t h, cudaStream_t st);
+tpmlp_status launch_moe_combine_bwd(const void* O, const int* slot_row, const float* weights, const void* dZ, void* dO, float* dweights,
+                                    int64_t tokens, int64_t rows, int k, int64_t h, cudaStream_t st);
+// Layer norm over rows of h elements (pitches in elements).
+int64_t layernorm_ws_bytes(int64_t rows, int64_t h);
+tpmlp_status launch_layernorm_fwd(const void* X, const void* gamma, const void* beta, void* Y, float* mean, float* rstd, int64_t rows,
+                                  int64_t h, int64_t ldx, int64_t ldy, float eps, bool f32, const DeviceInfo& dev, cudaStream_t st);
+tpmlp_status launch_layernorm_bwd(const void* X, const void* gamma, const float* mean, const float* rstd, const void* dY, void* dX,
+                                  void* dgamma, void* dbeta, void* ws, int64_t rows, int64_t h, int64_t ldx, int64_t lddy, int64_t lddx,
+                                  bool f32, bool grad_f32, const DeviceInfo& dev, cudaStream_t st);
+
 // How a bf16 GEMM launch of launch_tc_gemm would run, by the same tiling decision (false when
 // no tcgen05 variant takes it); nothing is launched.  A K-chunked fp32 contraction reports its
 // first launch.

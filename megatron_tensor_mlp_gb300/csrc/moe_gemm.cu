@@ -1,0 +1,202 @@
+// Host side of the products grouped by expert: tensor maps, launch.  And the bias gradients' sums over an expert's rows.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "moe_gemm.cuh"
+#include "per_device.h"
+
+namespace tpmlp {
+namespace {
+
+using namespace moe;
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// bf16 [slices][rows][cols], boxes of 64 columns x box_rows; rank 2 (one slice) for tile::gather4, box_rows 1.
+bool make_map(CUtensorMap* map, const void* ptr, uint64_t cols, uint64_t rows, uint64_t slices, uint32_t box_rows, uint32_t rank = 3) {
+    auto fn = encode_fn();
+    if (!fn) {
+        set_error("cuTensorMapEncodeTiled is not available from the driver");
+        return false;
+    }
+    const cuuint64_t dims[3] = {cols, rows, slices}, strides[2] = {cols * 2, cols * rows * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(BK), box_rows, 1}, estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled (experts) failed (%d): dims %llu x %llu x %llu", static_cast<int>(r),
+                  (unsigned long long)cols, (unsigned long long)rows, (unsigned long long)slices);
+        return false;
+    }
+    return true;
+}
+
+template <typename Kern>
+bool set_smem(Kern kern, int device, int bytes, PerDevice<bool>& done) {
+    return done.get(device, [&](bool& ok) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        return ok = e == cudaSuccess;
+    });
+}
+
+template <typename Kern, typename... A>
+tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluster, cudaStream_t st, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see griddep_wait
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        set_error("expert product launch: %s", cudaGetErrorString(e));
+        return TPMLP_ERR_CUDA;
+    }
+    count_launch();
+    return TPMLP_OK;
+}
+
+template <bool W_MN, int MODE>
+tpmlp_status launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x8, const Args& a, const DeviceInfo& dev,
+                         cudaStream_t st) {
+    static PerDevice<bool> done;
+    auto kern = rows_kernel<W_MN, MODE>;
+    if (!set_smem(kern, dev.device, Geom<MODE>::smem, done)) return TPMLP_ERR_CUDA;
+    const int64_t most = int64_t(a.m_blocks) * (a.rows / Geom<MODE>::tn + std::min(a.experts, a.rows));
+    const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(most, dev.sm_count / 2));
+    return launch(kern, dim3(2 * pairs), THREADS, Geom<MODE>::smem, 2, st, w, x, x8, a);
+}
+
+// Sums of an expert's rows by column: CTA (64 columns, expert), rows in steps of 32, added in that order.
+constexpr int SUM_THREADS = 256;
+__global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const __nv_bfloat16* in, const int* offsets, int rows, int cols, void* out,
+                                                           int out_f32) {
+    __shared__ float part[32][64 + 1];
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    const int e = blockIdx.y, c = blockIdx.x * 64 + (threadIdx.x & 7) * 8, r0 = threadIdx.x >> 3;
+    const int a = min(max(offsets[e], 0), rows), b = min(max(offsets[e + 1], 0), rows);
+    float s[8] = {};
+    if (c < cols) {
+        for (int r = a + r0; r < b; r += 32) {
+            float v[8];
+            tc::unpack_bf16x8(*reinterpret_cast<const uint4*>(in + static_cast<long long>(r) * cols + c), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] += v[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[r0][(threadIdx.x & 7) * 8 + i] = s[i];
+    __syncthreads();
+    const int col = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && col < cols) {
+        float v = 0.0f;
+        for (int r = 0; r < 32; ++r) v += part[r][threadIdx.x];
+        const long long at = static_cast<long long>(e) * cols + col;
+        if (out_f32) static_cast<float*>(out)[at] = v;
+        else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+    }
+}
+
+Args common(const MoeSpec& g, const DeviceInfo& dev) {
+    Args a{};
+    a.offsets = g.offsets;
+    a.src = g.src;
+    a.rows = static_cast<int>(g.rows);
+    a.tokens = static_cast<int>(g.tokens);
+    a.experts = g.experts;
+    a.status = dev.status;
+    a.timeout_ns = 2000000000ull;  // 2 s per wait
+    return a;
+}
+
+}  // namespace
+
+tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st) {
+    Args a = common(g, dev);
+    a.kb = static_cast<int>((g.K + BK - 1) / BK);
+    a.features = static_cast<int>(g.gated ? g.N / 2 : g.N);
+    a.m_blocks = (a.features + 255) / 256;
+    a.out = g.out;
+    a.ld = a.features;
+    a.out_f32 = g.out_f32;
+    a.bias = static_cast<const __nv_bfloat16*>(g.bias);
+    a.bias_ld = g.N;
+    a.h_out = static_cast<__nv_bfloat16*>(g.h);
+    a.h_ld = g.N;
+    CUtensorMap w, x, x8;
+    const uint64_t K = g.K, tokens = g.src ? g.tokens : g.rows;
+    if (!make_map(&w, g.w, g.N, K, g.experts, BK) ||
+        !(g.src ? make_map(&x, g.x, K, tokens, 1, 1, 2) : make_map(&x, g.x, K, tokens, 1, (g.gated ? Geom<SWIGLU>::tn : Geom<STORE>::tn) / 2)) ||
+        !make_map(&x8, g.x, K, tokens, 1, 8))
+        return TPMLP_ERR_CUDA;
+    return g.gated ? launch_rows<true, SWIGLU>(w, x, x8, a, dev, st) : launch_rows<true, STORE>(w, x, x8, a, dev, st);
+}
+
+tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st) {
+    Args a = common(g, dev);
+    a.kb = static_cast<int>((g.N + BK - 1) / BK);
+    a.features = static_cast<int>(g.K);
+    a.m_blocks = (a.features + 255) / 256;
+    a.out = g.out;
+    a.ld = g.gated ? 2 * g.K : g.K;
+    a.out_f32 = g.out_f32;
+    a.h_in = static_cast<const __nv_bfloat16*>(g.h);
+    a.h_ld = 2 * g.K;
+    CUtensorMap w, x, x8;
+    const uint64_t N = g.N, rows = g.rows;
+    if (!make_map(&w, g.w, N, g.K, g.experts, BM) || !make_map(&x, g.x, N, rows, 1, Geom<STORE>::tn / 2) || !make_map(&x8, g.x, N, rows, 1, 8))
+        return TPMLP_ERR_CUDA;
+    return g.gated ? launch_rows<false, DSWIGLU>(w, x, x8, a, dev, st) : launch_rows<false, STORE>(w, x, x8, a, dev, st);
+}
+
+tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st) {
+    Args a = common(g, dev);
+    a.features = static_cast<int>(g.K);
+    a.cols = static_cast<int>(g.N);
+    a.m_blocks = (a.features + 255) / 256;
+    a.n_blocks = (a.cols + 255) / 256;
+    a.out = g.out;
+    a.ld = g.N;
+    a.out_f32 = g.out_f32;
+    static PerDevice<bool> done;
+    if (!set_smem(dw_kernel, dev.device, DW_SMEM, done)) return TPMLP_ERR_CUDA;
+    CUtensorMap x, y;
+    const uint64_t K = g.K, rows = g.rows;
+    if (!(g.src ? make_map(&x, g.x, K, g.tokens, 1, 1, 2) : make_map(&x, g.x, K, rows, 1, BK)) || !make_map(&y, g.dy, g.N, rows, 1, BK))
+        return TPMLP_ERR_CUDA;
+    const int64_t tiles = int64_t(a.experts) * a.m_blocks * a.n_blocks;
+    const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles, dev.sm_count / 2));
+    const tpmlp_status st1 = launch(dw_kernel, dim3(2 * pairs), THREADS, DW_SMEM, 2, st, x, y, a);
+    if (st1 != TPMLP_OK || g.dbias == nullptr) return st1;
+    return launch(sums_kernel, dim3(static_cast<unsigned>((g.N + 63) / 64), static_cast<unsigned>(g.experts)), SUM_THREADS, 0, 1, st,
+                  static_cast<const __nv_bfloat16*>(g.dy), g.offsets, a.rows, a.cols, g.dbias, a.out_f32);
+}
+
+}  // namespace tpmlp

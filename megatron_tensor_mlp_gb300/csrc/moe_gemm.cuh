@@ -1,0 +1,818 @@
+// Products grouped by expert on the bf16 tensor cores (tcgen05, CTA pairs), rows sorted by expert, the
+// experts' row ranges read on the device.
+//
+//   rows kernel   Y[r][n] = sum_k X[src r][k] W[e][k][n]       (W as it is, "forward")
+//                 dX[r][k] = sum_n dY[r][n] W[e][k][n]         (W transposed, "dx")
+//   dw kernel     dW[e][k][n] = sum over rows r of e of X[src r][k] dY[r][n]
+//
+// The rows kernel puts the weights' features on the 256 rows of a pair's tile and the tokens on its columns, so a
+// tile holds any multiple of 16 tokens up to 256 and an expert with few rows costs the tensor cores, and the way
+// from L2, only what it has: the row range of an expert is cut into equal tiles, at most 256 tokens each.  (With
+// tokens on the tile's rows every expert would end in a partly empty tile of 256.)  Accumulators come out
+// transposed, a feature in each tensor-memory lane; they are read as 8x8 fragments and turned by stmatrix on the
+// way to rows in memory.
+//
+// The gated first layer keeps two accumulators of 128 tokens, gate and up features of the same indices on the
+// same lanes, fed from one copy of the tokens.
+#pragma once
+#include "gemm_tc.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace tpmlp {
+namespace moe {
+
+constexpr int MAX_EXPERTS = 1024;
+constexpr int BM = 128;  // features of one CTA's half of a tile (rows kernel)
+constexpr int BK = 64;   // contraction per ring stage: 128-byte rows
+constexpr int CHUNK = BK * 128;        // 64 features x 64 k, or 64 tokens x 64 k
+constexpr int THREADS = 384;           // warp 0 TMA, warp 1 MMA, warps 2-3 (dw: row tails), warps 4-11 epilogue
+constexpr int EPI_WARP = 4;
+constexpr int EPI_WARPS = 8;
+constexpr int GROUP = 16;              // token tiles walked together, so that tiles in flight share weights and tokens
+constexpr int TABLE = 2 * (MAX_EXPERTS + 1) * 4;
+
+enum Mode : int { STORE = 0, SWIGLU = 1, DSWIGLU = 2 };
+
+struct Args {
+    const int* offsets;  // [experts + 1]
+    const int* src;      // token of each row, may be null
+    int rows, tokens, experts;
+    int kb;              // rows kernel: blocks of 64 of the contraction
+    int features;        // rows kernel: features on the tile's rows (SWIGLU, DSWIGLU: gate features); dw: K
+    int cols;            // dw: N
+    int m_blocks;        // rows kernel: blocks of 256 features; dw: of K
+    int n_blocks;        // dw: blocks of 256 of N
+    void* out; long long ld;        // row pitch of out (elements)
+    int out_f32;
+    const __nv_bfloat16* bias;      // [experts][bias_ld], packed for SWIGLU
+    long long bias_ld;
+    __nv_bfloat16* h_out;           // SWIGLU: packed pre-activations, may be null; DSWIGLU reads h_in
+    const __nv_bfloat16* h_in;
+    long long h_ld;
+    uint32_t* status;
+    unsigned long long timeout_ns;
+};
+
+// Bounded waits.  They go by their time limit alone: a status word that a bad plan has set does not end them.
+__device__ __forceinline__ bool wait(const Args& p, uint64_t* bar, uint32_t parity, uint32_t where) {
+    return mbar_wait_bounded(bar, parity, p.status, p.timeout_ns, where, false);
+}
+__device__ __forceinline__ bool wait_warp(const Args& p, uint64_t* bar, uint32_t parity, uint32_t where) {
+    return mbar_wait_bounded_warp(bar, parity, p.status, p.timeout_ns, where, false);
+}
+
+// ---------------------------------------------------------------- the experts' row ranges and tiles
+// Row ranges are clamped to the rows that there are; a range that had to be is reported, its product left out or cut.
+struct Table {
+    int* off;    // [experts + 1] first row
+    int* first;  // [experts + 1] first tile
+    __device__ __forceinline__ explicit Table(void* smem)
+        : off(static_cast<int*>(smem)), first(static_cast<int*>(smem) + MAX_EXPERTS + 1) {}
+    __device__ __forceinline__ int count(int e) const { return max(off[e + 1] - off[e], 0); }
+    // All threads.  tile(n) gives the tiles of an expert of n rows.
+    template <int NTHREADS, typename F>
+    __device__ __forceinline__ void build(const Args& p, F&& tiles) {
+        bool bad = false;
+        for (int i = threadIdx.x; i <= p.experts; i += NTHREADS) {
+            const int v = p.offsets[i], c = min(max(v, 0), p.rows);
+            bad |= v != c;
+            off[i] = c;
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const int lane = threadIdx.x;
+            int carry = 0;
+            for (int e0 = 0; e0 < p.experts; e0 += 32) {
+                const int e = e0 + lane;
+                int v = 0;
+                if (e < p.experts) {
+                    bad |= off[e + 1] < off[e];
+                    v = tiles(count(e));
+                }
+                int sum = v;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                    if (lane >= d) sum += o;
+                }
+                if (e < p.experts) first[e] = carry + sum - v;
+                carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
+            }
+            if (lane == 0) first[p.experts] = carry;
+        }
+        if (bad && blockIdx.x == 0) atomicCAS(p.status, 0u, kStatusDevice);
+        __syncthreads();
+    }
+};
+
+// Tokens of a tile: an expert's n rows in ceil(n / TN) tiles of equal size, a multiple of 16.  (The last one is
+// never empty: with a size below TN there are fewer than TN / 16 tiles.)
+template <int TN>
+__device__ __forceinline__ int tile_tokens(int n) {
+    const int nt = (n + TN - 1) / TN;
+    return ((n + nt - 1) / nt + 15) & ~15;
+}
+
+struct Tile {
+    int e, mb, row0, n;  // expert, feature block, first row, rows (0: past the last tile)
+};
+// Tile t; e is where the walk stands (tiles come in increasing order).
+template <int TN>
+__device__ __forceinline__ Tile decode(const Args& p, const Table& tab, int t, int& e) {
+    while (e < p.experts && t >= tab.first[e + 1]) ++e;
+    if (e >= p.experts) return Tile{0, 0, 0, 0};
+    const int n = tab.count(e), nt = (n + TN - 1) / TN, sz = tile_tokens<TN>(n);
+    const int l = t - tab.first[e], per_group = GROUP * p.m_blocks;
+    const int g = l / per_group, r = l - g * per_group, gt = min(nt - g * GROUP, GROUP);
+    const int tb = g * GROUP + r % gt;
+    return Tile{e, r / gt, tab.off[e] + tb * sz, min(sz, n - tb * sz)};
+}
+
+// ---------------------------------------------------------------- epilogue pieces
+// A warp's staging of 32 tokens x 32 features, bf16: rows of 64 bytes, their four 16-byte pieces permuted so that
+// the eight rows of an 8x8 matrix lie in different banks.
+constexpr int STAGE = 32 * 64;
+__device__ __forceinline__ uint32_t stage_at(int token, int piece) {
+    return static_cast<uint32_t>(token * 64 + ((piece ^ ((token >> 1) & 3)) << 4));
+}
+// lo, hi: packed fragments of features 0-15 and 16-31, a word per (8 tokens, 8 features): index 2 i + j.
+__device__ __forceinline__ void stage_put(uint32_t buf, const uint32_t (&lo)[8], const uint32_t (&hi)[8], int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        stmatrix_x4_trans(buf + stage_at(i * 8 + (lane & 7), lane >> 3), lo[2 * i], lo[2 * i + 1], hi[2 * i], hi[2 * i + 1]);
+}
+__device__ __forceinline__ void stage_get(uint32_t buf, uint32_t (&lo)[8], uint32_t (&hi)[8], int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t r[4];
+        ldmatrix_x4_trans(buf + stage_at(i * 8 + (lane & 7), lane >> 3), r);
+        lo[2 * i] = r[0];
+        lo[2 * i + 1] = r[1];
+        hi[2 * i] = r[2];
+        hi[2 * i + 1] = r[3];
+    }
+}
+// The staged rows to memory: dst is row 0's first feature, n rows, nf features (a multiple of 8) of the 32.
+__device__ __forceinline__ void stage_store(const uint8_t* buf, __nv_bfloat16* dst, long long ld, int n, int nf, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = i * 8 + (lane >> 2), c = lane & 3;
+        if (t < n && c * 8 < nf) *reinterpret_cast<uint4*>(dst + t * ld + c * 8) = *reinterpret_cast<const uint4*>(buf + stage_at(t, c));
+    }
+}
+__device__ __forceinline__ void stage_load(uint8_t* buf, const uint4 (&v)[4], int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + stage_at(i * 8 + (lane >> 2), lane & 3)) = v[i];
+}
+__device__ __forceinline__ void rows_load(const __nv_bfloat16* src, long long ld, int n, int nf, int lane, uint4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = i * 8 + (lane >> 2), c = lane & 3;
+        v[i] = t < n && c * 8 < nf ? *reinterpret_cast<const uint4*>(src + t * ld + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// 32 lanes x 32 columns as fragments: a, lanes 0-15, b, lanes 16-31.
+__device__ __forceinline__ void load_frags(uint32_t taddr, uint32_t (&a)[16], uint32_t (&b)[16]) {
+    tmem_ld_16x256b_x4(taddr, a);
+    tmem_ld_16x256b_x4(taddr + (16u << 16), b);
+}
+// Bias of this thread's four features (t / 4 + 0, 8, 16, 24) of 32 from f0; zero past nf.
+__device__ __forceinline__ void load_bias(const __nv_bfloat16* bias, int nf, int lane, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int f = i * 8 + (lane >> 2);
+        v[i] = bias != nullptr && f < nf ? __bfloat162float(bias[f]) : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------- rows kernel
+template <int MODE>
+struct Geom {
+    static constexpr int tn = MODE == SWIGLU ? 128 : 256;              // tokens of a tile at most
+    static constexpr int a_bytes = (MODE == SWIGLU ? 2 : 1) * BM * 128;  // this CTA's features of a stage
+    static constexpr int b_bytes = tn / 2 * 128;                       // this CTA's half of the tokens
+    static constexpr int stage = a_bytes + b_bytes;
+    static constexpr int epi = (MODE == DSWIGLU ? 2 : 1) * STAGE;      // staging of an epilogue warp
+    static constexpr int stages = MODE == STORE ? 6 : 5;
+    static constexpr int smem = 1024 + stages * stage + EPI_WARPS * epi + TABLE + 256;
+    static_assert(smem <= 227 * 1024, "rows kernel shared memory");
+};
+
+template <bool W_MN, int MODE>
+__global__ void __launch_bounds__(THREADS, 1)
+    rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                const __grid_constant__ CUtensorMap tmX8, const Args p) {
+    using G = Geom<MODE>;
+    constexpr int S = G::stages, TN = G::tn;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + S * G::a_bytes;
+    uint8_t* sE = smem + S * G::stage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sE + EPI_WARPS * G::epi);
+    uint64_t* empty = full + S;
+    uint64_t* tfull = empty + S;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    Table tab(reinterpret_cast<uint8_t*>(full) + 256);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t prank = cluster_ctarank();
+    const bool leader = prank == 0;
+    const int cluster_id = blockIdx.x / 2, n_clusters = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull + a, 1);
+            mbar_init(tempty + a, 2 * EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmX8);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the peer may signal the leader's barriers from here on
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_wait();  // no global memory is touched before the kernel ahead has completed
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    tab.build<THREADS>(p, [&](int n) { return (n + TN - 1) / TN * p.m_blocks; });
+    const int n_tiles = tab.first[p.experts];
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer (both CTAs), a whole warp
+        int stage = 0, e = 0;
+        uint32_t phase = 0, armed = 0, last_parity = 0;
+        bool ok = true;
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+            const Tile c = decode<TN>(p, tab, t, e);
+            const int nn = (c.n + 15) & ~15, half = nn / 2;  // columns of the MMA, tokens of this CTA
+            const int row0 = c.row0 + static_cast<int>(prank) * half;
+            const int f0 = MODE == SWIGLU ? (c.mb * 2 + static_cast<int>(prank)) * 256 : c.mb * 256 + static_cast<int>(prank) * BM;
+            int4 at = make_int4(0, 0, 0, 0);
+            if (p.src != nullptr && lane * 4 < half) {
+                int* a = reinterpret_cast<int*>(&at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int v = p.src[min(row0 + lane * 4 + i, c.row0 + c.n - 1)], w = min(max(v, 0), p.tokens - 1);
+                    if (v != w) atomicCAS(p.status, 0u, kStatusDevice);
+                    a[i] = w;
+                }
+            }
+            for (int it = 0; it < p.kb; ++it) {
+                if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = full0 + stage * 8;
+                uint8_t* a_dst = sA + stage * G::a_bytes;
+                uint8_t* b_dst = sB + stage * G::b_bytes;
+                if (lane == 0) {
+                    if (leader) {
+                        mbar_arrive_expect_tx(full + stage, 2 * G::a_bytes + nn * 128);
+                        armed |= 1u << stage;
+                        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                    }
+                    if constexpr (!W_MN) {
+                        tma_load_3d_pair(a_dst, &tmW, bar, it * BK, f0, c.e);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < G::a_bytes / CHUNK; ++j)
+                            tma_load_3d_pair(a_dst + j * CHUNK, &tmW, bar, f0 + j * 64, it * BK, c.e);
+                    }
+                }
+                if (p.src != nullptr) {
+                    if (lane * 4 < half) tma_gather4_pair(b_dst + lane * 512, &tmX, bar, it * BK, at);
+                } else if (nn == TN) {
+                    if (lane == 0) tma_load_3d_pair(b_dst, &tmX, bar, it * BK, row0, 0);
+                } else if (lane * 8 < half) {
+                    tma_load_3d_pair(b_dst + lane * 1024, &tmX8, bar, it * BK, row0 + lane * 8, 0);
+                }
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (ok) {
+            // every stage's last use released: the commits' arrivals, possibly from the other SM, have landed
+            for (int i = 0; i < S; ++i) {
+                if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereDrain)) break;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        } else if (lane == 0) {
+            if (leader) {
+                for (int s = 0; s < S; ++s)  // the leader's barriers count both CTAs' copies: wait for all of them
+                    if (armed & (1u << s))
+                        wait(p, full + s, (last_parity >> s) & 1u, kWhereDrain);
+            } else {
+                spin_ns(200000);  // let this CTA's last copies land before either CTA can exit
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            if (leader) {
+                // -------------------------------------------------------- MMA issuer (leader)
+                const uint64_t a0 = W_MN ? sdesc_sw128(smem_u32(sA), CHUNK, 1024) : sdesc_sw128(smem_u32(sA), 16, 1024);
+                const uint64_t b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+                constexpr uint64_t a_step = W_MN ? (2048 >> 4) : (32 >> 4);
+                int stage = 0, lt = 0, e = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                for (int t = cluster_id; t < n_tiles && ok; t += n_clusters, ++lt) {
+                    const Tile c = decode<TN>(p, tab, t, e);
+                    const uint32_t idesc = idesc_bf16_f32(2 * BM, (c.n + 15) & ~15, W_MN, false);
+                    const int acc = lt & 1;
+                    if (!wait(p, tempty + acc, ((lt >> 1) & 1) ^ 1u, kWhereMma)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + acc * 256;
+                    for (int it = 0; it < p.kb; ++it) {
+                        if (!wait(p, full + stage, phase, kWhereMma)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t a = a0 + static_cast<uint64_t>(stage * (G::a_bytes >> 4));
+                        const uint64_t b = b0 + static_cast<uint64_t>(stage * (G::b_bytes >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            const uint32_t add = (it | kk) != 0 ? 1u : 0u;
+                            umma_f16_pair(d, a + kk * a_step, b + kk * 2, idesc, add);
+                            if constexpr (MODE == SWIGLU)
+                                umma_f16_pair(d + 128, a + (BM * 128 >> 4) + kk * a_step, b + kk * 2, idesc, add);
+                        }
+                        umma_commit_pair_mc(empty + stage, 0x3);
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (ok) umma_commit_pair_mc(tfull + acc, 0x3);
+                }
+                umma_commit_pair_mc(drain, 0x3);
+                // both accumulators' last releases land before this CTA can exit
+                for (int i = 0; ok && i < 2; ++i, ++lt)
+                    ok = wait(p, tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, kWhereDrain);
+            }
+            wait(p, drain, 0, kWhereDrain);
+        }
+    } else if (warp >= EPI_WARP) {
+        // ---------------------------------------------------------------- epilogue (both CTAs)
+        const int q = warp & 3, half = (warp - EPI_WARP) >> 2;
+        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+        uint8_t* buf = sE + (warp - EPI_WARP) * G::epi;
+        const uint32_t sbuf = smem_u32(buf);
+        int lt = 0, e = 0;
+        for (int t = cluster_id; t < n_tiles; t += n_clusters, ++lt) {
+            const Tile c = decode<TN>(p, tab, t, e);
+            const int acc = lt & 1;
+            int okw = 0;
+            if (lane == 0) okw = wait(p, tfull + acc, (lt >> 1) & 1, kWhereEpilogue);
+            okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
+            if (!okw) break;
+            tc_fence_after();
+            const int f0 = c.mb * 256 + static_cast<int>(prank) * BM + q * 32;  // features f0 .. f0 + 31 (of the gate's)
+            const int nf = min(p.features - f0, 32);
+            const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+            const long long packed = static_cast<long long>(f0 >> 7) * 256 + (f0 & 127);
+            [[maybe_unused]] float bias[4], bias_up[4];
+            if constexpr (MODE == STORE) {
+                load_bias(p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + f0, nf, lane, bias);
+            } else if constexpr (MODE == SWIGLU) {
+                const __nv_bfloat16* b = p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + packed;
+                load_bias(b, nf, lane, bias);
+                load_bias(b == nullptr ? nullptr : b + 128, nf, lane, bias_up);
+            }
+            for (int c0 = half * (TN / 2); c0 < (half + 1) * (TN / 2) && c0 < c.n && nf > 0; c0 += 32) {
+                const int n = min(c.n - c0, 32);
+                const long long row = c.row0 + c0;
+                if constexpr (MODE == STORE) {
+                    if (p.out_f32) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(lanes + c0, r);
+                        const float b = p.bias != nullptr && lane < nf ? __bfloat162float(p.bias[c.e * p.bias_ld + f0 + lane]) : 0.0f;
+                        tmem_ld_wait();
+                        float* dst = static_cast<float*>(p.out) + row * p.ld + f0 + lane;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < n && lane < nf) dst[j * p.ld] = __uint_as_float(r[j]) + b;
+                        continue;
+                    }
+                }
+                uint32_t a[16], b[16], lo[8], hi[8];
+                load_frags(lanes + c0, a, b);
+                if constexpr (MODE == STORE) {
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float ba = bias[i & 1], bb = bias[2 + (i & 1)];
+                        lo[i] = tc::pack_bf16x2(__uint_as_float(a[2 * i]) + ba, __uint_as_float(a[2 * i + 1]) + ba);
+                        hi[i] = tc::pack_bf16x2(__uint_as_float(b[2 * i]) + bb, __uint_as_float(b[2 * i + 1]) + bb);
+                    }
+                    stage_put(sbuf, lo, hi, lane);
+                    __syncwarp();
+                    stage_store(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, n, nf, lane);
+                    __syncwarp();
+                } else if constexpr (MODE == SWIGLU) {
+                    uint32_t ua[16], ub[16];
+                    load_frags(lanes + 128 + c0, ua, ub);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int j = (i >> 1) & 1;
+                        a[i] = __float_as_uint(__uint_as_float(a[i]) + bias[j]);
+                        b[i] = __float_as_uint(__uint_as_float(b[i]) + bias[2 + j]);
+                        ua[i] = __float_as_uint(__uint_as_float(ua[i]) + bias_up[j]);
+                        ub[i] = __float_as_uint(__uint_as_float(ub[i]) + bias_up[2 + j]);
+                    }
+                    if (p.h_out != nullptr) {
+                        __nv_bfloat16* h = p.h_out + row * p.h_ld + packed;
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                lo[i] = tc::pack_bf16x2(__uint_as_float((part ? ua : a)[2 * i]), __uint_as_float((part ? ua : a)[2 * i + 1]));
+                                hi[i] = tc::pack_bf16x2(__uint_as_float((part ? ub : b)[2 * i]), __uint_as_float((part ? ub : b)[2 * i + 1]));
+                            }
+                            stage_put(sbuf, lo, hi, lane);
+                            __syncwarp();
+                            stage_store(buf, h + part * 128, p.h_ld, n, nf, lane);
+                            __syncwarp();
+                        }
+                    }
+                    auto gated = [](uint32_t g, uint32_t u) {
+                        const float x = __uint_as_float(g);
+                        return x * tc::sigmoid_approx(x) * __uint_as_float(u);
+                    };
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        lo[i] = tc::pack_bf16x2(gated(a[2 * i], ua[2 * i]), gated(a[2 * i + 1], ua[2 * i + 1]));
+                        hi[i] = tc::pack_bf16x2(gated(b[2 * i], ub[2 * i]), gated(b[2 * i + 1], ub[2 * i + 1]));
+                    }
+                    stage_put(sbuf, lo, hi, lane);
+                    __syncwarp();
+                    stage_store(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, n, nf, lane);
+                    __syncwarp();
+                } else {
+                    const __nv_bfloat16* h = p.h_in + row * p.h_ld + packed;
+                    uint4 g4[4], u4[4];
+                    rows_load(h, p.h_ld, n, nf, lane, g4);
+                    rows_load(h + 128, p.h_ld, n, nf, lane, u4);
+                    stage_load(buf, g4, lane);
+                    stage_load(buf + STAGE, u4, lane);
+                    __syncwarp();
+                    uint32_t glo[8], ghi[8], ulo[8], uhi[8];
+                    stage_get(sbuf, glo, ghi, lane);
+                    stage_get(sbuf + STAGE, ulo, uhi, lane);
+                    tmem_ld_wait();
+                    __syncwarp();
+                    // dg = dy u silu'(g), du = dy silu(g)
+                    auto grad = [](float dy, float g, float u, float& dg, float& du) {
+                        const float s = tc::sigmoid_approx(g);
+                        du = dy * g * s;
+                        dg = dy * u * (s * (1.0f + g * (1.0f - s)));
+                    };
+                    auto pair = [&](uint32_t d0, uint32_t d1, uint32_t& g, uint32_t& u) {
+                        float g0, g1, u0, u1;
+                        grad(__uint_as_float(d0), lo_f(g), lo_f(u), g0, u0);
+                        grad(__uint_as_float(d1), hi_f(g), hi_f(u), g1, u1);
+                        g = tc::pack_bf16x2(g0, g1);
+                        u = tc::pack_bf16x2(u0, u1);
+                    };
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        pair(a[2 * i], a[2 * i + 1], glo[i], ulo[i]);
+                        pair(b[2 * i], b[2 * i + 1], ghi[i], uhi[i]);
+                    }
+                    stage_put(sbuf, glo, ghi, lane);
+                    stage_put(sbuf + STAGE, ulo, uhi, lane);
+                    __syncwarp();
+                    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.out) + row * p.ld + packed;
+                    stage_store(buf, d, p.ld, n, nf, lane);
+                    stage_store(buf + STAGE, d + 128, p.ld, n, nf, lane);
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + acc * 8);
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while its peer may still touch its shared or tensor memory
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------- dw kernel
+// dW[e] = X_e^T dY_e: both operands have the rows as their contraction, 64 to a stage.  An expert's last block may end
+// inside a stage: the rows behind it, the next expert's, are in the copy too and are set to zero in shared memory
+// (both operands': a zero times the other's infinity would be a NaN).  Such a stage's copies report to a barrier of
+// their own CTA; its warp 2 waits for them, clears the rows and tells the leader's MMA warp.
+constexpr int DW_STAGES = 6;
+constexpr int DW_A = BM * 128, DW_B = BM * 128, DW_STAGE = DW_A + DW_B;
+constexpr int DW_SMEM = 1024 + DW_STAGES * DW_STAGE + TABLE + 512;
+static_assert(DW_SMEM <= 227 * 1024, "dw kernel shared memory");
+
+__global__ void __launch_bounds__(THREADS, 1)
+    dw_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, const Args p) {
+    constexpr int S = DW_STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + S * DW_A;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * DW_STAGE);
+    uint64_t* empty = full + S;
+    uint64_t* tload = empty + S;  // a stage with an expert's last rows: this CTA's copies
+    uint64_t* tdone = tload + S;  // leader: both CTAs' rows behind the last cleared
+    uint64_t* tfull = tdone + S;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    Table tab(reinterpret_cast<uint8_t*>(full) + 512);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t prank = cluster_ctarank();
+    const bool leader = prank == 0;
+    const int cluster_id = blockIdx.x / 2, n_clusters = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+            mbar_init(tload + s, 1);
+            mbar_init(tdone + s, 2);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull + a, 1);
+            mbar_init(tempty + a, 2 * EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmY);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    tab.build<THREADS>(p, [&](int) { return p.m_blocks * p.n_blocks; });
+    const int n_tiles = tab.first[p.experts];  // every expert has its tiles, one without rows to write zeros
+    const int per_expert = p.m_blocks * p.n_blocks;
+    // tile t: expert, block of K, block of N; groups of GROUP blocks of K walked together
+    auto place = [&](int t, int& e, int& mb, int& nb) {
+        e = t / per_expert;
+        const int l = t - e * per_expert, per_group = GROUP * p.n_blocks;
+        const int g = l / per_group, r = l - g * per_group, gm = min(p.m_blocks - g * GROUP, GROUP);
+        mb = g * GROUP + r % gm;
+        nb = r / gm;
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer (both CTAs), a whole warp
+        int stage = 0;
+        uint32_t phase = 0, armed = 0, last_parity = 0, t_armed = 0, t_parity = 0;  // t_parity: a tail's next phase by stage
+        bool ok = true;
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+            int e, mb, nb;
+            place(t, e, mb, nb);
+            const int n = tab.count(e), base = tab.off[e], kb = (n + BK - 1) / BK;
+            const int a0 = mb * 256 + static_cast<int>(prank) * BM, b0 = nb * 256 + static_cast<int>(prank) * BM;
+            for (int it = 0; it < kb; ++it) {
+                const bool tail = (it + 1) * BK > n;
+                int4 at = make_int4(0, 0, 0, 0);
+                if (p.src != nullptr) {  // lanes 0-15 the first 64 features, lanes 16-31 the next
+                    int* a = reinterpret_cast<int*>(&at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int v = p.src[base + min(it * BK + (lane & 15) * 4 + i, n - 1)], w = min(max(v, 0), p.tokens - 1);
+                        if (v != w) atomicCAS(p.status, 0u, kStatusDevice);
+                        a[i] = w;
+                    }
+                }
+                if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* a_dst = sA + stage * DW_A;
+                uint8_t* b_dst = sB + stage * DW_B;
+                const uint32_t bar = tail ? smem_u32(tload + stage) : full0 + stage * 8;
+                if (lane == 0) {
+                    if (tail) {
+                        mbar_arrive_expect_tx(tload + stage, DW_STAGE);
+                        t_armed |= 1u << stage;
+                        t_parity ^= 1u << stage;
+                        if (leader) mbar_arrive(full + stage);
+                    } else if (leader) {
+                        mbar_arrive_expect_tx(full + stage, 2 * DW_STAGE);
+                        armed |= 1u << stage;
+                        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (p.src == nullptr) tma_load_3d_pair(a_dst + j * CHUNK, &tmX, bar, a0 + j * 64, base + it * BK, 0);
+                        tma_load_3d_pair(b_dst + j * CHUNK, &tmY, bar, b0 + j * 64, base + it * BK, 0);
+                    }
+                }
+                if (p.src != nullptr)
+                    tma_gather4_pair(a_dst + (lane >> 4) * CHUNK + (lane & 15) * 512, &tmX, bar, a0 + (lane >> 4) * 64, at);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (ok) {
+            for (int i = 0; i < S; ++i) {
+                if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereDrain)) break;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        } else if (lane == 0) {
+            for (int s = 0; s < S; ++s) {
+                if (t_armed & (1u << s))  // t_parity has passed on to the next phase
+                    wait(p, tload + s, ((t_parity >> s) & 1u) ^ 1u, kWhereDrain);
+                if (leader && (armed & (1u << s)))
+                    wait(p, full + s, (last_parity >> s) & 1u, kWhereDrain);
+            }
+            if (!leader) spin_ns(200000);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            if (leader) {
+                // -------------------------------------------------------- MMA issuer (leader)
+                constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, 2 * BM, true, true);
+                const uint64_t a0 = sdesc_sw128(smem_u32(sA), CHUNK, 1024), b0 = sdesc_sw128(smem_u32(sB), CHUNK, 1024);
+                int stage = 0, lt = 0;
+                uint32_t phase = 0, t_parity = 0;
+                bool ok = true;
+                for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+                    int e, mb, nb;
+                    place(t, e, mb, nb);
+                    const int n = tab.count(e), kb = (n + BK - 1) / BK;
+                    if (kb == 0) continue;
+                    const int acc = lt & 1;
+                    if (!wait(p, tempty + acc, ((lt >> 1) & 1) ^ 1u, kWhereMma)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + acc * 256;
+                    for (int it = 0; it < kb; ++it) {
+                        const bool tail = (it + 1) * BK > n;
+                        ok = wait(p, full + stage, phase, kWhereMma);
+                        if (ok && tail) {
+                            ok = mbar_wait_bounded_cluster(tdone + stage, (t_parity >> stage) & 1u, p.status, p.timeout_ns, kWhereMma, false);
+                            t_parity ^= 1u << stage;
+                            fence_proxy_async_all();
+                        }
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t a = a0 + static_cast<uint64_t>(stage * (DW_A >> 4));
+                        const uint64_t b = b0 + static_cast<uint64_t>(stage * (DW_B >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            umma_f16_pair(d, a + kk * (2048 >> 4), b + kk * (2048 >> 4), idesc, (it | kk) != 0 ? 1u : 0u);
+                        umma_commit_pair_mc(empty + stage, 0x3);
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (ok) umma_commit_pair_mc(tfull + acc, 0x3);
+                    ++lt;
+                }
+                umma_commit_pair_mc(drain, 0x3);
+                for (int i = 0; ok && i < 2; ++i, ++lt)
+                    ok = wait(p, tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, kWhereDrain);
+            }
+            wait(p, drain, 0, kWhereDrain);
+        }
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- rows behind an expert's last (both CTAs)
+        int stage = 0;
+        uint32_t t_parity = 0;
+        bool ok = true;
+        const uint32_t done0 = mapa_shared(smem_u32(tdone), 0);
+        for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+            int e, mb, nb;
+            place(t, e, mb, nb);
+            const int n = tab.count(e), kb = (n + BK - 1) / BK, live = n - (kb - 1) * BK;  // rows of the last block
+            stage = (stage + kb) % S;
+            if (kb == 0 || live == BK) continue;
+            const int s = (stage + S - 1) % S;
+            ok = wait_warp(p, tload + s, (t_parity >> s) & 1u, kWhereProducer);
+            t_parity ^= 1u << s;
+            if (!ok) break;
+            // 2 operands x 2 chunks of 64 rows of 128 bytes
+            const int gone = (BK - live) * 8;  // 16-byte pieces of a chunk
+            for (int i = lane; i < 4 * gone; i += 32) {
+                const int part = i / gone, at = live * 128 + (i - part * gone) * 16;
+                uint8_t* dst = (part < 2 ? sA + s * DW_A : sB + s * DW_B) + (part & 1) * CHUNK + at;
+                *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(done0 + s * 8);
+        }
+    } else if (warp >= EPI_WARP) {
+        // ---------------------------------------------------------------- epilogue (both CTAs)
+        const int q = warp & 3, half = (warp - EPI_WARP) >> 2;
+        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+        const bool st32 = ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) && (p.ld * (p.out_f32 ? 4 : 2)) % 32 == 0;
+        int lt = 0;
+        for (int t = cluster_id; t < n_tiles; t += n_clusters) {
+            int e, mb, nb;
+            place(t, e, mb, nb);
+            const bool none = tab.count(e) == 0;
+            const int acc = lt & 1;
+            if (!none) {
+                int okw = 0;
+                if (lane == 0) okw = wait(p, tfull + acc, (lt >> 1) & 1, kWhereEpilogue);
+                okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
+                if (!okw) break;
+                tc_fence_after();
+            }
+            const int k = mb * 256 + static_cast<int>(prank) * BM + q * 32 + lane;
+            const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+            for (int c0 = half * 128; c0 < half * 128 + 128 && nb * 256 + c0 < p.cols; c0 += 32) {
+                float v[32];
+                if (none) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                } else {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(lanes + c0, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                }
+                if (k < p.features) {
+                    const long long at = (static_cast<long long>(e) * p.features + k) * p.ld + nb * 256 + c0;
+                    const int nvalid = p.cols - (nb * 256 + c0);
+                    if (p.out_f32) tc::store_f32x32(static_cast<float*>(p.out) + at, v, nvalid, st32);
+                    else tc::store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + at, v, nvalid, st32);
+                }
+            }
+            if (none) continue;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + acc * 8);
+            ++lt;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+}  // namespace moe
+}  // namespace tpmlp

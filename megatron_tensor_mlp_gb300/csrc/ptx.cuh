@@ -256,12 +256,13 @@ __device__ __forceinline__ bool mbar_try_wait_acq_cluster(uint64_t* bar, uint32_
 }
 // mbar_wait_bounded with cluster-scope acquire (for barriers that other CTAs arrive on).
 __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_t parity, uint32_t* status,
-                                                          uint64_t timeout_ns, uint32_t where) {
+                                                          uint64_t timeout_ns, uint32_t where,
+                                                          bool watch_status = true) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t spin = 0;; ++spin) {
         if (mbar_try_wait_acq_cluster(bar, parity, 1000000u)) return true;
         if ((spin & 7u) == 7u) {
-            if (ld_volatile_u32(status) != 0u) return false;
+            if (watch_status && ld_volatile_u32(status) != 0u) return false;
             if (globaltimer_ns() - t0 > timeout_ns) {
                 atomicCAS(status, 0u, kStatusTimeout | where);
                 return false;
@@ -305,6 +306,48 @@ __device__ __forceinline__ void umma_commit_pair_mc(uint64_t* bar, uint16_t cta_
             smem_u32(bar)),
         "h"(cta_mask)
         : "memory");
+}
+// Four rows of a 2-D tensor, 64 bf16 columns from x of each, into consecutive 128-byte rows of shared memory
+// (tile::gather4; the map's box is one row high).  The swizzle goes by the shared-memory address, so eight rows
+// of two such loads make the same 1 KiB atom as a plain box of eight rows.
+__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x, int4 rows) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_gather4_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar_cluster_addr, int32_t x,
+                                                 int4 rows) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w),
+        "r"(bar_cluster_addr)
+        : "memory");
+}
+// 16 lanes x 32 consecutive 32-bit columns as 8x8 fragments: of columns 8 i .. 8 i + 7 thread t holds, in r[4 i + 0, 1],
+// columns 2 (t % 4) and the next of lane t / 4 and, in r[4 i + 2, 3], the same of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Four 8x8 matrices of 16-bit values between fragments and shared memory, transposed: lane l gives the address of 16
+// bytes, row l % 8 of matrix l / 8; in the fragment that row is a column.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr)
+                 : "memory");
 }
 // 3-D tiled tensor store shared -> global, tracked in this thread's bulk async-group.
 // Elements of the box outside the tensor are not written.

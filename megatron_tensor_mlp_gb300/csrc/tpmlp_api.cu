@@ -1029,7 +1029,7 @@ const char* tpmlp_status_string(tpmlp_status st) {
 
 const char* tpmlp_last_error(void) { return t_err; }
 
-int tpmlp_version(void) { return 300; }
+int tpmlp_version(void) { return 400; }
 
 uint64_t tpmlp_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 

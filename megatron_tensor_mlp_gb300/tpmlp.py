@@ -22,7 +22,7 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 BF16, F32 = 0, 1
-ACT_NONE, ACT_GELU_ERF = 0, 1
+ACT_NONE, ACT_GELU_ERF, ACT_SWIGLU = 0, 1, 2
 
 STATUS = {0: "TPMLP_OK", 1: "TPMLP_ERR_NULL", 2: "TPMLP_ERR_SHAPE", 3: "TPMLP_ERR_DIVISIBILITY",
           4: "TPMLP_ERR_DTYPE", 5: "TPMLP_ERR_ALIGNMENT", 6: "TPMLP_ERR_ALIAS", 7: "TPMLP_ERR_ARCH",
@@ -60,7 +60,15 @@ _SIGS = {
     "tpmlp_mxfp4_swiglu_mlp_fwd": [_vp] * 10 + [_i64] * 4 + [_i32, _i32, _vp],
     "tpmlp_mxfp4_swiglu_mlp_bwd": [_vp] * 13 + [_i64] * 4 + [_i32, _i32, _i32, _vp],
     "tpmlp_set_mxfp4_mode": [_i32],
-
+    "tpmlp_layernorm_fwd": [_vp] * 6 + [_i64] * 4 + [ctypes.c_float, _i32, _vp],
+    "tpmlp_layernorm_bwd": [_vp] * 9 + [_i64] * 5 + [_i32, _i32, _vp],
+    "tpmlp_moe_route": [_vp] * 7 + [_i64] * 2 + [_i32, _i32, _i32, _vp],
+    "tpmlp_moe_route_bwd": [_vp] * 5 + [_i64] * 2 + [_i32, _i32, _i32, _vp],
+    "tpmlp_moe_matmul": [_vp] * 7 + [_i64] * 5 + [_i32, _i32, _vp],
+    "tpmlp_moe_matmul_dx": [_vp] * 5 + [_i64] * 4 + [_i32, _i32, _vp],
+    "tpmlp_moe_matmul_dw": [_vp] * 6 + [_i64] * 5 + [_i32, _vp],
+    "tpmlp_moe_combine": [_vp] * 4 + [_i64] * 2 + [_i32, _i64, _vp],
+    "tpmlp_moe_combine_bwd": [_vp] * 6 + [_i64] * 2 + [_i32, _i64, _vp],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(lib, _name)
@@ -69,7 +77,8 @@ for _name, _args in _SIGS.items():
 lib.tpmlp_qkv_src_col.argtypes = [_i64, _i64, _i64]
 lib.tpmlp_qkv_src_col.restype = _i64
 for _name, _args in {"tpmlp_mxfp4_code_bytes": [_i64] * 2, "tpmlp_mxfp4_scale_bytes": [_i64] * 2,
-                     "tpmlp_mxfp4_swiglu_ws_bytes": [_i64] * 4 + [_i32, _i32]}.items():
+                     "tpmlp_mxfp4_swiglu_ws_bytes": [_i64] * 4 + [_i32, _i32], "tpmlp_layernorm_ws_bytes": [_i64] * 2,
+                     "tpmlp_moe_route_ws_bytes": [_i64] * 2 + [_i32]}.items():
     _f = getattr(lib, _name)
     _f.argtypes = _args
     _f.restype = _i64
@@ -270,6 +279,74 @@ def tpmlp_set_mxfp4_mode(mode, check=True):
 
 def tpmlp_get_mxfp4_mode() -> int:
     return int(lib.tpmlp_get_mxfp4_mode())
+
+
+def tpmlp_layernorm_fwd(X, gamma, beta, Y, mean, rstd, rows, h, ldx, ldy, eps=1e-5, dt=BF16, stream=None, check=True):
+    """Y = (X - mean) rstd gamma + beta row by row; mean and rstd (or two Nones) are saved for the backward."""
+    st = lib.tpmlp_layernorm_fwd(_ptr(X), _ptr(gamma), _ptr(beta), _ptr(Y), _ptr(mean), _ptr(rstd), rows, h, ldx, ldy, eps, dt,
+                                 _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_layernorm_ws_bytes(rows, h) -> int:
+    return int(lib.tpmlp_layernorm_ws_bytes(rows, h))
+
+
+def tpmlp_layernorm_bwd(X, gamma, mean, rstd, dY, dX, dgamma, dbeta, ws, rows, h, ldx, lddy, lddx, dt=BF16, grad_dt=F32, stream=None,
+                        check=True):
+    st = lib.tpmlp_layernorm_bwd(_ptr(X), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dY), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
+                                 rows, h, ldx, lddy, lddx, dt, grad_dt, _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_moe_route_ws_bytes(tokens, experts, k) -> int:
+    return int(lib.tpmlp_moe_route_ws_bytes(tokens, experts, k))
+
+
+def tpmlp_moe_route(logits, ids, weights, offsets, row_token, slot_row, ws, tokens, experts, k, chosen=1, dt=BF16, stream=None,
+                    check=True):
+    """Each token's k experts, their weights (softmax over all experts, or over the chosen ones) and the rows sorted by expert."""
+    st = lib.tpmlp_moe_route(_ptr(logits), _ptr(ids), _ptr(weights), _ptr(offsets), _ptr(row_token), _ptr(slot_row), _ptr(ws), tokens,
+                             experts, k, int(chosen), dt, _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_moe_route_bwd(logits, ids, weights, dweights, dlogits, tokens, experts, k, chosen=1, dt=BF16, stream=None, check=True):
+    st = lib.tpmlp_moe_route_bwd(_ptr(logits), _ptr(ids), _ptr(weights), _ptr(dweights), _ptr(dlogits), tokens, experts, k, int(chosen),
+                                 dt, _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_moe_matmul(X, row_token, offsets, W, bias, Y, H, tokens, rows, experts, K, N, act=ACT_NONE, out_dt=BF16, stream=None,
+                     check=True):
+    """Y[r] = act(X[row_token[r]] W[e] + bias[e]) for the rows r of each expert e."""
+    st = lib.tpmlp_moe_matmul(_ptr(X), _ptr(row_token), _ptr(offsets), _ptr(W), _ptr(bias), _ptr(Y), _ptr(H), tokens, rows, experts, K,
+                              N, act, out_dt, _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_moe_matmul_dx(dY, offsets, W, H, dX, rows, experts, K, N, act=ACT_NONE, dx_dt=BF16, stream=None, check=True):
+    """dX[r] = dY[r] W[e]^T, or the packed gradient of the gated activation's pre-activations H ahead of W."""
+    st = lib.tpmlp_moe_matmul_dx(_ptr(dY), _ptr(offsets), _ptr(W), _ptr(H), _ptr(dX), rows, experts, K, N, act, dx_dt, _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_moe_matmul_dw(X, row_token, offsets, dY, dW, dbias, tokens, rows, experts, K, N, grad_dt=F32, stream=None, check=True):
+    """dW[e] = X_e^T dY_e and dbias[e], the sum of dY_e's rows."""
+    st = lib.tpmlp_moe_matmul_dw(_ptr(X), _ptr(row_token), _ptr(offsets), _ptr(dY), _ptr(dW), _ptr(dbias), tokens, rows, experts, K, N,
+                                 grad_dt, _stream(stream))
+    return _done(st, check)
+
+
+def tpmlp_moe_combine(O, slot_row, weights, Z, tokens, rows, k, h, stream=None, check=True):
+    """Z[t] = sum_j weights[t][j] O[slot_row[t][j]]; weights None: 1."""
+    return _done(lib.tpmlp_moe_combine(_ptr(O), _ptr(slot_row), _ptr(weights), _ptr(Z), tokens, rows, k, h, _stream(stream)), check)
+
+
+def tpmlp_moe_combine_bwd(O, slot_row, weights, dZ, dO, dweights, tokens, rows, k, h, stream=None, check=True):
+    st = lib.tpmlp_moe_combine_bwd(_ptr(O), _ptr(slot_row), _ptr(weights), _ptr(dZ), _ptr(dO), _ptr(dweights), tokens, rows, k, h,
+                                   _stream(stream))
+    return _done(st, check)
 
 
 def tpmlp_row_bwd(Y_sh, B_sh, dZ, H_sh, dY_sh, dB_sh, db2, s, b, h, ffn, p, dt=BF16, grad_dt=F32, act=ACT_NONE,
