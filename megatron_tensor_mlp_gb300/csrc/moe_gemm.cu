@@ -27,7 +27,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// bf16 [slices][rows][cols], boxes of 64 columns x box_rows; rank 2 (one slice) for tile::gather4, box_rows 1.
+// bf16 [slices][rows][cols], boxes of 64 columns x box_rows; rank 2 (one slice) for tile::gather4, of one row.
 bool make_map(CUtensorMap* map, const void* ptr, uint64_t cols, uint64_t rows, uint64_t slices, uint32_t box_rows, uint32_t rank = 3) {
     auto fn = encode_fn();
     if (!fn) {
@@ -44,6 +44,31 @@ bool make_map(CUtensorMap* map, const void* ptr, uint64_t cols, uint64_t rows, u
                   (unsigned long long)cols, (unsigned long long)rows, (unsigned long long)slices);
         return false;
     }
+    return true;
+}
+
+// bf16 [slices][rows][cols], cols a multiple of 64, as [slices][cols / 64][rows][64]: boxes of `chunks` 64-column strips x 64 rows.
+bool make_chunks(CUtensorMap* map, const void* ptr, uint64_t cols, uint64_t rows, uint64_t slices, uint32_t chunks) {
+    auto fn = encode_fn();
+    if (!fn) {
+        set_error("cuTensorMapEncodeTiled is not available from the driver");
+        return false;
+    }
+    const cuuint64_t dims[4] = {BK, rows, cols / BK, slices}, strides[3] = {cols * 2, BK * 2, cols * rows * 2};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(BK), static_cast<cuuint32_t>(BK), chunks, 1}, estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled (experts, chunked) failed (%d)", static_cast<int>(r));
+        return false;
+    }
+    return true;
+}
+// The rows' maps of the rows kernel.
+bool make_boxes(Boxes* b, const void* ptr, uint64_t cols, uint64_t rows) {
+    for (int i = 0; i < 5; ++i)
+        if (!make_map(&b->m[i], ptr, cols, rows, 1, 8u << i)) return false;
     return true;
 }
 
@@ -83,14 +108,13 @@ tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluste
 }
 
 template <bool W_MN, int MODE>
-tpmlp_status launch_rows(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& x8, const Args& a, const DeviceInfo& dev,
-                         cudaStream_t st) {
+tpmlp_status launch_rows(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
     static PerDevice<bool> done;
     auto kern = rows_kernel<W_MN, MODE>;
     if (!set_smem(kern, dev.device, Geom<MODE>::smem, done)) return TPMLP_ERR_CUDA;
     const int64_t most = int64_t(a.m_blocks) * (a.rows / Geom<MODE>::tn + std::min(a.experts, a.rows));
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(most, dev.sm_count / 2));
-    return launch(kern, dim3(2 * pairs), THREADS, Geom<MODE>::smem, 2, st, w, x, x8, a);
+    return launch(kern, dim3(2 * pairs), THREADS, Geom<MODE>::smem, 2, st, w, x, a);
 }
 
 // Sums of an expert's rows by column: CTA (64 columns, expert), rows in steps of 32, added in that order.
@@ -131,6 +155,8 @@ Args common(const MoeSpec& g, const DeviceInfo& dev) {
     a.rows = static_cast<int>(g.rows);
     a.tokens = static_cast<int>(g.tokens);
     a.experts = g.experts;
+    a.x = static_cast<const __nv_bfloat16*>(g.x);
+    a.x_ld = static_cast<int>(g.K);
     a.status = dev.status;
     a.timeout_ns = 2000000000ull;  // 2 s per wait
     return a;
@@ -150,13 +176,12 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     a.bias_ld = g.N;
     a.h_out = static_cast<__nv_bfloat16*>(g.h);
     a.h_ld = g.N;
-    CUtensorMap w, x, x8;
-    const uint64_t K = g.K, tokens = g.src ? g.tokens : g.rows;
-    if (!make_map(&w, g.w, g.N, K, g.experts, BK) ||
-        !(g.src ? make_map(&x, g.x, K, tokens, 1, 1, 2) : make_map(&x, g.x, K, tokens, 1, (g.gated ? Geom<SWIGLU>::tn : Geom<STORE>::tn) / 2)) ||
-        !make_map(&x8, g.x, K, tokens, 1, 8))
-        return TPMLP_ERR_CUDA;
-    return g.gated ? launch_rows<true, SWIGLU>(w, x, x8, a, dev, st) : launch_rows<true, STORE>(w, x, x8, a, dev, st);
+    CUtensorMap w;
+    Boxes x{};
+    a.chunked = g.N % 64 == 0;
+    const bool mapped = a.chunked ? make_chunks(&w, g.w, g.N, g.K, g.experts, g.gated ? 4 : 2) : make_map(&w, g.w, g.N, g.K, g.experts, BK);
+    if (!mapped || !(g.src ? make_map(&x.m[0], g.x, g.K, g.tokens, 1, 1, 2) : make_boxes(&x, g.x, g.K, g.rows))) return TPMLP_ERR_CUDA;
+    return g.gated ? launch_rows<true, SWIGLU>(w, x, a, dev, st) : launch_rows<true, STORE>(w, x, a, dev, st);
 }
 
 tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st) {
@@ -169,11 +194,10 @@ tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaS
     a.out_f32 = g.out_f32;
     a.h_in = static_cast<const __nv_bfloat16*>(g.h);
     a.h_ld = 2 * g.K;
-    CUtensorMap w, x, x8;
-    const uint64_t N = g.N, rows = g.rows;
-    if (!make_map(&w, g.w, N, g.K, g.experts, BM) || !make_map(&x, g.x, N, rows, 1, Geom<STORE>::tn / 2) || !make_map(&x8, g.x, N, rows, 1, 8))
-        return TPMLP_ERR_CUDA;
-    return g.gated ? launch_rows<false, DSWIGLU>(w, x, x8, a, dev, st) : launch_rows<false, STORE>(w, x, x8, a, dev, st);
+    CUtensorMap w;
+    Boxes x;
+    if (!make_map(&w, g.w, g.N, g.K, g.experts, BM) || !make_boxes(&x, g.x, g.N, g.rows)) return TPMLP_ERR_CUDA;
+    return g.gated ? launch_rows<false, DSWIGLU>(w, x, a, dev, st) : launch_rows<false, STORE>(w, x, a, dev, st);
 }
 
 tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st) {
@@ -187,10 +211,9 @@ tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaS
     a.out_f32 = g.out_f32;
     static PerDevice<bool> done;
     if (!set_smem(dw_kernel, dev.device, DW_SMEM, done)) return TPMLP_ERR_CUDA;
-    CUtensorMap x, y;
-    const uint64_t K = g.K, rows = g.rows;
-    if (!(g.src ? make_map(&x, g.x, K, g.tokens, 1, 1, 2) : make_map(&x, g.x, K, rows, 1, BK)) || !make_map(&y, g.dy, g.N, rows, 1, BK))
-        return TPMLP_ERR_CUDA;
+    a.dy = static_cast<const __nv_bfloat16*>(g.dy);
+    CUtensorMap x{}, y;
+    if (!(g.src ? make_map(&x, g.x, g.K, g.tokens, 1, 1, 2) : make_map(&x, g.x, g.K, g.rows, 1, BK)) || !make_map(&y, g.dy, g.N, g.rows, 1, BK)) return TPMLP_ERR_CUDA;
     const int64_t tiles = int64_t(a.experts) * a.m_blocks * a.n_blocks;
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles, dev.sm_count / 2));
     const tpmlp_status st1 = launch(dw_kernel, dim3(2 * pairs), THREADS, DW_SMEM, 2, st, x, y, a);

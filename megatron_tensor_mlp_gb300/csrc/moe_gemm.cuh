@@ -26,7 +26,7 @@ constexpr int MAX_EXPERTS = 1024;
 constexpr int BM = 128;  // features of one CTA's half of a tile (rows kernel)
 constexpr int BK = 64;   // contraction per ring stage: 128-byte rows
 constexpr int CHUNK = BK * 128;        // 64 features x 64 k, or 64 tokens x 64 k
-constexpr int THREADS = 384;           // warp 0 TMA, warp 1 MMA, warps 2-3 (dw: row tails), warps 4-11 epilogue
+constexpr int THREADS = 384;           // warp 0 TMA, warp 1 MMA, warps 2-3 gathered rows, warps 4-11 epilogue
 constexpr int EPI_WARP = 4;
 constexpr int EPI_WARPS = 8;
 constexpr int GROUP = 16;              // token tiles walked together, so that tiles in flight share weights and tokens
@@ -37,10 +37,14 @@ enum Mode : int { STORE = 0, SWIGLU = 1, DSWIGLU = 2 };
 struct Args {
     const int* offsets;  // [experts + 1]
     const int* src;      // token of each row, may be null
+    const __nv_bfloat16* x;  // gathered rows, dw: X [tokens][x_ld]
+    int x_ld;
     int rows, tokens, experts;
     int kb;              // rows kernel: blocks of 64 of the contraction
+    int chunked;         // W's map is [experts][features / 64][K][64]: a stage's chunks in one copy
     int features;        // rows kernel: features on the tile's rows (SWIGLU, DSWIGLU: gate features); dw: K
     int cols;            // dw: N
+    const __nv_bfloat16* dy;  // dw: dY [rows][cols]
     int m_blocks;        // rows kernel: blocks of 256 features; dw: of K
     int n_blocks;        // dw: blocks of 256 of N
     void* out; long long ld;        // row pitch of out (elements)
@@ -61,6 +65,18 @@ __device__ __forceinline__ bool wait(const Args& p, uint64_t* bar, uint32_t pari
 __device__ __forceinline__ bool wait_warp(const Args& p, uint64_t* bar, uint32_t parity, uint32_t where) {
     return mbar_wait_bounded_warp(bar, parity, p.status, p.timeout_ns, where, false);
 }
+
+// Pieces of shared memory, one behind the other.
+struct Carve {
+    uint8_t* at;
+    template <typename T>
+    __device__ __forceinline__ T* take(int n) {
+        T* p = reinterpret_cast<T*>(at);
+        at += n * sizeof(T);
+        return p;
+    }
+};
+constexpr int most_barriers = 5 * 6 + 5;  // of either kernel, and the tensor memory's address
 
 // ---------------------------------------------------------------- the experts' row ranges and tiles
 // Row ranges are clamped to the rows that there are; a range that had to be is reported, its product left out or cut.
@@ -198,14 +214,63 @@ struct Geom {
     static constexpr int stage = a_bytes + b_bytes;
     static constexpr int epi = (MODE == DSWIGLU ? 2 : 1) * STAGE;      // staging of an epilogue warp
     static constexpr int stages = MODE == STORE ? 6 : 5;
-    static constexpr int smem = 1024 + stages * stage + EPI_WARPS * epi + TABLE + 256;
+    static constexpr int smem = 1024 + stages * stage + EPI_WARPS * epi + (most_barriers + 1) * 8 + TABLE;
     static_assert(smem <= 227 * 1024, "rows kernel shared memory");
+    static_assert(2 * stages + 5 <= most_barriers);
 };
+
+// The tokens' maps: boxes of 8, 16 .. 128 rows.  A CTA's half of a tile, any multiple of 8 rows, is copied as the largest
+// box that it holds and one more that holds the rest: few copies, at most a third more than is needed.  (A copy costs the
+// TMA unit some 75 cycles however small: 15 boxes of 8 rows took twice the MMAs' time.)
+struct Boxes {
+    CUtensorMap m[5];
+};
+struct Halves {
+    int first, second;  // boxes of 8 << first, 8 << second rows; second -1: none
+    __device__ __forceinline__ explicit Halves(int rows) {
+        first = 31 - __clz(rows >> 3);
+        const int rest = (rows >> 3) - (1 << first);
+        second = rest == 0 ? -1 : 32 - __clz(rest - 1);
+    }
+    __device__ __forceinline__ int rows() const { return (8 << first) + (second < 0 ? 0 : 8 << second); }
+};
+
+// Gathered rows come as TMA gathers of four rows, every second one from warp 2 and from warp 3: an elected lane issues
+// them in runs without a branch between, the row numbers in its registers.  (With a branch ahead of each, a copy took a
+// warp 88 cycles, and the product of 16384 rows x 5120 x 8192 1620 us; without, 910, where rows that lie in order take 780
+// as boxes.  Copies by cp.async took 2560: the proxy fence that the tensor cores need behind them waits for all copies
+// in flight, also from a warp of its own.)
+//
+// Token of row r.
+__device__ __forceinline__ int token_of(const Args& p, int r) {
+    const int v = p.src[r], t = min(max(v, 0), p.tokens - 1);
+    if (v != t) atomicCAS(p.status, 0u, kStatusDevice);
+    return t;
+}
+// Copies J .. J + N - 1 of a warp: groups of four rows, every second one of the operand.
+template <int J, int N, int PER>
+__device__ __forceinline__ void gather_run(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, const int4 (&at)[PER]) {
+#pragma unroll
+    for (int j = J; j < J + N; ++j) tma_gather4_pair(dst + j * 1024, map, bar, x, at[j]);
+}
+// n of at most 2^k copies from J on, by halves.
+template <int J, int MOST, int PER>
+__device__ __forceinline__ void gather_some(int n, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, const int4 (&at)[PER]) {
+    if (n == MOST) {
+        gather_run<J, MOST>(dst, map, bar, x, at);
+    } else if constexpr (MOST > 1) {
+        if (n >= MOST / 2) {
+            gather_run<J, MOST / 2>(dst, map, bar, x, at);
+            gather_some<J + MOST / 2, MOST / 2>(n - MOST / 2, dst, map, bar, x, at);
+        } else {
+            gather_some<J, MOST / 2>(n, dst, map, bar, x, at);
+        }
+    }
+}
 
 template <bool W_MN, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
-    rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                const __grid_constant__ CUtensorMap tmX8, const Args p) {
+    rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Boxes tmX, const Args p) {
     using G = Geom<MODE>;
     constexpr int S = G::stages, TN = G::tn;
     extern __shared__ uint8_t smem_raw[];
@@ -213,13 +278,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* sA = smem;
     uint8_t* sB = smem + S * G::a_bytes;
     uint8_t* sE = smem + S * G::stage;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sE + EPI_WARPS * G::epi);
-    uint64_t* empty = full + S;
-    uint64_t* tfull = empty + S;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-    Table tab(reinterpret_cast<uint8_t*>(full) + 256);
+    Carve carve{sE + EPI_WARPS * G::epi};
+    uint64_t* full = carve.take<uint64_t>(S);
+    uint64_t* empty = carve.take<uint64_t>(S);
+    uint64_t* tfull = carve.take<uint64_t>(2);
+    uint64_t* tempty = carve.take<uint64_t>(2);
+    uint64_t* drain = carve.take<uint64_t>(1);
+    uint32_t* tmem_slot = carve.take<uint32_t>(2);
+    Table tab(carve.take<int>(TABLE / 4));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t prank = cluster_ctarank();
@@ -239,8 +305,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         fence_mbarrier_init();
         fence_proxy_async_smem();
         tma_prefetch_desc(&tmW);
-        tma_prefetch_desc(&tmX);
-        tma_prefetch_desc(&tmX8);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -267,16 +331,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int nn = (c.n + 15) & ~15, half = nn / 2;  // columns of the MMA, tokens of this CTA
             const int row0 = c.row0 + static_cast<int>(prank) * half;
             const int f0 = MODE == SWIGLU ? (c.mb * 2 + static_cast<int>(prank)) * 256 : c.mb * 256 + static_cast<int>(prank) * BM;
-            int4 at = make_int4(0, 0, 0, 0);
-            if (p.src != nullptr && lane * 4 < half) {
-                int* a = reinterpret_cast<int*>(&at);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int v = p.src[min(row0 + lane * 4 + i, c.row0 + c.n - 1)], w = min(max(v, 0), p.tokens - 1);
-                    if (v != w) atomicCAS(p.status, 0u, kStatusDevice);
-                    a[i] = w;
-                }
-            }
+            const Halves box(half);
+            const uint32_t bytes = 2 * (G::a_bytes + (p.src == nullptr ? box.rows() : half) * 128);
             for (int it = 0; it < p.kb; ++it) {
                 if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer)) {
                     ok = false;
@@ -287,24 +343,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint8_t* b_dst = sB + stage * G::b_bytes;
                 if (lane == 0) {
                     if (leader) {
-                        mbar_arrive_expect_tx(full + stage, 2 * G::a_bytes + nn * 128);
+                        mbar_arrive_expect_tx(full + stage, bytes);
                         armed |= 1u << stage;
                         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
                     }
                     if constexpr (!W_MN) {
                         tma_load_3d_pair(a_dst, &tmW, bar, it * BK, f0, c.e);
                     } else {
+                        if (p.chunked) {
+                            tma_load_4d_pair(a_dst, &tmW, bar, 0, it * BK, f0 / 64, c.e);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < G::a_bytes / CHUNK; ++j)
-                            tma_load_3d_pair(a_dst + j * CHUNK, &tmW, bar, f0 + j * 64, it * BK, c.e);
+                            for (int j = 0; j < G::a_bytes / CHUNK; ++j)
+                                tma_load_3d_pair(a_dst + j * CHUNK, &tmW, bar, f0 + j * 64, it * BK, c.e);
+                        }
                     }
-                }
-                if (p.src != nullptr) {
-                    if (lane * 4 < half) tma_gather4_pair(b_dst + lane * 512, &tmX, bar, it * BK, at);
-                } else if (nn == TN) {
-                    if (lane == 0) tma_load_3d_pair(b_dst, &tmX, bar, it * BK, row0, 0);
-                } else if (lane * 8 < half) {
-                    tma_load_3d_pair(b_dst + lane * 1024, &tmX8, bar, it * BK, row0 + lane * 8, 0);
+                    if (p.src == nullptr) {
+                        tma_load_3d_pair(b_dst, &tmX.m[box.first], bar, it * BK, row0, 0);
+                        if (box.second >= 0)
+                            tma_load_3d_pair(b_dst + (1024 << box.first), &tmX.m[box.second], bar, it * BK, row0 + (8 << box.first), 0);
+                    }
                 }
                 if (++stage == S) {
                     stage = 0;
@@ -351,10 +409,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc_fence_after();
                     const uint32_t d = tmem_base + acc * 256;
                     for (int it = 0; it < p.kb; ++it) {
-                        if (!wait(p, full + stage, phase, kWhereMma)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = wait(p, full + stage, phase, kWhereMma);
+                        if (!ok) break;
                         tc_fence_after();
                         const uint64_t a = a0 + static_cast<uint64_t>(stage * (G::a_bytes >> 4));
                         const uint64_t b = b0 + static_cast<uint64_t>(stage * (G::b_bytes >> 4));
@@ -380,7 +436,45 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             wait(p, drain, 0, kWhereDrain);
         }
-    } else if (warp >= EPI_WARP) {
+    } else if (warp < EPI_WARP) {
+        if (p.src != nullptr) {
+            // ------------------------------------------------------------ gathered rows (both CTAs)
+            constexpr int PER = TN / 16;  // copies of a warp at most
+            int stage = 0, e = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const uint32_t full0 = mapa_shared(smem_u32(full), 0), dst0 = smem_u32(sB) + (warp - 2) * 512;
+            for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+                const Tile c = decode<TN>(p, tab, t, e);
+                const int half = ((c.n + 15) & ~15) / 2, copies = half / 8;  // (half is a multiple of 8)
+                const int row0 = c.row0 + static_cast<int>(prank) * half + (warp - 2) * 4;
+                int4 at[PER];
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    at[j] = make_int4(0, 0, 0, 0);
+                    if (j < copies) {
+                        const int last = c.row0 + c.n - 1, r = row0 + j * 8;
+                        at[j] = make_int4(token_of(p, min(r, last)), token_of(p, min(r + 1, last)), token_of(p, min(r + 2, last)),
+                                          token_of(p, min(r + 3, last)));
+                    }
+                }
+                for (int it = 0; it < p.kb; ++it) {
+                    if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one())
+                        gather_some<0, PER>(copies, dst0 + stage * G::b_bytes, &tmX.m[0], full0 + stage * 8, it * BK, at);
+                    __syncwarp();
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) spin_ns(200000);  // let the last copies land before either CTA can exit
+        }
+    } else {
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3, half = (warp - EPI_WARP) >> 2;
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
@@ -535,13 +629,24 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ---------------------------------------------------------------- dw kernel
-// dW[e] = X_e^T dY_e: both operands have the rows as their contraction, 64 to a stage.  An expert's last block may end
-// inside a stage: the rows behind it, the next expert's, are in the copy too and are set to zero in shared memory
-// (both operands': a zero times the other's infinity would be a NaN).  Such a stage's copies report to a barrier of
-// their own CTA; its warp 2 waits for them, clears the rows and tells the leader's MMA warp.
+// dW[e] = X_e^T dY_e: both operands have the rows as their contraction, 64 to a stage, and come by TMA; gathered rows of X
+// from warps 2 and 3, 64 features each.  Where an expert's last block ends inside a stage warp 2 copies it, both operands,
+// by cp.async: the rows behind the last, the next expert's, are zeros in shared memory then (in both operands, since a zero
+// times the other's infinity would be a NaN).  Warp 3 waits for the copies, makes them visible to the tensor cores (the
+// proxy fence, in a warp without copies of its own) and reports to the leader.
+//
+// A lane's place in a block of rows of 128 bytes, row r0 + 4 j: piece ^ (row % 8) of the row, as the swizzle has it.
+struct Lane {
+    int piece, r0;
+    __device__ __forceinline__ Lane() : piece(threadIdx.x & 7), r0((threadIdx.x >> 3) & 3) {}
+    __device__ __forceinline__ uint32_t at(int j) const {
+        return static_cast<uint32_t>(j * 512 + r0 * 128 + ((piece ^ (r0 + 4 * (j & 1))) << 4));
+    }
+};
 constexpr int DW_STAGES = 6;
 constexpr int DW_A = BM * 128, DW_B = BM * 128, DW_STAGE = DW_A + DW_B;
-constexpr int DW_SMEM = 1024 + DW_STAGES * DW_STAGE + TABLE + 512;
+constexpr int DW_SMEM = 1024 + DW_STAGES * DW_STAGE + 32 * 16 + (most_barriers + 1) * 8 + TABLE;
+static_assert(5 * DW_STAGES + 5 <= most_barriers);
 static_assert(DW_SMEM <= 227 * 1024, "dw kernel shared memory");
 
 __global__ void __launch_bounds__(THREADS, 1)
@@ -551,15 +656,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + S * DW_A;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * DW_STAGE);
-    uint64_t* empty = full + S;
-    uint64_t* tload = empty + S;  // a stage with an expert's last rows: this CTA's copies
-    uint64_t* tdone = tload + S;  // leader: both CTAs' rows behind the last cleared
-    uint64_t* tfull = tdone + S;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-    Table tab(reinterpret_cast<uint8_t*>(full) + 512);
+    Carve carve{smem + S * DW_STAGE};
+    int4* rows4 = carve.take<int4>(32);             // warps 2 and 3: a block's tokens
+    uint64_t* full = carve.take<uint64_t>(S);
+    uint64_t* empty = carve.take<uint64_t>(S);
+    uint64_t* begin = carve.take<uint64_t>(S);      // the stage is for an expert's last block: to warp 2
+    uint64_t* lfull = carve.take<uint64_t>(S);      // it is copied: to warp 3
+    uint64_t* gfull = carve.take<uint64_t>(S);      // leader: in both CTAs
+    uint64_t* tfull = carve.take<uint64_t>(2);
+    uint64_t* tempty = carve.take<uint64_t>(2);
+    uint64_t* drain = carve.take<uint64_t>(1);
+    uint32_t* tmem_slot = carve.take<uint32_t>(2);
+    Table tab(carve.take<int>(TABLE / 4));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t prank = cluster_ctarank();
@@ -570,8 +678,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int s = 0; s < S; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
-            mbar_init(tload + s, 1);
-            mbar_init(tdone + s, 2);
+            mbar_init(lfull + s, 32);
+            mbar_init(gfull + s, 2);
+            mbar_init(begin + s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull + a, 1);
@@ -609,7 +718,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0) {
         // ---------------------------------------------------------------- producer (both CTAs), a whole warp
         int stage = 0;
-        uint32_t phase = 0, armed = 0, last_parity = 0, t_armed = 0, t_parity = 0;  // t_parity: a tail's next phase by stage
+        uint32_t phase = 0, armed = 0, last_parity = 0;
         bool ok = true;
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);
         for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
@@ -619,42 +728,29 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int a0 = mb * 256 + static_cast<int>(prank) * BM, b0 = nb * 256 + static_cast<int>(prank) * BM;
             for (int it = 0; it < kb; ++it) {
                 const bool tail = (it + 1) * BK > n;
-                int4 at = make_int4(0, 0, 0, 0);
-                if (p.src != nullptr) {  // lanes 0-15 the first 64 features, lanes 16-31 the next
-                    int* a = reinterpret_cast<int*>(&at);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int v = p.src[base + min(it * BK + (lane & 15) * 4 + i, n - 1)], w = min(max(v, 0), p.tokens - 1);
-                        if (v != w) atomicCAS(p.status, 0u, kStatusDevice);
-                        a[i] = w;
-                    }
-                }
                 if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer)) {
                     ok = false;
                     break;
                 }
                 uint8_t* a_dst = sA + stage * DW_A;
                 uint8_t* b_dst = sB + stage * DW_B;
-                const uint32_t bar = tail ? smem_u32(tload + stage) : full0 + stage * 8;
+                const uint32_t bar = full0 + stage * 8;
                 if (lane == 0) {
-                    if (tail) {
-                        mbar_arrive_expect_tx(tload + stage, DW_STAGE);
-                        t_armed |= 1u << stage;
-                        t_parity ^= 1u << stage;
-                        if (leader) mbar_arrive(full + stage);
-                    } else if (leader) {
-                        mbar_arrive_expect_tx(full + stage, 2 * DW_STAGE);
+                    if (leader) {
+                        mbar_arrive_expect_tx(full + stage, tail ? 0 : 2 * DW_STAGE);
                         armed |= 1u << stage;
                         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
                     }
+                    if (tail) {
+                        mbar_arrive(begin + stage);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (p.src == nullptr) tma_load_3d_pair(a_dst + j * CHUNK, &tmX, bar, a0 + j * 64, base + it * BK, 0);
-                        tma_load_3d_pair(b_dst + j * CHUNK, &tmY, bar, b0 + j * 64, base + it * BK, 0);
+                        for (int j = 0; j < 2; ++j) {
+                            if (p.src == nullptr) tma_load_3d_pair(a_dst + j * CHUNK, &tmX, bar, a0 + j * 64, base + it * BK, 0);
+                            tma_load_3d_pair(b_dst + j * CHUNK, &tmY, bar, b0 + j * 64, base + it * BK, 0);
+                        }
                     }
                 }
-                if (p.src != nullptr)
-                    tma_gather4_pair(a_dst + (lane >> 4) * CHUNK + (lane & 15) * 512, &tmX, bar, a0 + (lane >> 4) * 64, at);
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1u;
@@ -670,12 +766,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         } else if (lane == 0) {
-            for (int s = 0; s < S; ++s) {
-                if (t_armed & (1u << s))  // t_parity has passed on to the next phase
-                    wait(p, tload + s, ((t_parity >> s) & 1u) ^ 1u, kWhereDrain);
-                if (leader && (armed & (1u << s)))
-                    wait(p, full + s, (last_parity >> s) & 1u, kWhereDrain);
-            }
+            for (int s = 0; leader && s < S; ++s)
+                if (armed & (1u << s)) wait(p, full + s, (last_parity >> s) & 1u, kWhereDrain);
             if (!leader) spin_ns(200000);
         }
     } else if (warp == 1) {
@@ -685,7 +777,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, 2 * BM, true, true);
                 const uint64_t a0 = sdesc_sw128(smem_u32(sA), CHUNK, 1024), b0 = sdesc_sw128(smem_u32(sB), CHUNK, 1024);
                 int stage = 0, lt = 0;
-                uint32_t phase = 0, t_parity = 0;
+                uint32_t phase = 0, g_parity = 0;  // a stage's next phase of gfull
                 bool ok = true;
                 for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
                     int e, mb, nb;
@@ -703,9 +795,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const bool tail = (it + 1) * BK > n;
                         ok = wait(p, full + stage, phase, kWhereMma);
                         if (ok && tail) {
-                            ok = mbar_wait_bounded_cluster(tdone + stage, (t_parity >> stage) & 1u, p.status, p.timeout_ns, kWhereMma, false);
-                            t_parity ^= 1u << stage;
-                            fence_proxy_async_all();
+                            ok = mbar_wait_bounded_cluster(gfull + stage, (g_parity >> stage) & 1u, p.status, p.timeout_ns, kWhereMma, false);
+                            g_parity ^= 1u << stage;
                         }
                         if (!ok) break;
                         tc_fence_after();
@@ -729,33 +820,87 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             wait(p, drain, 0, kWhereDrain);
         }
-    } else if (warp == 2) {
-        // ---------------------------------------------------------------- rows behind an expert's last (both CTAs)
+    } else if (warp < EPI_WARP) {
+        // ---------------------------------------------------------------- gathered rows and last blocks (both CTAs)
+        const Lane l;
+        const uint32_t sa = smem_u32(sA), sb = smem_u32(sB);
+        int4* const at = rows4 + (warp - 2) * 16;
         int stage = 0;
-        uint32_t t_parity = 0;
+        uint32_t phase = 0, t_parity = 0;  // a stage's next phase of `begin` or `lfull`
         bool ok = true;
-        const uint32_t done0 = mapa_shared(smem_u32(tdone), 0);
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0), gfull0 = mapa_shared(smem_u32(gfull), 0);
         for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
             int e, mb, nb;
             place(t, e, mb, nb);
-            const int n = tab.count(e), kb = (n + BK - 1) / BK, live = n - (kb - 1) * BK;  // rows of the last block
-            stage = (stage + kb) % S;
-            if (kb == 0 || live == BK) continue;
-            const int s = (stage + S - 1) % S;
-            ok = wait_warp(p, tload + s, (t_parity >> s) & 1u, kWhereProducer);
-            t_parity ^= 1u << s;
-            if (!ok) break;
-            // 2 operands x 2 chunks of 64 rows of 128 bytes
-            const int gone = (BK - live) * 8;  // 16-byte pieces of a chunk
-            for (int i = lane; i < 4 * gone; i += 32) {
-                const int part = i / gone, at = live * 128 + (i - part * gone) * 16;
-                uint8_t* dst = (part < 2 ? sA + s * DW_A : sB + s * DW_B) + (part & 1) * CHUNK + at;
-                *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+            const int n = tab.count(e), base = tab.off[e], whole = n / BK, a0 = mb * 256 + static_cast<int>(prank) * BM;
+            if (p.src != nullptr) {
+                int2 next = make_int2(0, 0);
+                auto look = [&](int it) {  // two tokens of block it, ahead of their use
+                    if (it < whole) next = make_int2(token_of(p, base + it * BK + lane * 2), token_of(p, base + it * BK + lane * 2 + 1));
+                };
+                look(0);
+                for (int it = 0; it < whole; ++it) {
+                    reinterpret_cast<int2*>(at)[lane] = next;
+                    look(it + 1);
+                    __syncwarp();
+                    int4 rows[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) rows[j] = at[j];
+                    ok = wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer);
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t dst = sa + stage * DW_A + (warp - 2) * CHUNK;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            tma_gather4_pair(dst + j * 512, &tmX, full0 + stage * 8, a0 + (warp - 2) * 64, rows[j]);
+                    }
+                    __syncwarp();
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+            } else {
+                stage = (stage + whole) % S;
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(done0 + s * 8);
+            if (whole * BK == n) continue;
+            if (warp == 3) {
+                ok = wait_warp(p, lfull + stage, (t_parity >> stage) & 1u, kWhereProducer);
+                if (ok) fence_proxy_async_smem();
+                if (ok && lane == 0) mbar_arrive_cluster(gfull0 + stage * 8);
+            } else {
+                int row[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    row[j] = base + min(whole * BK + j * 4 + l.r0, n - 1);
+                    if (p.src != nullptr) row[j] = token_of(p, row[j]);
+                }
+                ok = wait_warp(p, begin + stage, (t_parity >> stage) & 1u, kWhereProducer);
+                if (!ok) break;
+                const int b0 = nb * 256 + static_cast<int>(prank) * BM + l.piece * 8, x0 = a0 + l.piece * 8;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int i = whole * BK + j * 4 + l.r0;
+                    const __nv_bfloat16* x = p.x + static_cast<long long>(row[j]) * p.x_ld + x0;
+                    const __nv_bfloat16* y = p.dy + static_cast<long long>(base + min(i, n - 1)) * p.cols + b0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bool inx = i < n && x0 + h * 64 < p.x_ld, iny = i < n && b0 + h * 64 < p.cols;
+                        cp_async16(sa + stage * DW_A + h * CHUNK + l.at(j), inx ? x + h * 64 : p.x, inx);
+                        cp_async16(sb + stage * DW_B + h * CHUNK + l.at(j), iny ? y + h * 64 : p.dy, iny);
+                    }
+                }
+                cp_async_arrive(lfull + stage);
+            }
+            t_parity ^= 1u << stage;
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1u;  // (of a gather, which walks every stage)
+            }
         }
+        cp_async_drain();
+        if (!ok && p.src != nullptr) spin_ns(200000);  // let the last copies land before either CTA can exit
     } else if (warp >= EPI_WARP) {
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3, half = (warp - EPI_WARP) >> 2;

@@ -310,21 +310,24 @@ __device__ __forceinline__ void umma_commit_pair_mc(uint64_t* bar, uint16_t cta_
 // Four rows of a 2-D tensor, 64 bf16 columns from x of each, into consecutive 128-byte rows of shared memory
 // (tile::gather4; the map's box is one row high).  The swizzle goes by the shared-memory address, so eight rows
 // of two such loads make the same 1 KiB atom as a plain box of eight rows.
-__device__ __forceinline__ void tma_gather4(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x, int4 rows) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_gather4_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar_cluster_addr, int32_t x,
+__device__ __forceinline__ void tma_gather4_pair(uint32_t smem_dst, const CUtensorMap* map, uint32_t bar_cluster_addr, int32_t x,
                                                  int4 rows) {
     asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w),
         "r"(bar_cluster_addr)
         : "memory");
+}
+// 16 bytes global -> shared without registers (cp.async, past L1); zeros where !valid (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+// Wait until all of this thread's cp.async are complete.
+__device__ __forceinline__ void cp_async_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrive on `bar` (one of the arrivals that it was initialised for) when all of this thread's cp.async so far are complete.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // 16 lanes x 32 consecutive 32-bit columns as 8x8 fragments: of columns 8 i .. 8 i + 7 thread t holds, in r[4 i + 0, 1],
 // columns 2 (t % 4) and the next of lane t / 4 and, in r[4 i + 2, 3], the same of lane t / 4 + 8.
