@@ -168,7 +168,8 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     Args a = common(g, dev);
     a.kb = static_cast<int>((g.K + BK - 1) / BK);
     a.features = static_cast<int>(g.gated ? g.N / 2 : g.N);
-    a.m_blocks = (a.features + 255) / 256;
+    const int tile = g.gated ? Geom<SWIGLU>::f : Geom<STORE>::f;
+    a.m_blocks = (a.features + tile - 1) / tile;
     a.out = g.out;
     a.ld = a.features;
     a.out_f32 = g.out_f32;
@@ -178,8 +179,8 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     a.h_ld = g.N;
     CUtensorMap w;
     Boxes x{};
-    a.chunked = g.N % 64 == 0;
-    const bool mapped = a.chunked ? make_chunks(&w, g.w, g.N, g.K, g.experts, g.gated ? 4 : 2) : make_map(&w, g.w, g.N, g.K, g.experts, BK);
+    a.chunked = !g.gated && g.N % 64 == 0;
+    const bool mapped = a.chunked ? make_chunks(&w, g.w, g.N, g.K, g.experts, 2) : make_map(&w, g.w, g.N, g.K, g.experts, BK);
     if (!mapped || !(g.src ? make_map(&x.m[0], g.x, g.K, g.tokens, 1, 1, 2) : make_boxes(&x, g.x, g.K, g.rows))) return TPMLP_ERR_CUDA;
     return g.gated ? launch_rows<true, SWIGLU>(w, x, a, dev, st) : launch_rows<true, STORE>(w, x, a, dev, st);
 }

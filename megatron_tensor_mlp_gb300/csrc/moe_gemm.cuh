@@ -12,8 +12,10 @@
 // transposed, a feature in each tensor-memory lane; they are read as 8x8 fragments and turned by stmatrix on the
 // way to rows in memory.
 //
-// The gated first layer keeps two accumulators of 128 tokens, gate and up features of the same indices on the
-// same lanes, fed from one copy of the tokens.
+// The gated first layer has 64 gate and the 64 up features of the same indices on a CTA's 128 lanes.  The warps of the up
+// features pass their accumulators to those of the gate's through shared memory, 32 x 32 at a time.  (Gate and up as two
+// accumulators of 128 tokens on the same lanes need no exchange, but MMAs of 128 columns: their operands take all of the
+// shared memory's 128 bytes a cycle, and 16384 rows x 5120 x 8192 took 1011 us in order.)
 #pragma once
 #include "gemm_tc.cuh"
 #include "internal.h"
@@ -191,6 +193,21 @@ __device__ __forceinline__ void rows_load(const __nv_bfloat16* src, long long ld
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// A barrier of two warps.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// The same, and whether `ok` holds in both.
+__device__ __forceinline__ bool pair_and(int id, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(ok ? 1u : 0u), "r"(id)
+        : "memory");
+    return r != 0;
+}
 // 32 lanes x 32 columns as fragments: a, lanes 0-15, b, lanes 16-31.
 __device__ __forceinline__ void load_frags(uint32_t taddr, uint32_t (&a)[16], uint32_t (&b)[16]) {
     tmem_ld_16x256b_x4(taddr, a);
@@ -208,13 +225,15 @@ __device__ __forceinline__ void load_bias(const __nv_bfloat16* bias, int nf, int
 // ---------------------------------------------------------------- rows kernel
 template <int MODE>
 struct Geom {
-    static constexpr int tn = MODE == SWIGLU ? 128 : 256;              // tokens of a tile at most
-    static constexpr int a_bytes = (MODE == SWIGLU ? 2 : 1) * BM * 128;  // this CTA's features of a stage
-    static constexpr int b_bytes = tn / 2 * 128;                       // this CTA's half of the tokens
+    static constexpr int tn = 256;                      // tokens of a tile at most
+    static constexpr int f = MODE == SWIGLU ? 128 : 256;  // features of a tile (SWIGLU: gate and up of each)
+    static constexpr int a_bytes = BM * 128;            // this CTA's features of a stage
+    static constexpr int b_bytes = tn / 2 * 128;        // this CTA's half of the tokens
     static constexpr int stage = a_bytes + b_bytes;
-    static constexpr int epi = (MODE == DSWIGLU ? 2 : 1) * STAGE;      // staging of an epilogue warp
+    static constexpr int epi = (MODE == DSWIGLU ? 2 : 1) * STAGE;  // staging of an epilogue warp
+    static constexpr int pass = MODE == SWIGLU ? 4 * 4096 : 0;     // up accumulators on their way to the gate's warps
     static constexpr int stages = MODE == STORE ? 6 : 5;
-    static constexpr int smem = 1024 + stages * stage + EPI_WARPS * epi + (most_barriers + 1) * 8 + TABLE;
+    static constexpr int smem = 1024 + stages * stage + EPI_WARPS * epi + pass + (most_barriers + 1) * 8 + TABLE;
     static_assert(smem <= 227 * 1024, "rows kernel shared memory");
     static_assert(2 * stages + 5 <= most_barriers);
 };
@@ -241,12 +260,14 @@ struct Halves {
 // as boxes.  Copies by cp.async took 2560: the proxy fence that the tensor cores need behind them waits for all copies
 // in flight, also from a warp of its own.)
 //
-// Token of row r.
-__device__ __forceinline__ int token_of(const Args& p, int r) {
-    const int v = p.src[r], t = min(max(v, 0), p.tokens - 1);
+// A token read from src, cut to those that there are.
+__device__ __forceinline__ int checked(const Args& p, int v) {
+    const int t = min(max(v, 0), p.tokens - 1);
     if (v != t) atomicCAS(p.status, 0u, kStatusDevice);
     return t;
 }
+// Token of row r.
+__device__ __forceinline__ int token_of(const Args& p, int r) { return checked(p, p.src[r]); }
 // Copies J .. J + N - 1 of a warp: groups of four rows, every second one of the operand.
 template <int J, int N, int PER>
 __device__ __forceinline__ void gather_run(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, const int4 (&at)[PER]) {
@@ -278,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* sA = smem;
     uint8_t* sB = smem + S * G::a_bytes;
     uint8_t* sE = smem + S * G::stage;
-    Carve carve{sE + EPI_WARPS * G::epi};
+    Carve carve{sE + EPI_WARPS * G::epi + G::pass};
     uint64_t* full = carve.take<uint64_t>(S);
     uint64_t* empty = carve.take<uint64_t>(S);
     uint64_t* tfull = carve.take<uint64_t>(2);
@@ -330,7 +351,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const Tile c = decode<TN>(p, tab, t, e);
             const int nn = (c.n + 15) & ~15, half = nn / 2;  // columns of the MMA, tokens of this CTA
             const int row0 = c.row0 + static_cast<int>(prank) * half;
-            const int f0 = MODE == SWIGLU ? (c.mb * 2 + static_cast<int>(prank)) * 256 : c.mb * 256 + static_cast<int>(prank) * BM;
+            // (SWIGLU: 64 gate features of block mb, their up features 128 columns on)
+            const int f0 = c.mb * 256 + static_cast<int>(prank) * (MODE == SWIGLU ? 64 : BM);
             const Halves box(half);
             const uint32_t bytes = 2 * (G::a_bytes + (p.src == nullptr ? box.rows() : half) * 128);
             for (int it = 0; it < p.kb; ++it) {
@@ -350,12 +372,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if constexpr (!W_MN) {
                         tma_load_3d_pair(a_dst, &tmW, bar, it * BK, f0, c.e);
                     } else {
-                        if (p.chunked) {
+                        if (MODE != SWIGLU && p.chunked) {
                             tma_load_4d_pair(a_dst, &tmW, bar, 0, it * BK, f0 / 64, c.e);
                         } else {
 #pragma unroll
                             for (int j = 0; j < G::a_bytes / CHUNK; ++j)
-                                tma_load_3d_pair(a_dst + j * CHUNK, &tmW, bar, f0 + j * 64, it * BK, c.e);
+                                tma_load_3d_pair(a_dst + j * CHUNK, &tmW, bar, f0 + j * (MODE == SWIGLU ? 128 : 64), it * BK, c.e);
                         }
                     }
                     if (p.src == nullptr) {
@@ -415,12 +437,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint64_t a = a0 + static_cast<uint64_t>(stage * (G::a_bytes >> 4));
                         const uint64_t b = b0 + static_cast<uint64_t>(stage * (G::b_bytes >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk) {
-                            const uint32_t add = (it | kk) != 0 ? 1u : 0u;
-                            umma_f16_pair(d, a + kk * a_step, b + kk * 2, idesc, add);
-                            if constexpr (MODE == SWIGLU)
-                                umma_f16_pair(d + 128, a + (BM * 128 >> 4) + kk * a_step, b + kk * 2, idesc, add);
-                        }
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            umma_f16_pair(d, a + kk * a_step, b + kk * 2, idesc, (it | kk) != 0 ? 1u : 0u);
                         umma_commit_pair_mc(empty + stage, 0x3);
                         if (++stage == S) {
                             stage = 0;
@@ -487,20 +505,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             int okw = 0;
             if (lane == 0) okw = wait(p, tfull + acc, (lt >> 1) & 1, kWhereEpilogue);
             okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
+            if constexpr (MODE == SWIGLU) okw = pair_and(1 + half * 2 + (q & 1), okw);  // both or neither go on to meet
             if (!okw) break;
             tc_fence_after();
-            const int f0 = c.mb * 256 + static_cast<int>(prank) * BM + q * 32;  // features f0 .. f0 + 31 (of the gate's)
+            // features f0 .. f0 + 31 (SWIGLU: of gate and up, this warp's the gate where q < 2)
+            const int f0 = MODE == SWIGLU ? c.mb * 128 + static_cast<int>(prank) * 64 + (q & 1) * 32
+                                          : c.mb * 256 + static_cast<int>(prank) * BM + q * 32;
             const int nf = min(p.features - f0, 32);
             const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-            const long long packed = static_cast<long long>(f0 >> 7) * 256 + (f0 & 127);
-            [[maybe_unused]] float bias[4], bias_up[4];
-            if constexpr (MODE == STORE) {
-                load_bias(p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + f0, nf, lane, bias);
-            } else if constexpr (MODE == SWIGLU) {
-                const __nv_bfloat16* b = p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + packed;
-                load_bias(b, nf, lane, bias);
-                load_bias(b == nullptr ? nullptr : b + 128, nf, lane, bias_up);
-            }
+            const long long packed = static_cast<long long>(f0 >> 7) * 256 + (f0 & 127) + (MODE == SWIGLU ? (q >> 1) * 128 : 0);
+            [[maybe_unused]] float bias[4];
+            if constexpr (MODE != DSWIGLU)
+                load_bias(p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + (MODE == SWIGLU ? packed : f0), nf, lane, bias);
             for (int c0 = half * (TN / 2); c0 < (half + 1) * (TN / 2) && c0 < c.n && nf > 0; c0 += 32) {
                 const int n = min(c.n - c0, 32);
                 const long long row = c.row0 + c0;
@@ -532,45 +548,60 @@ __global__ void __launch_bounds__(THREADS, 1)
                     stage_store(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, n, nf, lane);
                     __syncwarp();
                 } else if constexpr (MODE == SWIGLU) {
-                    uint32_t ua[16], ub[16];
-                    load_frags(lanes + 128 + c0, ua, ub);
                     tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int j = (i >> 1) & 1;
                         a[i] = __float_as_uint(__uint_as_float(a[i]) + bias[j]);
                         b[i] = __float_as_uint(__uint_as_float(b[i]) + bias[2 + j]);
-                        ua[i] = __float_as_uint(__uint_as_float(ua[i]) + bias_up[j]);
-                        ub[i] = __float_as_uint(__uint_as_float(ub[i]) + bias_up[2 + j]);
                     }
-                    if (p.h_out != nullptr) {
-                        __nv_bfloat16* h = p.h_out + row * p.h_ld + packed;
+                    // the two warps of a pair of (gate, up) lanes and the same tokens: 64 threads
+                    const int pair = half * 2 + (q & 1);
+                    uint4* pass = reinterpret_cast<uint4*>(sE + EPI_WARPS * G::epi + pair * 4096) + lane;
+                    if (q >= 2) {
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                lo[i] = tc::pack_bf16x2(__uint_as_float((part ? ua : a)[2 * i]), __uint_as_float((part ? ua : a)[2 * i + 1]));
-                                hi[i] = tc::pack_bf16x2(__uint_as_float((part ? ub : b)[2 * i]), __uint_as_float((part ? ub : b)[2 * i + 1]));
-                            }
-                            stage_put(sbuf, lo, hi, lane);
-                            __syncwarp();
-                            stage_store(buf, h + part * 128, p.h_ld, n, nf, lane);
-                            __syncwarp();
+                        for (int i = 0; i < 4; ++i) {
+                            pass[i * 32] = make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+                            pass[(4 + i) * 32] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
                         }
                     }
-                    auto gated = [](uint32_t g, uint32_t u) {
-                        const float x = __uint_as_float(g);
-                        return x * tc::sigmoid_approx(x) * __uint_as_float(u);
-                    };
+                    pair_sync(1 + pair);
+                    uint32_t ua[16], ub[16];
+                    if (q < 2) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        lo[i] = tc::pack_bf16x2(gated(a[2 * i], ua[2 * i]), gated(a[2 * i + 1], ua[2 * i + 1]));
-                        hi[i] = tc::pack_bf16x2(gated(b[2 * i], ub[2 * i]), gated(b[2 * i + 1], ub[2 * i + 1]));
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 u = pass[i * 32], v = pass[(4 + i) * 32];
+                            ua[4 * i] = u.x, ua[4 * i + 1] = u.y, ua[4 * i + 2] = u.z, ua[4 * i + 3] = u.w;
+                            ub[4 * i] = v.x, ub[4 * i + 1] = v.y, ub[4 * i + 2] = v.z, ub[4 * i + 3] = v.w;
+                        }
                     }
-                    stage_put(sbuf, lo, hi, lane);
-                    __syncwarp();
-                    stage_store(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, n, nf, lane);
-                    __syncwarp();
+                    pair_sync(1 + pair);  // read: the next ones may be written
+                    if (p.h_out != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            lo[i] = tc::pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+                            hi[i] = tc::pack_bf16x2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+                        }
+                        stage_put(sbuf, lo, hi, lane);
+                        __syncwarp();
+                        stage_store(buf, p.h_out + row * p.h_ld + packed, p.h_ld, n, nf, lane);
+                        __syncwarp();
+                    }
+                    if (q < 2) {
+                        auto gated = [](uint32_t g, uint32_t u) {
+                            const float x = __uint_as_float(g);
+                            return x * tc::sigmoid_approx(x) * __uint_as_float(u);
+                        };
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            lo[i] = tc::pack_bf16x2(gated(a[2 * i], ua[2 * i]), gated(a[2 * i + 1], ua[2 * i + 1]));
+                            hi[i] = tc::pack_bf16x2(gated(b[2 * i], ub[2 * i]), gated(b[2 * i + 1], ub[2 * i + 1]));
+                        }
+                        stage_put(sbuf, lo, hi, lane);
+                        __syncwarp();
+                        stage_store(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, n, nf, lane);
+                        __syncwarp();
+                    }
                 } else {
                     const __nv_bfloat16* h = p.h_in + row * p.h_ld + packed;
                     uint4 g4[4], u4[4];
@@ -835,12 +866,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int n = tab.count(e), base = tab.off[e], whole = n / BK, a0 = mb * 256 + static_cast<int>(prank) * BM;
             if (p.src != nullptr) {
                 int2 next = make_int2(0, 0);
-                auto look = [&](int it) {  // two tokens of block it, ahead of their use
-                    if (it < whole) next = make_int2(token_of(p, base + it * BK + lane * 2), token_of(p, base + it * BK + lane * 2 + 1));
+                auto look = [&](int it) {  // two tokens of block it, ahead of their use (and of their check, which waits for them)
+                    if (it < whole) next = make_int2(p.src[base + it * BK + lane * 2], p.src[base + it * BK + lane * 2 + 1]);
                 };
                 look(0);
                 for (int it = 0; it < whole; ++it) {
-                    reinterpret_cast<int2*>(at)[lane] = next;
+                    reinterpret_cast<int2*>(at)[lane] = make_int2(checked(p, next.x), checked(p, next.y));
                     look(it + 1);
                     __syncwarp();
                     int4 rows[16];
