@@ -102,7 +102,7 @@ tpmlp_status check_experts(int64_t tokens, int64_t rows, int64_t experts, int64_
     }
     TP_TRY(check_matrix(experts * K, N, "the weights"));
     // tiles are counted in 32 bits
-    const int64_t blocks = ((K + 255) / 256) * ((N + 255) / 256), tiles = std::max((K + 255) / 256, (N + 255) / 256) * (rows / 128 + experts);
+    const int64_t blocks = ((K + 255) / 256) * ((N + 255) / 256), tiles = (std::max(K, N) / 64 + 1) * (rows / 64 + experts);
     if (blocks > kMaxDim / experts || tiles > kMaxDim) {
         set_error("shape too large: more than 2^31 tiles");
         return TPMLP_ERR_SHAPE;

@@ -117,6 +117,29 @@ tpmlp_status launch_rows(const CUtensorMap& w, const Boxes& x, const Args& a, co
     return launch(kern, dim3(2 * pairs), THREADS, Geom<MODE>::smem, 2, st, w, x, a);
 }
 
+// Whether the forward product runs on the few-rows kernel.  The row ranges are on the device, so this goes by the tiles that
+// the pairs would have if the rows were spread over the experts: where they fill about half of the pairs, or, with at most
+// 16 rows an expert, up to four rounds of them (which do not come out even).  4 tokens, 8 of 64 experts, 1024 x 8192 gated
+// (256 tiles): 28.2 us, pairs 33.8; 4096 x 1024 (32 tiles): 14.8, 26.0; 128 rows on 8 experts of that size 18.1, 23.8; 666
+// rows (40 tiles) 22.6, 24.7.  But 128 rows on 34 of 64 experts, gated (2112 tiles): 112, pairs 104; 1024 rows on 16
+// experts, 4096 x 1024 (80 tiles): 36.1, 27.4.
+bool few_rows(int64_t rows, int64_t experts, int64_t m_blocks, int pairs) {
+    const int64_t tiles = m_blocks * (std::min(rows, experts) + rows / 256);
+    return rows <= 16 * experts ? tiles <= 4 * pairs : 20 * tiles <= 11 * pairs;
+}
+
+template <bool GATED>
+tpmlp_status launch_few(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
+    static PerDevice<bool> done;
+    auto kern = few_kernel<GATED>;
+    if (!set_smem(kern, dev.device, FEW_SMEM, done)) return TPMLP_ERR_CUDA;
+    const int64_t tiles = int64_t(a.m_blocks) * (a.rows / FEW_TN + std::min(a.experts, a.rows));
+    // the contraction is split while all CTAs, two an SM, run at once and each has at least four blocks of it
+    int ranks = 1;
+    while (ranks < 8 && tiles * 2 * ranks <= 2 * dev.sm_count && a.kb >= 8 * ranks) ranks *= 2;
+    return launch(kern, dim3(static_cast<unsigned>(tiles * ranks)), FEW_THREADS, FEW_SMEM, ranks, st, w, x, a);
+}
+
 // Sums of an expert's rows by column: CTA (64 columns, expert), rows in steps of 32, added in that order.
 constexpr int SUM_THREADS = 256;
 __global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const __nv_bfloat16* in, const int* offsets, int rows, int cols, void* out,
@@ -170,6 +193,8 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     a.features = static_cast<int>(g.gated ? g.N / 2 : g.N);
     const int tile = g.gated ? Geom<SWIGLU>::f : Geom<STORE>::f;
     a.m_blocks = (a.features + tile - 1) / tile;
+    const bool few = few_rows(g.rows, g.experts, a.m_blocks, dev.sm_count / 2);
+    if (few) a.m_blocks = (a.features + tile / 2 - 1) / (tile / 2);
     a.out = g.out;
     a.ld = a.features;
     a.out_f32 = g.out_f32;
@@ -182,6 +207,7 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     a.chunked = !g.gated && g.N % 64 == 0;
     const bool mapped = a.chunked ? make_chunks(&w, g.w, g.N, g.K, g.experts, 2) : make_map(&w, g.w, g.N, g.K, g.experts, BK);
     if (!mapped || !(g.src ? make_map(&x.m[0], g.x, g.K, g.tokens, 1, 1, 2) : make_boxes(&x, g.x, g.K, g.rows))) return TPMLP_ERR_CUDA;
+    if (few) return g.gated ? launch_few<true>(w, x, a, dev, st) : launch_few<false>(w, x, a, dev, st);
     return g.gated ? launch_rows<true, SWIGLU>(w, x, a, dev, st) : launch_rows<true, STORE>(w, x, a, dev, st);
 }
 

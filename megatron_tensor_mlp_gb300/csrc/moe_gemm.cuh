@@ -268,23 +268,35 @@ __device__ __forceinline__ int checked(const Args& p, int v) {
 }
 // Token of row r.
 __device__ __forceinline__ int token_of(const Args& p, int r) { return checked(p, p.src[r]); }
+// Row numbers of a warp's copies: rows row0 + 8 j .. + 3, at most `last`.  (All loads before the first check, which waits.)
+template <int PER>
+__device__ __forceinline__ void gather_rows(const Args& p, int row0, int last, int copies, int4 (&at)[PER]) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int r = row0 + j * 8;
+        at[j] = j < copies ? make_int4(p.src[min(r, last)], p.src[min(r + 1, last)], p.src[min(r + 2, last)], p.src[min(r + 3, last)])
+                           : make_int4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) at[j] = make_int4(checked(p, at[j].x), checked(p, at[j].y), checked(p, at[j].z), checked(p, at[j].w));
+}
 // Copies J .. J + N - 1 of a warp: groups of four rows, every second one of the operand.
-template <int J, int N, int PER>
+template <bool PAIR, int J, int N, int PER>
 __device__ __forceinline__ void gather_run(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, const int4 (&at)[PER]) {
 #pragma unroll
-    for (int j = J; j < J + N; ++j) tma_gather4_pair(dst + j * 1024, map, bar, x, at[j]);
+    for (int j = J; j < J + N; ++j) tma_gather4<PAIR>(dst + j * 1024, map, bar, x, at[j]);
 }
 // n of at most 2^k copies from J on, by halves.
-template <int J, int MOST, int PER>
+template <bool PAIR, int J, int MOST, int PER>
 __device__ __forceinline__ void gather_some(int n, uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, const int4 (&at)[PER]) {
     if (n == MOST) {
-        gather_run<J, MOST>(dst, map, bar, x, at);
+        gather_run<PAIR, J, MOST>(dst, map, bar, x, at);
     } else if constexpr (MOST > 1) {
         if (n >= MOST / 2) {
-            gather_run<J, MOST / 2>(dst, map, bar, x, at);
-            gather_some<J + MOST / 2, MOST / 2>(n - MOST / 2, dst, map, bar, x, at);
+            gather_run<PAIR, J, MOST / 2>(dst, map, bar, x, at);
+            gather_some<PAIR, J + MOST / 2, MOST / 2>(n - MOST / 2, dst, map, bar, x, at);
         } else {
-            gather_some<J, MOST / 2>(n, dst, map, bar, x, at);
+            gather_some<PAIR, J, MOST / 2>(n, dst, map, bar, x, at);
         }
     }
 }
@@ -467,22 +479,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int half = ((c.n + 15) & ~15) / 2, copies = half / 8;  // (half is a multiple of 8)
                 const int row0 = c.row0 + static_cast<int>(prank) * half + (warp - 2) * 4;
                 int4 at[PER];
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    at[j] = make_int4(0, 0, 0, 0);
-                    if (j < copies) {
-                        const int last = c.row0 + c.n - 1, r = row0 + j * 8;
-                        at[j] = make_int4(token_of(p, min(r, last)), token_of(p, min(r + 1, last)), token_of(p, min(r + 2, last)),
-                                          token_of(p, min(r + 3, last)));
-                    }
-                }
+                gather_rows(p, row0, c.row0 + c.n - 1, copies, at);
                 for (int it = 0; it < p.kb; ++it) {
                     if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer)) {
                         ok = false;
                         break;
                     }
                     if (elect_one())
-                        gather_some<0, PER>(copies, dst0 + stage * G::b_bytes, &tmX.m[0], full0 + stage * 8, it * BK, at);
+                        gather_some<true, 0, PER>(copies, dst0 + stage * G::b_bytes, &tmX.m[0], full0 + stage * 8, it * BK, at);
                     __syncwarp();
                     if (++stage == S) {
                         stage = 0;
@@ -656,6 +660,259 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 1) {
         __syncwarp();
         tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+// The forward product for few rows an expert, where reading the weights bounds the time: one CTA per tile of 128 columns of W
+// and at most 64 tokens, two CTAs an SM, not persistent, so that many copies are in flight and the SMs even out.  Clusters of
+// up to 8 CTAs split the contraction; groups of 8 tokens go to the cluster's CTAs in turn, which add the partial sums through
+// distributed shared memory in the order of the ranks.  (4 tokens on 8 of 64 experts, 1024 x 8192: 134 MB of weights, 20 us
+// at a copy's rate.)
+constexpr int FEW_TN = 64, FEW_STAGES = 4, FEW_THREADS = 256;
+constexpr int FEW_A = BM * 128, FEW_B = FEW_TN * 128, FEW_STAGE = FEW_A + FEW_B;
+constexpr int FEW_SUMS = 8 * 4096;  // partial sums on their way: 8 (rank, group of 8 tokens) of 128 lanes
+constexpr int FEW_SMEM = 1024 + FEW_STAGES * FEW_STAGE + (2 * FEW_STAGES + 2) * 8 + 64;
+static_assert(FEW_SUMS <= FEW_STAGES * FEW_STAGE && 2 * (FEW_SMEM + 1024) <= 227 * 1024, "few kernel shared memory");
+
+template <bool GATED>
+__global__ void __launch_bounds__(FEW_THREADS, 2)
+    few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Boxes tmX, const Args p) {
+    constexpr int S = FEW_STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + S * FEW_A;
+    Carve carve{smem + S * FEW_STAGE};
+    uint64_t* full = carve.take<uint64_t>(S);
+    uint64_t* empty = carve.take<uint64_t>(S);
+    uint64_t* tfull = carve.take<uint64_t>(1);
+    uint32_t* tmem_slot = carve.take<uint32_t>(2);
+    int* tile = carve.take<int>(4);   // expert, first row, rows, feature block
+    int* sums = carve.take<int>(8);   // tiles of each warp's experts
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t ranks;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+    const int n_ranks = static_cast<int>(ranks), rank = static_cast<int>(cluster_ctarank());
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(tfull, 1);
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmW);
+        tile[2] = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, FEW_TN);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    // this cluster's tile: feature blocks of an expert's first 64 tokens, of its next ..; threads have four experts each
+    {
+        const int t = blockIdx.x / n_ranks, e0 = threadIdx.x * 4;
+        int off[5], n[4], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) off[i] = e0 + i <= p.experts ? p.offsets[e0 + i] : 0;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const int c = min(max(off[i], 0), p.rows);
+            bad |= c != off[i];
+            off[i] = c;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool there = e0 + i < p.experts;
+            bad |= there && off[i + 1] < off[i];
+            n[i] = there ? max(off[i + 1] - off[i], 0) : 0;
+            mine += (n[i] + FEW_TN - 1) / FEW_TN * p.m_blocks;
+        }
+        if (bad && blockIdx.x == 0) atomicCAS(p.status, 0u, kStatusDevice);
+        int sum = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (lane == 31) sums[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) sum += sums[w];
+        int first = sum - mine;
+        if (t >= first && t < sum) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int nt = (n[i] + FEW_TN - 1) / FEW_TN, tiles = nt * p.m_blocks;
+                if (t >= first && t < first + tiles) {
+                    const int tb = (t - first) / p.m_blocks, sz = tile_tokens<FEW_TN>(n[i]);
+                    tile[0] = e0 + i;
+                    tile[1] = off[i] + tb * sz;
+                    tile[2] = min(sz, n[i] - tb * sz);
+                    tile[3] = (t - first) - tb * p.m_blocks;
+                }
+                first += tiles;
+            }
+        }
+        __syncthreads();
+    }
+    const Tile c{tile[0], tile[3], tile[1], tile[2]};
+    const int nn = (c.n + 15) & ~15;
+    const int k0 = p.kb * rank / n_ranks, k1 = p.kb * (rank + 1) / n_ranks;
+    bool ok = true;
+
+    if (c.n > 0) {
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            const Halves box(nn);
+            const uint32_t bytes = FEW_A + (p.src == nullptr ? box.rows() : nn) * 128;
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int it = k0; it < k1; ++it) {
+                ok = wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t bar = smem_u32(full + stage);
+                    uint8_t *a_dst = sA + stage * FEW_A, *b_dst = sB + stage * FEW_B;
+                    mbar_arrive_expect_tx(full + stage, bytes);
+                    if constexpr (GATED) {
+                        tma_load_3d_bar(a_dst, &tmW, bar, (c.mb >> 1) * 256 + (c.mb & 1) * 64, it * BK, c.e);
+                        tma_load_3d_bar(a_dst + CHUNK, &tmW, bar, (c.mb >> 1) * 256 + (c.mb & 1) * 64 + 128, it * BK, c.e);
+                    } else if (p.chunked) {
+                        tma_load_4d(a_dst, &tmW, full + stage, 0, it * BK, c.mb * 2, c.e);
+                    } else {
+                        tma_load_3d_bar(a_dst, &tmW, bar, c.mb * 128, it * BK, c.e);
+                        tma_load_3d_bar(a_dst + CHUNK, &tmW, bar, c.mb * 128 + 64, it * BK, c.e);
+                    }
+                    if (p.src == nullptr) {
+                        tma_load_3d_bar(b_dst, &tmX.m[box.first], bar, it * BK, c.row0, 0);
+                        if (box.second >= 0)
+                            tma_load_3d_bar(b_dst + (1024 << box.first), &tmX.m[box.second], bar, it * BK, c.row0 + (8 << box.first), 0);
+                    }
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                const uint64_t a0 = sdesc_sw128(smem_u32(sA), CHUNK, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+                const uint32_t idesc = idesc_bf16_f32(BM, nn, true, false);
+                int stage = 0;
+                uint32_t phase = 0;
+                for (int it = k0; it < k1; ++it) {
+                    ok = wait(p, full + stage, phase, kWhereMma);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t a = a0 + static_cast<uint64_t>(stage * (FEW_A >> 4)), b = b0 + static_cast<uint64_t>(stage * (FEW_B >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        umma_f16(tmem, a + kk * (2048 >> 4), b + kk * 2, idesc, it > k0 || kk > 0 ? 1u : 0u);
+                    umma_commit(empty + stage);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                umma_commit(tfull);
+            }
+        } else if (warp < EPI_WARP && p.src != nullptr) {
+            // ------------------------------------------------------------ gathered rows
+            const int copies = nn / 8;
+            int4 at[FEW_TN / 8];
+            gather_rows(p, c.row0 + (warp - 2) * 4, c.row0 + c.n - 1, copies, at);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int it = k0; it < k1; ++it) {
+                ok = wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer);
+                if (!ok) break;
+                if (elect_one())
+                    gather_some<false, 0, FEW_TN / 8>(copies, smem_u32(sB) + stage * FEW_B + (warp - 2) * 512, &tmX.m[0], smem_u32(full + stage),
+                                               it * BK, at);
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        __syncwarp();
+        // every warp waits for the products: the ring is then free for the sums
+        const bool done = wait_warp(p, tfull, 0, kWhereEpilogue);
+        ok = ok && done;
+        tc_fence_after();
+        fence_proxy_async_all();
+    }
+    if (n_ranks > 1) cluster_sync_all();  // all of the cluster's rings
+    // slot (rank, group / ranks) of the CTA that finishes a group: [token][lane]
+    const int groups = (c.n + 7) / 8, per = (groups + n_ranks - 1) / n_ranks;
+    float* part = reinterpret_cast<float*>(smem);
+    if (c.n > 0 && warp >= EPI_WARP) {
+        const int q = warp & 3;
+        for (int g = 0; g < groups; ++g) {
+            uint32_t r[8];
+            tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(q * 32) << 16) + g * 8, r);
+            tmem_ld_wait();
+            const uint32_t at = smem_u32(part + ((rank * per + g / n_ranks) * 8) * 128 + q * 32 + lane);
+            const uint32_t to = mapa_shared(at, static_cast<uint32_t>(g % n_ranks));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) st_cluster_u32(to + j * 512, r[j]);
+        }
+        tc_fence_before();
+    }
+    if (n_ranks > 1) cluster_sync_all();
+    else __syncthreads();
+    if (c.n > 0 && warp >= EPI_WARP && __all_sync(0xFFFFFFFFu, ok)) {
+        const int l = threadIdx.x - EPI_WARP * 32;
+        auto sum = [&](int gi, int j, int at) {
+            float v = 0.0f;
+            for (int r = 0; r < n_ranks; ++r) v += part[((r * per + gi) * 8 + j) * 128 + at];
+            return v;
+        };
+        for (int g = rank; g < groups; g += n_ranks) {
+            const int gi = g / n_ranks, n = min(c.n - g * 8, 8);
+            const long long row = c.row0 + g * 8;
+            if constexpr (GATED) {
+                const int f = c.mb * 64 + (l & 63);
+                const long long packed = static_cast<long long>(c.mb >> 1) * 256 + (c.mb & 1) * 64 + (l & 63);
+                const __nv_bfloat16* b = p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + packed;
+                const float bg = b == nullptr ? 0.0f : __bfloat162float(b[0]), bu = b == nullptr ? 0.0f : __bfloat162float(b[128]);
+                for (int j = l >> 6; j < n; j += 2) {
+                    const float x = sum(gi, j, l & 63) + bg, u = sum(gi, j, 64 + (l & 63)) + bu;
+                    if (p.h_out != nullptr) {
+                        p.h_out[(row + j) * p.h_ld + packed] = __float2bfloat16_rn(x);
+                        p.h_out[(row + j) * p.h_ld + packed + 128] = __float2bfloat16_rn(u);
+                    }
+                    static_cast<__nv_bfloat16*>(p.out)[(row + j) * p.ld + f] = __float2bfloat16_rn(x * tc::sigmoid_approx(x) * u);
+                }
+            } else {
+                const int f = c.mb * 128 + l;
+                if (f >= p.features) break;
+                const float b = p.bias == nullptr ? 0.0f : __bfloat162float(p.bias[c.e * p.bias_ld + f]);
+                for (int j = 0; j < n; ++j) {
+                    const float v = sum(gi, j, l) + b;
+                    if (p.out_f32) static_cast<float*>(p.out)[(row + j) * p.ld + f] = v;
+                    else static_cast<__nv_bfloat16*>(p.out)[(row + j) * p.ld + f] = __float2bfloat16_rn(v);
+                }
+            }
+        }
+    }
+    if (!ok) spin_ns(200000);  // copies that were not waited for land before this CTA exits
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, FEW_TN);
     }
 }
 
@@ -883,7 +1140,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint32_t dst = sa + stage * DW_A + (warp - 2) * CHUNK;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            tma_gather4_pair(dst + j * 512, &tmX, full0 + stage * 8, a0 + (warp - 2) * 64, rows[j]);
+                            tma_gather4<true>(dst + j * 512, &tmX, full0 + stage * 8, a0 + (warp - 2) * 64, rows[j]);
                     }
                     __syncwarp();
                     if (++stage == S) {

@@ -102,6 +102,8 @@ def test_route_of_no_tokens(T):
 
 # ------------------------------------------------------------------ products
 COUNTS = [0, 1, 15, 16, 17, 0, 129, 255, 256, 257, 300, 513, 0]
+# few rows an expert on average, which the forward takes on another kernel (tiles of 64 tokens, a split contraction)
+FEW = [0, 1, 15, 16, 17, 0, 63, 64, 65, 130, 300] + [0] * 20
 SHAPES = [(8, 8), (64, 256), (72, 136), (200, 520), (1032, 264)]
 
 
@@ -117,25 +119,28 @@ def case(counts, K, gather, seed=0, tokens=None, behind=37):
     return rows, off, src, rnd(tokens, K, seed=seed)
 
 
-@pytest.mark.parametrize("K,N", SHAPES)
+@pytest.mark.parametrize("K,N", SHAPES + [(4104, 136)])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("out", [BF, F32])
-def test_matmul(T, K, N, gather, out):
-    rows, off, src, x = case(COUNTS, K, gather, seed=K)
-    e = len(COUNTS)
+@pytest.mark.parametrize("counts", [COUNTS, FEW, [3, 0, 70]], ids=["many", "few", "three"])
+def test_matmul(T, K, N, gather, out, counts):
+    rows, off, src, x = case(counts, K, gather, seed=K)
+    e = len(counts)
     w, b = rnd(e, K, N, seed=2, scale=K**-0.5), rnd(e, N, seed=3)
-    w[0], w[5] = NAN, float("inf")  # experts without rows
+    for i in (i for i, c in enumerate(counts) if c == 0):
+        w[i] = NAN  # experts without rows
     y = torch.full((rows, N), 7.0, dtype=out, device="cuda")
     T.tpmlp_moe_matmul(x, src, off, w, b, y, None, x.shape[0], rows, e, K, N, out_dt=0 if out == BF else 1)
-    n = sum(COUNTS)
+    n = sum(counts)
     ref, size = R.matmul((x if src is None else x[src.long()])[:n], off, w, b)
     R.close(y[:n], ref, R.product_bound(K) * size, "Y")
     assert (y[n:] == 7.0).all()  # rows behind the last
 
 
-def test_matmul_of_whole_numbers_is_exact(T):
+@pytest.mark.parametrize("counts", [[300, 0, 70, 513, 2], [30, 0, 7, 51, 2, 129]])
+def test_matmul_of_whole_numbers_is_exact(T, counts):
     """Sums that bf16 holds: every place of every tile, without a tolerance."""
-    K, N, counts = 80, 392, [300, 0, 70, 513, 2]
+    K, N = 80, 392
     rows, off, src, _ = case(counts, K, True, behind=0)
     g = torch.Generator(device="cuda").manual_seed(5)
     x = torch.randint(-1, 2, (rows // 2, K), generator=g, device="cuda").to(BF)
@@ -154,25 +159,26 @@ def test_matmul_of_whole_numbers_is_exact(T):
     assert torch.equal(dw.to(R.D), ref[0]) and torch.equal(db.to(R.D), ref[2])
 
 
-def test_a_row_is_not_touched_by_its_neighbours(T):
+@pytest.mark.parametrize("more", [0, 10])
+def test_a_row_is_not_touched_by_its_neighbours(T, more):
     """NaN and infinities in other rows of the same tile, the same expert and the next stay where they are."""
-    K, N, counts = 136, 264, [20, 70, 130]
+    K, N, counts = 136, 264, [20, 70, 130] + [0] * more
     rows, off, _, x = case(counts, K, False, behind=0)
-    w, dy = rnd(3, K, N, seed=2, scale=K**-0.5), rnd(rows, N, seed=4)
+    w, dy = rnd(3 + more, K, N, seed=2, scale=K**-0.5), rnd(rows, N, seed=4)
     bad = [3, 20, 89, 90, 219]
     x[bad], dy[bad] = NAN, float("inf")
     good = torch.ones(rows, dtype=torch.bool, device="cuda")
     good[bad] = False
     y, dx = torch.empty(rows, N, dtype=BF, device="cuda"), torch.empty(rows, K, dtype=BF, device="cuda")
-    T.tpmlp_moe_matmul(x, None, off, w, None, y, None, rows, rows, 3, K, N)
-    T.tpmlp_moe_matmul_dx(dy, off, w, None, dx, rows, 3, K, N)
+    T.tpmlp_moe_matmul(x, None, off, w, None, y, None, rows, rows, 3 + more, K, N)
+    T.tpmlp_moe_matmul_dx(dy, off, w, None, dx, rows, 3 + more, K, N)
     assert torch.isfinite(y[good]).all() and torch.isnan(y[~good]).all()
     assert torch.isfinite(dx[good]).all() and not torch.isfinite(dx[~good]).any()
     # an expert's weight gradient is of its own rows alone
     x, dy = rnd(rows, K, seed=7), rnd(rows, N, seed=8)
     x[20:90], dy[20:90] = NAN, float("inf")
-    dw, db = torch.empty(3, K, N, dtype=F32, device="cuda"), torch.empty(3, N, dtype=F32, device="cuda")
-    T.tpmlp_moe_matmul_dw(x, None, off, dy, dw, db, rows, rows, 3, K, N)
+    dw, db = torch.empty(3 + more, K, N, dtype=F32, device="cuda"), torch.empty(3 + more, N, dtype=F32, device="cuda")
+    T.tpmlp_moe_matmul_dw(x, None, off, dy, dw, db, rows, rows, 3 + more, K, N)
     assert torch.isfinite(dw[0]).all() and torch.isfinite(dw[2]).all() and torch.isnan(dw[1]).all()
     assert torch.isfinite(db[0]).all() and torch.isfinite(db[2]).all()
 
@@ -182,12 +188,13 @@ def gated_slack(g, u, eg, eu):
     return 1.1 * eg * (u.abs() + eu) + R.silu(g).abs() * eu + 2.0**-20 * (R.silu(g) * u).abs()
 
 
-@pytest.mark.parametrize("K,f", [(8, 128), (72, 384), (200, 256), (1032, 640)])
+@pytest.mark.parametrize("K,f", [(8, 128), (72, 384), (200, 256), (1032, 640), (4104, 128)])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("save", [False, True])
-def test_gated_forward(T, K, f, gather, save):
-    rows, off, src, x = case(COUNTS, K, gather, seed=f)
-    e, n = len(COUNTS), sum(COUNTS)
+@pytest.mark.parametrize("counts", [COUNTS, FEW, [3, 0, 70]], ids=["many", "few", "three"])
+def test_gated_forward(T, K, f, gather, save, counts):
+    rows, off, src, x = case(counts, K, gather, seed=f)
+    e, n = len(counts), sum(counts)
     w, b = rnd(e, K, 2 * f, seed=2, scale=1.5 * K**-0.5), rnd(e, 2 * f, seed=3)
     y = torch.full((rows, f), 7.0, dtype=BF, device="cuda")
     h = torch.full((rows, 2 * f), 7.0, dtype=BF, device="cuda") if save else None
