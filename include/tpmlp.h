@@ -379,7 +379,7 @@ tpmlp_status tpmlp_layernorm_fwd(const void* X, const void* gamma, const void* b
  *   dX = rstd (g - mean(g) - xhat mean(g xhat)),  g = dY gamma,  xhat = (X - mean) rstd
  *   dgamma = sum over rows of dY xhat,  dbeta = sum over rows of dY     (each may be NULL; grad_dt)
  *   X, gamma, mean, rstd as in the forward; dY [rows][h] dt, pitch lddy; dX [rows][h] dt, pitch lddx.
- *   ws: tpmlp_layernorm_ws_bytes(rows, h) bytes (NULL where neither dgamma nor dbeta is wanted).
+ *   ws: tpmlp_layernorm_ws_bytes(rows, h) bytes, 16-byte aligned (NULL where neither dgamma nor dbeta is wanted).
  * The sums over rows are added in a fixed order: the same call gives the same bits.  Without rows dgamma and dbeta are
  * set to zero.
  */

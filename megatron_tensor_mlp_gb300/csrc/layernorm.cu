@@ -14,14 +14,18 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "gemm_tc.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "ptx.cuh"
 
 namespace tpmlp {
 namespace {
 
-constexpr int MOST_PARTS = 304;  // CTAs of the backward, two an SM
+// CTAs of the backward: two an SM, more where rows are short.
+constexpr int most_parts(long long h) { return h <= 96 * 32 ? 608 : 304; }
 constexpr int WARP_ROW = 1024;   // elements of a row that one warp takes
 // Threads of a CTA at most, by the elements that each holds.
 constexpr int most_threads(int elements) { return elements <= 8 ? 1024 : 512; }
@@ -191,7 +195,7 @@ template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(most_threads(VEC * NV)) bwd_kernel(const BwdArgs p) {
     using R = typename Raw<T, VEC>::type;
     __shared__ float buf[2 * 32 * 2];
-    __shared__ float acc[WARP_ROW];  // rows on warps: their sums, added warp by warp
+    extern __shared__ __align__(16) float warps_sums[];
     int turn = 0;
     griddep_wait();
     if (threadIdx.x == 0 && threadIdx.y == 0) griddep_launch_dependents();
@@ -269,56 +273,377 @@ __global__ void __launch_bounds__(most_threads(VEC * NV)) bwd_kernel(const BwdAr
                 out[p.h + c * VEC + j] = dbeta[i][j];
             }
         }
-    } else if constexpr (32 * NV * VEC <= WARP_ROW) {
+    } else {
+        // rows on warps: [warp][2][h], then the warps' sums in order
+        float* mine = warps_sums + static_cast<size_t>(threadIdx.y) * 2 * p.h;
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            for (int w = 0; w < static_cast<int>(blockDim.y); ++w) {
-                __syncthreads();
-                if (static_cast<int>(threadIdx.y) != w) continue;
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * nx + tx;
+            if (c >= p.vecs) continue;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = i * nx + tx;
-                    if (c >= p.vecs) continue;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const float v = which ? dbeta[i][j] : dgamma[i][j];
-                        acc[c * VEC + j] = w == 0 ? v : acc[c * VEC + j] + v;
-                        if (w == static_cast<int>(blockDim.y) - 1) out[which * p.h + c * VEC + j] = acc[c * VEC + j];
-                    }
-                }
+            for (int j = 0; j < VEC; ++j) {
+                mine[c * VEC + j] = dgamma[i][j];
+                mine[p.h + c * VEC + j] = dbeta[i][j];
             }
+        }
+        __syncthreads();
+        for (int c = threadIdx.y * nx + tx; c < 2 * p.h; c += nx * static_cast<int>(blockDim.y)) {
+            float v = 0.0f;
+            for (int w = 0; w < static_cast<int>(blockDim.y); ++w) v += warps_sums[static_cast<size_t>(w) * 2 * p.h + c];
+            out[c] = v;
         }
     }
 }
 
-// Sums of the parts' columns: 32 columns a CTA, part i on thread row i % 8, the eight sums added in order.
-__global__ void __launch_bounds__(256) parts_kernel(const float* part, int parts, int h, void* dgamma, void* dbeta, int f32) {
-    __shared__ float sum[8][33];
+// ---------------------------------------------------------------- many wide rows
+// The same for rows on a CTA that are aligned to 16 bytes, where there are more rows than CTAs: a CTA's next rows come by bulk
+// copies into a ring of shared memory while it works on one, since what its threads can hold in registers does not keep the
+// memory busy.  Sums in pairs of fp32 (add, mul and fma of two values an instruction: the arithmetic alone would take 23 us of
+// the backward's 40 at 8192 x 5120 otherwise).
+struct Ring {
+    uint8_t* at;        // slots of `bytes`
+    uint64_t* full;
+    uint32_t bytes;
+    int slots, slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void init(uint64_t* bars) {
+        full = bars;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < slots; ++i) mbar_init(full + i, 1);
+            fence_mbarrier_init();
+            fence_proxy_async_smem();
+        }
+        __syncthreads();
+    }
+    // A row that never comes is recorded in the status word; the walk goes on without waiting, so that all threads meet.
+    bool live = true;
+    __device__ __forceinline__ void wait(uint32_t* status) {
+        if (live) live = mbar_wait_bounded(full + slot, phase, status, 2000000000ull, kWhereProducer, false);  // 2 s
+    }
+    __device__ __forceinline__ void next() {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+constexpr int MOST_SLOTS = 8;
+
+// row_sum for a row on a CTA of at most 16 warps: every thread adds the warps' sums, in order, as it reads them (buf: two
+// sets of 16 x N floats, used in turn).
+template <int N>
+__device__ __forceinline__ void cta_sum(float (&v)[N], float* buf, int& turn) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
+    float* b = buf + turn * 16 * N;
+    turn ^= 1;
+    const int warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) b[i * 16 + (threadIdx.x >> 5)] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float4* q = reinterpret_cast<const float4*>(b + i * 16);
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // (places past the last warp hold zeros)
+            if (j * 4 >= warps) break;
+            const float4 w = q[j];
+            s += w.x;
+            s += w.y;
+            s += w.z;
+            s += w.w;
+        }
+        v[i] = s;
+    }
+}
+
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 both(float v) { return tc::f2_pack(v, v); }
+// Sum of a pair's halves over N pairs.
+__device__ __forceinline__ float halves_sum(f2 v) {
+    float a, b;
+    tc::f2_unpack(v, a, b);
+    return a + b;
+}
+// A piece of 16 bytes as pairs.
+template <typename T>
+__device__ __forceinline__ void pairs(const uint4& r, f2 (&f)[sizeof(T) == 2 ? 4 : 2]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = tc::f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) f[i] = tc::f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 unpair(const f2 (&f)[sizeof(T) == 2 ? 4 : 2]) {
+    uint32_t w[4];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            tc::f2_unpack(f[i], a, b);
+            w[i] = tc::pack_bf16x2(a, b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float a, b;
+            tc::f2_unpack(f[i], a, b);
+            w[2 * i] = __float_as_uint(a);
+            w[2 * i + 1] = __float_as_uint(b);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T, int NV, int THREADS, int PER_SM>
+__global__ void __launch_bounds__(THREADS, PER_SM) fwd_ring_kernel(const FwdArgs p, int slots, uint32_t* status) {
+    constexpr int P = sizeof(T) == 2 ? 4 : 2;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint64_t bars[MOST_SLOTS];
+    __shared__ __align__(16) float buf[2 * 16];
+    if (threadIdx.x < 2 * 16) buf[threadIdx.x] = 0.0f;
+    int turn = 0;
+    const uint32_t bytes = static_cast<uint32_t>(p.h) * sizeof(T);
+    Ring ring{smem, nullptr, bytes, slots};
+    ring.init(bars);
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    const int col = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5, which = blockIdx.y;
+    const int tx = threadIdx.x, nx = blockDim.x;
+    auto load = [&](long long row, int slot) {
+        if (tx == 0 && row < p.rows) {
+            mbar_arrive_expect_tx(ring.full + slot, bytes);
+            bulk_load(ring.at + static_cast<size_t>(slot) * bytes, static_cast<const T*>(p.x) + row * p.ldx, bytes, ring.full + slot);
+        }
+    };
+    for (int i = 0; i < slots; ++i) load(blockIdx.x + static_cast<long long>(i) * gridDim.x, i);
+    const uint32_t one = sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u;
+    uint4 gamma[NV], beta[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * nx + tx;
+        gamma[i] = make_uint4(one, one, one, one);
+        beta[i] = make_uint4(0, 0, 0, 0);
+        if (c < p.vecs && p.gamma != nullptr) gamma[i] = static_cast<const uint4*>(p.gamma)[c];
+        if (c < p.vecs && p.beta != nullptr) beta[i] = static_cast<const uint4*>(p.beta)[c];
+    }
+    const float inv = 1.0f / static_cast<float>(p.h);
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        ring.wait(status);
+        const uint4* x = reinterpret_cast<const uint4*>(ring.at + static_cast<size_t>(ring.slot) * bytes);
+        f2 v[NV][P], sum = 0;  // (the bits of two zeros)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * nx + tx;
+            if (c >= p.vecs) continue;
+            pairs<T>(x[c], v[i]);
+#pragma unroll
+            for (int j = 0; j < P; ++j) sum = tc::f2_add(sum, v[i][j]);
+        }
+        float s[1] = {halves_sum(sum)};
+        cta_sum<1>(s, buf, turn);
+        load(row + static_cast<long long>(slots) * gridDim.x, ring.slot);  // (all threads have read the slot)
+        ring.next();
+        const float mean = s[0] * inv;
+        const f2 less = both(-mean);
+        sum = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (i * nx + tx >= p.vecs) continue;
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                v[i][j] = tc::f2_add(v[i][j], less);
+                sum = tc::f2_fma(v[i][j], v[i][j], sum);
+            }
+        }
+        s[0] = halves_sum(sum);
+        cta_sum<1>(s, buf, turn);
+        const float rstd = rsqrtf(s[0] * inv + p.eps);
+        if (tx == 0 && p.mean != nullptr) {
+            p.mean[row] = mean;
+            p.rstd[row] = rstd;
+        }
+        const f2 r2 = both(rstd);
+        uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(p.y) + row * p.ldy);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * nx + tx;
+            if (c >= p.vecs) continue;
+            f2 g[P], b[P];
+            pairs<T>(gamma[i], g);
+            pairs<T>(beta[i], b);
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                v[i][j] = tc::f2_fma(tc::f2_mul(v[i][j], r2), g[j], b[j]);
+            y[c] = unpair<T>(v[i]);
+        }
+    }
+}
+
+template <typename T, int NV, int THREADS, int PER_SM>
+__global__ void __launch_bounds__(THREADS, PER_SM) bwd_ring_kernel(const BwdArgs p, int slots, uint32_t* status) {
+    constexpr int P = sizeof(T) == 2 ? 4 : 2;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint64_t bars[MOST_SLOTS];
+    __shared__ __align__(16) float buf[2 * 16 * 2];
+    if (threadIdx.x < 2 * 16 * 2) buf[threadIdx.x] = 0.0f;
+    int turn = 0;
+    const uint32_t bytes = static_cast<uint32_t>(p.h) * sizeof(T);  // a slot: x, then dy
+    Ring ring{smem, nullptr, 2 * bytes, slots};
+    ring.init(bars);
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    const int tx = threadIdx.x, nx = blockDim.x;
+    auto load = [&](long long row, int slot) {
+        if (tx == 0 && row < p.rows) {
+            uint8_t* at = ring.at + static_cast<size_t>(slot) * 2 * bytes;
+            mbar_arrive_expect_tx(ring.full + slot, 2 * bytes);
+            bulk_load(at, static_cast<const T*>(p.x) + row * p.ldx, bytes, ring.full + slot);
+            bulk_load(at + bytes, static_cast<const T*>(p.dy) + row * p.lddy, bytes, ring.full + slot);
+        }
+    };
+    for (int i = 0; i < slots; ++i) load(blockIdx.x + static_cast<long long>(i) * gridDim.x, i);
+    const uint32_t one = sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u;
+    uint4 gamma[NV];
+    f2 dgamma[NV][P], dbeta[NV][P];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * nx + tx;
+        gamma[i] = make_uint4(one, one, one, one);
+        if (c < p.vecs && p.gamma != nullptr) gamma[i] = static_cast<const uint4*>(p.gamma)[c];
+#pragma unroll
+        for (int j = 0; j < P; ++j) dgamma[i][j] = dbeta[i][j] = 0;
+    }
+    const float inv = 1.0f / static_cast<float>(p.h);
+    // the statistics of this row and the next three: a load takes longer than a row
+    constexpr int AHEAD = 4;
+    float means[AHEAD], rstds[AHEAD];
+    auto stat = [&](int i, long long row) {
+        means[i] = row < p.rows ? p.mean[row] : 0.0f;
+        rstds[i] = row < p.rows ? p.rstd[row] : 0.0f;
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) stat(i, blockIdx.x + static_cast<long long>(i) * gridDim.x);
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const float mean = means[0], rstd = rstds[0];
+#pragma unroll
+        for (int i = 0; i + 1 < AHEAD; ++i) {
+            means[i] = means[i + 1];
+            rstds[i] = rstds[i + 1];
+        }
+        stat(AHEAD - 1, row + static_cast<long long>(AHEAD) * gridDim.x);
+        ring.wait(status);
+        const uint4* x = reinterpret_cast<const uint4*>(ring.at + static_cast<size_t>(ring.slot) * 2 * bytes);
+        const uint4* dy = reinterpret_cast<const uint4*>(ring.at + static_cast<size_t>(ring.slot) * 2 * bytes + bytes);
+        const f2 less = both(-mean), r2 = both(rstd);
+        f2 s0 = 0, s1 = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * nx + tx;
+            if (c >= p.vecs) continue;
+            f2 n[P], d[P], w[P];
+            pairs<T>(x[c], n);
+            pairs<T>(dy[c], d);
+            pairs<T>(gamma[i], w);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                n[j] = tc::f2_mul(tc::f2_add(n[j], less), r2);
+                dgamma[i][j] = tc::f2_fma(d[j], n[j], dgamma[i][j]);
+                dbeta[i][j] = tc::f2_add(dbeta[i][j], d[j]);
+                d[j] = tc::f2_mul(d[j], w[j]);
+                s0 = tc::f2_add(s0, d[j]);
+                s1 = tc::f2_fma(d[j], n[j], s1);
+            }
+        }
+        float s[2] = {halves_sum(s0), halves_sum(s1)};
+        cta_sum<2>(s, buf, turn);
+        // all threads are past the row before: its slot may be filled again
+        if (row != blockIdx.x) load(row + static_cast<long long>(slots - 1) * gridDim.x, ring.slot == 0 ? slots - 1 : ring.slot - 1);
+        ring.next();
+        // rstd (g - a - n b), from the slot once more
+        const f2 a = both(-s[0] * inv), b = both(-s[1] * inv);
+        uint4* dx = reinterpret_cast<uint4*>(static_cast<T*>(p.dx) + row * p.lddx);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * nx + tx;
+            if (c >= p.vecs) continue;
+            f2 n[P], d[P], w[P];
+            pairs<T>(x[c], n);
+            pairs<T>(dy[c], d);
+            pairs<T>(gamma[i], w);
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                d[j] = tc::f2_mul(r2, tc::f2_fma(tc::f2_mul(tc::f2_add(n[j], less), r2), b, tc::f2_fma(d[j], w[j], a)));
+            dx[c] = unpair<T>(d);
+        }
+    }
+    if (p.part == nullptr) return;
+    float* out = p.part + static_cast<long long>(blockIdx.x) * 2 * p.h;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * nx + tx;
+        if (c >= p.vecs) continue;
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            reinterpret_cast<ulonglong2*>(out)[(c * P + j) / 2] = make_ulonglong2(dgamma[i][j], dgamma[i][j + 1]);
+            reinterpret_cast<ulonglong2*>(out + p.h)[(c * P + j) / 2] = make_ulonglong2(dbeta[i][j], dbeta[i][j + 1]);
+        }
+    }
+}
+
+// Sums of the parts' columns: 32 V columns a CTA, part i on warp i % 16, the warps' sums added in order.  All of a warp's
+// loads are on their way at once.
+constexpr int PART_WARPS = 16;
+template <int V>
+__global__ void __launch_bounds__(32 * PART_WARPS) parts_kernel(const float* part, int parts, int h, void* dgamma, void* dbeta, int f32) {
+    using R = typename std::conditional<V == 4, float4, float>::type;
+    __shared__ __align__(16) float sum[PART_WARPS][32 * V];
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, which = blockIdx.y, col = (blockIdx.x * 32 + lane) * V;
     void* out = which ? dbeta : dgamma;
     if (out == nullptr) return;
-    float s = 0.0f;
-    if (col < h)
-#pragma unroll 8
-        for (int i = r; i < parts; i += 8) s += part[(static_cast<long long>(i) * 2 + which) * h + col];
-    sum[r][threadIdx.x & 31] = s;
-    __syncthreads();
-    if (r == 0 && col < h) {
-        s = 0.0f;
+    float s[V] = {};
+    if (col < h) {
+        constexpr int BATCH = 19;
+        for (int i0 = r; i0 < parts; i0 += BATCH * PART_WARPS) {
+            R v[BATCH];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += sum[i][threadIdx.x];
-        if (f32) static_cast<float*>(out)[col] = s;
-        else static_cast<__nv_bfloat16*>(out)[col] = __float2bfloat16_rn(s);
+            for (int i = 0; i < BATCH; ++i) {
+                const int at = i0 + i * PART_WARPS;
+                v[i] = at < parts ? *reinterpret_cast<const R*>(part + (static_cast<long long>(at) * 2 + which) * h + col) : R{};
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] += reinterpret_cast<const float*>(v + i)[j];
+        }
+    }
+    *reinterpret_cast<R*>(&sum[r][lane * V]) = *reinterpret_cast<R*>(s);
+    __syncthreads();
+    const int c = blockIdx.x * 32 * V + threadIdx.x;
+    if (threadIdx.x < 32 * V && c < h) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PART_WARPS; ++i) t += sum[i][threadIdx.x];
+        if (f32) static_cast<float*>(out)[c] = t;
+        else static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(t);
     }
 }
 
 template <typename... P, typename... A>
-tpmlp_status launch(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t st, const A&... args) {
+tpmlp_status launch(void (*kern)(P...), dim3 grid, dim3 block, int smem, cudaStream_t st, const A&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see griddep_wait
@@ -370,9 +695,54 @@ bool wide_rows(int64_t h, int es, std::initializer_list<const void*> ptrs, std::
     return ok;
 }
 
+// How the ring kernels run: threads of a CTA at most, elements of each, CTAs an SM in the forward and in the backward.  Few
+// threads with much to do: what a thread does once a row (waits, the sums across the CTA) is as much work as 10 elements.
+// 8192 x 5120 bf16, backward without dgamma, dbeta: 16 elements a thread 52 us, 32 45 (floor 37); forward 36, 29 (25).
+template <int THREADS, int ELEMENTS, int FWD, int BWD>
+struct Conf {
+    static constexpr int threads = THREADS, elements = ELEMENTS, fwd = FWD, bwd = BWD;
+};
+struct RingShape {
+    int threads, slots;
+};
+RingShape ring_shape(int vecs, int nv, int per_sm, int64_t slot_bytes) {
+    return {(vecs + 32 * nv - 1) / (32 * nv) * 32,
+            static_cast<int>(std::min<int64_t>(MOST_SLOTS, (216 * 1024 / per_sm - 2048) / slot_bytes))};
+}
+
+template <typename Kern>
+bool allow_smem(Kern kern, const DeviceInfo& dev, int bytes, PerDevice<bool>& done) {
+    return done.get(dev.device, [&](bool& ok) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        return ok = e == cudaSuccess;
+    });
+}
+
+template <typename Kern, typename A>
+tpmlp_status launch_ring(Kern kern, PerDevice<bool>& done, int grid, const RingShape& r, int64_t slot_bytes, const A& a,
+                         const DeviceInfo& dev, cudaStream_t st) {
+    if (!allow_smem(kern, dev, 216 * 1024, done)) return TPMLP_ERR_CUDA;
+    return launch(kern, dim3(grid), dim3(r.threads), static_cast<int>(r.slots * slot_bytes), st, a, r.slots, dev.status);
+}
+
+// Calls f(type, configuration) for rows of `vecs` pieces that the ring kernels take; whether it ran.
+template <typename F>
+bool with_ring(bool f32, bool wide, int vecs, F&& f) {
+    const int h = vecs * (f32 ? 4 : 8);
+    if (!wide || h <= WARP_ROW) return false;
+    auto pick = [&](auto t) {
+        if (h <= 96 * 32) return f(t, Conf<96, 32, 5, 4>{});
+        if (h <= 160 * 32) return f(t, Conf<160, 32, 3, 2>{});
+        if (h <= 256 * 32) return f(t, Conf<256, 32, 2, 2>{});
+        return h <= 384 * 32 && f(t, Conf<384, 32, 1, 1>{});
+    };
+    return f32 ? pick(float{}) : pick(__nv_bfloat16{});
+}
+
 }  // namespace
 
-int64_t layernorm_ws_bytes(int64_t rows, int64_t h) { return std::min<int64_t>(rows, MOST_PARTS) * 2 * h * 4; }
+int64_t layernorm_ws_bytes(int64_t rows, int64_t h) { return std::min<int64_t>(rows, most_parts(h)) * 2 * h * 4; }
 
 tpmlp_status launch_layernorm_fwd(const void* X, const void* gamma, const void* beta, void* Y, float* mean, float* rstd, int64_t rows,
                                   int64_t h, int64_t ldx, int64_t ldy, float eps, bool f32, const DeviceInfo& dev, cudaStream_t st) {
@@ -380,10 +750,23 @@ tpmlp_status launch_layernorm_fwd(const void* X, const void* gamma, const void* 
     const bool wide = wide_rows(h, es, {X, gamma, beta, Y}, {ldx, ldy});
     const int vec = wide ? 16 / es : 1;
     const FwdArgs a{X, gamma, beta, Y, mean, rstd, rows, ldx, ldy, static_cast<int>(h), static_cast<int>(h / vec), eps};
+    tpmlp_status r = TPMLP_OK;
+    if (with_ring(f32, wide, a.vecs, [&](auto t, auto conf) {
+            using T = decltype(t);
+            using C = decltype(conf);
+            constexpr int NV = C::elements * static_cast<int>(sizeof(T)) / 16;
+            static PerDevice<bool> done;
+            const RingShape q = ring_shape(a.vecs, NV, C::fwd, h * es);
+            const int grid = C::fwd * dev.sm_count;
+            if (q.slots < 2 || rows <= 2 * grid) return false;
+            r = launch_ring(fwd_ring_kernel<T, NV, C::threads, C::fwd>, done, grid, q, h * es, a, dev, st);
+            return true;
+        }))
+        return r;
     const Shape s = shape_of(vec, a.vecs);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((rows + s.y - 1) / s.y, int64_t(dev.sm_count) * 64));
     return by_shape(f32, wide, s.nv, [&](auto t, auto v, auto nv) {
-        return launch(fwd_kernel<decltype(t), decltype(v)::value, decltype(nv)::value>, dim3(grid), dim3(s.x, s.y), st, a);
+        return launch(fwd_kernel<decltype(t), decltype(v)::value, decltype(nv)::value>, dim3(grid), dim3(s.x, s.y), 0, st, a);
     });
 }
 
@@ -395,13 +778,32 @@ tpmlp_status launch_layernorm_bwd(const void* X, const void* gamma, const float*
     const int vec = wide ? 16 / es : 1;
     const BwdArgs a{X, gamma, dY, mean, rstd, dX, sums ? static_cast<float*>(ws) : nullptr, rows, ldx, lddy, lddx, static_cast<int>(h),
                     static_cast<int>(h / vec)};
-    const Shape s = shape_of(vec, a.vecs);
-    const int grid = static_cast<int>(std::min<int64_t>({(rows + s.y - 1) / s.y, 2 * int64_t(dev.sm_count), MOST_PARTS}));
-    const tpmlp_status r = by_shape(f32, wide, s.nv, [&](auto t, auto v, auto nv) {
-        return launch(bwd_kernel<decltype(t), decltype(v)::value, decltype(nv)::value>, dim3(grid), dim3(s.x, s.y), st, a);
-    });
+    tpmlp_status r = TPMLP_OK;
+    int grid = 0;
+    if (!with_ring(f32, wide, a.vecs, [&](auto t, auto conf) {
+            using T = decltype(t);
+            using C = decltype(conf);
+            constexpr int NV = C::elements * static_cast<int>(sizeof(T)) / 16;
+            static PerDevice<bool> done;
+            const RingShape q = ring_shape(a.vecs, NV, C::bwd, 2 * h * es);
+            grid = std::min(C::bwd * dev.sm_count, most_parts(h));
+            if (q.slots < 2 || rows <= 2 * grid) return false;
+            r = launch_ring(bwd_ring_kernel<T, NV, C::threads, C::bwd>, done, grid, q, 2 * h * es, a, dev, st);
+            return true;
+        })) {
+        const Shape s = shape_of(vec, a.vecs);
+        grid = static_cast<int>(std::min<int64_t>({(rows + s.y - 1) / s.y, 2 * int64_t(dev.sm_count), most_parts(h)}));
+        const int smem = s.y > 1 && sums ? static_cast<int>(s.y * 2 * h * 4) : 0;
+        r = by_shape(f32, wide, s.nv, [&](auto t, auto v, auto nv) {
+            auto kern = bwd_kernel<decltype(t), decltype(v)::value, decltype(nv)::value>;
+            static PerDevice<bool> done;
+            return allow_smem(kern, dev, 8 * 2 * WARP_ROW * 4, done) ? launch(kern, dim3(grid), dim3(s.x, s.y), smem, st, a) : TPMLP_ERR_CUDA;
+        });
+    }
     if (r != TPMLP_OK || !sums) return r;
-    return launch(parts_kernel, dim3(static_cast<unsigned>((h + 31) / 32), 2), dim3(256), st, static_cast<const float*>(ws), grid,
+    const bool four = h % 4 == 0;  // 16 bytes at a time
+    const dim3 cols(static_cast<unsigned>((h + (four ? 127 : 31)) / (four ? 128 : 32)), 2);
+    return launch(four ? parts_kernel<4> : parts_kernel<1>, cols, dim3(32 * PART_WARPS), 0, st, static_cast<const float*>(ws), grid,
                   static_cast<int>(h), dgamma, dbeta, grad_f32 ? 1 : 0);
 }
 

@@ -171,7 +171,8 @@ tpmlp_status tpmlp_layernorm_bwd(const void* X, const void* gamma, const void* m
     const int es = esize(dt), gs = esize(grad_dt);
     TP_TRY(check_elements({X, gamma, dY, dX}, es));
     TP_TRY(check_elements({dgamma, dbeta}, gs));
-    TP_TRY(check_elements({mean, rstd, ws}, 4));
+    TP_TRY(check_elements({mean, rstd}, 4));
+    TP_TRY(check_aligned({sums ? ws : nullptr}));
     TP_TRY(check_alias({{dX, pitched(rows, h, lddx, es)}, {dgamma, h * gs}, {dbeta, h * gs}, {sums ? ws : nullptr, layernorm_ws_bytes(rows, h)}},
                        {{X, pitched(rows, h, ldx, es)}, {gamma, h * es}, {mean, rows * 4}, {rstd, rows * 4}, {dY, pitched(rows, h, lddy, es)}}));
     const DeviceInfo* dev;

@@ -26,7 +26,7 @@ def data(rows, h, dtype, seed=0, mean=0.5):
     return x, (1 + 0.3 * n(h)).to(dtype), (0.2 * n(h)).to(dtype), n(rows, h).to(dtype)
 
 
-# A sum of h terms: at most 32 in a thread and 10 levels across threads, each a rounding of 2^-24 of the magnitudes.
+# A sum of h terms: at most 32 in a thread and 16 across threads, each a rounding of 2^-24 of the magnitudes.
 SUM = 48 * 2.0**-24
 
 
@@ -69,7 +69,8 @@ def test_forward_and_backward(T, h, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("rows,h", [(1, 5120), (3, 64), (1000, 72), (5000, 136), (1303, 1001)])
+@pytest.mark.parametrize("rows,h", [(1, 5120), (3, 64), (1000, 72), (5000, 136), (1303, 1001), (2500, 1024), (1300, 1032), (1001, 3080),
+                                    (1001, 5120), (700, 8192), (700, 12288), (650, 16384), (650, 5121)])
 def test_row_counts_and_gradient_types(T, rows, h, dtype):
     """More rows than CTAs, fewer rows than CTAs; bf16 gradients; one of the two sums."""
     dt = 0 if dtype == BF else 1
@@ -78,7 +79,7 @@ def test_row_counts_and_gradient_types(T, rows, h, dtype):
     mean, rstd = rm.float(), rr.float()
     rdx, rdg, rdb = R.norm_bwd(x, gamma, mean, rstd, dy)
     ws = torch.empty(T.tpmlp_layernorm_ws_bytes(rows, h), dtype=torch.uint8, device="cuda")
-    # rows / 152 in a thread, up to 304 / 8 of parts, 8 at the end
+    # rows / 152 in a thread, 8 warps, up to 608 / 16 parts, 16 at the end
     slack = (rows / 152 + 64) * 2.0**-24
     xhat = (x.to(R.D) - mean.to(R.D)[:, None]).abs() * rstd.to(R.D)[:, None]
     sizes = (dy.to(R.D).abs() * xhat).sum(0), dy.to(R.D).abs().sum(0)
@@ -121,6 +122,30 @@ def test_strides_and_alignment(T, ld, shift, dtype):
     R.close(dxs[:, :h], rdx, 2 * SUM * s * (g + g.mean(1, keepdim=True) + xhat * (g * xhat).mean(1, keepdim=True)), "dx")
     if ld > h:
         assert (ys[:, h:] == 7.0).all() and (dxs[:, h:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,h", [(1900, 1032), (1000, 3080), (1001, 5120), (700, 8192), (700, 12288)])
+def test_many_wide_rows(T, rows, h, dtype):
+    """More rows than CTAs, which go through a ring in shared memory: with a pitch, without gamma or beta too."""
+    dt, ld = 0 if dtype == BF else 1, h + 8
+    x, gamma, beta, dy = data(rows, h, dtype, seed=h)
+    room = lambda t=None: torch.full((rows, ld), 7.0, dtype=dtype, device="cuda") if t is None else torch.nn.functional.pad(t, (0, 8), value=7.0)  # noqa: E731
+    xs, dys = room(x), room(dy)
+    for g, b in ((gamma, beta), (None, None), (gamma, None)):
+        y, dx = room(), room()
+        mean, rstd = torch.full((rows,), NAN, device="cuda"), torch.full((rows,), NAN, device="cuda")
+        T.tpmlp_layernorm_fwd(xs, g, b, y, mean, rstd, rows, h, ld, ld, 1e-5, dt)
+        ry, rm, rr = R.norm(x, g, b, 1e-5)
+        R.close(mean, rm, SUM * x.to(R.D).abs().mean(1), "mean")
+        R.close(rstd, rr, rr * (SUM + (SUM * x.to(R.D).abs().amax(1) * rr) ** 2), "rstd")
+        R.close(y[:, :h], ry, fwd_slack(x, g, rr, rm) + 2.0**-23 * (0 if b is None else b.to(R.D).abs()), "y")
+        T.tpmlp_layernorm_bwd(xs, g, mean, rstd, dys, dx, None, None, None, rows, h, ld, ld, ld, dt, 1)
+        rdx, _, _ = R.norm_bwd(x, g, mean, rstd, dy)
+        s = rstd.to(R.D)[:, None]
+        xhat, gg = (x.to(R.D) - mean.to(R.D)[:, None]).abs() * s, (dy.to(R.D) * (1 if g is None else g.to(R.D))).abs()
+        R.close(dx[:, :h], rdx, 2 * SUM * s * (gg + gg.mean(1, keepdim=True) + xhat * (gg * xhat).mean(1, keepdim=True)), "dx")
+        assert (y[:, h:] == 7.0).all() and (dx[:, h:] == 7.0).all()
 
 
 def test_without_gamma_and_beta(T):

@@ -63,7 +63,7 @@ def test_layernorm_refusals():
     assert norm_bwd(mean=None) == T.ERR_NULL and norm_bwd(ws=None) == T.ERR_NULL and norm_bwd(dX=None) == T.ERR_NULL
     assert norm_bwd(lddx=63) == T.ERR_SHAPE and norm_bwd(h=20000, ldx=20000, lddy=20000, lddx=20000) == T.ERR_SHAPE
     assert norm_bwd(grad_dt=7) == T.ERR_DTYPE and norm_bwd(dt=7) == T.ERR_DTYPE
-    assert norm_bwd(dgamma=addr(6) + 2) == T.ERR_ALIGNMENT and norm_bwd(ws=addr(8) + 2) == T.ERR_ALIGNMENT
+    assert norm_bwd(dgamma=addr(6) + 2) == T.ERR_ALIGNMENT and norm_bwd(ws=addr(8) + 8) == T.ERR_ALIGNMENT
     assert norm_bwd(dX=addr(4)) == T.ERR_ALIAS and norm_bwd(ws=addr(6) + 16) == T.ERR_ALIAS and norm_bwd(dbeta=addr(6)) == T.ERR_ALIAS
     for ok in (dict(), dict(dgamma=None), dict(dgamma=None, dbeta=None, ws=None), dict(gamma=None), dict(dgamma=addr(6) + 2, grad_dt=T.BF16)):
         assert norm_bwd(**ok) in REACHED
