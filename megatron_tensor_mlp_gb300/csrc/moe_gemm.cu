@@ -107,14 +107,15 @@ tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluste
     return TPMLP_OK;
 }
 
-template <bool W_MN, int MODE>
+template <bool W_MN, int MODE, bool WIDE = false>
 tpmlp_status launch_rows(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
     static PerDevice<bool> done;
-    auto kern = rows_kernel<W_MN, MODE>;
-    if (!set_smem(kern, dev.device, Geom<MODE>::smem, done)) return TPMLP_ERR_CUDA;
-    const int64_t most = int64_t(a.m_blocks) * (a.rows / Geom<MODE>::tn + std::min(a.experts, a.rows));
+    using G = Geom<MODE, WIDE>;
+    auto kern = rows_kernel<W_MN, MODE, WIDE>;
+    if (!set_smem(kern, dev.device, G::smem, done)) return TPMLP_ERR_CUDA;
+    const int64_t most = int64_t(a.m_blocks) * (a.rows / G::tn + std::min(a.experts, a.rows));
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(most, dev.sm_count / 2));
-    return launch(kern, dim3(2 * pairs), THREADS, Geom<MODE>::smem, 2, st, w, x, a);
+    return launch(kern, dim3(2 * pairs), THREADS, G::smem, 2, st, w, x, a);
 }
 
 // Whether the forward product runs on the few-rows kernel.  The row ranges are on the device, so this goes by the tiles that
@@ -127,6 +128,13 @@ bool few_rows(int64_t rows, int64_t experts, int64_t m_blocks, int pairs) {
     const int64_t tiles = m_blocks * (std::min(rows, experts) + rows / 256);
     return rows <= 16 * experts ? tiles <= 4 * pairs : 20 * tiles <= 11 * pairs;
 }
+
+// Whether the rows kernel runs on wide tiles.  For gathered rows, whose copies they halve: 16384 rows on 8 experts, 5120 x 8192
+// 735 us, narrow 811; 8192 rows on 64 experts, 1024 x 2048 gated 57, 79; where rows are few and weights large the other way
+// (2048 rows on 8 experts, 5120 x 8192: 152, 143).  For rows in order only where much is done for each byte (the first case
+// 801, 821, its gradient of the inputs 826, 875), since a tile's epilogue is not hidden (8192 rows on 16 experts, 4096 x 2048
+// 113, 106; the last case 151, 136).
+bool wide_tiles(const Args& a) { return a.src != nullptr || (a.rows >= 1024 * int64_t(a.experts) && a.kb >= 64); }
 
 template <bool GATED>
 tpmlp_status launch_few(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
@@ -194,7 +202,11 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     const int tile = g.gated ? Geom<SWIGLU>::f : Geom<STORE>::f;
     a.m_blocks = (a.features + tile - 1) / tile;
     const bool few = few_rows(g.rows, g.experts, a.m_blocks, dev.sm_count / 2);
-    if (few) a.m_blocks = (a.features + tile / 2 - 1) / (tile / 2);
+    const bool wide = !few && wide_tiles(a);
+    if (few || wide) {
+        const int t = few ? tile / 2 : tile * 2;
+        a.m_blocks = (a.features + t - 1) / t;
+    }
     a.out = g.out;
     a.ld = a.features;
     a.out_f32 = g.out_f32;
@@ -204,10 +216,13 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     a.h_ld = g.N;
     CUtensorMap w;
     Boxes x{};
-    a.chunked = !g.gated && g.N % 64 == 0;
-    const bool mapped = a.chunked ? make_chunks(&w, g.w, g.N, g.K, g.experts, 2) : make_map(&w, g.w, g.N, g.K, g.experts, BK);
+    // a CTA's columns of a stage in one copy: two chunks of 64 next to one another, the wide gated tile's four
+    const uint32_t chunks = g.gated ? (wide ? 4 : 0) : 2;
+    a.chunked = chunks > 0 && g.N % 64 == 0;
+    const bool mapped = a.chunked ? make_chunks(&w, g.w, g.N, g.K, g.experts, chunks) : make_map(&w, g.w, g.N, g.K, g.experts, BK);
     if (!mapped || !(g.src ? make_map(&x.m[0], g.x, g.K, g.tokens, 1, 1, 2) : make_boxes(&x, g.x, g.K, g.rows))) return TPMLP_ERR_CUDA;
     if (few) return g.gated ? launch_few<true>(w, x, a, dev, st) : launch_few<false>(w, x, a, dev, st);
+    if (wide) return g.gated ? launch_rows<true, SWIGLU, true>(w, x, a, dev, st) : launch_rows<true, STORE, true>(w, x, a, dev, st);
     return g.gated ? launch_rows<true, SWIGLU>(w, x, a, dev, st) : launch_rows<true, STORE>(w, x, a, dev, st);
 }
 
@@ -224,7 +239,12 @@ tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaS
     CUtensorMap w;
     Boxes x;
     if (!make_map(&w, g.w, g.N, g.K, g.experts, BM) || !make_boxes(&x, g.x, g.N, g.rows)) return TPMLP_ERR_CUDA;
-    return g.gated ? launch_rows<false, DSWIGLU>(w, x, a, dev, st) : launch_rows<false, STORE>(w, x, a, dev, st);
+    if (g.gated) return launch_rows<false, DSWIGLU>(w, x, a, dev, st);
+    if (wide_tiles(a)) {
+        a.m_blocks = (a.features + 511) / 512;
+        return launch_rows<false, STORE, true>(w, x, a, dev, st);
+    }
+    return launch_rows<false, STORE>(w, x, a, dev, st);
 }
 
 tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st) {

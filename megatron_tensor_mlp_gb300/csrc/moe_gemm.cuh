@@ -190,6 +190,34 @@ __device__ __forceinline__ void rows_load(const __nv_bfloat16* src, long long ld
         v[i] = t < n && c * 8 < nf ? *reinterpret_cast<const uint4*>(src + t * ld + c * 8) : make_uint4(0, 0, 0, 0);
     }
 }
+// Packed fragments of 32 tokens x 32 features to their rows in memory.
+__device__ __forceinline__ void put_rows(uint8_t* buf, __nv_bfloat16* dst, long long ld, const uint32_t (&lo)[8], const uint32_t (&hi)[8],
+                                         int n, int nf, int lane) {
+    stage_put(smem_u32(buf), lo, hi, lane);
+    __syncwarp();
+    stage_store(buf, dst, ld, n, nf, lane);
+    __syncwarp();
+}
+__device__ __forceinline__ void pack_frags(const uint32_t (&a)[16], const uint32_t (&b)[16], uint32_t (&lo)[8], uint32_t (&hi)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo[i] = tc::pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+        hi[i] = tc::pack_bf16x2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+    }
+}
+// silu(gate) up, packed
+__device__ __forceinline__ void gate_frags(const uint32_t (&a)[16], const uint32_t (&b)[16], const uint32_t (&ua)[16],
+                                           const uint32_t (&ub)[16], uint32_t (&lo)[8], uint32_t (&hi)[8]) {
+    auto gated = [](uint32_t g, uint32_t u) {
+        const float x = __uint_as_float(g);
+        return x * tc::sigmoid_approx(x) * __uint_as_float(u);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo[i] = tc::pack_bf16x2(gated(a[2 * i], ua[2 * i]), gated(a[2 * i + 1], ua[2 * i + 1]));
+        hi[i] = tc::pack_bf16x2(gated(b[2 * i], ub[2 * i]), gated(b[2 * i + 1], ub[2 * i + 1]));
+    }
+}
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -223,16 +251,19 @@ __device__ __forceinline__ void load_bias(const __nv_bfloat16* bias, int nf, int
 }
 
 // ---------------------------------------------------------------- rows kernel
-template <int MODE>
+// WIDE: two accumulators of 256 tokens, twice the features, for gathered rows: a stage's copies of rows, which bound the
+// narrow tile's time, then feed twice the MMAs.  Both take all of tensor memory, so a tile's epilogue and the next tile's
+// products do not overlap.
+template <int MODE, bool WIDE = false>
 struct Geom {
     static constexpr int tn = 256;                      // tokens of a tile at most
-    static constexpr int f = MODE == SWIGLU ? 128 : 256;  // features of a tile (SWIGLU: gate and up of each)
-    static constexpr int a_bytes = BM * 128;            // this CTA's features of a stage
+    static constexpr int f = (MODE == SWIGLU ? 128 : 256) * (WIDE ? 2 : 1);  // features of a tile (SWIGLU: gate and up of each)
+    static constexpr int a_bytes = BM * 128 * (WIDE ? 2 : 1);  // this CTA's features of a stage
     static constexpr int b_bytes = tn / 2 * 128;        // this CTA's half of the tokens
     static constexpr int stage = a_bytes + b_bytes;
     static constexpr int epi = (MODE == DSWIGLU ? 2 : 1) * STAGE;  // staging of an epilogue warp
-    static constexpr int pass = MODE == SWIGLU ? 4 * 4096 : 0;     // up accumulators on their way to the gate's warps
-    static constexpr int stages = MODE == STORE ? 6 : 5;
+    static constexpr int pass = MODE == SWIGLU && !WIDE ? 4 * 4096 : 0;  // up accumulators on their way to the gate's warps
+    static constexpr int stages = WIDE ? 4 : MODE == STORE ? 6 : 5;
     static constexpr int smem = 1024 + stages * stage + EPI_WARPS * epi + pass + (most_barriers + 1) * 8 + TABLE;
     static_assert(smem <= 227 * 1024, "rows kernel shared memory");
     static_assert(2 * stages + 5 <= most_barriers);
@@ -301,10 +332,11 @@ __device__ __forceinline__ void gather_some(int n, uint32_t dst, const CUtensorM
     }
 }
 
-template <bool W_MN, int MODE>
+template <bool W_MN, int MODE, bool WIDE = false>
 __global__ void __launch_bounds__(THREADS, 1)
     rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Boxes tmX, const Args p) {
-    using G = Geom<MODE>;
+    using G = Geom<MODE, WIDE>;
+    static_assert(MODE != DSWIGLU || !WIDE);
     constexpr int S = G::stages, TN = G::tn;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -363,8 +395,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             const Tile c = decode<TN>(p, tab, t, e);
             const int nn = (c.n + 15) & ~15, half = nn / 2;  // columns of the MMA, tokens of this CTA
             const int row0 = c.row0 + static_cast<int>(prank) * half;
-            // (SWIGLU: 64 gate features of block mb, their up features 128 columns on)
-            const int f0 = c.mb * 256 + static_cast<int>(prank) * (MODE == SWIGLU ? 64 : BM);
+            // first column of W of this CTA's (SWIGLU: 64, or 128, gate features of block mb, their up features 128 columns on)
+            const int f0 = MODE != SWIGLU ? c.mb * G::f + static_cast<int>(prank) * BM
+                           : WIDE         ? (c.mb * 2 + static_cast<int>(prank)) * 256
+                                          : c.mb * 256 + static_cast<int>(prank) * 64;
             const Halves box(half);
             const uint32_t bytes = 2 * (G::a_bytes + (p.src == nullptr ? box.rows() : half) * 128);
             for (int it = 0; it < p.kb; ++it) {
@@ -383,13 +417,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     if constexpr (!W_MN) {
                         tma_load_3d_pair(a_dst, &tmW, bar, it * BK, f0, c.e);
+                        if constexpr (WIDE) tma_load_3d_pair(a_dst + BM * 128, &tmW, bar, it * BK, f0 + 256, c.e);
                     } else {
-                        if (MODE != SWIGLU && p.chunked) {
+                        // chunks of 64 columns, SWIGLU's narrow tile every second one, STORE's wide tile two and, 256 on, two
+                        if (p.chunked) {
                             tma_load_4d_pair(a_dst, &tmW, bar, 0, it * BK, f0 / 64, c.e);
+                            if constexpr (MODE == STORE && WIDE) tma_load_4d_pair(a_dst + 2 * CHUNK, &tmW, bar, 0, it * BK, f0 / 64 + 4, c.e);
                         } else {
 #pragma unroll
                             for (int j = 0; j < G::a_bytes / CHUNK; ++j)
-                                tma_load_3d_pair(a_dst + j * CHUNK, &tmW, bar, f0 + j * (MODE == SWIGLU ? 128 : 64), it * BK, c.e);
+                                tma_load_3d_pair(a_dst + j * CHUNK, &tmW, bar,
+                                                 f0 + (MODE == SWIGLU && !WIDE ? j * 128 : j * 64 + (MODE == STORE ? j / 2 * 128 : 0)),
+                                                 it * BK, c.e);
                         }
                     }
                     if (p.src == nullptr) {
@@ -435,8 +474,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int t = cluster_id; t < n_tiles && ok; t += n_clusters, ++lt) {
                     const Tile c = decode<TN>(p, tab, t, e);
                     const uint32_t idesc = idesc_bf16_f32(2 * BM, (c.n + 15) & ~15, W_MN, false);
-                    const int acc = lt & 1;
-                    if (!wait(p, tempty + acc, ((lt >> 1) & 1) ^ 1u, kWhereMma)) {
+                    const int acc = WIDE ? 0 : lt & 1;
+                    const uint32_t turn = WIDE ? lt & 1 : (lt >> 1) & 1;
+                    if (!wait(p, tempty + acc, turn ^ 1u, kWhereMma)) {
                         ok = false;
                         break;
                     }
@@ -449,8 +489,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint64_t a = a0 + static_cast<uint64_t>(stage * (G::a_bytes >> 4));
                         const uint64_t b = b0 + static_cast<uint64_t>(stage * (G::b_bytes >> 4));
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
+                        for (int kk = 0; kk < BK / 16; ++kk) {
                             umma_f16_pair(d, a + kk * a_step, b + kk * 2, idesc, (it | kk) != 0 ? 1u : 0u);
+                            if constexpr (WIDE)
+                                umma_f16_pair(d + 256, a + (BM * 128 >> 4) + kk * a_step, b + kk * 2, idesc, (it | kk) != 0 ? 1u : 0u);
+                        }
                         umma_commit_pair_mc(empty + stage, 0x3);
                         if (++stage == S) {
                             stage = 0;
@@ -460,8 +503,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (ok) umma_commit_pair_mc(tfull + acc, 0x3);
                 }
                 umma_commit_pair_mc(drain, 0x3);
-                // both accumulators' last releases land before this CTA can exit
-                for (int i = 0; ok && i < 2; ++i, ++lt)
+                // the accumulators' last releases land before this CTA can exit
+                if (WIDE) ok = ok && wait(p, tempty, (lt & 1) ^ 1u, kWhereDrain);
+                for (int i = 0; !WIDE && ok && i < 2; ++i, ++lt)
                     ok = wait(p, tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, kWhereDrain);
             }
             wait(p, drain, 0, kWhereDrain);
@@ -505,22 +549,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         int lt = 0, e = 0;
         for (int t = cluster_id; t < n_tiles; t += n_clusters, ++lt) {
             const Tile c = decode<TN>(p, tab, t, e);
-            const int acc = lt & 1;
+            const int acc = WIDE ? 0 : lt & 1;
             int okw = 0;
-            if (lane == 0) okw = wait(p, tfull + acc, (lt >> 1) & 1, kWhereEpilogue);
+            if (lane == 0) okw = wait(p, tfull + acc, WIDE ? lt & 1 : (lt >> 1) & 1, kWhereEpilogue);
             okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
-            if constexpr (MODE == SWIGLU) okw = pair_and(1 + half * 2 + (q & 1), okw);  // both or neither go on to meet
+            if constexpr (MODE == SWIGLU && !WIDE) okw = pair_and(1 + half * 2 + (q & 1), okw);  // both or neither go on to meet
             if (!okw) break;
             tc_fence_after();
-            // features f0 .. f0 + 31 (SWIGLU: of gate and up, this warp's the gate where q < 2)
-            const int f0 = MODE == SWIGLU ? c.mb * 128 + static_cast<int>(prank) * 64 + (q & 1) * 32
-                                          : c.mb * 256 + static_cast<int>(prank) * BM + q * 32;
+          for (int part = 0; part < (WIDE && MODE == STORE ? 2 : 1); ++part) {  // (the wide tile's accumulators)
+            // features f0 .. f0 + 31 (SWIGLU: of gate and up; narrow, this warp's the gate where q < 2)
+            const int f0 = MODE == SWIGLU && !WIDE ? c.mb * 128 + static_cast<int>(prank) * 64 + (q & 1) * 32
+                                                   : c.mb * G::f + part * 256 + static_cast<int>(prank) * BM + q * 32;
             const int nf = min(p.features - f0, 32);
-            const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-            const long long packed = static_cast<long long>(f0 >> 7) * 256 + (f0 & 127) + (MODE == SWIGLU ? (q >> 1) * 128 : 0);
-            [[maybe_unused]] float bias[4];
-            if constexpr (MODE != DSWIGLU)
-                load_bias(p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + (MODE == SWIGLU ? packed : f0), nf, lane, bias);
+            const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc + part) * 256;
+            const long long packed = static_cast<long long>(f0 >> 7) * 256 + (f0 & 127) + (MODE == SWIGLU && !WIDE ? (q >> 1) * 128 : 0);
+            [[maybe_unused]] float bias[4], bias_up[4];
+            if constexpr (MODE != DSWIGLU) {
+                const __nv_bfloat16* at = p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + (MODE == SWIGLU ? packed : f0);
+                load_bias(at, nf, lane, bias);
+                if constexpr (MODE == SWIGLU && WIDE) load_bias(at == nullptr ? nullptr : at + 128, nf, lane, bias_up);
+            }
             for (int c0 = half * (TN / 2); c0 < (half + 1) * (TN / 2) && c0 < c.n && nf > 0; c0 += 32) {
                 const int n = min(c.n - c0, 32);
                 const long long row = c.row0 + c0;
@@ -547,10 +595,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                         lo[i] = tc::pack_bf16x2(__uint_as_float(a[2 * i]) + ba, __uint_as_float(a[2 * i + 1]) + ba);
                         hi[i] = tc::pack_bf16x2(__uint_as_float(b[2 * i]) + bb, __uint_as_float(b[2 * i + 1]) + bb);
                     }
-                    stage_put(sbuf, lo, hi, lane);
-                    __syncwarp();
-                    stage_store(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, n, nf, lane);
-                    __syncwarp();
+                    put_rows(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, lo, hi, n, nf, lane);
+                } else if constexpr (MODE == SWIGLU && WIDE) {
+                    uint32_t ua[16], ub[16];
+                    load_frags(lanes + 256 + c0, ua, ub);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int j = (i >> 1) & 1;
+                        a[i] = __float_as_uint(__uint_as_float(a[i]) + bias[j]);
+                        b[i] = __float_as_uint(__uint_as_float(b[i]) + bias[2 + j]);
+                        ua[i] = __float_as_uint(__uint_as_float(ua[i]) + bias_up[j]);
+                        ub[i] = __float_as_uint(__uint_as_float(ub[i]) + bias_up[2 + j]);
+                    }
+                    if (p.h_out != nullptr) {
+                        __nv_bfloat16* h = p.h_out + row * p.h_ld + packed;
+                        pack_frags(a, b, lo, hi);
+                        put_rows(buf, h, p.h_ld, lo, hi, n, nf, lane);
+                        pack_frags(ua, ub, lo, hi);
+                        put_rows(buf, h + 128, p.h_ld, lo, hi, n, nf, lane);
+                    }
+                    gate_frags(a, b, ua, ub, lo, hi);
+                    put_rows(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, lo, hi, n, nf, lane);
                 } else if constexpr (MODE == SWIGLU) {
                     tmem_ld_wait();
 #pragma unroll
@@ -581,30 +647,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     pair_sync(1 + pair);  // read: the next ones may be written
                     if (p.h_out != nullptr) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            lo[i] = tc::pack_bf16x2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
-                            hi[i] = tc::pack_bf16x2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
-                        }
-                        stage_put(sbuf, lo, hi, lane);
-                        __syncwarp();
-                        stage_store(buf, p.h_out + row * p.h_ld + packed, p.h_ld, n, nf, lane);
-                        __syncwarp();
+                        pack_frags(a, b, lo, hi);
+                        put_rows(buf, p.h_out + row * p.h_ld + packed, p.h_ld, lo, hi, n, nf, lane);
                     }
                     if (q < 2) {
-                        auto gated = [](uint32_t g, uint32_t u) {
-                            const float x = __uint_as_float(g);
-                            return x * tc::sigmoid_approx(x) * __uint_as_float(u);
-                        };
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            lo[i] = tc::pack_bf16x2(gated(a[2 * i], ua[2 * i]), gated(a[2 * i + 1], ua[2 * i + 1]));
-                            hi[i] = tc::pack_bf16x2(gated(b[2 * i], ub[2 * i]), gated(b[2 * i + 1], ub[2 * i + 1]));
-                        }
-                        stage_put(sbuf, lo, hi, lane);
-                        __syncwarp();
-                        stage_store(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, n, nf, lane);
-                        __syncwarp();
+                        gate_frags(a, b, ua, ub, lo, hi);
+                        put_rows(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, lo, hi, n, nf, lane);
                     }
                 } else {
                     const __nv_bfloat16* h = p.h_in + row * p.h_ld + packed;
@@ -646,6 +694,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                 }
             }
+          }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + acc * 8);
