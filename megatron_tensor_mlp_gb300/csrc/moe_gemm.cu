@@ -65,6 +65,25 @@ bool make_chunks(CUtensorMap* map, const void* ptr, uint64_t cols, uint64_t rows
     }
     return true;
 }
+// The output [slices][rows][cols] in boxes of 64 bytes x 32 rows, 64-byte swizzle.
+bool make_out_map(CUtensorMap* map, void* ptr, uint64_t cols, uint64_t rows, uint64_t slices, bool f32) {
+    auto fn = encode_fn();
+    if (!fn) {
+        set_error("cuTensorMapEncodeTiled is not available from the driver");
+        return false;
+    }
+    const uint64_t es = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {cols, rows, slices}, strides[2] = {cols * es, cols * rows * es};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / es), 32, 1}, estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled (experts, output) failed (%d)", static_cast<int>(r));
+        return false;
+    }
+    return true;
+}
 // The rows' maps of the rows kernel.
 bool make_boxes(Boxes* b, const void* ptr, uint64_t cols, uint64_t rows) {
     for (int i = 0; i < 5; ++i)
@@ -146,6 +165,14 @@ tpmlp_status launch_few(const CUtensorMap& w, const Boxes& x, const Args& a, con
     int ranks = 1;
     while (ranks < 8 && tiles * 2 * ranks <= 2 * dev.sm_count && a.kb >= 8 * ranks) ranks *= 2;
     return launch(kern, dim3(static_cast<unsigned>(tiles * ranks)), FEW_THREADS, FEW_SMEM, ranks, st, w, x, a);
+}
+
+template <bool WIDE>
+tpmlp_status launch_dw(const CUtensorMap& x, const CUtensorMap& y, const CUtensorMap& o, const Args& a, unsigned pairs, const DeviceInfo& dev, cudaStream_t st) {
+    static PerDevice<bool> done;
+    auto kern = dw_kernel<WIDE>;
+    if (!set_smem(kern, dev.device, DwGeom<WIDE>::smem, done)) return TPMLP_ERR_CUDA;
+    return launch(kern, dim3(2 * pairs), THREADS, DwGeom<WIDE>::smem, 2, st, x, y, o, a);
 }
 
 // Sums of an expert's rows by column: CTA (64 columns, expert), rows in steps of 32, added in that order.
@@ -252,18 +279,19 @@ tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaS
     a.features = static_cast<int>(g.K);
     a.cols = static_cast<int>(g.N);
     a.m_blocks = (a.features + 255) / 256;
-    a.n_blocks = (a.cols + 255) / 256;
+    const bool wide = g.src != nullptr;  // (see wide_tiles; without a gather narrow tiles are as fast or faster: WDW)
+    a.n_blocks = (a.cols + (wide ? 511 : 255)) / (wide ? 512 : 256);
     a.out = g.out;
     a.ld = g.N;
     a.out_f32 = g.out_f32;
-    static PerDevice<bool> done;
-    if (!set_smem(dw_kernel, dev.device, DW_SMEM, done)) return TPMLP_ERR_CUDA;
     a.dy = static_cast<const __nv_bfloat16*>(g.dy);
-    CUtensorMap x{}, y;
-    if (!(g.src ? make_map(&x, g.x, g.K, g.tokens, 1, 1, 2) : make_map(&x, g.x, g.K, g.rows, 1, BK)) || !make_map(&y, g.dy, g.N, g.rows, 1, BK)) return TPMLP_ERR_CUDA;
+    CUtensorMap x{}, y, o;
+    if (!(g.src ? make_map(&x, g.x, g.K, g.tokens, 1, 1, 2) : make_map(&x, g.x, g.K, g.rows, 1, BK)) || !make_map(&y, g.dy, g.N, g.rows, 1, BK) ||
+        !make_out_map(&o, g.out, g.N, g.K, g.experts, g.out_f32))
+        return TPMLP_ERR_CUDA;
     const int64_t tiles = int64_t(a.experts) * a.m_blocks * a.n_blocks;
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles, dev.sm_count / 2));
-    const tpmlp_status st1 = launch(dw_kernel, dim3(2 * pairs), THREADS, DW_SMEM, 2, st, x, y, a);
+    const tpmlp_status st1 = wide ? launch_dw<true>(x, y, o, a, pairs, dev, st) : launch_dw<false>(x, y, o, a, pairs, dev, st);
     if (st1 != TPMLP_OK || g.dbias == nullptr) return st1;
     return launch(sums_kernel, dim3(static_cast<unsigned>((g.N + 63) / 64), static_cast<unsigned>(g.experts)), SUM_THREADS, 0, 1, st,
                   static_cast<const __nv_bfloat16*>(g.dy), g.offsets, a.rows, a.cols, g.dbias, a.out_f32);

@@ -980,20 +980,48 @@ struct Lane {
         return static_cast<uint32_t>(j * 512 + r0 * 128 + ((piece ^ (r0 + 4 * (j & 1))) << 4));
     }
 };
-constexpr int DW_STAGES = 6;
-constexpr int DW_A = BM * 128, DW_B = BM * 128, DW_STAGE = DW_A + DW_B;
-constexpr int DW_SMEM = 1024 + DW_STAGES * DW_STAGE + 32 * 16 + (most_barriers + 1) * 8 + TABLE;
-static_assert(5 * DW_STAGES + 5 <= most_barriers);
-static_assert(DW_SMEM <= 227 * 1024, "dw kernel shared memory");
+// WIDE: two accumulators, 512 columns of dY, for gathered rows, as in the rows kernel.
+constexpr int DW_A = BM * 128;
+template <bool WIDE>
+struct DwGeom {
+    static constexpr int n = WIDE ? 512 : 256;           // columns of a tile
+    static constexpr int parts = WIDE ? 2 : 1;           // accumulators of a tile, of 256 columns
+    static constexpr int b_bytes = parts * BM * 128;     // this CTA's half of each
+    static constexpr int stage = DW_A + b_bytes;
+    static constexpr int stages = WIDE ? 4 : 6;
+    static constexpr int smem = 1024 + stages * stage + EPI_WARPS * STAGE + 32 * 16 + (most_barriers + 1) * 8 + TABLE;
+    static_assert(smem <= 227 * 1024, "dw kernel shared memory");
+    static_assert(5 * stages + 5 <= most_barriers);
+};
 
+// 64 bytes of each of a warp's 32 rows through its box of shared memory to the output: a store of its own per lane would
+// touch 32 rows an instruction.  (8192 rows on 64 experts, 1024 x 2048, whose contractions are short: DWSTORE.)
+__device__ __forceinline__ void put_box(uint8_t* box, const CUtensorMap* map, const uint32_t (&w)[32], int x, int y, int z, int lane) {
+    if (lane == 0) bulk_wait_group_read<0>();  // the box has been read
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(box + stage_at(lane, i)) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_3d(map, box, x, y, z);
+        bulk_commit_group();
+    }
+}
+
+template <bool WIDE>
 __global__ void __launch_bounds__(THREADS, 1)
-    dw_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, const Args p) {
-    constexpr int S = DW_STAGES;
+    dw_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmO,
+              const Args p) {
+    using G = DwGeom<WIDE>;
+    constexpr int S = G::stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = smem + S * DW_A;
-    Carve carve{smem + S * DW_STAGE};
+    uint8_t* sE = smem + S * G::stage;
+    Carve carve{sE + EPI_WARPS * STAGE};
     int4* rows4 = carve.take<int4>(32);             // warps 2 and 3: a block's tokens
     uint64_t* full = carve.take<uint64_t>(S);
     uint64_t* empty = carve.take<uint64_t>(S);
@@ -1062,7 +1090,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int e, mb, nb;
             place(t, e, mb, nb);
             const int n = tab.count(e), base = tab.off[e], kb = (n + BK - 1) / BK;
-            const int a0 = mb * 256 + static_cast<int>(prank) * BM, b0 = nb * 256 + static_cast<int>(prank) * BM;
+            const int a0 = mb * 256 + static_cast<int>(prank) * BM, b0 = nb * G::n + static_cast<int>(prank) * BM;
             for (int it = 0; it < kb; ++it) {
                 const bool tail = (it + 1) * BK > n;
                 if (!wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer)) {
@@ -1070,11 +1098,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     break;
                 }
                 uint8_t* a_dst = sA + stage * DW_A;
-                uint8_t* b_dst = sB + stage * DW_B;
+                uint8_t* b_dst = sB + stage * G::b_bytes;
                 const uint32_t bar = full0 + stage * 8;
                 if (lane == 0) {
                     if (leader) {
-                        mbar_arrive_expect_tx(full + stage, tail ? 0 : 2 * DW_STAGE);
+                        mbar_arrive_expect_tx(full + stage, tail ? 0 : 2 * G::stage);
                         armed |= 1u << stage;
                         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
                     }
@@ -1082,10 +1110,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         mbar_arrive(begin + stage);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
+                        for (int j = 0; j < 2; ++j)
                             if (p.src == nullptr) tma_load_3d_pair(a_dst + j * CHUNK, &tmX, bar, a0 + j * 64, base + it * BK, 0);
-                            tma_load_3d_pair(b_dst + j * CHUNK, &tmY, bar, b0 + j * 64, base + it * BK, 0);
-                        }
+#pragma unroll
+                        for (int j = 0; j < 2 * G::parts; ++j)
+                            tma_load_3d_pair(b_dst + j * CHUNK, &tmY, bar, b0 + j / 2 * 256 + j % 2 * 64, base + it * BK, 0);
                     }
                 }
                 if (++stage == S) {
@@ -1121,8 +1150,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     place(t, e, mb, nb);
                     const int n = tab.count(e), kb = (n + BK - 1) / BK;
                     if (kb == 0) continue;
-                    const int acc = lt & 1;
-                    if (!wait(p, tempty + acc, ((lt >> 1) & 1) ^ 1u, kWhereMma)) {
+                    const int acc = WIDE ? 0 : lt & 1;
+                    if (!wait(p, tempty + acc, (WIDE ? lt & 1 : (lt >> 1) & 1) ^ 1u, kWhereMma)) {
                         ok = false;
                         break;
                     }
@@ -1138,10 +1167,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t a = a0 + static_cast<uint64_t>(stage * (DW_A >> 4));
-                        const uint64_t b = b0 + static_cast<uint64_t>(stage * (DW_B >> 4));
+                        const uint64_t b = b0 + static_cast<uint64_t>(stage * (G::b_bytes >> 4));
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
-                            umma_f16_pair(d, a + kk * (2048 >> 4), b + kk * (2048 >> 4), idesc, (it | kk) != 0 ? 1u : 0u);
+#pragma unroll
+                            for (int part = 0; part < G::parts; ++part)
+                                umma_f16_pair(d + part * 256, a + kk * (2048 >> 4), b + part * (BM * 128 >> 4) + kk * (2048 >> 4), idesc,
+                                              (it | kk) != 0 ? 1u : 0u);
                         umma_commit_pair_mc(empty + stage, 0x3);
                         if (++stage == S) {
                             stage = 0;
@@ -1152,7 +1184,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ++lt;
                 }
                 umma_commit_pair_mc(drain, 0x3);
-                for (int i = 0; ok && i < 2; ++i, ++lt)
+                if (WIDE) ok = ok && wait(p, tempty, (lt & 1) ^ 1u, kWhereDrain);
+                for (int i = 0; !WIDE && ok && i < 2; ++i, ++lt)
                     ok = wait(p, tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, kWhereDrain);
             }
             wait(p, drain, 0, kWhereDrain);
@@ -1215,7 +1248,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 ok = wait_warp(p, begin + stage, (t_parity >> stage) & 1u, kWhereProducer);
                 if (!ok) break;
-                const int b0 = nb * 256 + static_cast<int>(prank) * BM + l.piece * 8, x0 = a0 + l.piece * 8;
+                const int b0 = nb * G::n + static_cast<int>(prank) * BM + l.piece * 8, x0 = a0 + l.piece * 8;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const int i = whole * BK + j * 4 + l.r0;
@@ -1223,9 +1256,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const __nv_bfloat16* y = p.dy + static_cast<long long>(base + min(i, n - 1)) * p.cols + b0;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const bool inx = i < n && x0 + h * 64 < p.x_ld, iny = i < n && b0 + h * 64 < p.cols;
-                        cp_async16(sa + stage * DW_A + h * CHUNK + l.at(j), inx ? x + h * 64 : p.x, inx);
-                        cp_async16(sb + stage * DW_B + h * CHUNK + l.at(j), iny ? y + h * 64 : p.dy, iny);
+                        const bool in = i < n && x0 + h * 64 < p.x_ld;
+                        cp_async16(sa + stage * DW_A + h * CHUNK + l.at(j), in ? x + h * 64 : p.x, in);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2 * G::parts; ++h) {
+                        const int col = h / 2 * 256 + h % 2 * 64;
+                        const bool in = i < n && b0 + col < p.cols;
+                        cp_async16(sb + stage * G::b_bytes + h * CHUNK + l.at(j), in ? y + col : p.dy, in);
                     }
                 }
                 cp_async_arrive(lfull + stage);
@@ -1242,39 +1280,44 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3, half = (warp - EPI_WARP) >> 2;
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
-        const bool st32 = ((reinterpret_cast<uintptr_t>(p.out) & 31) == 0) && (p.ld * (p.out_f32 ? 4 : 2)) % 32 == 0;
+        uint8_t* box = sE + (warp - EPI_WARP) * STAGE;  // 32 rows of 64 bytes, 64-byte swizzle
         int lt = 0;
         for (int t = cluster_id; t < n_tiles; t += n_clusters) {
             int e, mb, nb;
             place(t, e, mb, nb);
             const bool none = tab.count(e) == 0;
-            const int acc = lt & 1;
+            const int acc = WIDE ? 0 : lt & 1;
             if (!none) {
                 int okw = 0;
-                if (lane == 0) okw = wait(p, tfull + acc, (lt >> 1) & 1, kWhereEpilogue);
+                if (lane == 0) okw = wait(p, tfull + acc, WIDE ? lt & 1 : (lt >> 1) & 1, kWhereEpilogue);
                 okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
                 if (!okw) break;
                 tc_fence_after();
             }
-            const int k = mb * 256 + static_cast<int>(prank) * BM + q * 32 + lane;
+            const int k0 = mb * 256 + static_cast<int>(prank) * BM + q * 32;  // this warp's first row of dW
             const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-            for (int c0 = half * 128; c0 < half * 128 + 128 && nb * 256 + c0 < p.cols; c0 += 32) {
-                float v[32];
+            for (int c0 = half * (G::n / 2); c0 < (half + 1) * (G::n / 2) && nb * G::n + c0 < p.cols && k0 < p.features; c0 += 32) {
+                uint32_t r[32];
                 if (none) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    for (int j = 0; j < 32; ++j) r[j] = 0;
                 } else {
-                    uint32_t r[32];
                     tmem_ld_32x32b_x32(lanes + c0, r);
                     tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
                 }
-                if (k < p.features) {
-                    const long long at = (static_cast<long long>(e) * p.features + k) * p.ld + nb * 256 + c0;
-                    const int nvalid = p.cols - (nb * 256 + c0);
-                    if (p.out_f32) tc::store_f32x32(static_cast<float*>(p.out) + at, v, nvalid, st32);
-                    else tc::store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + at, v, nvalid, st32);
+                uint32_t w[32];  // 32 columns as bf16, or 16 at a time
+                if (!p.out_f32)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = tc::pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                else
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) w[j] = r[j];
+                const int col = nb * G::n + c0;
+                put_box(box, &tmO, w, col, k0, e, lane);
+                if (p.out_f32 && col + 16 < p.cols) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = w[16 + j];
+                    put_box(box, &tmO, w, col + 16, k0, e, lane);
                 }
             }
             if (none) continue;
@@ -1283,6 +1326,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + acc * 8);
             ++lt;
         }
+        if (lane == 0) bulk_wait_group_all();  // this warp's stores are complete
     }
 
     __syncwarp();
