@@ -32,7 +32,8 @@ constexpr int THREADS = 384;           // warp 0 TMA, warp 1 MMA, warps 2-3 gath
 constexpr int EPI_WARP = 4;
 constexpr int EPI_WARPS = 8;
 constexpr int GROUP = 16;              // token tiles walked together, so that tiles in flight share weights and tokens
-constexpr int TABLE = 2 * (MAX_EXPERTS + 1) * 4;
+constexpr int TABLE = 2 * (MAX_EXPERTS + 1) * 4 + MAX_EXPERTS * 2;
+constexpr int SORTED = 128;            // experts up to which their tiles are walked largest first
 
 enum Mode : int { STORE = 0, SWIGLU = 1, DSWIGLU = 2 };
 
@@ -83,30 +84,45 @@ constexpr int most_barriers = 5 * 6 + 5;  // of either kernel, and the tensor me
 // ---------------------------------------------------------------- the experts' row ranges and tiles
 // Row ranges are clamped to the rows that there are; a range that had to be is reported, its product left out or cut.
 struct Table {
-    int* off;    // [experts + 1] first row
-    int* first;  // [experts + 1] first tile
+    int* off;       // [experts + 1] first row
+    int* first;     // [experts + 1] first tile of the expert at that place of the order
+    uint16_t* at;   // [experts] the order: as they are or, where they are few, by falling tiles
     __device__ __forceinline__ explicit Table(void* smem)
-        : off(static_cast<int*>(smem)), first(static_cast<int*>(smem) + MAX_EXPERTS + 1) {}
+        : off(static_cast<int*>(smem)), first(off + MAX_EXPERTS + 1), at(reinterpret_cast<uint16_t*>(first + MAX_EXPERTS + 1)) {}
     __device__ __forceinline__ int count(int e) const { return max(off[e + 1] - off[e], 0); }
-    // All threads.  tile(n) gives the tiles of an expert of n rows.
-    template <int NTHREADS, typename F>
-    __device__ __forceinline__ void build(const Args& p, F&& tiles) {
+    // All threads.  tiles(n) gives the tiles of an expert of n rows, cost(n) what one of them takes (BY_COST: order by it).
+    template <int NTHREADS, bool BY_COST, typename F, typename C>
+    __device__ __forceinline__ void build(const Args& p, F&& tiles, C&& cost) {
         bool bad = false;
         for (int i = threadIdx.x; i <= p.experts; i += NTHREADS) {
             const int v = p.offsets[i], c = min(max(v, 0), p.rows);
             bad |= v != c;
             off[i] = c;
+            if (i < p.experts) at[i] = static_cast<uint16_t>(i);
         }
         __syncthreads();
+        if (BY_COST && p.experts <= SORTED) {
+            // each expert's place: the experts with larger tiles, and those ahead of it with equal ones
+            const int e = threadIdx.x;
+            if (e < p.experts) first[e] = cost(count(e));
+            __syncthreads();
+            if (e < p.experts) {
+                const int mine = first[e];
+                int place = 0;
+                for (int i = 0; i < p.experts; ++i) place += first[i] > mine || (first[i] == mine && i < e) ? 1 : 0;
+                at[place] = static_cast<uint16_t>(e);
+            }
+            __syncthreads();
+        }
         if (threadIdx.x < 32) {
             const int lane = threadIdx.x;
             int carry = 0;
-            for (int e0 = 0; e0 < p.experts; e0 += 32) {
-                const int e = e0 + lane;
+            for (int i0 = 0; i0 < p.experts; i0 += 32) {
+                const int i = i0 + lane;
                 int v = 0;
-                if (e < p.experts) {
-                    bad |= off[e + 1] < off[e];
-                    v = tiles(count(e));
+                if (i < p.experts) {
+                    bad |= off[i + 1] < off[i];
+                    v = tiles(count(at[i]));
                 }
                 int sum = v;
 #pragma unroll
@@ -114,7 +130,7 @@ struct Table {
                     const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
                     if (lane >= d) sum += o;
                 }
-                if (e < p.experts) first[e] = carry + sum - v;
+                if (i < p.experts) first[i] = carry + sum - v;
                 carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
             }
             if (lane == 0) first[p.experts] = carry;
@@ -123,6 +139,14 @@ struct Table {
         __syncthreads();
     }
 };
+// Round i's tile of pair c of n.  BACK: there and back, so that who has a large tile in one round has a small one in the next.
+// (Together with the order by cost: weight gradients of 8192 rows on 64 experts, 1024 x 2048, 78 -> 71 us in order, 101 -> 82
+// gathered; wide tiles of 2048 rows on 8 experts, 5120 x 8192, 152 -> 140.  Narrow tiles, which overlap their epilogues, gain
+// nothing, up to 4 % of their time is lost.)
+template <bool BACK>
+__device__ __forceinline__ int round_tile(int i, int c, int n) {
+    return i * n + (BACK && (i & 1) ? n - 1 - c : c);
+}
 
 // Tokens of a tile: an expert's n rows in ceil(n / TN) tiles of equal size, a multiple of 16.  (The last one is
 // never empty: with a size below TN there are fewer than TN / 16 tiles.)
@@ -135,13 +159,13 @@ __device__ __forceinline__ int tile_tokens(int n) {
 struct Tile {
     int e, mb, row0, n;  // expert, feature block, first row, rows (0: past the last tile)
 };
-// Tile t; e is where the walk stands (tiles come in increasing order).
+// Tile t; i is where the walk over the order stands (tiles come in increasing order).
 template <int TN>
-__device__ __forceinline__ Tile decode(const Args& p, const Table& tab, int t, int& e) {
-    while (e < p.experts && t >= tab.first[e + 1]) ++e;
-    if (e >= p.experts) return Tile{0, 0, 0, 0};
-    const int n = tab.count(e), nt = (n + TN - 1) / TN, sz = tile_tokens<TN>(n);
-    const int l = t - tab.first[e], per_group = GROUP * p.m_blocks;
+__device__ __forceinline__ Tile decode(const Args& p, const Table& tab, int t, int& i) {
+    while (i < p.experts && t >= tab.first[i + 1]) ++i;
+    if (i >= p.experts) return Tile{0, 0, 0, 0};
+    const int e = tab.at[i], n = tab.count(e), nt = (n + TN - 1) / TN, sz = tile_tokens<TN>(n);
+    const int l = t - tab.first[i], per_group = GROUP * p.m_blocks;
     const int g = l / per_group, r = l - g * per_group, gt = min(nt - g * GROUP, GROUP);
     const int tb = g * GROUP + r % gt;
     return Tile{e, r / gt, tab.off[e] + tb * sz, min(sz, n - tb * sz)};
@@ -382,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     griddep_wait();  // no global memory is touched before the kernel ahead has completed
     if (threadIdx.x == 0) griddep_launch_dependents();
-    tab.build<THREADS>(p, [&](int n) { return (n + TN - 1) / TN * p.m_blocks; });
+    tab.build<THREADS, WIDE>(p, [&](int n) { return (n + TN - 1) / TN * p.m_blocks; }, [](int n) { return n > 0 ? tile_tokens<TN>(n) : 0; });
     const int n_tiles = tab.first[p.experts];
 
     if (warp == 0) {
@@ -391,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t phase = 0, armed = 0, last_parity = 0;
         bool ok = true;
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-        for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+        for (int i = 0, t; (t = round_tile<WIDE>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
             const Tile c = decode<TN>(p, tab, t, e);
             const int nn = (c.n + 15) & ~15, half = nn / 2;  // columns of the MMA, tokens of this CTA
             const int row0 = c.row0 + static_cast<int>(prank) * half;
@@ -471,7 +495,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 int stage = 0, lt = 0, e = 0;
                 uint32_t phase = 0;
                 bool ok = true;
-                for (int t = cluster_id; t < n_tiles && ok; t += n_clusters, ++lt) {
+                for (int i = 0, t; (t = round_tile<WIDE>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i, ++lt) {
                     const Tile c = decode<TN>(p, tab, t, e);
                     const uint32_t idesc = idesc_bf16_f32(2 * BM, (c.n + 15) & ~15, W_MN, false);
                     const int acc = WIDE ? 0 : lt & 1;
@@ -518,7 +542,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint32_t phase = 0;
             bool ok = true;
             const uint32_t full0 = mapa_shared(smem_u32(full), 0), dst0 = smem_u32(sB) + (warp - 2) * 512;
-            for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+            for (int i = 0, t; (t = round_tile<WIDE>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
                 const Tile c = decode<TN>(p, tab, t, e);
                 const int half = ((c.n + 15) & ~15) / 2, copies = half / 8;  // (half is a multiple of 8)
                 const int row0 = c.row0 + static_cast<int>(prank) * half + (warp - 2) * 4;
@@ -547,9 +571,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint8_t* buf = sE + (warp - EPI_WARP) * G::epi;
         const uint32_t sbuf = smem_u32(buf);
         int lt = 0, e = 0;
-        for (int t = cluster_id; t < n_tiles; t += n_clusters, ++lt) {
+        for (int i = 0, t; (t = round_tile<WIDE>(i, cluster_id, n_clusters)) < n_tiles; ++i, ++lt) {
             const Tile c = decode<TN>(p, tab, t, e);
             const int acc = WIDE ? 0 : lt & 1;
+            // the saved pre-activations of 32 tokens are loaded a step ahead, the first ones while the products are computed
+            [[maybe_unused]] uint4 g4[4], u4[4];
+            [[maybe_unused]] auto ahead = [&](int c0) {
+                const int f0 = c.mb * 256 + static_cast<int>(prank) * BM + q * 32, n = min(c.n - c0, 32);
+                const __nv_bfloat16* h = p.h_in + (c.row0 + c0) * p.h_ld + static_cast<long long>(f0 >> 7) * 256 + (f0 & 127);
+                if (c0 < (half + 1) * (TN / 2)) {
+                    rows_load(h, p.h_ld, n, p.features - f0, lane, g4);
+                    rows_load(h + 128, p.h_ld, n, p.features - f0, lane, u4);
+                }
+            };
+            if constexpr (MODE == DSWIGLU) ahead(half * (TN / 2));
             int okw = 0;
             if (lane == 0) okw = wait(p, tfull + acc, WIDE ? lt & 1 : (lt >> 1) & 1, kWhereEpilogue);
             okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
@@ -655,13 +690,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         put_rows(buf, static_cast<__nv_bfloat16*>(p.out) + row * p.ld + f0, p.ld, lo, hi, n, nf, lane);
                     }
                 } else {
-                    const __nv_bfloat16* h = p.h_in + row * p.h_ld + packed;
-                    uint4 g4[4], u4[4];
-                    rows_load(h, p.h_ld, n, nf, lane, g4);
-                    rows_load(h + 128, p.h_ld, n, nf, lane, u4);
                     stage_load(buf, g4, lane);
                     stage_load(buf + STAGE, u4, lane);
                     __syncwarp();
+                    ahead(c0 + 32);
                     uint32_t glo[8], ghi[8], ulo[8], uhi[8];
                     stage_get(sbuf, glo, ghi, lane);
                     stage_get(sbuf + STAGE, ulo, uhi, lane);
@@ -1068,13 +1100,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    tab.build<THREADS>(p, [&](int) { return p.m_blocks * p.n_blocks; });
+    tab.build<THREADS, true>(p, [&](int) { return p.m_blocks * p.n_blocks; }, [](int n) { return n; });
     const int n_tiles = tab.first[p.experts];  // every expert has its tiles, one without rows to write zeros
     const int per_expert = p.m_blocks * p.n_blocks;
     // tile t: expert, block of K, block of N; groups of GROUP blocks of K walked together
     auto place = [&](int t, int& e, int& mb, int& nb) {
-        e = t / per_expert;
-        const int l = t - e * per_expert, per_group = GROUP * p.n_blocks;
+        const int i = t / per_expert, l = t - i * per_expert, per_group = GROUP * p.n_blocks;
+        e = tab.at[i];
         const int g = l / per_group, r = l - g * per_group, gm = min(p.m_blocks - g * GROUP, GROUP);
         mb = g * GROUP + r % gm;
         nb = r / gm;
@@ -1086,7 +1118,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t phase = 0, armed = 0, last_parity = 0;
         bool ok = true;
         const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-        for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+        for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
             int e, mb, nb;
             place(t, e, mb, nb);
             const int n = tab.count(e), base = tab.off[e], kb = (n + BK - 1) / BK;
@@ -1145,7 +1177,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 int stage = 0, lt = 0;
                 uint32_t phase = 0, g_parity = 0;  // a stage's next phase of gfull
                 bool ok = true;
-                for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+                for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
                     int e, mb, nb;
                     place(t, e, mb, nb);
                     const int n = tab.count(e), kb = (n + BK - 1) / BK;
@@ -1199,7 +1231,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t phase = 0, t_parity = 0;  // a stage's next phase of `begin` or `lfull`
         bool ok = true;
         const uint32_t full0 = mapa_shared(smem_u32(full), 0), gfull0 = mapa_shared(smem_u32(gfull), 0);
-        for (int t = cluster_id; t < n_tiles && ok; t += n_clusters) {
+        for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
             int e, mb, nb;
             place(t, e, mb, nb);
             const int n = tab.count(e), base = tab.off[e], whole = n / BK, a0 = mb * 256 + static_cast<int>(prank) * BM;
@@ -1282,7 +1314,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
         uint8_t* box = sE + (warp - EPI_WARP) * STAGE;  // 32 rows of 64 bytes, 64-byte swizzle
         int lt = 0;
-        for (int t = cluster_id; t < n_tiles; t += n_clusters) {
+        for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles; ++i) {
             int e, mb, nb;
             place(t, e, mb, nb);
             const bool none = tab.count(e) == 0;
