@@ -401,8 +401,8 @@ int64_t tpmlp_layernorm_ws_bytes(int64_t rows, int64_t h);
  *   offsets   [experts + 1] int32: expert e has rows offsets[e] .. offsets[e + 1] - 1
  *   row_token [tokens * k] int32: the token of each row, -1 past the last row
  *   slot_row  [tokens][k] int32: the row of each slot (-1: none)
- *   ws        tpmlp_moe_route_ws_bytes(tokens, experts, k) bytes
- * experts at most 1024, k at most 32 and at most experts.  Pointers need the alignment of their elements only.  Without
+ *   ws        tpmlp_moe_route_ws_bytes(tokens, experts, k) bytes, 16-byte aligned
+ * experts at most 1024, k at most 32 and at most experts.  The other pointers need the alignment of their elements only.  Without
  * tokens the offsets are set to zero.  The plan stays on the device: nothing has to be read back before the products.
  */
 tpmlp_status tpmlp_moe_route(const void* logits, void* ids, void* weights, void* offsets, void* row_token, void* slot_row, void* ws,

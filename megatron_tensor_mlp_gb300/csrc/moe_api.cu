@@ -199,7 +199,8 @@ tpmlp_status tpmlp_moe_route(const void* logits, void* ids, void* weights, void*
     TP_TRY(check_dtype(dt));
     const int es = esize(dt);
     TP_TRY(check_elements({logits}, es));
-    TP_TRY(check_elements({ids, weights, offsets, row_token, slot_row, ws}, 4));
+    TP_TRY(check_elements({ids, weights, offsets, row_token, slot_row}, 4));
+    TP_TRY(check_aligned({ws}));
     const int64_t slots = tokens * k * 4;
     TP_TRY(check_alias({{ids, slots}, {weights, slots}, {offsets, (experts + 1) * 4}, {row_token, slots}, {slot_row, slots},
                         {ws, moe_route_ws_bytes(tokens, static_cast<int>(experts))}},

@@ -279,7 +279,7 @@ tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaS
     a.features = static_cast<int>(g.K);
     a.cols = static_cast<int>(g.N);
     a.m_blocks = (a.features + 255) / 256;
-    const bool wide = g.src != nullptr;  // (see wide_tiles; without a gather narrow tiles are as fast or faster: WDW)
+    const bool wide = g.src != nullptr;  // (gathered 816 us, narrow 1230; in order narrow is faster: 800, 840)
     a.n_blocks = (a.cols + (wide ? 511 : 255)) / (wide ? 512 : 256);
     a.out = g.out;
     a.ld = g.N;

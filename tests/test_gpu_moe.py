@@ -335,8 +335,8 @@ def test_combine_and_backward(T, t, k, h, weighted):
     at = sr.clamp(min=0).long()
     there = (sr >= 0)[:, :, None]
     prod = torch.where(there, o[at].to(R.D) * dz.to(R.D)[:, None], torch.zeros((), dtype=R.D, device="cuda"))
-    # a thread adds up to h / 2048 + 1 groups of 8 products, then 5 + 8 sums across threads
-    R.close(dw, prod.sum(2), (h / 256 + 32) * 2.0**-24 * prod.abs().sum(2), "dweights")
+    # a lane adds h / 256 + 1 groups of 8 products, then 5 sums across lanes
+    R.close(dw, prod.sum(2), (h / 32 + 32) * 2.0**-24 * prod.abs().sum(2), "dweights")
     ww = (torch.ones(t, k, device="cuda") if w is None else w)[:, :, None].to(R.D) * dz.to(R.D)[:, None]
     R.close(do[sr[sr >= 0].long()], ww[sr >= 0], 2.0**-24 * ww[sr >= 0].abs(), "dO")
     if weighted:

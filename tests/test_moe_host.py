@@ -92,6 +92,7 @@ def test_route_refusals():
     assert route(tokens=1 << 27) == T.ERR_SHAPE
     assert route(dt=2) == T.ERR_DTYPE
     assert route(ids=addr(1) + 2) == T.ERR_ALIGNMENT and route(logits=addr(0) + 1) == T.ERR_ALIGNMENT
+    assert route(ws=addr(6) + 4) == T.ERR_ALIGNMENT
     assert route(ids=addr(0)) == T.ERR_ALIAS and route(slot_row=addr(4)) == T.ERR_ALIAS
     assert route() in REACHED
     for name in ("logits", "ids", "weights", "dweights", "dlogits"):
