@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const __nv_bfloat16* 
     const int a = min(max(offsets[e], 0), rows), b = min(max(offsets[e + 1], 0), rows);
     float s[8] = {};
     if (c < cols) {
+#pragma unroll 4
         for (int r = a + r0; r < b; r += 32) {
             float v[8];
             tc::unpack_bf16x8(*reinterpret_cast<const uint4*>(in + static_cast<long long>(r) * cols + c), v);

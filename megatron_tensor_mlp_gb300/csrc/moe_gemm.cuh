@@ -754,7 +754,7 @@ constexpr int FEW_TN = 64, FEW_STAGES = 4, FEW_THREADS = 256;
 constexpr int FEW_A = BM * 128, FEW_B = FEW_TN * 128, FEW_STAGE = FEW_A + FEW_B;
 constexpr int FEW_SUMS = 8 * 4096;  // partial sums on their way: 8 (rank, group of 8 tokens) of 128 lanes
 constexpr int FEW_SMEM = 1024 + FEW_STAGES * FEW_STAGE + (2 * FEW_STAGES + 2) * 8 + 64;
-static_assert(FEW_SUMS <= FEW_STAGES * FEW_STAGE && 2 * (FEW_SMEM + 1024) <= 227 * 1024, "few kernel shared memory");
+static_assert(FEW_TN >= 32 && FEW_SUMS <= FEW_STAGES * FEW_STAGE && 2 * (FEW_SMEM + 1024) <= 227 * 1024, "few kernel shared memory");
 
 template <bool GATED>
 __global__ void __launch_bounds__(FEW_THREADS, 2)
