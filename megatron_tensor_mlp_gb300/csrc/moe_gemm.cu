@@ -140,8 +140,8 @@ tpmlp_status launch_rows(const CUtensorMap& w, const Boxes& x, const Args& a, co
 // Whether the forward product runs on the few-rows kernel.  The row ranges are on the device, so this goes by the tiles that
 // the pairs would have if the rows were spread over the experts: where they fill about half of the pairs, or, with at most
 // 16 rows an expert, up to four rounds of them (which do not come out even).  4 tokens, 8 of 64 experts, 1024 x 8192 gated
-// (256 tiles): 28.2 us, pairs 33.8; 4096 x 1024 (32 tiles): 14.8, 26.0; 128 rows on 8 experts of that size 18.1, 23.8; 666
-// rows (40 tiles) 22.6, 24.7.  But 128 rows on 34 of 64 experts, gated (2112 tiles): 112, pairs 104; 1024 rows on 16
+// (256 tiles): 28.0 us, pairs 33.8; 4096 x 1024 (32 tiles): 14.6, 26.0; 128 rows on 8 experts of that size 16.6, 23.8; 666
+// rows (40 tiles) 19.3, 24.7.  But 128 rows on 34 of 64 experts, gated (2112 tiles): 112, pairs 91; 1024 rows on 16
 // experts, 4096 x 1024 (80 tiles): 36.1, 27.4.
 bool few_rows(int64_t rows, int64_t experts, int64_t m_blocks, int pairs) {
     const int64_t tiles = m_blocks * (std::min(rows, experts) + rows / 256);
@@ -175,32 +175,48 @@ tpmlp_status launch_dw(const CUtensorMap& x, const CUtensorMap& y, const CUtenso
     return launch(kern, dim3(2 * pairs), THREADS, DwGeom<WIDE>::smem, 2, st, x, y, o, a);
 }
 
-// Sums of an expert's rows by column: CTA (64 columns, expert), rows in steps of 32, added in that order.
-constexpr int SUM_THREADS = 256;
+// Sums of an expert's rows by column: CTA (64 columns, expert), a warp four rows at a time, 128 a CTA; a lane adds its rows in
+// their order, then its warp's four lanes of a column, then the 32 warps.  (3992 x 2048 on 16 experts: 6.6 us, with eight
+// warps 12.)
+constexpr int SUM_WARPS = 32, SUM_THREADS = 32 * SUM_WARPS;
 __global__ void __launch_bounds__(SUM_THREADS) sums_kernel(const __nv_bfloat16* in, const int* offsets, int rows, int cols, void* out,
                                                            int out_f32) {
-    __shared__ float part[32][64 + 1];
+    __shared__ float part[SUM_WARPS][64];
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    const int e = blockIdx.y, c = blockIdx.x * 64 + (threadIdx.x & 7) * 8, r0 = threadIdx.x >> 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = blockIdx.y, c = blockIdx.x * 64 + (lane & 7) * 8, r0 = threadIdx.x >> 3;
     const int a = min(max(offsets[e], 0), rows), b = min(max(offsets[e + 1], 0), rows);
     float s[8] = {};
     if (c < cols) {
-#pragma unroll 4
-        for (int r = a + r0; r < b; r += 32) {
-            float v[8];
-            tc::unpack_bf16x8(*reinterpret_cast<const uint4*>(in + static_cast<long long>(r) * cols + c), v);
+        for (int r = a + r0; r < b; r += 4 * 4 * SUM_WARPS) {
+            uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] += v[i];
+            for (int i = 0; i < 4; ++i) {
+                const int at = r + i * 4 * SUM_WARPS;
+                v[i] = at < b ? *reinterpret_cast<const uint4*>(in + static_cast<long long>(at) * cols + c) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[8];
+                tc::unpack_bf16x8(v[i], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] += f[j];
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[r0][(threadIdx.x & 7) * 8 + i] = s[i];
+    for (int j = 0; j < 8; ++j) {
+        s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], 8);
+        s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], 16);
+        if (lane < 8) part[warp][lane * 8 + j] = s[j];
+    }
     __syncthreads();
     const int col = blockIdx.x * 64 + threadIdx.x;
     if (threadIdx.x < 64 && col < cols) {
         float v = 0.0f;
-        for (int r = 0; r < 32; ++r) v += part[r][threadIdx.x];
+#pragma unroll
+        for (int w = 0; w < SUM_WARPS; ++w) v += part[w][threadIdx.x];
         const long long at = static_cast<long long>(e) * cols + col;
         if (out_f32) static_cast<float*>(out)[at] = v;
         else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);

@@ -847,6 +847,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
     }
     const Tile c{tile[0], tile[3], tile[1], tile[2]};
     const int nn = (c.n + 15) & ~15;
+    // what this thread stores: column `col` of its rows (GATED: of the gate; the up feature is 128 on), feature f
+    const int l = threadIdx.x & 127;
+    const int f = GATED ? c.mb * 64 + (l & 63) : c.mb * 128 + l;
+    const long long col = GATED ? static_cast<long long>(c.mb >> 1) * 256 + (c.mb & 1) * 64 + (l & 63) : f;
+    float bias = 0.0f, bias_up = 0.0f;
+    if (c.n > 0 && warp >= EPI_WARP && p.bias != nullptr && f < p.features) {
+        bias = __bfloat162float(p.bias[c.e * p.bias_ld + col]);
+        if (GATED) bias_up = __bfloat162float(p.bias[c.e * p.bias_ld + col + 128]);
+    }
     const int k0 = p.kb * rank / n_ranks, k1 = p.kb * (rank + 1) / n_ranks;
     bool ok = true;
 
@@ -941,50 +950,57 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
     float* part = reinterpret_cast<float*>(smem);
     if (c.n > 0 && warp >= EPI_WARP) {
         const int q = warp & 3;
-        for (int g = 0; g < groups; ++g) {
-            uint32_t r[8];
-            tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(q * 32) << 16) + g * 8, r);
+        for (int g0 = 0; g0 < groups; g0 += 4) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + g0 * 8, r);
             tmem_ld_wait();
-            const uint32_t at = smem_u32(part + ((rank * per + g / n_ranks) * 8) * 128 + q * 32 + lane);
-            const uint32_t to = mapa_shared(at, static_cast<uint32_t>(g % n_ranks));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) st_cluster_u32(to + j * 512, r[j]);
+            for (int i = 0; i < 4; ++i) {
+                const int g = g0 + i;
+                if (g >= groups) break;
+                const uint32_t at = smem_u32(part + ((rank * per + g / n_ranks) * 8) * 128 + q * 32 + lane);
+                const uint32_t to = mapa_shared(at, static_cast<uint32_t>(g % n_ranks));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) st_cluster_u32(to + j * 512, r[i * 8 + j]);
+            }
         }
         tc_fence_before();
     }
     if (n_ranks > 1) cluster_sync_all();
     else __syncthreads();
-    if (c.n > 0 && warp >= EPI_WARP && __all_sync(0xFFFFFFFFu, ok)) {
-        const int l = threadIdx.x - EPI_WARP * 32;
-        auto sum = [&](int gi, int j, int at) {
-            float v = 0.0f;
-            for (int r = 0; r < n_ranks; ++r) v += part[((r * per + gi) * 8 + j) * 128 + at];
-            return v;
-        };
+    if (c.n > 0 && warp >= EPI_WARP && __all_sync(0xFFFFFFFFu, ok) && f < p.features) {
+        // a thread adds eight tokens of its lane at once (GATED: four, of gate and up), in the order of the ranks
+        constexpr int AT_ONCE = GATED ? 4 : 8;
+        const int j0 = GATED ? (l >> 6) * 4 : 0, lane0 = GATED ? l & 63 : l;
         for (int g = rank; g < groups; g += n_ranks) {
-            const int gi = g / n_ranks, n = min(c.n - g * 8, 8);
-            const long long row = c.row0 + g * 8;
-            if constexpr (GATED) {
-                const int f = c.mb * 64 + (l & 63);
-                const long long packed = static_cast<long long>(c.mb >> 1) * 256 + (c.mb & 1) * 64 + (l & 63);
-                const __nv_bfloat16* b = p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + packed;
-                const float bg = b == nullptr ? 0.0f : __bfloat162float(b[0]), bu = b == nullptr ? 0.0f : __bfloat162float(b[128]);
-                for (int j = l >> 6; j < n; j += 2) {
-                    const float x = sum(gi, j, l & 63) + bg, u = sum(gi, j, 64 + (l & 63)) + bu;
-                    if (p.h_out != nullptr) {
-                        p.h_out[(row + j) * p.h_ld + packed] = __float2bfloat16_rn(x);
-                        p.h_out[(row + j) * p.h_ld + packed + 128] = __float2bfloat16_rn(u);
-                    }
-                    static_cast<__nv_bfloat16*>(p.out)[(row + j) * p.ld + f] = __float2bfloat16_rn(x * tc::sigmoid_approx(x) * u);
+            float v[AT_ONCE], u[AT_ONCE];
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) v[j] = u[j] = 0.0f;
+            for (int r = 0; r < n_ranks; ++r) {
+                const float* at = part + ((r * per + g / n_ranks) * 8 + j0) * 128 + lane0;
+#pragma unroll
+                for (int j = 0; j < AT_ONCE; ++j) {
+                    v[j] += at[j * 128];
+                    if (GATED) u[j] += at[j * 128 + 64];
                 }
-            } else {
-                const int f = c.mb * 128 + l;
-                if (f >= p.features) break;
-                const float b = p.bias == nullptr ? 0.0f : __bfloat162float(p.bias[c.e * p.bias_ld + f]);
-                for (int j = 0; j < n; ++j) {
-                    const float v = sum(gi, j, l) + b;
-                    if (p.out_f32) static_cast<float*>(p.out)[(row + j) * p.ld + f] = v;
-                    else static_cast<__nv_bfloat16*>(p.out)[(row + j) * p.ld + f] = __float2bfloat16_rn(v);
+            }
+            const int n = c.n - g * 8 - j0;
+            const long long row = c.row0 + g * 8 + j0;
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
+                if (j >= n) break;
+                const float x = v[j] + bias;
+                if constexpr (GATED) {
+                    const float up = u[j] + bias_up;
+                    if (p.h_out != nullptr) {
+                        p.h_out[(row + j) * p.h_ld + col] = __float2bfloat16_rn(x);
+                        p.h_out[(row + j) * p.h_ld + col + 128] = __float2bfloat16_rn(up);
+                    }
+                    static_cast<__nv_bfloat16*>(p.out)[(row + j) * p.ld + f] = __float2bfloat16_rn(x * tc::sigmoid_approx(x) * up);
+                } else if (p.out_f32) {
+                    static_cast<float*>(p.out)[(row + j) * p.ld + f] = x;
+                } else {
+                    static_cast<__nv_bfloat16*>(p.out)[(row + j) * p.ld + f] = __float2bfloat16_rn(x);
                 }
             }
         }

@@ -122,7 +122,7 @@ def case(counts, K, gather, seed=0, tokens=None, behind=37):
 @pytest.mark.parametrize("K,N", SHAPES + [(4104, 136)])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("out", [BF, F32])
-@pytest.mark.parametrize("counts", [COUNTS, FEW, [3, 0, 70]], ids=["many", "few", "three"])
+@pytest.mark.parametrize("counts", [COUNTS, FEW, [3, 0, 70], [100, 20, 129, 64, 0]], ids=["many", "few", "three", "middle"])
 def test_matmul(T, K, N, gather, out, counts):
     rows, off, src, x = case(counts, K, gather, seed=K)
     e = len(counts)
@@ -191,7 +191,7 @@ def gated_slack(g, u, eg, eu):
 @pytest.mark.parametrize("K,f", [(8, 128), (72, 384), (200, 256), (1032, 640), (4104, 128)])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("save", [False, True])
-@pytest.mark.parametrize("counts", [COUNTS, FEW, [3, 0, 70]], ids=["many", "few", "three"])
+@pytest.mark.parametrize("counts", [COUNTS, FEW, [3, 0, 70], [100, 20, 129, 64, 0]], ids=["many", "few", "three", "middle"])
 def test_gated_forward(T, K, f, gather, save, counts):
     rows, off, src, x = case(counts, K, gather, seed=f)
     e, n = len(counts), sum(counts)
