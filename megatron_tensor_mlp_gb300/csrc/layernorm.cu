@@ -792,7 +792,8 @@ tpmlp_status launch_layernorm_bwd(const void* X, const void* gamma, const float*
             return true;
         })) {
         const Shape s = shape_of(vec, a.vecs);
-        grid = static_cast<int>(std::min<int64_t>({(rows + s.y - 1) / s.y, 2 * int64_t(dev.sm_count), most_parts(h)}));
+        const int per_sm = s.y == 1 && s.x <= 256 && s.nv * vec <= 8 ? 4 : 2;  // (few registers: more rows at once)
+        grid = static_cast<int>(std::min<int64_t>({(rows + s.y - 1) / s.y, int64_t(per_sm) * dev.sm_count, most_parts(h)}));
         const int smem = s.y > 1 && sums ? static_cast<int>(s.y * 2 * h * 4) : 0;
         r = by_shape(f32, wide, s.nv, [&](auto t, auto v, auto nv) {
             auto kern = bwd_kernel<decltype(t), decltype(v)::value, decltype(nv)::value>;
