@@ -172,7 +172,7 @@ tpmlp_status launch_dw(const CUtensorMap& x, const CUtensorMap& y, const CUtenso
     static PerDevice<bool> done;
     auto kern = dw_kernel<WIDE>;
     if (!set_smem(kern, dev.device, DwGeom<WIDE>::smem, done)) return TPMLP_ERR_CUDA;
-    return launch(kern, dim3(2 * pairs), THREADS, DwGeom<WIDE>::smem, 2, st, x, y, o, a);
+    return launch(kern, dim3(2 * pairs), DW_THREADS, DwGeom<WIDE>::smem, 2, st, x, y, o, a);
 }
 
 // Sums of an expert's rows by column: CTA (64 columns, expert), a warp four rows at a time, 128 a CTA; a lane adds its rows in

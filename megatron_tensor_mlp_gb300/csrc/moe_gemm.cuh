@@ -1015,10 +1015,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
 
 // ---------------------------------------------------------------- dw kernel
 // dW[e] = X_e^T dY_e: both operands have the rows as their contraction, 64 to a stage, and come by TMA; gathered rows of X
-// from warps 2 and 3, 64 features each.  Where an expert's last block ends inside a stage warp 2 copies it, both operands,
-// by cp.async: the rows behind the last, the next expert's, are zeros in shared memory then (in both operands, since a zero
-// times the other's infinity would be a NaN).  Warp 3 waits for the copies, makes them visible to the tensor cores (the
-// proxy fence, in a warp without copies of its own) and reports to the leader.
+// from warps 2 and 3, 64 features each.  Where an expert's last block ends inside a stage warps 12 and 13 copy it, both
+// operands, by cp.async: the rows behind the last, the next expert's, are zeros in shared memory then (in both operands,
+// since a zero times the other's infinity would be a NaN).  Warp 14 waits for these copies, makes them visible to the tensor
+// cores and reports to the leader: the proxy fence that it takes holds up a warp that has copied (8192 rows on 64 experts,
+// 1024 x 2048 in order: 87 us with the fence in the copying warps, 68 with it in a warp of its own).
 //
 // A lane's place in a block of rows of 128 bytes, row r0 + 4 j: piece ^ (row % 8) of the row, as the swizzle has it.
 struct Lane {
@@ -1030,6 +1031,8 @@ struct Lane {
 };
 // WIDE: two accumulators, 512 columns of dY, for gathered rows, as in the rows kernel.
 constexpr int DW_A = BM * 128;
+constexpr int TAIL_WARP = EPI_WARP + EPI_WARPS, TAIL_WARPS = 2;  // and a warp behind them that reports
+constexpr int DW_THREADS = THREADS + 32 * (TAIL_WARPS + 1);
 template <bool WIDE>
 struct DwGeom {
     static constexpr int n = WIDE ? 512 : 256;           // columns of a tile
@@ -1060,7 +1063,7 @@ __device__ __forceinline__ void put_box(uint8_t* box, const CUtensorMap* map, co
 }
 
 template <bool WIDE>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(DW_THREADS, 1)
     dw_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmO,
               const Args p) {
     using G = DwGeom<WIDE>;
@@ -1074,8 +1077,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     int4* rows4 = carve.take<int4>(32);             // warps 2 and 3: a block's tokens
     uint64_t* full = carve.take<uint64_t>(S);
     uint64_t* empty = carve.take<uint64_t>(S);
-    uint64_t* begin = carve.take<uint64_t>(S);      // the stage is for an expert's last block: to warp 2
-    uint64_t* lfull = carve.take<uint64_t>(S);      // it is copied: to warp 3
+    uint64_t* begin = carve.take<uint64_t>(S);      // the stage is for an expert's last block: to the tail (and gather) warps
+    uint64_t* lfull = carve.take<uint64_t>(S);      // it is copied in this CTA: to the warp behind them
     uint64_t* gfull = carve.take<uint64_t>(S);      // leader: in both CTAs
     uint64_t* tfull = carve.take<uint64_t>(2);
     uint64_t* tempty = carve.take<uint64_t>(2);
@@ -1092,8 +1095,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int s = 0; s < S; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
-            mbar_init(lfull + s, 32);
-            mbar_init(gfull + s, 2);
+            mbar_init(lfull + s, 32 * TAIL_WARPS);
+            mbar_init(gfull + s, 2 * (1 + (p.src != nullptr ? 2 : 0)));
             mbar_init(begin + s, 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -1117,7 +1120,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    tab.build<THREADS, true>(p, [&](int) { return p.m_blocks * p.n_blocks; }, [](int n) { return n; });
+    tab.build<DW_THREADS, true>(p, [&](int) { return p.m_blocks * p.n_blocks; }, [](int n) { return n; });
     const int n_tiles = tab.first[p.experts];  // every expert has its tiles, one without rows to write zeros
     const int per_expert = p.m_blocks * p.n_blocks;
     // tile t: expert, block of K, block of N; groups of GROUP blocks of K walked together
@@ -1200,131 +1203,183 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int n = tab.count(e), kb = (n + BK - 1) / BK;
                     if (kb == 0) continue;
                     const int acc = WIDE ? 0 : lt & 1;
-                    if (!wait(p, tempty + acc, (WIDE ? lt & 1 : (lt >> 1) & 1) ^ 1u, kWhereMma)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                    const uint32_t turn = (WIDE ? lt & 1 : (lt >> 1) & 1) ^ 1u;
                     const uint32_t d = tmem_base + acc * 256;
-                    for (int it = 0; it < kb; ++it) {
-                        const bool tail = (it + 1) * BK > n;
-                        ok = wait(p, full + stage, phase, kWhereMma);
-                        if (ok && tail) {
-                            ok = mbar_wait_bounded_cluster(gfull + stage, (g_parity >> stage) & 1u, p.status, p.timeout_ns, kWhereMma, false);
+                    auto arrived = [&](int it) {  // the operands of block it
+                        bool in = wait(p, full + stage, phase, kWhereMma);
+                        if (in && (it + 1) * BK > n) {
+                            in = mbar_wait_bounded_cluster(gfull + stage, (g_parity >> stage) & 1u, p.status, p.timeout_ns, kWhereMma, false);
                             g_parity ^= 1u << stage;
                         }
-                        if (!ok) break;
                         tc_fence_after();
+                        return in;
+                    };
+                    auto multiply = [&](int it, int part) {
                         const uint64_t a = a0 + static_cast<uint64_t>(stage * (DW_A >> 4));
-                        const uint64_t b = b0 + static_cast<uint64_t>(stage * (G::b_bytes >> 4));
+                        const uint64_t b = b0 + static_cast<uint64_t>(stage * (G::b_bytes >> 4) + part * (BM * 128 >> 4));
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
-#pragma unroll
-                            for (int part = 0; part < G::parts; ++part)
-                                umma_f16_pair(d + part * 256, a + kk * (2048 >> 4), b + part * (BM * 128 >> 4) + kk * (2048 >> 4), idesc,
-                                              (it | kk) != 0 ? 1u : 0u);
-                        umma_commit_pair_mc(empty + stage, 0x3);
+                            umma_f16_pair(d + part * 256, a + kk * (2048 >> 4), b + kk * (2048 >> 4), idesc, (it | kk) != 0 ? 1u : 0u);
+                    };
+                    auto next = [&] {
                         if (++stage == S) {
                             stage = 0;
                             phase ^= 1u;
                         }
+                    };
+                    ok = wait(p, tempty + acc, turn, kWhereMma);
+                    if (!ok) break;
+                    tc_fence_after();
+                    int it = 0;
+                    if constexpr (WIDE) {
+                        // as many blocks as the ring holds into the first accumulator, while the second one is read out
+                        const int first = min(kb, S), stage0 = stage;
+                        const uint32_t phase0 = phase;
+                        for (; it < first && ok; ++it) {
+                            ok = arrived(it);
+                            if (ok) multiply(it, 0);
+                            next();
+                        }
+                        ok = ok && wait(p, tempty + 1, turn, kWhereMma);
+                        if (!ok) break;
+                        tc_fence_after();
+                        stage = stage0;
+                        phase = phase0;
+                        for (int j = 0; j < first; ++j) {
+                            multiply(j, 1);
+                            umma_commit_pair_mc(empty + stage, 0x3);
+                            next();
+                        }
+                    }
+                    for (; it < kb; ++it) {
+                        ok = arrived(it);
+                        if (!ok) break;
+#pragma unroll
+                        for (int part = 0; part < G::parts; ++part) multiply(it, part);
+                        umma_commit_pair_mc(empty + stage, 0x3);
+                        next();
                     }
                     if (ok) umma_commit_pair_mc(tfull + acc, 0x3);
                     ++lt;
                 }
                 umma_commit_pair_mc(drain, 0x3);
-                if (WIDE) ok = ok && wait(p, tempty, (lt & 1) ^ 1u, kWhereDrain);
-                for (int i = 0; !WIDE && ok && i < 2; ++i, ++lt)
-                    ok = wait(p, tempty + (lt & 1), ((lt >> 1) & 1) ^ 1u, kWhereDrain);
+                for (int i = 0; ok && i < 2; ++i)
+                    ok = WIDE ? wait(p, tempty + i, (lt & 1) ^ 1u, kWhereDrain)
+                              : wait(p, tempty + ((lt + i) & 1), (((lt + i) >> 1) & 1) ^ 1u, kWhereDrain);
             }
             wait(p, drain, 0, kWhereDrain);
         }
     } else if (warp < EPI_WARP) {
-        // ---------------------------------------------------------------- gathered rows and last blocks (both CTAs)
-        const Lane l;
-        const uint32_t sa = smem_u32(sA), sb = smem_u32(sB);
-        int4* const at = rows4 + (warp - 2) * 16;
-        int stage = 0;
-        uint32_t phase = 0, t_parity = 0;  // a stage's next phase of `begin` or `lfull`
-        bool ok = true;
-        const uint32_t full0 = mapa_shared(smem_u32(full), 0), gfull0 = mapa_shared(smem_u32(gfull), 0);
-        for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
-            int e, mb, nb;
-            place(t, e, mb, nb);
-            const int n = tab.count(e), base = tab.off[e], whole = n / BK, a0 = mb * 256 + static_cast<int>(prank) * BM;
-            if (p.src != nullptr) {
+        if (p.src != nullptr) {
+            // ------------------------------------------------------------ gathered rows (both CTAs)
+            const uint32_t sa = smem_u32(sA), full0 = mapa_shared(smem_u32(full), 0), gfull0 = mapa_shared(smem_u32(gfull), 0);
+            int4* const at = rows4 + (warp - 2) * 16;
+            int stage = 0;
+            uint32_t phase = 0, b_parity = 0;  // a stage's next phase of `begin`
+            bool ok = true;
+            for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
+                int e, mb, nb;
+                place(t, e, mb, nb);
+                const int n = tab.count(e), base = tab.off[e], whole = n / BK, a0 = mb * 256 + static_cast<int>(prank) * BM;
                 int2 next = make_int2(0, 0);
                 auto look = [&](int it) {  // two tokens of block it, ahead of their use (and of their check, which waits for them)
                     if (it < whole) next = make_int2(p.src[base + it * BK + lane * 2], p.src[base + it * BK + lane * 2 + 1]);
                 };
                 look(0);
-                for (int it = 0; it < whole; ++it) {
-                    reinterpret_cast<int2*>(at)[lane] = make_int2(checked(p, next.x), checked(p, next.y));
-                    look(it + 1);
-                    __syncwarp();
+                for (int it = 0; it * BK < n; ++it) {
                     int4 rows[16];
+                    if (it < whole) {
+                        reinterpret_cast<int2*>(at)[lane] = make_int2(checked(p, next.x), checked(p, next.y));
+                        look(it + 1);
+                        __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) rows[j] = at[j];
-                    ok = wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer);
-                    if (!ok) break;
-                    if (elect_one()) {
-                        const uint32_t dst = sa + stage * DW_A + (warp - 2) * CHUNK;
+                        for (int j = 0; j < 16; ++j) rows[j] = at[j];
+                        ok = wait_warp(p, empty + stage, phase ^ 1u, kWhereProducer);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            const uint32_t dst = sa + stage * DW_A + (warp - 2) * CHUNK;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            tma_gather4<true>(dst + j * 512, &tmX, full0 + stage * 8, a0 + (warp - 2) * 64, rows[j]);
+                            for (int j = 0; j < 16; ++j)
+                                tma_gather4<true>(dst + j * 512, &tmX, full0 + stage * 8, a0 + (warp - 2) * 64, rows[j]);
+                        }
+                        __syncwarp();
+                    } else {
+                        // A last block is not theirs, but they report it too: no stage passes without them, so that they can
+                        // neither run ahead of the ring nor fall behind it (a barrier two phases on looks like the one before).
+                        ok = wait_warp(p, begin + stage, (b_parity >> stage) & 1u, kWhereProducer);
+                        if (!ok) break;
+                        b_parity ^= 1u << stage;
+                        if (lane == 0) mbar_arrive_cluster(gfull0 + stage * 8);
                     }
-                    __syncwarp();
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (!ok) break;
-            } else {
-                stage = (stage + whole) % S;
             }
+            if (!ok) spin_ns(200000);  // let the last copies land before either CTA can exit
+        }
+    } else if (warp >= TAIL_WARP) {
+        // ---------------------------------------------------------------- last blocks (both CTAs)
+        // A lane has 16 bytes of every fourth row of 32, in each chunk of 64 columns.  The warps walk past the other blocks
+        // without a look at `empty`, of which they could miss phases, and are called by the producer, once for each block that
+        // cannot pass without them.
+        const Lane l;
+        const int r0 = (warp - TAIL_WARP) * 32;
+        const uint32_t sa = smem_u32(sA), sb = smem_u32(sB), gfull0 = mapa_shared(smem_u32(gfull), 0);
+        int stage = 0;
+        uint32_t b_parity = 0;  // a stage's next phase of `begin` or `lfull`
+        bool ok = true;
+        for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
+            int e, mb, nb;
+            place(t, e, mb, nb);
+            const int n = tab.count(e), base = tab.off[e], whole = n / BK;
+            stage = (stage + whole) % S;
             if (whole * BK == n) continue;
-            if (warp == 3) {
-                ok = wait_warp(p, lfull + stage, (t_parity >> stage) & 1u, kWhereProducer);
-                if (ok) fence_proxy_async_smem();
-                if (ok && lane == 0) mbar_arrive_cluster(gfull0 + stage * 8);
-            } else {
-                int row[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    row[j] = base + min(whole * BK + j * 4 + l.r0, n - 1);
-                    if (p.src != nullptr) row[j] = token_of(p, row[j]);
-                }
-                ok = wait_warp(p, begin + stage, (t_parity >> stage) & 1u, kWhereProducer);
+            if (warp == TAIL_WARP + TAIL_WARPS) {
+                ok = wait_warp(p, lfull + stage, (b_parity >> stage) & 1u, kWhereProducer);
                 if (!ok) break;
-                const int b0 = nb * G::n + static_cast<int>(prank) * BM + l.piece * 8, x0 = a0 + l.piece * 8;
+                b_parity ^= 1u << stage;
+                fence_proxy_async_smem();
+                if (lane == 0) mbar_arrive_cluster(gfull0 + stage * 8);
+                if (++stage == S) stage = 0;
+                continue;
+            }
+            int row[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int i = whole * BK + j * 4 + l.r0;
-                    const __nv_bfloat16* x = p.x + static_cast<long long>(row[j]) * p.x_ld + x0;
-                    const __nv_bfloat16* y = p.dy + static_cast<long long>(base + min(i, n - 1)) * p.cols + b0;
+            for (int j = 0; j < 8; ++j) {
+                row[j] = base + min(whole * BK + r0 + j * 4 + l.r0, n - 1);
+                if (p.src != nullptr) row[j] = p.src[row[j]];
+            }
+            if (p.src != nullptr)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const bool in = i < n && x0 + h * 64 < p.x_ld;
-                        cp_async16(sa + stage * DW_A + h * CHUNK + l.at(j), in ? x + h * 64 : p.x, in);
-                    }
+                for (int j = 0; j < 8; ++j) row[j] = checked(p, row[j]);
+            ok = wait_warp(p, begin + stage, (b_parity >> stage) & 1u, kWhereProducer);
+            if (!ok) break;
+            b_parity ^= 1u << stage;
+            const int x0 = mb * 256 + static_cast<int>(prank) * BM + l.piece * 8, y0 = nb * G::n + static_cast<int>(prank) * BM + l.piece * 8;
 #pragma unroll
-                    for (int h = 0; h < 2 * G::parts; ++h) {
-                        const int col = h / 2 * 256 + h % 2 * 64;
-                        const bool in = i < n && b0 + col < p.cols;
-                        cp_async16(sb + stage * G::b_bytes + h * CHUNK + l.at(j), in ? y + col : p.dy, in);
-                    }
+            for (int j = 0; j < 8; ++j) {
+                const int r = whole * BK + r0 + j * 4 + l.r0;
+                const uint32_t at = r0 * 128 + l.at(j);
+                const __nv_bfloat16* x = p.x + static_cast<long long>(row[j]) * p.x_ld + x0;
+                const __nv_bfloat16* y = p.dy + static_cast<long long>(base + min(r, n - 1)) * p.cols + y0;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const bool in = r < n && x0 + c * 64 < p.x_ld;
+                    cp_async16(sa + stage * DW_A + c * CHUNK + at, in ? x + c * 64 : p.x, in);
                 }
-                cp_async_arrive(lfull + stage);
+#pragma unroll
+                for (int c = 0; c < 2 * G::parts; ++c) {
+                    const int col = c / 2 * 256 + c % 2 * 64;
+                    const bool in = r < n && y0 + col < p.cols;
+                    cp_async16(sb + stage * G::b_bytes + c * CHUNK + at, in ? y + col : p.dy, in);
+                }
             }
-            t_parity ^= 1u << stage;
-            if (++stage == S) {
-                stage = 0;
-                phase ^= 1u;  // (of a gather, which walks every stage)
-            }
+            cp_async_arrive(lfull + stage);
+            if (++stage == S) stage = 0;
         }
         cp_async_drain();
-        if (!ok && p.src != nullptr) spin_ns(200000);  // let the last copies land before either CTA can exit
     } else if (warp >= EPI_WARP) {
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3, half = (warp - EPI_WARP) >> 2;
@@ -1344,36 +1399,38 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after();
             }
             const int k0 = mb * 256 + static_cast<int>(prank) * BM + q * 32;  // this warp's first row of dW
-            const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-            for (int c0 = half * (G::n / 2); c0 < (half + 1) * (G::n / 2) && nb * G::n + c0 < p.cols && k0 < p.features; c0 += 32) {
-                uint32_t r[32];
-                if (none) {
+            for (int part = 0; part < G::parts; ++part) {
+                const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc + part) * 256;
+                for (int c0 = half * 128; c0 < half * 128 + 128; c0 += 32) {
+                    const int col = nb * G::n + part * 256 + c0;
+                    if (col >= p.cols || k0 >= p.features) break;
+                    uint32_t r[32];
+                    if (none) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = 0;
-                } else {
-                    tmem_ld_32x32b_x32(lanes + c0, r);
-                    tmem_ld_wait();
+                        for (int j = 0; j < 32; ++j) r[j] = 0;
+                    } else {
+                        tmem_ld_32x32b_x32(lanes + c0, r);
+                        tmem_ld_wait();
+                    }
+                    if (p.out_f32) {  // 16 columns at a time
+                        put_box(box, &tmO, r, col, k0, e, lane);
+                        if (col + 16 < p.cols) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) r[j] = r[16 + j];
+                            put_box(box, &tmO, r, col + 16, k0, e, lane);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) r[j] = tc::pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                        put_box(box, &tmO, r, col, k0, e, lane);
+                    }
                 }
-                uint32_t w[32];  // 32 columns as bf16, or 16 at a time
-                if (!p.out_f32)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = tc::pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                else
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) w[j] = r[j];
-                const int col = nb * G::n + c0;
-                put_box(box, &tmO, w, col, k0, e, lane);
-                if (p.out_f32 && col + 16 < p.cols) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = w[16 + j];
-                    put_box(box, &tmO, w, col + 16, k0, e, lane);
-                }
+                if (none) continue;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + (acc + part) * 8);
             }
-            if (none) continue;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + acc * 8);
-            ++lt;
+            if (!none) ++lt;
         }
         if (lane == 0) bulk_wait_group_all();  // this warp's stores are complete
     }

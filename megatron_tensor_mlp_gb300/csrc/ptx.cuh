@@ -340,12 +340,12 @@ __device__ __forceinline__ void tma_gather4(uint32_t smem_dst, const CUtensorMap
 __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
-// Wait until all of this thread's cp.async are complete.
-__device__ __forceinline__ void cp_async_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Arrive on `bar` (one of the arrivals that it was initialised for) when all of this thread's cp.async so far are complete.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// Wait until all of this thread's cp.async are complete.
+__device__ __forceinline__ void cp_async_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // 16 lanes x 32 consecutive 32-bit columns as 8x8 fragments: of columns 8 i .. 8 i + 7 thread t holds, in r[4 i + 0, 1],
 // columns 2 (t % 4) and the next of lane t / 4 and, in r[4 i + 2, 3], the same of lane t / 4 + 8.
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
