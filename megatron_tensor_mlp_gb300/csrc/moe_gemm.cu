@@ -296,7 +296,9 @@ tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaS
     a.features = static_cast<int>(g.K);
     a.cols = static_cast<int>(g.N);
     a.m_blocks = (a.features + 255) / 256;
-    const bool wide = g.src != nullptr;  // (gathered 816 us, narrow 1230; in order narrow is faster: 800, 840)
+    // Wide tiles for gathered rows (see wide_tiles; 16384 rows on 8 experts, 5120 x 8192: 793 us, narrow 1230) and where
+    // contractions are long (the same in order: 739, 804; 8192 rows on 16 experts, 4096 x 2048: 119, 116).
+    const bool wide = g.src != nullptr || g.rows >= 1024 * int64_t(g.experts);
     a.n_blocks = (a.cols + (wide ? 511 : 255)) / (wide ? 512 : 256);
     a.out = g.out;
     a.ld = g.N;
