@@ -24,8 +24,8 @@
 namespace tpmlp {
 namespace {
 
-// CTAs of the backward: two an SM, more where rows are short.
-constexpr int most_parts(long long h) { return h <= 96 * 32 ? 608 : 304; }
+// CTAs of the backward: two an SM, more where rows take few threads.
+constexpr int most_parts(long long h) { return h <= 4096 ? 608 : 304; }
 constexpr int WARP_ROW = 1024;   // elements of a row that one warp takes
 // Threads of a CTA at most, by the elements that each holds.
 constexpr int most_threads(int elements) { return elements <= 8 ? 1024 : 512; }
@@ -698,6 +698,8 @@ bool wide_rows(int64_t h, int es, std::initializer_list<const void*> ptrs, std::
 // How the ring kernels run: threads of a CTA at most, elements of each, CTAs an SM in the forward and in the backward.  Few
 // threads with much to do: what a thread does once a row (waits, the sums across the CTA) is as much work as 10 elements.
 // 8192 x 5120 bf16, backward without dgamma, dbeta: 16 elements a thread 52 us, 32 45 (floor 37); forward 36, 29 (25).
+// Which CTAs fit an SM goes by registers, so each width has its own: 8192 x 4096 with CTAs of 160 threads at most, three and
+// two an SM, 25.6 and 43.6 us, of 128, four and three, 23.8 and 40.6; x 2048 with 128 21.2 and 32.7, of 96 17.6 and 30.1.
 template <int THREADS, int ELEMENTS, int FWD, int BWD>
 struct Conf {
     static constexpr int threads = THREADS, elements = ELEMENTS, fwd = FWD, bwd = BWD;
@@ -732,10 +734,12 @@ bool with_ring(bool f32, bool wide, int vecs, F&& f) {
     const int h = vecs * (f32 ? 4 : 8);
     if (!wide || h <= WARP_ROW) return false;
     auto pick = [&](auto t) {
-        if (h <= 96 * 32) return f(t, Conf<96, 32, 5, 4>{});
-        if (h <= 160 * 32) return f(t, Conf<160, 32, 3, 2>{});
-        if (h <= 256 * 32) return f(t, Conf<256, 32, 2, 2>{});
-        return h <= 384 * 32 && f(t, Conf<384, 32, 1, 1>{});
+        const int threads = (h + 31) / 32;
+        if (threads <= 96) return f(t, Conf<96, 32, 5, 4>{});
+        if (threads <= 128) return f(t, Conf<128, 32, 4, 3>{});
+        if (threads <= 160) return f(t, Conf<160, 32, 3, 2>{});
+        if (threads <= 256) return f(t, Conf<256, 32, 2, 2>{});
+        return threads <= 384 && f(t, Conf<384, 32, 1, 1>{});
     };
     return f32 ? pick(float{}) : pick(__nv_bfloat16{});
 }
