@@ -28,7 +28,8 @@
  *     frees or synchronises inside these calls, and creates no streams or
  *     events: every kernel of a call goes to `stream`, or to a side stream the
  *     caller has registered (tpmlp_set_side_stream).  Workspaces are passed
- *     in with the sizes stated.  Calls are stream ordered and asynchronous: they return after
+ *     in with the sizes stated; calls, or captured graphs, that may run at the
+ *     same time need workspaces of their own.  Calls are stream ordered and asynchronous: they return after
  *     the kernels are enqueued on `stream` (a cudaStream_t; NULL = legacy
  *     default stream).  The GEMM kernels are launched with programmatic
  *     dependent launch: their set-up may overlap the end of the preceding
@@ -48,7 +49,9 @@
  *     (TPMLP_ERR_ALIAS: no output overlaps an input or another output), then
  *     the device (TPMLP_ERR_ARCH unless compute capability 10.3).  An empty
  *     batch (s * b == 0) is valid and enqueues nothing.  There is no CPU
- *     fallback.
+ *     fallback.  (Layer norm and the expert operators: NULL is refused where the
+ *     tensor has elements; sizes and alignment as stated there; without rows,
+ *     gradients that are sums over them, and a plan's offsets, are set to zero.)
  *   Errors.  A failed launch returns TPMLP_ERR_CUDA.  Kernels never trap: a
  *     device-side wait that runs past its time limit records a status word
  *     and returns; tpmlp_device_status() reports it as TPMLP_ERR_TIMEOUT.
@@ -469,6 +472,8 @@ tpmlp_status tpmlp_moe_combine(const void* O, const void* slot_row, const void* 
 /*
  * Its backward: for each slot with a row, dO[row] = weights[t][j] dZ[t] and dweights[t][j] = dZ[t] . O[row] (0 without a
  * row).  dO [rows][h] bf16 (rows of no slot are left as they were); dweights [tokens][k] fp32 or NULL (O may then be NULL).
+ * A row stands in one slot at most, as in tpmlp_moe_route's plan: with a row in several, each of its
+ * elements in dO is the gradient of any one of them.
  */
 tpmlp_status tpmlp_moe_combine_bwd(const void* O, const void* slot_row, const void* weights, const void* dZ, void* dO, void* dweights,
                                    int64_t tokens, int64_t rows, int k, int64_t h, void* stream);

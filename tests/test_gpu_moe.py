@@ -255,6 +255,65 @@ def test_dw(T, K, N, gather, out):
     assert (dw[0] == 0).all() and (db[5] == 0).all()
 
 
+# many rows an expert and long contractions, where rows in order run on tiles of two accumulators as well
+LONG = [[1300, 0, 1801], [1217], [1023, 1090]]
+
+
+@pytest.mark.parametrize("counts", LONG)
+@pytest.mark.parametrize("N", [136, 520, 1032])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_many_rows_in_order(T, counts, N, out):
+    K, e, n, dt = 4104, len(counts), sum(counts), 0 if out == BF else 1
+    rows, off, _, x = case(counts, K, False, seed=N)
+    w, b = rnd(e, K, N, seed=2, scale=K**-0.5), rnd(e, N, seed=3)
+    y = torch.full((rows, N), 7.0, dtype=out, device="cuda")
+    T.tpmlp_moe_matmul(x, None, off, w, b, y, None, rows, rows, e, K, N, out_dt=dt)
+    ref, size = R.matmul(x[:n], off, w, b)
+    R.close(y[:n], ref, R.product_bound(K) * size, "Y")
+    assert (y[n:] == 7.0).all()
+    dx = torch.full((rows, N), 7.0, dtype=out, device="cuda")
+    v = w.transpose(1, 2).contiguous()
+    T.tpmlp_moe_matmul_dx(x, off, v, None, dx, rows, e, N, K, dx_dt=dt)
+    ref, size = R.matmul(x[:n], off, w)
+    R.close(dx[:n], ref, R.product_bound(K) * size, "dX")
+    assert (dx[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("counts", LONG)
+@pytest.mark.parametrize("f", [128, 640])
+def test_many_rows_in_order_gated(T, counts, f):
+    K, e, n = 4104, len(counts), sum(counts)
+    rows, off, _, x = case(counts, K, False, seed=f)
+    w, b = rnd(e, K, 2 * f, seed=2, scale=K**-0.5), rnd(e, 2 * f, seed=3)
+    y, h = torch.full((rows, f), 7.0, dtype=BF, device="cuda"), torch.full((rows, 2 * f), 7.0, dtype=BF, device="cuda")
+    T.tpmlp_moe_matmul(x, None, off, w, b, y, h, rows, rows, e, K, 2 * f, act=T.ACT_SWIGLU)
+    ref, size = R.matmul(x[:n], off, w, b)
+    R.close(h[:n], ref, R.product_bound(K) * size, "H")
+    g, u = R.halves(ref)
+    eg, eu = R.halves(R.product_bound(K) * size)
+    R.close(y[:n], R.silu(g) * u, gated_slack(g, u, eg, eu), "Y")
+    assert (y[n:] == 7.0).all() and (h[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("counts", LONG)
+@pytest.mark.parametrize("K,N", [(8, 8), (72, 520), (520, 136), (264, 1032)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_many_rows_dw_in_order(T, counts, K, N, out):
+    rows, off, _, x = case(counts, K, False, seed=K)
+    e, n = len(counts), sum(counts)
+    dy = rnd(rows, N, seed=4)
+    x[n:], dy[n:] = NAN, NAN  # rows behind the last
+    dw, db = (torch.full(s, NAN, dtype=out, device="cuda") for s in ((e, K, N), (e, N)))
+    T.tpmlp_moe_matmul_dw(x, None, off, dy, dw, db, rows, rows, e, K, N, grad_dt=0 if out == BF else 1)
+    ref, size, rb, sb = R.dw(x[:n], off, dy[:n], e)
+    R.close(dw, ref, R.product_bound(max(counts)) * size, "dW")
+    R.close(db, rb, (max(counts) / 32 + 32) * 2.0**-24 * sb, "dbias")
+    x[off[e - 1]:], dy[off[e - 1]:] = float("inf"), NAN  # of the last expert: the others' stay as they are
+    again = torch.full_like(dw, NAN)
+    T.tpmlp_moe_matmul_dw(x, None, off, dy, again, None, rows, rows, e, K, N, grad_dt=0 if out == BF else 1)
+    assert torch.equal(again[: e - 1], dw[: e - 1])
+
+
 @pytest.mark.parametrize("counts", [[5], [0, 0, 700], [64, 64], [1] * 100, [0] * 1023 + [40]])
 def test_other_distributions(T, counts):
     """One expert, everything on the last, one row each, the most experts."""
