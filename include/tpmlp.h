@@ -24,7 +24,8 @@
  *     bytes as B [f, h] row-major), b1_sh [p][f/p] (the same bytes as b1 [f]),
  *     Y_sh / H_sh / dH [p][M][f/p].  All matrices are row-major.
  *   Memory.  Every pointer is caller-owned device memory (for example
- *     allocated by PyTorch).  The library never allocates device memory,
+ *     allocated by PyTorch) of the calling thread's current device, to which
+ *     `stream` belongs too.  The library never allocates device memory,
  *     frees or synchronises inside these calls, and creates no streams or
  *     events: every kernel of a call goes to `stream`, or to a side stream the
  *     caller has registered (tpmlp_set_side_stream).  Workspaces are passed
@@ -405,8 +406,8 @@ int64_t tpmlp_layernorm_ws_bytes(int64_t rows, int64_t h);
  *   row_token [tokens * k] int32: the token of each row, -1 past the last row
  *   slot_row  [tokens][k] int32: the row of each slot (-1: none)
  *   ws        tpmlp_moe_route_ws_bytes(tokens, experts, k) bytes, 16-byte aligned
- * experts at most 1024, k at most 32 and at most experts.  The other pointers need the alignment of their elements only.  Without
- * tokens the offsets are set to zero.  The plan stays on the device: nothing has to be read back before the products.
+ * experts at most 1024, k at most 32 and at most experts, tokens below 2^25.  The other pointers need the alignment of
+ * their elements only.  Without tokens the offsets are set to zero.  The plan stays on the device: nothing has to be read back before the products.
  */
 tpmlp_status tpmlp_moe_route(const void* logits, void* ids, void* weights, void* offsets, void* row_token, void* slot_row, void* ws,
                              int64_t tokens, int64_t experts, int k, int chosen, tpmlp_dtype dt, void* stream);

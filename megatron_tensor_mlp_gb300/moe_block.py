@@ -28,6 +28,8 @@ class ExpertLayer:
         experts a multiple of 8, ffn of 128."""
         self.experts, self.h, self.ffn = gate.shape
         self.k, self.device = k, gate.device
+        if self.device.type != "cuda":
+            raise ValueError(f"the weights must be on a GPU, not on {self.device}")
         self.W1 = torch.empty((self.experts, self.h, 2 * self.ffn), dtype=BF, device=self.device)
         self.load(gamma, beta, router, gate, up, down)
 
@@ -38,7 +40,8 @@ class ExpertLayer:
                                ("up", up, (e, h, f)), ("down", down, (e, f, h))):
             self._check(name, t, *shape)
         self.gamma, self.beta, self.router, self.W2 = gamma, beta, router, down
-        T.tpmlp_swiglu_pack(gate, up, self.W1, e * h, f, 1)
+        with torch.cuda.device(self.device):  # (calls go to the current device)
+            T.tpmlp_swiglu_pack(gate, up, self.W1, e * h, f, 1)
 
     def _check(self, name, t, *shape):
         """The entry points take addresses: a tensor of another form would be read as if it were this one."""
@@ -58,7 +61,10 @@ class ExpertLayer:
         offsets, row_token, slot_row = self._new(e + 1, dtype=I32), self._new(t * k, dtype=I32), self._new(t, k, dtype=I32)
         Z, Y, O = self._new(t, h), self._new(t * k, f), self._new(t * k, h)  # noqa: E741
         H = self._new(t * k, 2 * f) if save else None
-        if t > 0:  # (an empty tensor has no address to pass)
+        out = (Z, (X, n, mean, rstd, logits, ids, w, offsets, row_token, slot_row, Y, O, H)) if save else Z
+        if t == 0:  # (an empty tensor has no address to pass)
+            return out
+        with torch.cuda.device(self.device):
             ws = self._new(T.tpmlp_moe_route_ws_bytes(t, e, k), dtype=torch.uint8)
             T.tpmlp_layernorm_fwd(X, self.gamma, self.beta, n, mean, rstd, t, h, h, h)
             T.tpmlp_column_fwd(n, self.router, None, logits, None, t, 1, h, e, 1, act=T.ACT_NONE)
@@ -66,7 +72,7 @@ class ExpertLayer:
             T.tpmlp_moe_matmul(n, row_token, offsets, self.W1, None, Y, H, t, t * k, e, h, 2 * f, act=T.ACT_SWIGLU)
             T.tpmlp_moe_matmul(Y, None, offsets, self.W2, None, O, None, t * k, t * k, e, f, h)
             T.tpmlp_moe_combine(O, slot_row, w, Z, t, t * k, k, h)
-        return (Z, (X, n, mean, rstd, logits, ids, w, offsets, row_token, slot_row, Y, O, H)) if save else Z
+        return out
 
     def backward(self, saved, dZ):
         """The gradients of X (bf16) and, fp32, of gamma, beta, router, gate, up and down."""
@@ -83,17 +89,18 @@ class ExpertLayer:
         dO, dH, dR = self._new(r, h), self._new(r, 2 * f), self._new(r, h)
         dw, dlogits, dn, dn_router = self._new(t, k, dtype=F32), self._new(t, e), self._new(t, h), self._new(t, h)
         ws = self._new(T.tpmlp_layernorm_ws_bytes(t, h), dtype=torch.uint8)
-        T.tpmlp_moe_combine_bwd(O, slot_row, w, dZ, dO, dw, t, r, k, h)
-        T.tpmlp_moe_matmul_dx(dO, offsets, self.W2, H, dH, r, e, f, h, act=T.ACT_SWIGLU)
-        T.tpmlp_moe_matmul_dw(Y, None, offsets, dO, dW2, None, r, r, e, f, h)
-        T.tpmlp_moe_matmul_dx(dH, offsets, self.W1, None, dR, r, e, h, 2 * f)
-        T.tpmlp_moe_matmul_dw(n, row_token, offsets, dH, dW1, None, t, r, e, h, 2 * f)
-        T.tpmlp_moe_combine(dR, slot_row, None, dn, t, r, k, h)
-        T.tpmlp_moe_route_bwd(logits, ids, w, dw, dlogits, t, e, k)
-        T.tpmlp_column_bwd(n, self.router, dlogits, dn_router, grads[2], None, t, 1, h, e, 1)
-        dn.add_(dn_router)
-        T.tpmlp_layernorm_bwd(X, self.gamma, mean, rstd, dn, dX, grads[0], grads[1], ws, t, h, h, h, h)
-        T.tpmlp_swiglu_pack(G, U, dW1, e * h, f, 1, T.F32, inverse=1)
+        with torch.cuda.device(self.device):
+            T.tpmlp_moe_combine_bwd(O, slot_row, w, dZ, dO, dw, t, r, k, h)
+            T.tpmlp_moe_matmul_dx(dO, offsets, self.W2, H, dH, r, e, f, h, act=T.ACT_SWIGLU)
+            T.tpmlp_moe_matmul_dw(Y, None, offsets, dO, dW2, None, r, r, e, f, h)
+            T.tpmlp_moe_matmul_dx(dH, offsets, self.W1, None, dR, r, e, h, 2 * f)
+            T.tpmlp_moe_matmul_dw(n, row_token, offsets, dH, dW1, None, t, r, e, h, 2 * f)
+            T.tpmlp_moe_combine(dR, slot_row, None, dn, t, r, k, h)
+            T.tpmlp_moe_route_bwd(logits, ids, w, dw, dlogits, t, e, k)
+            T.tpmlp_column_bwd(n, self.router, dlogits, dn_router, grads[2], None, t, 1, h, e, 1)
+            dn.add_(dn_router)
+            T.tpmlp_layernorm_bwd(X, self.gamma, mean, rstd, dn, dX, grads[0], grads[1], ws, t, h, h, h, h)
+            T.tpmlp_swiglu_pack(G, U, dW1, e * h, f, 1, T.F32, inverse=1)
         return dX, *grads, G, U, dW2
 
 

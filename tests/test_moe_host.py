@@ -89,7 +89,7 @@ def test_route_refusals():
     assert route(offsets=None, tokens=0) == T.ERR_NULL
     assert route(tokens=-1) == T.ERR_SHAPE and route(experts=0) == T.ERR_SHAPE and route(experts=1025) == T.ERR_SHAPE
     assert route(k=0) == T.ERR_SHAPE and route(k=9) == T.ERR_SHAPE and route(k=33, experts=64) == T.ERR_SHAPE
-    assert route(tokens=1 << 27) == T.ERR_SHAPE
+    assert route(tokens=1 << 27) == T.ERR_SHAPE and route(tokens=1 << 25) == T.ERR_SHAPE
     assert route(dt=2) == T.ERR_DTYPE
     assert route(ids=addr(1) + 2) == T.ERR_ALIGNMENT and route(logits=addr(0) + 1) == T.ERR_ALIGNMENT
     assert route(ws=addr(6) + 4) == T.ERR_ALIGNMENT
@@ -270,3 +270,11 @@ def test_an_expert_s_tiles_are_never_empty():
             nt = -(-n // tn)
             size = (-(-n // nt) + 15) // 16 * 16
             assert size <= tn and (nt - 1) * size < n <= nt * size, (tn, n)
+
+
+def test_a_layer_on_the_cpu_is_refused():
+    """Its calls would hand over addresses that the GPU cannot read."""
+    from megatron_tensor_mlp_gb300.moe_block import ExpertLayer
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises(ValueError):
+        ExpertLayer(z(8), z(8), z(8, 8), z(8, 8, 128), z(8, 8, 128), z(8, 128, 8), 2)
