@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "moe_gemm.cuh"
@@ -148,12 +149,25 @@ bool few_rows(int64_t rows, int64_t experts, int64_t m_blocks, int pairs) {
     return rows <= 16 * experts ? tiles <= 4 * pairs : 20 * tiles <= 11 * pairs;
 }
 
-// Whether the rows kernel runs on wide tiles.  For gathered rows, whose copies they halve: 16384 rows on 8 experts, 5120 x 8192
-// 735 us, narrow 811; 8192 rows on 64 experts, 1024 x 2048 gated 57, 79; where rows are few and weights large the other way
-// (2048 rows on 8 experts, 5120 x 8192: 152, 143).  For rows in order only where much is done for each byte (the first case
-// 801, 821, its gradient of the inputs 826, 875), since a tile's epilogue is not hidden (8192 rows on 16 experts, 4096 x 2048
-// 113, 106; the last case 151, 136).
-bool wide_tiles(const Args& a) { return a.src != nullptr || (a.rows >= 1024 * int64_t(a.experts) && a.kb >= 64); }
+// Whether tiles of twice the size keep the pairs as busy: they come in half as many rounds, or in so many that the last, partly
+// empty one weighs little.  (36 of them instead of 72, on 76 pairs: 1.6 times as long; 128 instead of 256: 0.95; 102 instead of
+// 204, two rounds for three: 1.16.)
+bool busy(double wide, double narrow, int pairs) {
+    const double w = std::ceil(wide / pairs), n = std::ceil(narrow / pairs);
+    return 2 * w <= n || w >= 3;
+}
+
+// Whether the rows kernel runs on wide tiles (a: as for narrow ones), if they keep the pairs busy.  For gathered rows, whose
+// copies they halve: 16384 rows on 8 experts, 5120 x 8192 735 us, narrow 811; 8192 rows on 64 experts, 1024 x 2048 gated 57, 79;
+// in 30 of 33 other cases 2-18 % less.  For rows in order where much is done for each byte, since a tile's epilogue is not
+// hidden: 6000 rows on 8 experts, 5120 x 8192 gated 314, 342, plain 287, 318, its gradient of the inputs 330, 362; but 16384
+// rows on 16 experts, 1024 x 4096 gated 102, 98, plain 103, 92, and 8192 rows on 8 experts, 2048 x 4096 gated 94, 97, plain 98, 95.
+bool wide_tiles(const Args& a, bool gated, int pairs) {
+    if (a.src == nullptr && a.kb < (gated ? 32 : 64)) return false;
+    // tiles of tokens: of one expert, or, as the ranges are on the device, with the last of each half full
+    const double t = a.experts == 1 ? (a.rows + 255) / 256 : a.rows / 256.0 + std::min(a.experts, a.rows) / 2.0;
+    return busy(t * ((a.m_blocks + 1) / 2), t * a.m_blocks, pairs);
+}
 
 template <bool GATED>
 tpmlp_status launch_few(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
@@ -246,7 +260,7 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     const int tile = g.gated ? Geom<SWIGLU>::f : Geom<STORE>::f;
     a.m_blocks = (a.features + tile - 1) / tile;
     const bool few = few_rows(g.rows, g.experts, a.m_blocks, dev.sm_count / 2);
-    const bool wide = !few && wide_tiles(a);
+    const bool wide = !few && wide_tiles(a, g.gated, dev.sm_count / 2);
     if (few || wide) {
         const int t = few ? tile / 2 : tile * 2;
         a.m_blocks = (a.features + t - 1) / t;
@@ -284,7 +298,7 @@ tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaS
     Boxes x;
     if (!make_map(&w, g.w, g.N, g.K, g.experts, BM) || !make_boxes(&x, g.x, g.N, g.rows)) return TPMLP_ERR_CUDA;
     if (g.gated) return launch_rows<false, DSWIGLU>(w, x, a, dev, st);
-    if (wide_tiles(a)) {
+    if (wide_tiles(a, false, dev.sm_count / 2)) {
         a.m_blocks = (a.features + 511) / 512;
         return launch_rows<false, STORE, true>(w, x, a, dev, st);
     }
@@ -297,9 +311,12 @@ tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaS
     a.cols = static_cast<int>(g.N);
     a.m_blocks = (a.features + 255) / 256;
     // Wide tiles for gathered rows (see wide_tiles; 16384 rows on 8 experts, 5120 x 8192: 793 us, narrow 1230) and where
-    // contractions are long (the same in order: 739, 804; 8192 rows on 16 experts, 4096 x 2048: 119, 116).
-    const bool wide = g.src != nullptr || g.rows >= 1024 * int64_t(g.experts);
-    a.n_blocks = (a.cols + (wide ? 511 : 255)) / (wide ? 512 : 256);
+    // contractions are long (the same in order: 739, 804; 8192 rows on 16 experts, 4096 x 2048: 119, 116), if they keep the
+    // pairs busy.
+    const int narrow = (a.cols + 255) / 256, half = (a.cols + 511) / 512;
+    const bool wide = (g.src != nullptr || g.rows >= 1280 * int64_t(g.experts)) &&
+                      busy(1.0 * a.experts * a.m_blocks * half, 1.0 * a.experts * a.m_blocks * narrow, dev.sm_count / 2);
+    a.n_blocks = wide ? half : narrow;
     a.out = g.out;
     a.ld = g.N;
     a.out_f32 = g.out_f32;
