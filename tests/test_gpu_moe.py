@@ -255,12 +255,12 @@ def test_dw(T, K, N, gather, out):
     assert (dw[0] == 0).all() and (db[5] == 0).all()
 
 
-# many rows an expert and long contractions, where rows in order run on tiles of two accumulators as well
-LONG = [[1300, 0, 1801], [1217], [1023, 1090]]
+# many rows an expert, long contractions and, with the last sizes, enough tiles that rows in order run on two accumulators too
+LONG = [[1300, 0, 1801], [2700], [1023, 1090]]
 
 
 @pytest.mark.parametrize("counts", LONG)
-@pytest.mark.parametrize("N", [136, 520, 1032])
+@pytest.mark.parametrize("N", [136, 1032, 2000])
 @pytest.mark.parametrize("out", [BF, F32])
 def test_many_rows_in_order(T, counts, N, out):
     K, e, n, dt = 4104, len(counts), sum(counts), 0 if out == BF else 1
@@ -280,7 +280,7 @@ def test_many_rows_in_order(T, counts, N, out):
 
 
 @pytest.mark.parametrize("counts", LONG)
-@pytest.mark.parametrize("f", [128, 640])
+@pytest.mark.parametrize("f", [128, 1152])
 def test_many_rows_in_order_gated(T, counts, f):
     K, e, n = 4104, len(counts), sum(counts)
     rows, off, _, x = case(counts, K, False, seed=f)
@@ -295,8 +295,8 @@ def test_many_rows_in_order_gated(T, counts, f):
     assert (y[n:] == 7.0).all() and (h[n:] == 7.0).all()
 
 
-@pytest.mark.parametrize("counts", LONG)
-@pytest.mark.parametrize("K,N", [(8, 8), (72, 520), (520, 136), (264, 1032)])
+@pytest.mark.parametrize("counts", LONG + [[2700, 61], [3, 2900]])
+@pytest.mark.parametrize("K,N", [(8, 8), (72, 520), (520, 136), (2056, 1032), (1032, 4616)])
 @pytest.mark.parametrize("out", [BF, F32])
 def test_many_rows_dw_in_order(T, counts, K, N, out):
     rows, off, _, x = case(counts, K, False, seed=K)
@@ -312,6 +312,58 @@ def test_many_rows_dw_in_order(T, counts, K, N, out):
     again = torch.full_like(dw, NAN)
     T.tpmlp_moe_matmul_dw(x, None, off, dy, again, None, rows, rows, e, K, N, grad_dt=0 if out == BF else 1)
     assert torch.equal(again[: e - 1], dw[: e - 1])
+
+
+@pytest.mark.parametrize("K", [8, 72, 200, 1032])
+@pytest.mark.parametrize("N", [1544, 1600])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_gathered_rows_of_many_tiles(T, K, N, out):
+    """Enough tiles that gathered rows run on two accumulators."""
+    rows, off, src, x = case(COUNTS, K, True, seed=K)
+    e, n, dt = len(COUNTS), sum(COUNTS), 0 if out == BF else 1
+    w, b, dy = rnd(e, K, N, seed=2, scale=K**-0.5), rnd(e, N, seed=3), rnd(rows, N, seed=4)
+    w[0] = NAN  # an expert without rows
+    y = torch.full((rows, N), 7.0, dtype=out, device="cuda")
+    T.tpmlp_moe_matmul(x, src, off, w, b, y, None, x.shape[0], rows, e, K, N, out_dt=dt)
+    xs = x[src.long()][:n]
+    ref, size = R.matmul(xs, off, w, b)
+    R.close(y[:n], ref, R.product_bound(K) * size, "Y")
+    assert (y[n:] == 7.0).all()
+    dw, db = (torch.full(s, NAN, dtype=out, device="cuda") for s in ((e, K, N), (e, N)))
+    T.tpmlp_moe_matmul_dw(x, src, off, dy, dw, db, x.shape[0], rows, e, K, N, grad_dt=dt)
+    ref, size, rb, sb = R.dw(xs, off, dy[:n], e)
+    R.close(dw, ref, R.product_bound(max(COUNTS)) * size, "dW")
+    R.close(db, rb, (max(COUNTS) / 32 + 32) * 2.0**-24 * sb, "dbias")
+    assert (dw[0] == 0).all() and (db[5] == 0).all()
+    # the last expert with rows reads a token of its own that is not finite: the others' results stay as they are
+    last = max(i for i, c in enumerate(COUNTS) if c)
+    lo, hi = int(off[last]), int(off[last + 1])
+    x2 = torch.cat([x, torch.full((1, K), float("inf"), dtype=BF, device="cuda")])
+    src2, dy2 = src.clone(), dy.clone()
+    src2[lo:hi], dy2[lo:hi] = x.shape[0], NAN
+    y2, dw2 = torch.full_like(y, 7.0), torch.full_like(dw, NAN)
+    T.tpmlp_moe_matmul(x2, src2, off, w, b, y2, None, x2.shape[0], rows, e, K, N, out_dt=dt)
+    T.tpmlp_moe_matmul_dw(x2, src2, off, dy2, dw2, None, x2.shape[0], rows, e, K, N, grad_dt=dt)
+    assert torch.equal(y2[:lo], y[:lo]) and torch.equal(dw2[:last], dw[:last]) and not torch.isfinite(dw2[last]).any()
+
+
+@pytest.mark.parametrize("K", [8, 200, 1032])
+@pytest.mark.parametrize("save", [False, True])
+def test_gathered_rows_of_many_tiles_gated(T, K, save):
+    f = 896
+    rows, off, src, x = case(COUNTS, K, True, seed=K)
+    e, n = len(COUNTS), sum(COUNTS)
+    w, b = rnd(e, K, 2 * f, seed=2, scale=1.5 * K**-0.5), rnd(e, 2 * f, seed=3)
+    y = torch.full((rows, f), 7.0, dtype=BF, device="cuda")
+    h = torch.full((rows, 2 * f), 7.0, dtype=BF, device="cuda") if save else None
+    T.tpmlp_moe_matmul(x, src, off, w, b, y, h, x.shape[0], rows, e, K, 2 * f, act=T.ACT_SWIGLU)
+    ref, size = R.matmul(x[src.long()][:n], off, w, b)
+    (g, u), (eg, eu) = R.halves(ref), R.halves(R.product_bound(K) * size)
+    R.close(y[:n], R.silu(g) * u, gated_slack(g, u, eg, eu), "Y")
+    assert (y[n:] == 7.0).all()
+    if save:
+        R.close(h[:n], ref, R.product_bound(K) * size, "H")
+        assert (h[n:] == 7.0).all()
 
 
 @pytest.mark.parametrize("counts", [[5], [0, 0, 700], [64, 64], [1] * 100, [0] * 1023 + [40]])
