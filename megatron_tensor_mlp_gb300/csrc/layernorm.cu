@@ -700,6 +700,7 @@ bool wide_rows(int64_t h, int es, std::initializer_list<const void*> ptrs, std::
 // 8192 x 5120 bf16, backward without dgamma, dbeta: 16 elements a thread 52 us, 32 45 (floor 37); forward 36, 29 (25).
 // Which CTAs fit an SM goes by registers, so each width has its own: 8192 x 4096 with CTAs of 160 threads at most, three and
 // two an SM, 25.6 and 43.6 us, of 128, four and three, 23.8 and 40.6; x 2048 with 128 21.2 and 32.7, of 96 17.6 and 30.1.
+// 4096 x 16384 47 and 82, by the kernels above 85 and 147.
 template <int THREADS, int ELEMENTS, int FWD, int BWD>
 struct Conf {
     static constexpr int threads = THREADS, elements = ELEMENTS, fwd = FWD, bwd = BWD;
@@ -739,7 +740,8 @@ bool with_ring(bool f32, bool wide, int vecs, F&& f) {
         if (threads <= 128) return f(t, Conf<128, 32, 4, 3>{});
         if (threads <= 160) return f(t, Conf<160, 32, 3, 2>{});
         if (threads <= 256) return f(t, Conf<256, 32, 2, 2>{});
-        return threads <= 384 && f(t, Conf<384, 32, 1, 1>{});
+        if (threads <= 384) return f(t, Conf<384, 32, 1, 1>{});
+        return threads <= 512 && f(t, Conf<512, 32, 1, 1>{});
     };
     return f32 ? pick(float{}) : pick(__nv_bfloat16{});
 }

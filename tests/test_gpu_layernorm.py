@@ -126,7 +126,7 @@ def test_strides_and_alignment(T, ld, shift, dtype):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,h", [(1900, 1032), (1000, 3080), (1300, 3608), (1301, 4096), (1300, 4104), (1001, 5120), (700, 8192),
-                                    (700, 12288)])
+                                    (700, 12288), (400, 14336), (401, 16384)])
 def test_many_wide_rows(T, rows, h, dtype):
     """More rows than CTAs, which go through a ring in shared memory: with a pitch, without gamma or beta too."""
     dt, ld = 0 if dtype == BF else 1, h + 8
