@@ -138,14 +138,18 @@ tpmlp_status launch_rows(const CUtensorMap& w, const Boxes& x, const Args& a, co
     return launch(kern, dim3(2 * pairs), THREADS, G::smem, 2, st, w, x, a);
 }
 
-// Whether the forward product runs on the few-rows kernel.  The row ranges are on the device, so this goes by the tiles that
-// the pairs would have if the rows were spread over the experts: where they fill about half of the pairs, or, with at most
-// 16 rows an expert, up to four rounds of them (which do not come out even).  4 tokens, 8 of 64 experts, 1024 x 8192 gated
-// (256 tiles): 28.0 us, pairs 33.8; 4096 x 1024 (32 tiles): 14.6, 26.0; 128 rows on 8 experts of that size 16.6, 23.8; 666
-// rows (40 tiles) 19.3, 24.7.  But 128 rows on 34 of 64 experts, gated (2112 tiles): 112, pairs 91; 1024 rows on 16
-// experts, 4096 x 1024 (80 tiles): 36.1, 27.4.
-bool few_rows(int64_t rows, int64_t experts, int64_t m_blocks, int pairs) {
+// Whether a product runs on the few-rows kernel.  The row ranges are on the device, so this goes by the tiles that the pairs
+// would have if the rows were spread over the experts: where they fill about half of the pairs, or, with at most 16 rows an
+// expert, up to four rounds of them (which do not come out even).  4 tokens, 8 of 64 experts, 1024 x 8192 gated (256 tiles):
+// 28.0 us, pairs 33.8; 4096 x 1024 (32 tiles): 14.6, 26.0; 128 rows on 8 experts of that size 16.6, 23.8; 666 rows (40 tiles)
+// 19.3, 24.7.  But 128 rows on 34 of 64 experts, gated (2112 tiles): 112, pairs 91; 1024 rows on 16 experts, 4096 x 1024 (80
+// tiles): 36.1, 27.4.  Gradients of the inputs: 30 rows on 8 experts, 3840 -> 624 (24 tiles) 11.5, 22.3; 1000 rows, 2048 -> 1024
+// (44 tiles) 17.1, 15.8.  Through the gated activation a thread handles a feature's pre-activations one by one, so for fewer
+// tiles: 8 rows, 5120 -> 4096 (128 tiles) 43, 61; 1400 rows, 1024 -> 512 (26 tiles) 14.7, 17.1; but 600 rows on 64 experts,
+// 1024 -> 1024 (264 tiles) 33, 27; 400 rows on 8 (36 tiles) 14.6, 13.5.
+bool few_rows(int64_t rows, int64_t experts, int64_t m_blocks, int pairs, bool gated_dx = false) {
     const int64_t tiles = m_blocks * (std::min(rows, experts) + rows / 256);
+    if (gated_dx) return rows <= 8 * experts ? tiles <= 2 * pairs : 20 * tiles <= 8 * pairs;
     return rows <= 16 * experts ? tiles <= 4 * pairs : 20 * tiles <= 11 * pairs;
 }
 
@@ -169,10 +173,10 @@ bool wide_tiles(const Args& a, bool gated, int pairs) {
     return busy(t * ((a.m_blocks + 1) / 2), t * a.m_blocks, pairs);
 }
 
-template <bool GATED>
+template <bool W_MN, int MODE>
 tpmlp_status launch_few(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
     static PerDevice<bool> done;
-    auto kern = few_kernel<GATED>;
+    auto kern = few_kernel<W_MN, MODE>;
     if (!set_smem(kern, dev.device, FEW_SMEM, done)) return TPMLP_ERR_CUDA;
     const int64_t tiles = int64_t(a.m_blocks) * (a.rows / FEW_TN + std::min(a.experts, a.rows));
     // the contraction is split while all CTAs, two an SM, run at once and each has at least four blocks of it
@@ -279,7 +283,7 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     a.chunked = chunks > 0 && g.N % 64 == 0;
     const bool mapped = a.chunked ? make_chunks(&w, g.w, g.N, g.K, g.experts, chunks) : make_map(&w, g.w, g.N, g.K, g.experts, BK);
     if (!mapped || !(g.src ? make_map(&x.m[0], g.x, g.K, g.tokens, 1, 1, 2) : make_boxes(&x, g.x, g.K, g.rows))) return TPMLP_ERR_CUDA;
-    if (few) return g.gated ? launch_few<true>(w, x, a, dev, st) : launch_few<false>(w, x, a, dev, st);
+    if (few) return g.gated ? launch_few<true, SWIGLU>(w, x, a, dev, st) : launch_few<true, STORE>(w, x, a, dev, st);
     if (wide) return g.gated ? launch_rows<true, SWIGLU, true>(w, x, a, dev, st) : launch_rows<true, STORE, true>(w, x, a, dev, st);
     return g.gated ? launch_rows<true, SWIGLU>(w, x, a, dev, st) : launch_rows<true, STORE>(w, x, a, dev, st);
 }
@@ -297,6 +301,10 @@ tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaS
     CUtensorMap w;
     Boxes x;
     if (!make_map(&w, g.w, g.N, g.K, g.experts, BM) || !make_boxes(&x, g.x, g.N, g.rows)) return TPMLP_ERR_CUDA;
+    if (few_rows(g.rows, g.experts, a.m_blocks, dev.sm_count / 2, g.gated)) {
+        a.m_blocks = (a.features + BM - 1) / BM;
+        return g.gated ? launch_few<false, DSWIGLU>(w, x, a, dev, st) : launch_few<false, STORE>(w, x, a, dev, st);
+    }
     if (g.gated) return launch_rows<false, DSWIGLU>(w, x, a, dev, st);
     if (wide_tiles(a, false, dev.sm_count / 2)) {
         a.m_blocks = (a.features + 511) / 512;

@@ -242,6 +242,12 @@ __device__ __forceinline__ void gate_frags(const uint32_t (&a)[16], const uint32
         hi[i] = tc::pack_bf16x2(gated(b[2 * i], ub[2 * i]), gated(b[2 * i + 1], ub[2 * i + 1]));
     }
 }
+// dg = dy u silu'(g), du = dy silu(g)
+__device__ __forceinline__ void gated_gradient(float dy, float g, float u, float& dg, float& du) {
+    const float s = tc::sigmoid_approx(g);
+    du = dy * g * s;
+    dg = dy * u * (s * (1.0f + g * (1.0f - s)));
+}
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -699,16 +705,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     stage_get(sbuf + STAGE, ulo, uhi, lane);
                     tmem_ld_wait();
                     __syncwarp();
-                    // dg = dy u silu'(g), du = dy silu(g)
-                    auto grad = [](float dy, float g, float u, float& dg, float& du) {
-                        const float s = tc::sigmoid_approx(g);
-                        du = dy * g * s;
-                        dg = dy * u * (s * (1.0f + g * (1.0f - s)));
-                    };
                     auto pair = [&](uint32_t d0, uint32_t d1, uint32_t& g, uint32_t& u) {
                         float g0, g1, u0, u1;
-                        grad(__uint_as_float(d0), lo_f(g), lo_f(u), g0, u0);
-                        grad(__uint_as_float(d1), hi_f(g), hi_f(u), g1, u1);
+                        gated_gradient(__uint_as_float(d0), lo_f(g), lo_f(u), g0, u0);
+                        gated_gradient(__uint_as_float(d1), hi_f(g), hi_f(u), g1, u1);
                         g = tc::pack_bf16x2(g0, g1);
                         u = tc::pack_bf16x2(u0, u1);
                     };
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ---------------------------------------------------------------- few rows
-// The forward product for few rows an expert, where reading the weights bounds the time: one CTA per tile of 128 columns of W
+// The rows kernel's products for few rows an expert, where reading the weights bounds the time: one CTA per tile of 128 features
 // and at most 64 tokens, two CTAs an SM, not persistent, so that many copies are in flight and the SMs even out.  Clusters of
 // up to 8 CTAs split the contraction; groups of 8 tokens go to the cluster's CTAs in turn, which add the partial sums through
 // distributed shared memory in the order of the ranks.  (4 tokens on 8 of 64 experts, 1024 x 8192: 134 MB of weights, 20 us
@@ -756,10 +756,12 @@ constexpr int FEW_SUMS = 8 * 4096;  // partial sums on their way: 8 (rank, group
 constexpr int FEW_SMEM = 1024 + FEW_STAGES * FEW_STAGE + (2 * FEW_STAGES + 2) * 8 + 64;
 static_assert(FEW_TN >= 32 && FEW_SUMS <= FEW_STAGES * FEW_STAGE && 2 * (FEW_SMEM + 1024) <= 227 * 1024, "few kernel shared memory");
 
-template <bool GATED>
+template <bool W_MN, int MODE>
 __global__ void __launch_bounds__(FEW_THREADS, 2)
     few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Boxes tmX, const Args p) {
     constexpr int S = FEW_STAGES;
+    constexpr bool GATED = MODE == SWIGLU;
+    static_assert(MODE == STORE || W_MN == GATED);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
@@ -856,6 +858,20 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
         bias = __bfloat162float(p.bias[c.e * p.bias_ld + col]);
         if (GATED) bias_up = __bfloat162float(p.bias[c.e * p.bias_ld + col + 128]);
     }
+    // DSWIGLU: the pre-activations of eight tokens of a group, the first one's while the products are computed
+    [[maybe_unused]] float hg[8], hu[8];
+    [[maybe_unused]] const long long packed = static_cast<long long>(f >> 7) * 256 + (f & 127);
+    [[maybe_unused]] auto saved = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = g * 8 + j < c.n && f < p.features;
+            const __nv_bfloat16* h = p.h_in + (c.row0 + g * 8 + j) * p.h_ld + packed;
+            hg[j] = in ? __bfloat162float(h[0]) : 0.0f;
+            hu[j] = in ? __bfloat162float(h[128]) : 0.0f;
+        }
+    };
+    if constexpr (MODE == DSWIGLU)
+        if (warp >= EPI_WARP) saved(rank);
     const int k0 = p.kb * rank / n_ranks, k1 = p.kb * (rank + 1) / n_ranks;
     bool ok = true;
 
@@ -876,6 +892,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                     if constexpr (GATED) {
                         tma_load_3d_bar(a_dst, &tmW, bar, (c.mb >> 1) * 256 + (c.mb & 1) * 64, it * BK, c.e);
                         tma_load_3d_bar(a_dst + CHUNK, &tmW, bar, (c.mb >> 1) * 256 + (c.mb & 1) * 64 + 128, it * BK, c.e);
+                    } else if constexpr (!W_MN) {
+                        tma_load_3d_bar(a_dst, &tmW, bar, it * BK, c.mb * BM, c.e);
                     } else if (p.chunked) {
                         tma_load_4d(a_dst, &tmW, full + stage, 0, it * BK, c.mb * 2, c.e);
                     } else {
@@ -897,8 +915,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
             if (lane == 0) {
-                const uint64_t a0 = sdesc_sw128(smem_u32(sA), CHUNK, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
-                const uint32_t idesc = idesc_bf16_f32(BM, nn, true, false);
+                const uint64_t a0 = sdesc_sw128(smem_u32(sA), W_MN ? CHUNK : 16, 1024), b0 = sdesc_sw128(smem_u32(sB), 16, 1024);
+                const uint32_t idesc = idesc_bf16_f32(BM, nn, W_MN, false);
                 int stage = 0;
                 uint32_t phase = 0;
                 for (int it = k0; it < k1; ++it) {
@@ -908,7 +926,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                     const uint64_t a = a0 + static_cast<uint64_t>(stage * (FEW_A >> 4)), b = b0 + static_cast<uint64_t>(stage * (FEW_B >> 4));
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        umma_f16(tmem, a + kk * (2048 >> 4), b + kk * 2, idesc, it > k0 || kk > 0 ? 1u : 0u);
+                        umma_f16(tmem, a + kk * ((W_MN ? 2048 : 32) >> 4), b + kk * 2, idesc, it > k0 || kk > 0 ? 1u : 0u);
                     umma_commit(empty + stage);
                     if (++stage == S) {
                         stage = 0;
@@ -976,6 +994,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
             float v[AT_ONCE], u[AT_ONCE];
 #pragma unroll
             for (int j = 0; j < AT_ONCE; ++j) v[j] = u[j] = 0.0f;
+            if constexpr (MODE == DSWIGLU)
+                if (g != rank) saved(g);
             for (int r = 0; r < n_ranks; ++r) {
                 const float* at = part + ((r * per + g / n_ranks) * 8 + j0) * 128 + lane0;
 #pragma unroll
@@ -990,7 +1010,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
             for (int j = 0; j < AT_ONCE; ++j) {
                 if (j >= n) break;
                 const float x = v[j] + bias;
-                if constexpr (GATED) {
+                if constexpr (MODE == DSWIGLU) {
+                    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.out) + (row + j) * p.ld + packed;
+                    float dg, du;
+                    gated_gradient(x, hg[j], hu[j], dg, du);
+                    d[0] = __float2bfloat16_rn(dg);
+                    d[128] = __float2bfloat16_rn(du);
+                } else if constexpr (GATED) {
                     const float up = u[j] + bias_up;
                     if (p.h_out != nullptr) {
                         p.h_out[(row + j) * p.h_ld + col] = __float2bfloat16_rn(x);

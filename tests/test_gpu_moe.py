@@ -240,6 +240,44 @@ def test_gated_dx(T, f, N):
     assert (dh[n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("K,N", SHAPES + [(136, 4104), (2056, 72)])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("counts", [COUNTS, FEW, [3, 0, 70], [100, 20, 129, 64, 0], [1]], ids=["many", "few", "three", "middle", "one"])
+def test_dx_of_few_and_many_rows(T, K, N, out, counts):
+    rows, off, _, dy = case(counts, N, False, seed=K)
+    e, n = len(counts), sum(counts)
+    dy[n:] = NAN  # rows behind the last
+    w = rnd(e, K, N, seed=2, scale=N**-0.5)
+    for i in (i for i, c in enumerate(counts) if c == 0):
+        w[i] = NAN
+    dx = torch.full((rows, K), 7.0, dtype=out, device="cuda")
+    T.tpmlp_moe_matmul_dx(dy, off, w, None, dx, rows, e, K, N, dx_dt=0 if out == BF else 1)
+    ref, size = R.matmul(dy[:n], off, w.transpose(1, 2))
+    R.close(dx[:n], ref, R.product_bound(N) * size, "dX")
+    assert (dx[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("f,N", [(128, 8), (384, 72), (640, 1032), (128, 4104), (1152, 200), (2048, 72)])
+@pytest.mark.parametrize("counts", [COUNTS, FEW, [3, 0, 70], [100, 20, 129, 64, 0], [1]], ids=["many", "few", "three", "middle", "one"])
+def test_gated_dx_of_few_and_many_rows(T, f, N, counts):
+    rows, off, _, dy = case(counts, N, False, seed=f)
+    e, n = len(counts), sum(counts)
+    w, h = rnd(e, f, N, seed=2, scale=N**-0.5), rnd(rows, 2 * f, seed=3, scale=2.0)
+    dy[n:], h[n:] = NAN, NAN
+    for i in (i for i, c in enumerate(counts) if c == 0):
+        w[i] = NAN
+    dh = torch.full((rows, 2 * f), 7.0, dtype=BF, device="cuda")
+    T.tpmlp_moe_matmul_dx(dy, off, w, h, dh, rows, e, f, N, act=T.ACT_SWIGLU)
+    d, size = R.matmul(dy[:n], off, w.transpose(1, 2))
+    g, u = R.halves(h[:n].to(R.D))
+    ed = R.product_bound(N) * size
+    # (slack as in test_gated_dx)
+    slack = R.packed(u.abs() * (ed * R.dsilu(g).abs() + d.abs() * 2.0**-20 * (1 + 2 * g.abs())),
+                     ed * R.silu(g).abs() + 2.0**-20 * (d * R.silu(g)).abs())
+    R.close(dh[:n], R.packed(d * u * R.dsilu(g), d * R.silu(g)), slack, "dH")
+    assert (dh[n:] == 7.0).all()
+
+
 @pytest.mark.parametrize("K,N", SHAPES)
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("out", [BF, F32])
