@@ -351,9 +351,9 @@ struct CombineArgs {
 // Z[t] = sum_j w[t][j] O[row(t, j)], slots in order, in 32 bits.  A CTA takes a token, a thread four pieces of 16 bytes at a
 // time, of two slots, so that their row numbers are waited for once and eight loads then are on their way.  (16384 rows of 5120
 // into 8192 tokens: 41 us, a piece of a slot at a time 47, at a copy's rate 37.  One slot a token: half the registers and
-// twice the threads an SM, 28 us, with two slots' 37, at a copy's rate 25.)
-constexpr int PIECES = 4;
-template <int AT_ONCE>
+// twice the threads an SM, 28 us, with two slots' 37, at a copy's rate 25.  Where half the pieces do for a row: of 2560, three
+// slots, 8192 tokens 34 us with four, 30 with two; of 5120, two slots, 43, 46.)
+template <int AT_ONCE, int PIECES>
 __global__ void __launch_bounds__(AT_ONCE == 1 ? 512 : 256) combine_kernel(const CombineArgs p) {
     griddep_wait();
     if (threadIdx.x == 0 && threadIdx.y == 0) griddep_launch_dependents();
@@ -396,6 +396,8 @@ __global__ void __launch_bounds__(AT_ONCE == 1 ? 512 : 256) combine_kernel(const
 }
 
 // dO[row] = w dZ[t], dw[t][j] = dZ[t] . O[row]: a warp takes a slot (the slots of a token, next to one another, find dZ in L1).
+// (Rows of 512, three slots, 8192 tokens: 11.4 us with four pieces a lane, two of which are empty, 8.7 with two.)
+template <int PIECES>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const CombineArgs p) {
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
@@ -529,9 +531,11 @@ tpmlp_status launch_moe_combine(const void* O, const int* slot_row, const float*
     a.rows = static_cast<int>(rows);
     a.k = k;
     a.vecs = static_cast<int>(h / 8);
-    const int x = std::min(256, (a.vecs + 32 * PIECES - 1) / (32 * PIECES) * 32), y = k == 1 ? 256 / x : 1;
+    const int pieces = k > 1 && a.vecs <= 512 ? 2 : 4;
+    const int x = std::min(256, (a.vecs + 32 * pieces - 1) / (32 * pieces) * 32), y = k == 1 ? 256 / x : 1;
     const int64_t ctas = std::min<int64_t>((tokens + y - 1) / y, 1 << 20);
-    return launch(k == 1 ? combine_kernel<1> : combine_kernel<2>, dim3(static_cast<unsigned>(ctas)), dim3(x, y), st, a);
+    const auto kern = k == 1 ? combine_kernel<1, 4> : pieces == 2 ? combine_kernel<2, 2> : combine_kernel<2, 4>;
+    return launch(kern, dim3(static_cast<unsigned>(ctas)), dim3(x, y), st, a);
 }
 
 tpmlp_status launch_moe_combine_bwd(const void* O, const int* slot_row, const float* weights, const void* dZ, void* dO, float* dweights,
@@ -547,7 +551,7 @@ tpmlp_status launch_moe_combine_bwd(const void* O, const int* slot_row, const fl
     a.rows = static_cast<int>(rows);
     a.k = k;
     a.vecs = static_cast<int>(h / 8);
-    return launch(combine_bwd_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((tokens * k + 7) / 8, 1 << 20))), 256, st, a);
+    return launch(a.vecs <= 128 ? combine_bwd_kernel<2> : combine_bwd_kernel<4>, dim3(static_cast<unsigned>(std::min<int64_t>((tokens * k + 7) / 8, 1 << 20))), 256, st, a);
 }
 
 }  // namespace tpmlp
