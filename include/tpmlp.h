@@ -372,7 +372,8 @@ int tpmlp_get_mxfp4_mode(void);
  *   Y[r] = (X[r] - mean[r]) rstd[r] gamma + beta,   rstd = 1 / sqrt(mean of (X - mean)^2 + eps)
  *   X [rows][h] dt, row pitch ldx >= h (elements); gamma, beta [h] dt, each may be NULL (1, 0);
  *   Y [rows][h] dt, row pitch ldy; mean, rstd [rows] fp32, both or neither, for the backward.
- * Statistics in fp32.  h at most 16384.  Pointers and pitches need the alignment of their elements only; rows are
+ * Statistics in fp32; the error of Y goes by the differences from the mean, however large the mean is against them (a row of one
+ * value gives beta; the saved mean is rounded to fp32).  h at most 16384.  Pointers and pitches need the alignment of their elements only; rows are
  * read 16 bytes at a time where all of h, the pitches and the addresses of X, Y, gamma and beta are multiples of 16 bytes.
  */
 tpmlp_status tpmlp_layernorm_fwd(const void* X, const void* gamma, const void* beta, void* Y, void* mean, void* rstd,

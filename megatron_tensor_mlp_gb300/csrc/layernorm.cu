@@ -4,10 +4,16 @@
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)),  g = dy gamma,  xhat = (x - mean) rstd
 //   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
 //
-// A row is read once and lies in registers: a thread holds NV pieces of VEC elements.  Means are of the values, variances
-// of the differences from the mean, both in 32 bits.  The backward's CTAs walk over rows with the same columns on the
-// same threads, so the sums of dgamma and dbeta stay in registers until a CTA's last row; the CTAs' sums go to the
-// workspace and a second kernel adds them in a fixed order (no atomics: the same bits every time).
+// A row is read once and lies in registers: a thread holds NV pieces of VEC elements.  Sums are in 32 bits.  The mean of the
+// values, m0, is off by a few 2^-24 of their size, which rstd magnifies by up to 1 / sqrt(eps) where the values are large against
+// their spread; so the differences from it, d = x - m0, are summed along with their squares: m0 + mean(d) is the mean,
+// d - mean(d) the difference that is normalised, mean(d^2) - mean(d)^2 the variance (mean(d) is small against m0: nothing
+// cancels).  A constant row's d are multiples of one step, their sum exact, the differences zero and y beta, to the bit.
+// (Forward of 8192 x 5120 bf16: 31.1 us, with the mean left as it is 28.6; 8192 x 4096 24.6, 23.4; x 1000 12.0, 11.8.)
+//
+// The backward's CTAs walk over rows with the same columns on the same threads, so the sums of dgamma and dbeta stay in
+// registers until a CTA's last row; the CTAs' sums go to the workspace and a second kernel adds them in a fixed order (no
+// atomics: the same bits every time).
 //
 // Rows whose start is not aligned to 16 bytes (an odd width, pitch or base) are read element by element (VEC 1).
 #include <cuda_bf16.h>
@@ -88,6 +94,20 @@ __device__ __forceinline__ typename Raw<T, VEC>::type narrow(const float (&f)[VE
     }
 }
 
+// Sums of N values over a warp: of one in every lane, of two in half the shuffles, the first's in lanes 0-15 and the second's
+// in 16-31 (as v[0]).
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
+    static_assert(N == 1 || N == 2);
+    if constexpr (N == 2) {
+        const bool second = (threadIdx.x & 16) != 0;
+        const float mine = second ? v[1] : v[0], other = second ? v[0] : v[1];
+        v[0] = mine + __shfl_xor_sync(0xFFFFFFFFu, other, 16);
+    }
+#pragma unroll
+    for (int d = N == 2 ? 8 : 16; d > 0; d >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], d);
+}
+
 // Sums of N values over a row's threads, the same in each of them: a warp, or the whole CTA (buf: two sets of 32 x N
 // floats used in turn, so that one barrier a row is enough).
 template <int N>
@@ -112,6 +132,19 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* buf, int& turn) {
     }
 }
 
+// From the sums of the differences d from m0 and of their squares: the mean of d, by which m0 is off (divided by h, not
+// multiplied by a rounded 1 / h: that of a constant row comes out exact), and rstd.  A variance below zero is a rounding; a NaN
+// stays one, and squares past the range stay infinite (fma: not infinity less infinity).
+__device__ __forceinline__ void spread(float sum, float squares, int h, float inv, float eps, float& off, float& rstd, bool& far) {
+    off = sum / static_cast<float>(h);
+    float var = fmaf(-sum, off, squares) * inv;
+    var = var < 0.0f ? 0.0f : var;
+    rstd = rsqrtf(var + eps);
+    far = off * off > 0x1p-48f * var;  // m0 is off by more than a rounding of differences of the spread's size
+}
+// The mean: m0 itself where it is infinite.
+__device__ __forceinline__ float corrected(float m0, float off) { return isinf(m0) ? m0 : m0 + off; }
+
 struct FwdArgs {
     const void *x, *gamma, *beta;
     void* y;
@@ -121,22 +154,34 @@ struct FwdArgs {
     float eps;
 };
 
-// Row: blockDim.x threads; blockDim.y rows a CTA (more than one only with 32 threads a row).
+// Threads of a row.  Where a thread has many pieces each loop over them takes it anew, as far as the compiler can see: it would
+// hold the places of all pieces over the whole walk, and spill them (2000 fp32 rows of 8191 elements: 202 us, so 44).
+template <int NV>
+__device__ __forceinline__ int width() {
+    int nx = blockDim.x;
+    if constexpr (NV > 8) asm volatile("" : "+r"(nx));
+    return nx;
+}
+
+// Row: blockDim.x threads; blockDim.y rows a CTA (more than one only with 32 threads a row).  Two CTAs an SM where a thread has
+// many pieces (2000 bf16 rows of 8191: 50 us, 58 with one, whose threads have 94 registers).
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(most_threads(VEC * NV)) fwd_kernel(const FwdArgs p) {
+__global__ void __launch_bounds__(most_threads(VEC * NV), NV > 8 ? 2 : 0) fwd_kernel(const FwdArgs p) {
     using R = typename Raw<T, VEC>::type;
-    __shared__ float buf[2 * 32];
+    __shared__ float buf[2 * 32 * 2];  // (one value in turn 0, two in turn 1)
     int turn = 0;
     griddep_wait();
     if (threadIdx.x == 0 && threadIdx.y == 0) griddep_launch_dependents();
+    const int tx = threadIdx.x;
     const float inv = 1.0f / static_cast<float>(p.h);
     for (long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y; row < p.rows;
          row += static_cast<long long>(gridDim.x) * blockDim.y) {
         const R* x = reinterpret_cast<const R*>(static_cast<const T*>(p.x) + row * p.ldx);
         float v[NV][VEC], s[1] = {0.0f};
+        int nx = width<NV>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
+            const int c = i * nx + tx;
             if (c < p.vecs) {
                 widen<T, VEC>(x[c], v[i]);
             } else {
@@ -147,33 +192,44 @@ __global__ void __launch_bounds__(most_threads(VEC * NV)) fwd_kernel(const FwdAr
             for (int j = 0; j < VEC; ++j) s[0] += v[i][j];
         }
         row_sum<1>(s, buf, turn);
-        const float mean = s[0] * inv;
-        s[0] = 0.0f;
+        const float m0 = s[0] * inv;
+        float d[2] = {0.0f, 0.0f};
+        nx = width<NV>();
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x) < p.vecs)
+            if (i * nx + tx < p.vecs)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    const float d = v[i][j] - mean;
-                    s[0] = fmaf(d, d, s[0]);
+                    v[i][j] -= m0;
+                    d[0] += v[i][j];
+                    d[1] = fmaf(v[i][j], v[i][j], d[1]);
                 }
-        row_sum<1>(s, buf, turn);
-        const float rstd = rsqrtf(s[0] * inv + p.eps);
+        row_sum<2>(d, buf, turn);
+        float off, rstd;
+        bool far;
+        spread(d[0], d[1], p.h, inv, p.eps, off, rstd, far);
         if (threadIdx.x == 0 && p.mean != nullptr) {
-            p.mean[row] = mean;
+            p.mean[row] = corrected(m0, off);
             p.rstd[row] = rstd;
         }
+        if (far) {  // (the same in all of a row's threads; most rows' are not)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[i][j] -= off;
+        }
         R* y = reinterpret_cast<R*>(static_cast<T*>(p.y) + row * p.ldy);
+        nx = width<NV>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
+            const int c = i * nx + tx;
             if (c >= p.vecs) continue;
             float g[VEC], b[VEC], o[VEC];
             if (p.gamma != nullptr) widen<T, VEC>(static_cast<const R*>(p.gamma)[c], g);
             if (p.beta != nullptr) widen<T, VEC>(static_cast<const R*>(p.beta)[c], b);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float n = (v[i][j] - mean) * rstd;
+                const float n = v[i][j] * rstd;
                 o[j] = fmaf(n, p.gamma != nullptr ? g[j] : 1.0f, p.beta != nullptr ? b[j] : 0.0f);
             }
             y[c] = narrow<T, VEC>(o);
@@ -338,16 +394,11 @@ constexpr int MOST_SLOTS = 8;
 // sets of 16 x N floats, used in turn).
 template <int N>
 __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf, int& turn) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
+    warp_sums<N>(v);
     float* b = buf + turn * 16 * N;
     turn ^= 1;
     const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) b[i * 16 + (threadIdx.x >> 5)] = v[i];
+    if ((threadIdx.x & (N == 2 ? 15 : 31)) == 0) b[(threadIdx.x & 16) + (threadIdx.x >> 5)] = v[0];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -368,7 +419,7 @@ __device__ __forceinline__ void cta_sum(float (&v)[N], float* buf, int& turn) {
 
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 both(float v) { return tc::f2_pack(v, v); }
-// Sum of a pair's halves over N pairs.
+// Sum of a pair's halves.
 __device__ __forceinline__ float halves_sum(f2 v) {
     float a, b;
     tc::f2_unpack(v, a, b);
@@ -413,8 +464,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) fwd_ring_kernel(const FwdArgs
     constexpr int P = sizeof(T) == 2 ? 4 : 2;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint64_t bars[MOST_SLOTS];
-    __shared__ __align__(16) float buf[2 * 16];
-    if (threadIdx.x < 2 * 16) buf[threadIdx.x] = 0.0f;
+    __shared__ __align__(16) float buf[2 * 16 * 2];  // (one value in turn 0, two in turn 1)
+    if (threadIdx.x < 2 * 16 * 2) buf[threadIdx.x] = 0.0f;
     int turn = 0;
     const uint32_t bytes = static_cast<uint32_t>(p.h) * sizeof(T);
     Ring ring{smem, nullptr, bytes, slots};
@@ -456,8 +507,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) fwd_ring_kernel(const FwdArgs
         cta_sum<1>(s, buf, turn);
         load(row + static_cast<long long>(slots) * gridDim.x, ring.slot);  // (all threads have read the slot)
         ring.next();
-        const float mean = s[0] * inv;
-        const f2 less = both(-mean);
+        const float m0 = s[0] * inv;
+        f2 less = both(-m0), squares = 0;
         sum = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -465,15 +516,25 @@ __global__ void __launch_bounds__(THREADS, PER_SM) fwd_ring_kernel(const FwdArgs
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 v[i][j] = tc::f2_add(v[i][j], less);
-                sum = tc::f2_fma(v[i][j], v[i][j], sum);
+                sum = tc::f2_add(sum, v[i][j]);
+                squares = tc::f2_fma(v[i][j], v[i][j], squares);
             }
         }
-        s[0] = halves_sum(sum);
-        cta_sum<1>(s, buf, turn);
-        const float rstd = rsqrtf(s[0] * inv + p.eps);
+        float d[2] = {halves_sum(sum), halves_sum(squares)};
+        cta_sum<2>(d, buf, turn);
+        float off, rstd;
+        bool far;
+        spread(d[0], d[1], p.h, inv, p.eps, off, rstd, far);
         if (tx == 0 && p.mean != nullptr) {
-            p.mean[row] = mean;
+            p.mean[row] = corrected(m0, off);
             p.rstd[row] = rstd;
+        }
+        if (far) {  // (the same in all threads; most rows' are not)
+            less = both(-off);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[i][j] = tc::f2_add(v[i][j], less);
         }
         const f2 r2 = both(rstd);
         uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(p.y) + row * p.ldy);
@@ -702,7 +763,8 @@ bool wide_rows(int64_t h, int es, std::initializer_list<const void*> ptrs, std::
 
 // How the ring kernels run: threads of a CTA at most, elements of each, CTAs an SM in the forward and in the backward.  Few
 // threads with much to do: what a thread does once a row (waits, the sums across the CTA) is as much work as 10 elements.
-// 8192 x 5120 bf16, backward without dgamma, dbeta: 16 elements a thread 52 us, 32 45 (floor 37); forward 36, 29 (25).
+// 8192 x 5120 bf16, backward without dgamma, dbeta: 16 elements a thread 52 us, 32 45 (floor 37); forward 36, 29 (25; this and
+// the forward's figures below before its mean was corrected, which takes 2 to 9 % of the time).
 // Which CTAs fit an SM goes by registers, so each width has its own: 8192 x 4096 with CTAs of 160 threads at most, three and
 // two an SM, 25.6 and 43.6 us, of 128, four and three, 23.8 and 40.6; x 2048 with 128 21.2 and 32.7, of 96 17.6 and 30.1.
 // 4096 x 16384 47 and 82, by the kernels above 85 and 147.
