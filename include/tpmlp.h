@@ -541,9 +541,10 @@ tpmlp_status tpmlp_qkv_interleave(const void* W_qkv, void* W_out, int64_t rows, 
 int64_t tpmlp_qkv_src_col(int64_t dst_col, int64_t h, int64_t n_heads);
 
 /*
- * Synchronises `stream`, then reads and clears this device's status word.
- * TPMLP_OK, TPMLP_ERR_TIMEOUT (a device-side wait gave up), TPMLP_ERR_DEVICE (another
- * recorded device error) or TPMLP_ERR_CUDA.
+ * Synchronises `stream`, then reads and clears what this device's kernels have recorded.
+ * TPMLP_OK, TPMLP_ERR_TIMEOUT (a device-side wait gave up: outputs of calls since the last reading may be incomplete),
+ * TPMLP_ERR_DEVICE (an expert product's plan was cut; no other call is touched by it) or TPMLP_ERR_CUDA.  Where both were
+ * recorded the timeout is returned and tpmlp_last_error() names both.
  */
 tpmlp_status tpmlp_device_status(void* stream);
 

@@ -66,7 +66,7 @@ struct DeviceInfo {
     int device;
     int sm_count;
     int cc_major, cc_minor;
-    uint32_t* status;  // device address of this device's status word
+    uint32_t* status;  // device address of this device's status words (ptx.cuh)
 };
 
 // Per-device cached properties; nullptr (with last error set) on failure.

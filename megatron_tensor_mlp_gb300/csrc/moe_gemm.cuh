@@ -61,13 +61,17 @@ struct Args {
     unsigned long long timeout_ns;
 };
 
-// Bounded waits.  They go by their time limit alone: a status word that a bad plan has set does not end them.
+// Bounded waits.  They go by their time limit alone: a wait that gave up in another call does not end them.
 __device__ __forceinline__ bool wait(const Args& p, uint64_t* bar, uint32_t parity, uint32_t where) {
     return mbar_wait_bounded(bar, parity, p.status, p.timeout_ns, where, false);
 }
 __device__ __forceinline__ bool wait_warp(const Args& p, uint64_t* bar, uint32_t parity, uint32_t where) {
     return mbar_wait_bounded_warp(bar, parity, p.status, p.timeout_ns, where, false);
 }
+
+// A plan that reaches outside of its tensors is cut, and recorded in a word of its own: the first one ends the waits of other
+// GEMM kernels, whose calls have nothing to do with it.
+__device__ __forceinline__ void record_cut(const Args& p) { atomicExch(p.status + kPlanWord, kStatusDevice); }
 
 // Pieces of shared memory, one behind the other.
 struct Carve {
@@ -135,7 +139,7 @@ struct Table {
             }
             if (lane == 0) first[p.experts] = carry;
         }
-        if (bad && blockIdx.x == 0) atomicCAS(p.status, 0u, kStatusDevice);
+        if (bad && blockIdx.x == 0) record_cut(p);
         __syncthreads();
     }
 };
@@ -324,7 +328,7 @@ struct Halves {
 // A token read from src, cut to those that there are.
 __device__ __forceinline__ int checked(const Args& p, int v) {
     const int t = min(max(v, 0), p.tokens - 1);
-    if (v != t) atomicCAS(p.status, 0u, kStatusDevice);
+    if (v != t) record_cut(p);
     return t;
 }
 // Token of row r.
@@ -820,7 +824,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
             n[i] = there ? max(off[i + 1] - off[i], 0) : 0;
             mine += (n[i] + FEW_TN - 1) / FEW_TN * p.m_blocks;
         }
-        if (bad && blockIdx.x == 0) atomicCAS(p.status, 0u, kStatusDevice);
+        if (bad && blockIdx.x == 0) record_cut(p);
         int sum = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {

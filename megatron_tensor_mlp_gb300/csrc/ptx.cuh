@@ -7,7 +7,8 @@
 
 namespace tpmlp {
 
-// Device status word codes (see tpmlp_device_status).
+// Device status words and their codes (see tpmlp_device_status): word 0 of waits, kPlanWord of plans that were cut.
+constexpr int kStatusWords = 2, kPlanWord = 1;
 enum : uint32_t {
     kStatusTimeout = 0x10000u,  // | where
     kStatusDevice = 0x20000u,

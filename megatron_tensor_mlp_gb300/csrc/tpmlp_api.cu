@@ -15,8 +15,9 @@
 
 namespace tpmlp {
 
-// Device status word: written by kernels whose bounded waits give up.
-__device__ uint32_t g_status_word;
+// Device status words: the first is written by kernels whose bounded waits give up, and ends the waits of others; the second by
+// kernels that had to cut a plan, and ends nothing.
+__device__ uint32_t g_status_words[kStatusWords];
 
 namespace {
 thread_local char t_err[512] = "";
@@ -535,7 +536,7 @@ const DeviceInfo* device_info() {
         }
         if (d.cc_major == 10 && d.cc_minor == 3) {
             void* addr = nullptr;
-            if ((e = cudaGetSymbolAddress(&addr, g_status_word)) != cudaSuccess) {
+            if ((e = cudaGetSymbolAddress(&addr, g_status_words)) != cudaSuccess) {
                 set_error("cudaGetSymbolAddress(status word): %s", cudaGetErrorString(e));
                 return nullptr;
             }
@@ -981,22 +982,24 @@ tpmlp_status tpmlp_device_status(void* stream) {
         set_error("cudaStreamSynchronize: %s", cudaGetErrorString(e));
         return TPMLP_ERR_CUDA;
     }
-    uint32_t v = 0;
-    if ((e = cudaMemcpy(&v, dev->status, sizeof(v), cudaMemcpyDeviceToHost)) != cudaSuccess) {
-        set_error("reading the status word: %s", cudaGetErrorString(e));
+    uint32_t v[kStatusWords] = {};
+    if ((e = cudaMemcpy(v, dev->status, sizeof(v), cudaMemcpyDeviceToHost)) != cudaSuccess) {
+        set_error("reading the status words: %s", cudaGetErrorString(e));
         return TPMLP_ERR_CUDA;
     }
-    if (v == 0) return TPMLP_OK;
-    const uint32_t zero = 0;
-    if ((e = cudaMemcpy(dev->status, &zero, sizeof(zero), cudaMemcpyHostToDevice)) != cudaSuccess) {
-        set_error("clearing the status word: %s", cudaGetErrorString(e));
+    const uint32_t wait = v[0], plan = v[kPlanWord];
+    if (wait == 0 && plan == 0) return TPMLP_OK;
+    const uint32_t zeros[kStatusWords] = {};
+    if ((e = cudaMemcpy(dev->status, zeros, sizeof(zeros), cudaMemcpyHostToDevice)) != cudaSuccess) {
+        set_error("clearing the status words: %s", cudaGetErrorString(e));
         return TPMLP_ERR_CUDA;
     }
-    if (v & kStatusTimeout) {
-        set_error("a device-side wait gave up (where=%u)", v & 0xFFFFu);
+    const char* cut = "a plan reached outside of its tensors and was cut";
+    if (wait != 0) {
+        set_error("a device-side wait gave up (where=%u)%s%s", wait & 0xFFFFu, plan ? "; " : "", plan ? cut : "");
         return TPMLP_ERR_TIMEOUT;
     }
-    set_error("device status word 0x%x", v);
+    set_error("%s", cut);
     return TPMLP_ERR_DEVICE;
 }
 
