@@ -375,6 +375,7 @@ int tpmlp_get_mxfp4_mode(void);
  * Statistics in fp32; the error of Y goes by the differences from the mean, however large the mean is against them (a row of one
  * value gives beta; the saved mean is rounded to fp32).  h at most 16384.  Pointers and pitches need the alignment of their elements only; rows are
  * read 16 bytes at a time where all of h, the pitches and the addresses of X, Y, gamma and beta are multiples of 16 bytes.
+ * Tensors of one pitch may be columns of one larger tensor; of different pitches their address ranges must not meet.
  */
 tpmlp_status tpmlp_layernorm_fwd(const void* X, const void* gamma, const void* beta, void* Y, void* mean, void* rstd,
                                  int64_t rows, int64_t h, int64_t ldx, int64_t ldy, float eps, tpmlp_dtype dt, void* stream);

@@ -14,15 +14,21 @@ inline int esize(tpmlp_dtype dt) { return dt == TPMLP_F32 ? 4 : 2; }
 struct Range {
     const void* p;
     int64_t bytes;
+    int64_t row = 0, pitch = 0;  // rows of `row` bytes, `pitch` apart, of which the range is made (0: all of it)
 };
 
 inline bool overlap(const Range& a, const Range& b) {
     if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
     auto a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + static_cast<uintptr_t>(b.bytes) && b0 < a0 + static_cast<uintptr_t>(a.bytes);
+    if (a0 >= b0 + static_cast<uintptr_t>(b.bytes) || b0 >= a0 + static_cast<uintptr_t>(a.bytes)) return false;
+    if (a.pitch <= 0 || a.pitch != b.pitch) return true;
+    // rows of one pitch, columns of one tensor for instance: b's start behind the start of one of a's rows
+    const auto pitch = static_cast<uintptr_t>(a.pitch);
+    const auto behind = static_cast<int64_t>(b0 >= a0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch);
+    return behind < a.row || behind + b.row > a.pitch;
 }
 
-// Outputs must not overlap inputs or each other.
+// Outputs must not overlap inputs or each other.  (Between rows of a pitch another tensor of the same pitch may lie.)
 inline tpmlp_status check_alias(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
     int i = 0;
     for (const Range& o : outs) {

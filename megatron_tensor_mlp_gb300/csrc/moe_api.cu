@@ -67,7 +67,9 @@ tpmlp_status check_norm(int64_t rows, int64_t h, std::initializer_list<int64_t> 
     }
     return check_dtype(dt);
 }
-int64_t pitched(int64_t rows, int64_t h, int64_t ld, int es) { return rows == 0 ? 0 : ((rows - 1) * ld + h) * es; }
+Range pitched(const void* p, int64_t rows, int64_t h, int64_t ld, int es) {
+    return {p, rows == 0 ? 0 : ((rows - 1) * ld + h) * es, h * es, ld * es};
+}
 
 tpmlp_status check_choice(int64_t tokens, int64_t experts, int k) {
     if (tokens < 0 || experts < 1 || experts > kMaxExperts || k < 1 || k > kMaxChoice || k > experts) {
@@ -148,8 +150,8 @@ tpmlp_status tpmlp_layernorm_fwd(const void* X, const void* gamma, const void* b
     const int es = esize(dt);
     TP_TRY(check_elements({X, gamma, beta, Y}, es));
     TP_TRY(check_elements({mean, rstd}, 4));
-    TP_TRY(check_alias({{Y, pitched(rows, h, ldy, es)}, {mean, rows * 4}, {rstd, rows * 4}},
-                       {{X, pitched(rows, h, ldx, es)}, {gamma, h * es}, {beta, h * es}}));
+    TP_TRY(check_alias({pitched(Y, rows, h, ldy, es), {mean, rows * 4}, {rstd, rows * 4}},
+                       {pitched(X, rows, h, ldx, es), {gamma, h * es}, {beta, h * es}}));
     const DeviceInfo* dev;
     TP_TRY(get_device(&dev));
     if (rows == 0) return TPMLP_OK;
@@ -173,8 +175,8 @@ tpmlp_status tpmlp_layernorm_bwd(const void* X, const void* gamma, const void* m
     TP_TRY(check_elements({dgamma, dbeta}, gs));
     TP_TRY(check_elements({mean, rstd}, 4));
     TP_TRY(check_aligned({sums ? ws : nullptr}));
-    TP_TRY(check_alias({{dX, pitched(rows, h, lddx, es)}, {dgamma, h * gs}, {dbeta, h * gs}, {sums ? ws : nullptr, layernorm_ws_bytes(rows, h)}},
-                       {{X, pitched(rows, h, ldx, es)}, {gamma, h * es}, {mean, rows * 4}, {rstd, rows * 4}, {dY, pitched(rows, h, lddy, es)}}));
+    TP_TRY(check_alias({pitched(dX, rows, h, lddx, es), {dgamma, h * gs}, {dbeta, h * gs}, {sums ? ws : nullptr, layernorm_ws_bytes(rows, h)}},
+                       {pitched(X, rows, h, ldx, es), {gamma, h * es}, {mean, rows * 4}, {rstd, rows * 4}, pitched(dY, rows, h, lddy, es)}));
     const DeviceInfo* dev;
     TP_TRY(get_device(&dev));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
