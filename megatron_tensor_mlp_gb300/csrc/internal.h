@@ -171,7 +171,7 @@ struct MoeSpec {
 tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st);
 tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st);
 tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st);
-// Routing: top-k, weights and the plan of rows; workspace: MoeRouteWs (moe_route.cu).
+// Routing: top-k, weights and the plan of rows; workspace: counts, [chunks of tokens][experts, to a multiple of 4].
 int64_t moe_route_ws_bytes(int64_t tokens, int experts);
 tpmlp_status launch_moe_route(const void* logits, int* ids, float* weights, int* offsets, int* row_token, int* slot_row, void* ws,
                               int64_t tokens, int experts, int k, bool chosen, bool f32, cudaStream_t st);

@@ -30,7 +30,8 @@
 namespace tpmlp {
 namespace {
 
-// CTAs of the backward: two an SM, more where rows take few threads.
+// CTAs of the backward at most, whatever the device (the workspace is sized without one): two an SM of a GB300's 152, four where
+// rows take few threads.
 constexpr int most_parts(long long h) { return h <= 4096 ? 608 : 304; }
 constexpr int WARP_ROW = 1024;   // elements of a row that one warp takes
 // Threads of a CTA at most, by the elements that each holds.

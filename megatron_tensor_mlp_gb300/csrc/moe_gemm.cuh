@@ -331,8 +331,6 @@ __device__ __forceinline__ int checked(const Args& p, int v) {
     if (v != t) record_cut(p);
     return t;
 }
-// Token of row r.
-__device__ __forceinline__ int token_of(const Args& p, int r) { return checked(p, p.src[r]); }
 // Row numbers of a warp's copies: rows row0 + 8 j .. + 3, at most `last`.  (All loads before the first check, which waits.)
 template <int PER>
 __device__ __forceinline__ void gather_rows(const Args& p, int row0, int last, int copies, int4 (&at)[PER]) {

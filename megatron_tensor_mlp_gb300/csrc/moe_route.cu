@@ -463,6 +463,7 @@ tpmlp_status launch(void (*kern)(P...), dim3 grid, dim3 threads, cudaStream_t st
 // Chunks of tokens: a token a warp while they fit the SMs once, twice where tokens are many; each chunk sums the counts of all
 // others, so not more.  (2048 tokens, k 8 of 64 experts: 64 chunks 7.2 us, 128 6.1; 8192, k 8 of 256: 256 chunks 26.8, 152
 // 20.5; 65536, k 8 of 64: 152 chunks 52.9, 304 42.1.)  A single one, without the second kernel, for up to two a warp.
+// (152 SMs are a GB300's; the workspace is sized without a device.)
 int route_chunks(int64_t tokens) {
     if (tokens <= 2 * ROUTE_WARPS) return tokens > 0 ? 1 : 0;
     return static_cast<int>(std::min<int64_t>(tokens < 16384 ? 152 : 304, (tokens + ROUTE_WARPS - 1) / ROUTE_WARPS));
