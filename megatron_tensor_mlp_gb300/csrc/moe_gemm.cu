@@ -4,9 +4,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <mutex>
 
+#include "moe_choice.h"
 #include "moe_gemm.cuh"
 #include "per_device.h"
 
@@ -14,6 +14,8 @@ namespace tpmlp {
 namespace {
 
 using namespace moe;
+
+static_assert(Geom<STORE>::f == kFeatures && Geom<DSWIGLU>::f == kFeatures && Geom<SWIGLU>::f == kGatedFeatures && BK == kContraction);
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -138,41 +140,6 @@ tpmlp_status launch_rows(const CUtensorMap& w, const Boxes& x, const Args& a, co
     return launch(kern, dim3(2 * pairs), THREADS, G::smem, 2, st, w, x, a);
 }
 
-// Whether a product runs on the few-rows kernel.  The row ranges are on the device, so this goes by the tiles that the pairs
-// would have if the rows were spread over the experts: where they fill about half of the pairs, or, with at most 16 rows an
-// expert, up to four rounds of them (which do not come out even).  4 tokens, 8 of 64 experts, 1024 x 8192 gated (256 tiles):
-// 28.0 us, pairs 33.8; 4096 x 1024 (32 tiles): 14.6, 26.0; 128 rows on 8 experts of that size 16.6, 23.8; 666 rows (40 tiles)
-// 19.3, 24.7.  But 128 rows on 34 of 64 experts, gated (2112 tiles): 112, pairs 91; 1024 rows on 16 experts, 4096 x 1024 (80
-// tiles): 36.1, 27.4.  Gradients of the inputs: 30 rows on 8 experts, 3840 -> 624 (24 tiles) 11.5, 22.3; 1000 rows, 2048 -> 1024
-// (44 tiles) 17.1, 15.8.  Through the gated activation a thread handles a feature's pre-activations one by one, so for fewer
-// tiles: 8 rows, 5120 -> 4096 (128 tiles) 43, 61; 1400 rows, 1024 -> 512 (26 tiles) 14.7, 17.1; but 600 rows on 64 experts,
-// 1024 -> 1024 (264 tiles) 33, 27; 400 rows on 8 (36 tiles) 14.6, 13.5.
-bool few_rows(int64_t rows, int64_t experts, int64_t m_blocks, int pairs, bool gated_dx = false) {
-    const int64_t tiles = m_blocks * (std::min(rows, experts) + rows / 256);
-    if (gated_dx) return rows <= 8 * experts ? tiles <= 2 * pairs : 20 * tiles <= 8 * pairs;
-    return rows <= 16 * experts ? tiles <= 4 * pairs : 20 * tiles <= 11 * pairs;
-}
-
-// Whether tiles of twice the size keep the pairs as busy: they come in half as many rounds, or in so many that the last, partly
-// empty one weighs little.  (36 of them instead of 72, on 76 pairs: 1.6 times as long; 128 instead of 256: 0.95; 102 instead of
-// 204, two rounds for three: 1.16.)
-bool busy(double wide, double narrow, int pairs) {
-    const double w = std::ceil(wide / pairs), n = std::ceil(narrow / pairs);
-    return 2 * w <= n || w >= 3;
-}
-
-// Whether the rows kernel runs on wide tiles (a: as for narrow ones), if they keep the pairs busy.  For gathered rows, whose
-// copies they halve: 16384 rows on 8 experts, 5120 x 8192 735 us, narrow 811; 8192 rows on 64 experts, 1024 x 2048 gated 57, 79;
-// in 30 of 33 other cases 2-18 % less.  For rows in order where much is done for each byte, since a tile's epilogue is not
-// hidden: 6000 rows on 8 experts, 5120 x 8192 gated 314, 342, plain 287, 318, its gradient of the inputs 330, 362; but 16384
-// rows on 16 experts, 1024 x 4096 gated 102, 98, plain 103, 92, and 8192 rows on 8 experts, 2048 x 4096 gated 94, 97, plain 98, 95.
-bool wide_tiles(const Args& a, bool gated, int pairs) {
-    if (a.src == nullptr && a.kb < (gated ? 32 : 64)) return false;
-    // tiles of tokens: of one expert, or, as the ranges are on the device, with the last of each half full
-    const double t = a.experts == 1 ? (a.rows + 255) / 256 : a.rows / 256.0 + std::min(a.experts, a.rows) / 2.0;
-    return busy(t * ((a.m_blocks + 1) / 2), t * a.m_blocks, pairs);
-}
-
 template <bool W_MN, int MODE>
 tpmlp_status launch_few(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
     static PerDevice<bool> done;
@@ -261,14 +228,10 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     Args a = common(g, dev);
     a.kb = static_cast<int>((g.K + BK - 1) / BK);
     a.features = static_cast<int>(g.gated ? g.N / 2 : g.N);
+    const Kernel kernel = forward_kernel(g.rows, g.experts, g.K, g.N, g.gated, g.src != nullptr, dev.sm_count / 2);
+    const bool few = kernel == FEW, wide = kernel == WIDE;
     const int tile = g.gated ? Geom<SWIGLU>::f : Geom<STORE>::f;
-    a.m_blocks = (a.features + tile - 1) / tile;
-    const bool few = few_rows(g.rows, g.experts, a.m_blocks, dev.sm_count / 2);
-    const bool wide = !few && wide_tiles(a, g.gated, dev.sm_count / 2);
-    if (few || wide) {
-        const int t = few ? tile / 2 : tile * 2;
-        a.m_blocks = (a.features + t - 1) / t;
-    }
+    a.m_blocks = static_cast<int>(blocks(a.features, few ? tile / 2 : wide ? tile * 2 : tile));
     a.out = g.out;
     a.ld = a.features;
     a.out_f32 = g.out_f32;
@@ -292,7 +255,8 @@ tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaS
     Args a = common(g, dev);
     a.kb = static_cast<int>((g.N + BK - 1) / BK);
     a.features = static_cast<int>(g.K);
-    a.m_blocks = (a.features + 255) / 256;
+    const Kernel kernel = dx_kernel(g.rows, g.experts, g.K, g.N, g.gated, dev.sm_count / 2);
+    a.m_blocks = static_cast<int>(blocks(a.features, kernel == FEW ? BM : kernel == WIDE ? 512 : 256));
     a.out = g.out;
     a.ld = g.gated ? 2 * g.K : g.K;
     a.out_f32 = g.out_f32;
@@ -301,16 +265,9 @@ tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaS
     CUtensorMap w;
     Boxes x;
     if (!make_map(&w, g.w, g.N, g.K, g.experts, BM) || !make_boxes(&x, g.x, g.N, g.rows)) return TPMLP_ERR_CUDA;
-    if (few_rows(g.rows, g.experts, a.m_blocks, dev.sm_count / 2, g.gated)) {
-        a.m_blocks = (a.features + BM - 1) / BM;
-        return g.gated ? launch_few<false, DSWIGLU>(w, x, a, dev, st) : launch_few<false, STORE>(w, x, a, dev, st);
-    }
+    if (kernel == FEW) return g.gated ? launch_few<false, DSWIGLU>(w, x, a, dev, st) : launch_few<false, STORE>(w, x, a, dev, st);
     if (g.gated) return launch_rows<false, DSWIGLU>(w, x, a, dev, st);
-    if (wide_tiles(a, false, dev.sm_count / 2)) {
-        a.m_blocks = (a.features + 511) / 512;
-        return launch_rows<false, STORE, true>(w, x, a, dev, st);
-    }
-    return launch_rows<false, STORE>(w, x, a, dev, st);
+    return kernel == WIDE ? launch_rows<false, STORE, true>(w, x, a, dev, st) : launch_rows<false, STORE>(w, x, a, dev, st);
 }
 
 tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st) {
@@ -318,13 +275,8 @@ tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaS
     a.features = static_cast<int>(g.K);
     a.cols = static_cast<int>(g.N);
     a.m_blocks = (a.features + 255) / 256;
-    // Wide tiles for gathered rows (see wide_tiles; 16384 rows on 8 experts, 5120 x 8192: 793 us, narrow 1230) and where
-    // contractions are long (the same in order: 739, 804; 8192 rows on 16 experts, 4096 x 2048: 119, 116), if they keep the
-    // pairs busy.
-    const int narrow = (a.cols + 255) / 256, half = (a.cols + 511) / 512;
-    const bool wide = (g.src != nullptr || g.rows >= 1280 * int64_t(g.experts)) &&
-                      busy(1.0 * a.experts * a.m_blocks * half, 1.0 * a.experts * a.m_blocks * narrow, dev.sm_count / 2);
-    a.n_blocks = wide ? half : narrow;
+    const bool wide = dw_kernel(g.rows, g.experts, g.K, g.N, g.src != nullptr, dev.sm_count / 2) == WIDE;
+    a.n_blocks = static_cast<int>(blocks(a.cols, wide ? 512 : 256));
     a.out = g.out;
     a.ld = g.N;
     a.out_f32 = g.out_f32;
