@@ -87,8 +87,8 @@ typedef enum {
 
 typedef enum { TPMLP_BF16 = 0, TPMLP_F32 = 1 } tpmlp_dtype;
 
-/* TPMLP_ACT_SWIGLU: the products grouped by expert only. */
-typedef enum { TPMLP_ACT_NONE = 0, TPMLP_ACT_GELU_ERF = 1, TPMLP_ACT_SWIGLU = 2 } tpmlp_act;
+/* TPMLP_ACT_SWIGLU, _H32: the products grouped by expert only; their saved pre-activations are bf16, fp32. */
+typedef enum { TPMLP_ACT_NONE = 0, TPMLP_ACT_GELU_ERF = 1, TPMLP_ACT_SWIGLU = 2, TPMLP_ACT_SWIGLU_H32 = 3 } tpmlp_act;
 
 /*
  * Column-parallel layer for all p shards in one launch
@@ -435,6 +435,9 @@ tpmlp_status tpmlp_moe_route_bwd(const void* logits, const void* ids, const void
  *             TPMLP_ACT_SWIGLU: N = 2 f packed in blocks of 256 columns, 128 gate features and then their up features
  *             (tpmlp_swiglu_pack with p = 1), Y = silu(gate) up [rows][f] bf16, from fp32; H [rows][N] bf16, the packed
  *             pre-activations for the backward, or NULL.  f a multiple of 128.
+ *             TPMLP_ACT_SWIGLU_H32: the same with H [rows][N] fp32.  The backward multiplies by gate's and up's functions
+ *             themselves, so H in bf16, half the bytes, costs it digits: dX through both layers, rounded to bf16, is off by 3.0e-3
+ *             in the Frobenius norm (dW of the first layer 2.5e-3), with H in fp32 by 2.3e-3 (1.7e-3).
  * experts at most 1024; K and N multiples of 8.  row_token and offsets are read on the device.  Rows that no expert has
  * are left as they were.  Row ranges past `rows`, or tokens past `tokens`, are cut to what there is, and
  * tpmlp_device_status reports TPMLP_ERR_DEVICE.
@@ -448,6 +451,7 @@ tpmlp_status tpmlp_moe_matmul(const void* X, const void* row_token, const void* 
  *   act TPMLP_ACT_NONE:   dX[r] = dY[r] W[e]^T,  dX [rows][K] dx_dt, H NULL
  *   act TPMLP_ACT_SWIGLU: W is the layer behind the gated activation: with D = dY[r] W[e]^T (f = K values) and the packed
  *   pre-activations H [rows][2 K] bf16, dX [rows][2 K] bf16 is their packed gradient (D up silu'(gate), D silu(gate)).
+ *   act TPMLP_ACT_SWIGLU_H32: the same with H [rows][2 K] fp32.
  *   dY [rows][N] bf16, W [experts][K][N] bf16, offsets as above.
  * (For rows that were read through row_token, tpmlp_moe_combine without weights adds dX up into the tokens.)
  */

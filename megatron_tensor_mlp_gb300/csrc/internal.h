@@ -166,6 +166,7 @@ struct MoeSpec {
     bool out_f32;
     bool gated;        // the gated activation (forward) or its derivative (dx)
     void* h;           // packed pre-activations: forward saves them here (may be null), dx reads them
+    bool h_f32;        // they are fp32 (bf16 otherwise)
     void* dbias;       // dw: [experts][N], may be null
 };
 tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStream_t st);

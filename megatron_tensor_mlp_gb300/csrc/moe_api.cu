@@ -113,7 +113,7 @@ tpmlp_status check_experts(int64_t tokens, int64_t rows, int64_t experts, int64_
 }
 
 tpmlp_status check_act(tpmlp_act act) {
-    if (act != TPMLP_ACT_NONE && act != TPMLP_ACT_SWIGLU) {
+    if (act != TPMLP_ACT_NONE && act != TPMLP_ACT_SWIGLU && act != TPMLP_ACT_SWIGLU_H32) {
         set_error("activation %d: none or the gated one", (int)act);
         return TPMLP_ERR_SHAPE;
     }
@@ -237,7 +237,8 @@ tpmlp_status tpmlp_moe_route_bwd(const void* logits, const void* ids, const void
 tpmlp_status tpmlp_moe_matmul(const void* X, const void* row_token, const void* offsets, const void* W, const void* bias, void* Y, void* H,
                               int64_t tokens, int64_t rows, int64_t experts, int64_t K, int64_t N, tpmlp_act act, tpmlp_dtype out_dt,
                               void* stream) {
-    const bool some = rows > 0, gated = act == TPMLP_ACT_SWIGLU;
+    const bool some = rows > 0, h_f32 = act == TPMLP_ACT_SWIGLU_H32, gated = act == TPMLP_ACT_SWIGLU || h_f32;
+    const int hs = h_f32 ? 4 : 2;
     TP_TRY(need({{X, some}, {offsets, true}, {W, true}, {Y, some}}));
     TP_TRY(check_experts(tokens, rows, experts, K, N, row_token != nullptr));
     TP_TRY(check_act(act));
@@ -255,7 +256,7 @@ tpmlp_status tpmlp_moe_matmul(const void* X, const void* row_token, const void* 
     TP_TRY(check_elements({row_token, offsets}, 4));
     TP_TRY(check_pitch(K, TPMLP_BF16, "K"));
     TP_TRY(check_pitch(N, TPMLP_BF16, "N"));
-    TP_TRY(check_alias({{Y, rows * (gated ? N / 2 : N) * esize(out_dt)}, {H, rows * N * 2}},
+    TP_TRY(check_alias({{Y, rows * (gated ? N / 2 : N) * esize(out_dt)}, {H, rows * N * hs}},
                        {{X, tokens * K * 2}, {row_token, rows * 4}, {offsets, (experts + 1) * 4}, {W, experts * K * N * 2}, {bias, experts * N * 2}}));
     const DeviceInfo* dev;
     TP_TRY(get_device(&dev));
@@ -263,13 +264,14 @@ tpmlp_status tpmlp_moe_matmul(const void* X, const void* row_token, const void* 
     MoeSpec g{};
     g.rows = rows; g.tokens = tokens; g.K = K; g.N = N; g.experts = static_cast<int>(experts);
     g.offsets = static_cast<const int*>(offsets); g.src = static_cast<const int*>(row_token);
-    g.x = X; g.w = W; g.bias = bias; g.out = Y; g.out_f32 = out_dt == TPMLP_F32; g.gated = gated; g.h = H;
+    g.x = X; g.w = W; g.bias = bias; g.out = Y; g.out_f32 = out_dt == TPMLP_F32; g.gated = gated; g.h = H; g.h_f32 = h_f32;
     return launch_moe_matmul(g, *dev, static_cast<cudaStream_t>(stream));
 }
 
 tpmlp_status tpmlp_moe_matmul_dx(const void* dY, const void* offsets, const void* W, const void* H, void* dX, int64_t rows, int64_t experts,
                                  int64_t K, int64_t N, tpmlp_act act, tpmlp_dtype dx_dt, void* stream) {
-    const bool some = rows > 0, gated = act == TPMLP_ACT_SWIGLU;
+    const bool some = rows > 0, h_f32 = act == TPMLP_ACT_SWIGLU_H32, gated = act == TPMLP_ACT_SWIGLU || h_f32;
+    const int hs = h_f32 ? 4 : 2;
     TP_TRY(need({{dY, some}, {offsets, true}, {W, true}, {H, some && gated}, {dX, some}}));
     TP_TRY(check_experts(rows, rows, experts, K, N, false));
     TP_TRY(check_act(act));
@@ -291,14 +293,14 @@ tpmlp_status tpmlp_moe_matmul_dx(const void* dY, const void* offsets, const void
     TP_TRY(check_pitch(K, TPMLP_BF16, "K"));
     TP_TRY(check_pitch(N, TPMLP_BF16, "N"));
     TP_TRY(check_alias({{dX, rows * (gated ? 2 * K : K) * esize(dx_dt)}},
-                       {{dY, rows * N * 2}, {offsets, (experts + 1) * 4}, {W, experts * K * N * 2}, {H, gated ? rows * 2 * K * 2 : 0}}));
+                       {{dY, rows * N * 2}, {offsets, (experts + 1) * 4}, {W, experts * K * N * 2}, {H, gated ? rows * 2 * K * hs : 0}}));
     const DeviceInfo* dev;
     TP_TRY(get_device(&dev));
     if (rows == 0) return TPMLP_OK;
     MoeSpec g{};
     g.rows = rows; g.tokens = rows; g.K = K; g.N = N; g.experts = static_cast<int>(experts);
     g.offsets = static_cast<const int*>(offsets);
-    g.x = dY; g.w = W; g.out = dX; g.out_f32 = dx_dt == TPMLP_F32; g.gated = gated; g.h = const_cast<void*>(H);
+    g.x = dY; g.w = W; g.out = dX; g.out_f32 = dx_dt == TPMLP_F32; g.gated = gated; g.h = const_cast<void*>(H); g.h_f32 = h_f32;
     return launch_moe_matmul_dx(g, *dev, static_cast<cudaStream_t>(stream));
 }
 

@@ -129,21 +129,21 @@ tpmlp_status launch(Kern kern, dim3 grid, int threads, int smem, unsigned cluste
     return TPMLP_OK;
 }
 
-template <bool W_MN, int MODE, bool WIDE = false>
+template <bool W_MN, int MODE, bool WIDE = false, bool H32 = false>
 tpmlp_status launch_rows(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
     static PerDevice<bool> done;
     using G = Geom<MODE, WIDE>;
-    auto kern = rows_kernel<W_MN, MODE, WIDE>;
+    auto kern = rows_kernel<W_MN, MODE, WIDE, H32>;
     if (!set_smem(kern, dev.device, G::smem, done)) return TPMLP_ERR_CUDA;
     const int64_t most = int64_t(a.m_blocks) * (a.rows / G::tn + std::min(a.experts, a.rows));
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(most, dev.sm_count / 2));
     return launch(kern, dim3(2 * pairs), THREADS, G::smem, 2, st, w, x, a);
 }
 
-template <bool W_MN, int MODE>
+template <bool W_MN, int MODE, bool H32 = false>
 tpmlp_status launch_few(const CUtensorMap& w, const Boxes& x, const Args& a, const DeviceInfo& dev, cudaStream_t st) {
     static PerDevice<bool> done;
-    auto kern = few_kernel<W_MN, MODE>;
+    auto kern = few_kernel<W_MN, MODE, H32>;
     if (!set_smem(kern, dev.device, FEW_SMEM, done)) return TPMLP_ERR_CUDA;
     const int64_t tiles = int64_t(a.m_blocks) * (a.rows / FEW_TN + std::min(a.experts, a.rows));
     // the contraction is split while all CTAs, two an SM, run at once and each has at least four blocks of it
@@ -237,7 +237,7 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     a.out_f32 = g.out_f32;
     a.bias = static_cast<const __nv_bfloat16*>(g.bias);
     a.bias_ld = g.N;
-    a.h_out = static_cast<__nv_bfloat16*>(g.h);
+    a.h_out = g.h;
     a.h_ld = g.N;
     CUtensorMap w;
     Boxes x{};
@@ -246,6 +246,10 @@ tpmlp_status launch_moe_matmul(const MoeSpec& g, const DeviceInfo& dev, cudaStre
     a.chunked = chunks > 0 && g.N % 64 == 0;
     const bool mapped = a.chunked ? make_chunks(&w, g.w, g.N, g.K, g.experts, chunks) : make_map(&w, g.w, g.N, g.K, g.experts, BK);
     if (!mapped || !(g.src ? make_map(&x.m[0], g.x, g.K, g.tokens, 1, 1, 2) : make_boxes(&x, g.x, g.K, g.rows))) return TPMLP_ERR_CUDA;
+    if (g.gated && g.h && g.h_f32) {
+        if (few) return launch_few<true, SWIGLU, true>(w, x, a, dev, st);
+        return wide ? launch_rows<true, SWIGLU, true, true>(w, x, a, dev, st) : launch_rows<true, SWIGLU, false, true>(w, x, a, dev, st);
+    }
     if (few) return g.gated ? launch_few<true, SWIGLU>(w, x, a, dev, st) : launch_few<true, STORE>(w, x, a, dev, st);
     if (wide) return g.gated ? launch_rows<true, SWIGLU, true>(w, x, a, dev, st) : launch_rows<true, STORE, true>(w, x, a, dev, st);
     return g.gated ? launch_rows<true, SWIGLU>(w, x, a, dev, st) : launch_rows<true, STORE>(w, x, a, dev, st);
@@ -260,11 +264,13 @@ tpmlp_status launch_moe_matmul_dx(const MoeSpec& g, const DeviceInfo& dev, cudaS
     a.out = g.out;
     a.ld = g.gated ? 2 * g.K : g.K;
     a.out_f32 = g.out_f32;
-    a.h_in = static_cast<const __nv_bfloat16*>(g.h);
+    a.h_in = g.h;
     a.h_ld = 2 * g.K;
     CUtensorMap w;
     Boxes x;
     if (!make_map(&w, g.w, g.N, g.K, g.experts, BM) || !make_boxes(&x, g.x, g.N, g.rows)) return TPMLP_ERR_CUDA;
+    if (g.gated && g.h_f32)
+        return kernel == FEW ? launch_few<false, DSWIGLU, true>(w, x, a, dev, st) : launch_rows<false, DSWIGLU, false, true>(w, x, a, dev, st);
     if (kernel == FEW) return g.gated ? launch_few<false, DSWIGLU>(w, x, a, dev, st) : launch_few<false, STORE>(w, x, a, dev, st);
     if (g.gated) return launch_rows<false, DSWIGLU>(w, x, a, dev, st);
     return kernel == WIDE ? launch_rows<false, STORE, true>(w, x, a, dev, st) : launch_rows<false, STORE>(w, x, a, dev, st);

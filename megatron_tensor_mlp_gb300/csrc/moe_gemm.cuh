@@ -17,6 +17,8 @@
 // accumulators of 128 tokens on the same lanes need no exchange, but MMAs of 128 columns: their operands take all of the
 // shared memory's 128 bytes a cycle, and 16384 rows x 5120 x 8192 took 1011 us in order.)
 #pragma once
+#include <type_traits>
+
 #include "gemm_tc.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -54,8 +56,8 @@ struct Args {
     int out_f32;
     const __nv_bfloat16* bias;      // [experts][bias_ld], packed for SWIGLU
     long long bias_ld;
-    __nv_bfloat16* h_out;           // SWIGLU: packed pre-activations, may be null; DSWIGLU reads h_in
-    const __nv_bfloat16* h_in;
+    void* h_out;                    // SWIGLU: packed pre-activations (fp32 with H32), may be null; DSWIGLU reads h_in
+    const void* h_in;
     long long h_ld;
     uint32_t* status;
     unsigned long long timeout_ns;
@@ -364,11 +366,53 @@ __device__ __forceinline__ void gather_some(int n, uint32_t dst, const CUtensorM
     }
 }
 
-template <bool W_MN, int MODE, bool WIDE = false>
+// Pre-activations in fp32 (H32): a lane has a feature and goes from token to token, 128 bytes of a warp in each row.  Gate and up
+// rounded to bf16 each cost the gradients a rounding of their own (dX through both layers 3.0e-3 off, from fp32 2.3e-3), twice
+// the bytes time: 16384 rows on 8 experts, 5120 x 8192 gated and saved 754-774 us, in fp32 793-857; 8192 rows on 64 experts,
+// 1024 x 2048 68, 74, gradient of 1024 features 45, 58.
+template <bool H32>
+using PreAct = typename std::conditional<H32, float, __nv_bfloat16>::type;
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void store_as(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// 32 lanes x 32 columns of an accumulator and the lane's bias to n rows.
+__device__ __forceinline__ void store_rows_f32(uint32_t taddr, float bias, float* dst, long long ld, int n) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j < n) dst[j * ld] = __uint_as_float(r[j]) + bias;
+}
+// Gate and up of this lane's feature for 16 rows, n of which there are.
+__device__ __forceinline__ void load_rows_f32(const float* h, long long ld, int n, float (&g)[16], float (&u)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        g[j] = j < n ? h[j * ld] : 0.0f;
+        u[j] = j < n ? h[j * ld + 128] : 0.0f;
+    }
+}
+// Their gradients from 16 columns of the accumulator.
+template <int FIRST>
+__device__ __forceinline__ void gated_rows(const uint32_t (&d)[32], const float (&g)[16], const float (&u)[16], __nv_bfloat16* dst, long long ld, int n) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float dg, du;
+        gated_gradient(__uint_as_float(d[FIRST + j]), g[j], u[j], dg, du);
+        if (j < n) {
+            dst[j * ld] = __float2bfloat16_rn(dg);
+            dst[j * ld + 128] = __float2bfloat16_rn(du);
+        }
+    }
+}
+
+template <bool W_MN, int MODE, bool WIDE = false, bool H32 = false>
 __global__ void __launch_bounds__(THREADS, 1)
     rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Boxes tmX, const Args p) {
     using G = Geom<MODE, WIDE>;
     static_assert(MODE != DSWIGLU || !WIDE);
+    static_assert(MODE != STORE || !H32);
     constexpr int S = G::stages, TN = G::tn;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -584,15 +628,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int acc = WIDE ? 0 : lt & 1;
             // the saved pre-activations of 32 tokens are loaded a step ahead, the first ones while the products are computed
             [[maybe_unused]] uint4 g4[4], u4[4];
+            [[maybe_unused]] float hg[2][16], hu[2][16];
+            [[maybe_unused]] auto ahead16 = [&](int c0, float (&g)[16], float (&u)[16]) {  // (H32: of 16 tokens)
+                const int f0 = c.mb * 256 + static_cast<int>(prank) * BM + q * 32;
+                const bool in = c0 < (half + 1) * (TN / 2) && f0 < p.features;
+                load_rows_f32(static_cast<const float*>(p.h_in) + (c.row0 + c0) * p.h_ld + static_cast<long long>(f0 >> 7) * 256 + (f0 & 127) + lane,
+                              p.h_ld, in ? c.n - c0 : 0, g, u);
+            };
             [[maybe_unused]] auto ahead = [&](int c0) {
                 const int f0 = c.mb * 256 + static_cast<int>(prank) * BM + q * 32, n = min(c.n - c0, 32);
-                const __nv_bfloat16* h = p.h_in + (c.row0 + c0) * p.h_ld + static_cast<long long>(f0 >> 7) * 256 + (f0 & 127);
+                const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(p.h_in) + (c.row0 + c0) * p.h_ld + static_cast<long long>(f0 >> 7) * 256 + (f0 & 127);
                 if (c0 < (half + 1) * (TN / 2)) {
                     rows_load(h, p.h_ld, n, p.features - f0, lane, g4);
                     rows_load(h + 128, p.h_ld, n, p.features - f0, lane, u4);
                 }
             };
-            if constexpr (MODE == DSWIGLU) ahead(half * (TN / 2));
+            if constexpr (MODE == DSWIGLU && H32) {
+                ahead16(half * (TN / 2), hg[0], hu[0]);
+                ahead16(half * (TN / 2) + 16, hg[1], hu[1]);
+            } else if constexpr (MODE == DSWIGLU) {
+                ahead(half * (TN / 2));
+            }
             int okw = 0;
             if (lane == 0) okw = wait(p, tfull + acc, WIDE ? lt & 1 : (lt >> 1) & 1, kWhereEpilogue);
             okw = __shfl_sync(0xFFFFFFFFu, okw, 0);
@@ -606,9 +662,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int nf = min(p.features - f0, 32);
             const uint32_t lanes = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc + part) * 256;
             const long long packed = static_cast<long long>(f0 >> 7) * 256 + (f0 & 127) + (MODE == SWIGLU && !WIDE ? (q >> 1) * 128 : 0);
-            [[maybe_unused]] float bias[4], bias_up[4];
+            [[maybe_unused]] float bias[4], bias_up[4], own = 0.0f, own_up = 0.0f;  // (H32: of this lane's feature)
             if constexpr (MODE != DSWIGLU) {
                 const __nv_bfloat16* at = p.bias == nullptr ? nullptr : p.bias + c.e * p.bias_ld + (MODE == SWIGLU ? packed : f0);
+                if constexpr (H32)
+                    if (at != nullptr && lane < nf) {
+                        own = __bfloat162float(at[lane]);
+                        if (WIDE) own_up = __bfloat162float(at[128 + lane]);
+                    }
                 load_bias(at, nf, lane, bias);
                 if constexpr (MODE == SWIGLU && WIDE) load_bias(at == nullptr ? nullptr : at + 128, nf, lane, bias_up);
             }
@@ -627,6 +688,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                             if (j < n && lane < nf) dst[j * p.ld] = __uint_as_float(r[j]) + b;
                         continue;
                     }
+                }
+                if constexpr (MODE == SWIGLU && H32) {
+                    float* h = static_cast<float*>(p.h_out) + row * p.h_ld + packed + lane;
+                    store_rows_f32(lanes + c0, own, h, p.h_ld, n);
+                    if constexpr (WIDE) store_rows_f32(lanes + 256 + c0, own_up, h + 128, p.h_ld, n);
+                }
+                if constexpr (MODE == DSWIGLU && H32) {
+                    uint32_t d[32];
+                    tmem_ld_32x32b_x32(lanes + c0, d);
+                    tmem_ld_wait();
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + row * p.ld + packed + lane;
+                    gated_rows<0>(d, hg[0], hu[0], dst, p.ld, n);
+                    ahead16(c0 + 32, hg[0], hu[0]);
+                    gated_rows<16>(d, hg[1], hu[1], dst + 16 * p.ld, p.ld, n - 16);
+                    ahead16(c0 + 48, hg[1], hu[1]);
+                    continue;
                 }
                 uint32_t a[16], b[16], lo[8], hi[8];
                 load_frags(lanes + c0, a, b);
@@ -651,8 +728,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ua[i] = __float_as_uint(__uint_as_float(ua[i]) + bias_up[j]);
                         ub[i] = __float_as_uint(__uint_as_float(ub[i]) + bias_up[2 + j]);
                     }
-                    if (p.h_out != nullptr) {
-                        __nv_bfloat16* h = p.h_out + row * p.h_ld + packed;
+                    if (!H32 && p.h_out != nullptr) {
+                        __nv_bfloat16* h = static_cast<__nv_bfloat16*>(p.h_out) + row * p.h_ld + packed;
                         pack_frags(a, b, lo, hi);
                         put_rows(buf, h, p.h_ld, lo, hi, n, nf, lane);
                         pack_frags(ua, ub, lo, hi);
@@ -689,9 +766,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                     pair_sync(1 + pair);  // read: the next ones may be written
-                    if (p.h_out != nullptr) {
+                    if (!H32 && p.h_out != nullptr) {
                         pack_frags(a, b, lo, hi);
-                        put_rows(buf, p.h_out + row * p.h_ld + packed, p.h_ld, lo, hi, n, nf, lane);
+                        put_rows(buf, static_cast<__nv_bfloat16*>(p.h_out) + row * p.h_ld + packed, p.h_ld, lo, hi, n, nf, lane);
                     }
                     if (q < 2) {
                         gate_frags(a, b, ua, ub, lo, hi);
@@ -758,12 +835,13 @@ constexpr int FEW_SUMS = 8 * 4096;  // partial sums on their way: 8 (rank, group
 constexpr int FEW_SMEM = 1024 + FEW_STAGES * FEW_STAGE + (2 * FEW_STAGES + 2) * 8 + 64;
 static_assert(FEW_TN >= 32 && FEW_SUMS <= FEW_STAGES * FEW_STAGE && 2 * (FEW_SMEM + 1024) <= 227 * 1024, "few kernel shared memory");
 
-template <bool W_MN, int MODE>
+template <bool W_MN, int MODE, bool H32 = false>
 __global__ void __launch_bounds__(FEW_THREADS, 2)
     few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Boxes tmX, const Args p) {
     constexpr int S = FEW_STAGES;
     constexpr bool GATED = MODE == SWIGLU;
     static_assert(MODE == STORE || W_MN == GATED);
+    using HT = PreAct<H32>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
@@ -867,9 +945,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const bool in = g * 8 + j < c.n && f < p.features;
-            const __nv_bfloat16* h = p.h_in + (c.row0 + g * 8 + j) * p.h_ld + packed;
-            hg[j] = in ? __bfloat162float(h[0]) : 0.0f;
-            hu[j] = in ? __bfloat162float(h[128]) : 0.0f;
+            const HT* h = static_cast<const HT*>(p.h_in) + (c.row0 + g * 8 + j) * p.h_ld + packed;
+            hg[j] = in ? as_f32(h[0]) : 0.0f;
+            hu[j] = in ? as_f32(h[128]) : 0.0f;
         }
     };
     if constexpr (MODE == DSWIGLU)
@@ -1021,8 +1099,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 2)
                 } else if constexpr (GATED) {
                     const float up = u[j] + bias_up;
                     if (p.h_out != nullptr) {
-                        p.h_out[(row + j) * p.h_ld + col] = __float2bfloat16_rn(x);
-                        p.h_out[(row + j) * p.h_ld + col + 128] = __float2bfloat16_rn(up);
+                        HT* h = static_cast<HT*>(p.h_out) + (row + j) * p.h_ld + col;
+                        store_as(h, x);
+                        store_as(h + 128, up);
                     }
                     static_cast<__nv_bfloat16*>(p.out)[(row + j) * p.ld + f] = __float2bfloat16_rn(x * tc::sigmoid_approx(x) * up);
                 } else if (p.out_f32) {

@@ -60,7 +60,7 @@ class ExpertLayer:
         logits, ids, w = self._new(t, e), self._new(t, k, dtype=I32), self._new(t, k, dtype=F32)
         offsets, row_token, slot_row = self._new(e + 1, dtype=I32), self._new(t * k, dtype=I32), self._new(t, k, dtype=I32)
         Z, Y, O = self._new(t, h), self._new(t * k, f), self._new(t * k, h)  # noqa: E741
-        H = self._new(t * k, 2 * f) if save else None
+        H = self._new(t * k, 2 * f, dtype=F32) if save else None
         out = (Z, (X, n, mean, rstd, logits, ids, w, offsets, row_token, slot_row, Y, O, H)) if save else Z
         if t == 0:  # (an empty tensor has no address to pass)
             return out
@@ -69,7 +69,7 @@ class ExpertLayer:
             T.tpmlp_layernorm_fwd(X, self.gamma, self.beta, n, mean, rstd, t, h, h, h)
             T.tpmlp_column_fwd(n, self.router, None, logits, None, t, 1, h, e, 1, act=T.ACT_NONE)
             T.tpmlp_moe_route(logits, ids, w, offsets, row_token, slot_row, ws, t, e, k)
-            T.tpmlp_moe_matmul(n, row_token, offsets, self.W1, None, Y, H, t, t * k, e, h, 2 * f, act=T.ACT_SWIGLU)
+            T.tpmlp_moe_matmul(n, row_token, offsets, self.W1, None, Y, H, t, t * k, e, h, 2 * f, act=T.ACT_SWIGLU_H32)
             T.tpmlp_moe_matmul(Y, None, offsets, self.W2, None, O, None, t * k, t * k, e, f, h)
             T.tpmlp_moe_combine(O, slot_row, w, Z, t, t * k, k, h)
         return out
@@ -91,7 +91,7 @@ class ExpertLayer:
         ws = self._new(T.tpmlp_layernorm_ws_bytes(t, h), dtype=torch.uint8)
         with torch.cuda.device(self.device):
             T.tpmlp_moe_combine_bwd(O, slot_row, w, dZ, dO, dw, t, r, k, h)
-            T.tpmlp_moe_matmul_dx(dO, offsets, self.W2, H, dH, r, e, f, h, act=T.ACT_SWIGLU)
+            T.tpmlp_moe_matmul_dx(dO, offsets, self.W2, H, dH, r, e, f, h, act=T.ACT_SWIGLU_H32)
             T.tpmlp_moe_matmul_dw(Y, None, offsets, dO, dW2, None, r, r, e, f, h)
             T.tpmlp_moe_matmul_dx(dH, offsets, self.W1, None, dR, r, e, h, 2 * f)
             T.tpmlp_moe_matmul_dw(n, row_token, offsets, dH, dW1, None, t, r, e, h, 2 * f)

@@ -22,7 +22,7 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 BF16, F32 = 0, 1
-ACT_NONE, ACT_GELU_ERF, ACT_SWIGLU = 0, 1, 2
+ACT_NONE, ACT_GELU_ERF, ACT_SWIGLU, ACT_SWIGLU_H32 = 0, 1, 2, 3
 
 STATUS = {0: "TPMLP_OK", 1: "TPMLP_ERR_NULL", 2: "TPMLP_ERR_SHAPE", 3: "TPMLP_ERR_DIVISIBILITY",
           4: "TPMLP_ERR_DTYPE", 5: "TPMLP_ERR_ALIGNMENT", 6: "TPMLP_ERR_ALIAS", 7: "TPMLP_ERR_ARCH",
@@ -319,7 +319,7 @@ def tpmlp_moe_route_bwd(logits, ids, weights, dweights, dlogits, tokens, experts
 
 def tpmlp_moe_matmul(X, row_token, offsets, W, bias, Y, H, tokens, rows, experts, K, N, act=ACT_NONE, out_dt=BF16, stream=None,
                      check=True):
-    """Y[r] = act(X[row_token[r]] W[e] + bias[e]) for the rows r of each expert e."""
+    """Y[r] = act(X[row_token[r]] W[e] + bias[e]) for the rows r of each expert e; H: bf16 with ACT_SWIGLU, fp32 with ACT_SWIGLU_H32."""
     st = lib.tpmlp_moe_matmul(_ptr(X), _ptr(row_token), _ptr(offsets), _ptr(W), _ptr(bias), _ptr(Y), _ptr(H), tokens, rows, experts, K,
                               N, act, out_dt, _stream(stream))
     return _done(st, check)
