@@ -293,8 +293,16 @@ tpmlp_status launch_moe_matmul_dw(const MoeSpec& g, const DeviceInfo& dev, cudaS
         return TPMLP_ERR_CUDA;
     const int64_t tiles = int64_t(a.experts) * a.m_blocks * a.n_blocks;
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles, dev.sm_count / 2));
-    const tpmlp_status st1 = wide ? launch_dw<true>(x, y, o, a, pairs, dev, st) : launch_dw<false>(x, y, o, a, pairs, dev, st);
-    if (st1 != TPMLP_OK || g.dbias == nullptr) return st1;
+    // (an expert may have all rows: as many launches as those take, the later ones short where it has not)
+    const int64_t chunk = g.out_f32 ? int64_t(get_k_chunk_blocks()) * BK : g.rows;
+    for (int64_t r = 0; r < g.rows; r += chunk) {
+        a.skip = static_cast<int>(r);
+        a.most = static_cast<int>(std::min(chunk, g.rows - r));
+        a.add = r > 0;
+        const tpmlp_status s = wide ? launch_dw<true>(x, y, o, a, pairs, dev, st) : launch_dw<false>(x, y, o, a, pairs, dev, st);
+        if (s != TPMLP_OK) return s;
+    }
+    if (g.dbias == nullptr) return TPMLP_OK;
     return launch(sums_kernel, dim3(static_cast<unsigned>((g.N + 63) / 64), static_cast<unsigned>(g.experts)), SUM_THREADS, 0, 1, st,
                   static_cast<const __nv_bfloat16*>(g.dy), g.offsets, a.rows, a.cols, g.dbias, a.out_f32);
 }

@@ -50,6 +50,8 @@ struct Args {
     int features;        // rows kernel: features on the tile's rows (SWIGLU, DSWIGLU: gate features); dw: K
     int cols;            // dw: N
     const __nv_bfloat16* dy;  // dw: dY [rows][cols]
+    int skip, most;      // dw: each expert's rows past its first `skip`, at most `most` of them
+    int add;             // dw: to the (fp32) output
     int m_blocks;        // rows kernel: blocks of 256 features; dw: of K
     int n_blocks;        // dw: blocks of 256 of N
     void* out; long long ld;        // row pitch of out (elements)
@@ -1137,6 +1139,10 @@ struct Lane {
     }
 };
 // WIDE: two accumulators, 512 columns of dY, for gathered rows, as in the rows kernel.
+//
+// The tensor cores' additions drop what lies below the running sum's last places, always towards zero: an error that grows
+// with the steps (700000 rows of terms of one sign: 4.6e-3 of the sum).  fp32 gradients are therefore computed a chunk of each
+// expert's rows to a launch (262144, as in the dense weight gradients), the later ones added to the output, rounded to nearest.
 constexpr int DW_A = BM * 128;
 constexpr int TAIL_WARP = EPI_WARP + EPI_WARPS, TAIL_WARPS = 2;  // and a warp behind them that reports
 constexpr int DW_THREADS = THREADS + 32 * (TAIL_WARPS + 1);
@@ -1155,7 +1161,8 @@ struct DwGeom {
 // 64 bytes of each of a warp's 32 rows through its box of shared memory to the output: a store of its own per lane would
 // touch 32 rows an instruction.  (8192 rows on 64 experts, 1024 x 2048, whose contractions are short: 84 us
 // so, 80 through the boxes; gathered 129 and 108.)
-__device__ __forceinline__ void put_box(uint8_t* box, const CUtensorMap* map, const uint32_t (&w)[32], int x, int y, int z, int lane) {
+__device__ __forceinline__ void put_box(uint8_t* box, const CUtensorMap* map, const uint32_t (&w)[32], int x, int y, int z, int lane,
+                                        bool add) {
     if (lane == 0) bulk_wait_group_read<0>();  // the box has been read
     __syncwarp();
 #pragma unroll
@@ -1164,7 +1171,8 @@ __device__ __forceinline__ void put_box(uint8_t* box, const CUtensorMap* map, co
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-        tma_store_3d(map, box, x, y, z);
+        if (add) tma_add_f32_3d(map, box, x, y, z);
+        else tma_store_3d(map, box, x, y, z);
         bulk_commit_group();
     }
 }
@@ -1230,6 +1238,9 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
     tab.build<DW_THREADS, true>(p, [&](int) { return p.m_blocks * p.n_blocks; }, [](int n) { return n; });
     const int n_tiles = tab.first[p.experts];  // every expert has its tiles, one without rows to write zeros
     const int per_expert = p.m_blocks * p.n_blocks;
+    // an expert's rows of this launch
+    auto rows_of = [&](int e) { return min(max(tab.count(e) - p.skip, 0), p.most); };
+    auto first_of = [&](int e) { return rows_of(e) > 0 ? tab.off[e] + p.skip : 0; };
     // tile t: expert, block of K, block of N; groups of GROUP blocks of K walked together
     auto place = [&](int t, int& e, int& mb, int& nb) {
         const int i = t / per_expert, l = t - i * per_expert, per_group = GROUP * p.n_blocks;
@@ -1248,7 +1259,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
             int e, mb, nb;
             place(t, e, mb, nb);
-            const int n = tab.count(e), base = tab.off[e], kb = (n + BK - 1) / BK;
+            const int n = rows_of(e), base = first_of(e), kb = (n + BK - 1) / BK;
             const int a0 = mb * 256 + static_cast<int>(prank) * BM, b0 = nb * G::n + static_cast<int>(prank) * BM;
             for (int it = 0; it < kb; ++it) {
                 const bool tail = (it + 1) * BK > n;
@@ -1307,7 +1318,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                 for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
                     int e, mb, nb;
                     place(t, e, mb, nb);
-                    const int n = tab.count(e), kb = (n + BK - 1) / BK;
+                    const int n = rows_of(e), kb = (n + BK - 1) / BK;
                     if (kb == 0) continue;
                     const int acc = WIDE ? 0 : lt & 1;
                     const uint32_t turn = (WIDE ? lt & 1 : (lt >> 1) & 1) ^ 1u;
@@ -1387,7 +1398,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
             for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
                 int e, mb, nb;
                 place(t, e, mb, nb);
-                const int n = tab.count(e), base = tab.off[e], whole = n / BK, a0 = mb * 256 + static_cast<int>(prank) * BM;
+                const int n = rows_of(e), base = first_of(e), whole = n / BK, a0 = mb * 256 + static_cast<int>(prank) * BM;
                 int2 next = make_int2(0, 0);
                 auto look = [&](int it) {  // two tokens of block it, ahead of their use (and of their check, which waits for them)
                     if (it < whole) next = make_int2(p.src[base + it * BK + lane * 2], p.src[base + it * BK + lane * 2 + 1]);
@@ -1440,7 +1451,7 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles && ok; ++i) {
             int e, mb, nb;
             place(t, e, mb, nb);
-            const int n = tab.count(e), base = tab.off[e], whole = n / BK;
+            const int n = rows_of(e), base = first_of(e), whole = n / BK;
             stage = (stage + whole) % S;
             if (whole * BK == n) continue;
             if (warp == TAIL_WARP + TAIL_WARPS) {
@@ -1496,7 +1507,8 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
         for (int i = 0, t; (t = round_tile<true>(i, cluster_id, n_clusters)) < n_tiles; ++i) {
             int e, mb, nb;
             place(t, e, mb, nb);
-            const bool none = tab.count(e) == 0;
+            const bool none = rows_of(e) == 0;
+            if (none && p.add) continue;
             const int acc = WIDE ? 0 : lt & 1;
             if (!none) {
                 int okw = 0;
@@ -1520,16 +1532,16 @@ __global__ void __launch_bounds__(DW_THREADS, 1)
                         tmem_ld_wait();
                     }
                     if (p.out_f32) {  // 16 columns at a time
-                        put_box(box, &tmO, r, col, k0, e, lane);
+                        put_box(box, &tmO, r, col, k0, e, lane, p.add);
                         if (col + 16 < p.cols) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) r[j] = r[16 + j];
-                            put_box(box, &tmO, r, col + 16, k0, e, lane);
+                            put_box(box, &tmO, r, col + 16, k0, e, lane, p.add);
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) r[j] = tc::pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                        put_box(box, &tmO, r, col, k0, e, lane);
+                        put_box(box, &tmO, r, col, k0, e, lane, p.add);
                     }
                 }
                 if (none) continue;
