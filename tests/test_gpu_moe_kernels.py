@@ -133,3 +133,56 @@ def test_a_layer_of_many_small_experts(T):
     ref, size = R.combine(o, sr, w)
     R.close(z, ref, k * 2.0**-23 * size, "Z")
     assert (z[::50] == 0).all()
+
+
+@pytest.mark.parametrize("case", C.CASES, ids=C.name)
+def test_kernel_without_rows_and_with_rows_of_nobody_ahead(T, case):
+    """Plans that leave every expert empty, at either end of the rows: outputs stay as they were, weight gradients are zero.
+    And one whose first range starts behind rows that no expert has."""
+    op, _, counts, behind, K, N, gathered = case
+    e, rows = len(counts), sum(counts) + behind
+    long = N if "dx" in op else K
+    tokens = max(rows // 2, 1) if gathered else rows
+    x = rnd(tokens, long, seed=1)
+    src = torch.arange(rows, dtype=I32, device="cuda") % tokens if gathered else None
+    w = None if op == "dw" else rnd(e, K, N, seed=3, scale=long**-0.5)
+    other = rnd(rows, 2 * K if op == "gated dx" else N, seed=5)  # H, dY
+
+    def call(off):
+        new = lambda *s, dtype=BF: torch.full(s, 7.0, dtype=dtype, device="cuda")  # noqa: E731
+        if op == "forward":
+            out = [new(rows, N)]
+            T.tpmlp_moe_matmul(x, src, off, w, None, *out, None, tokens, rows, e, K, N)
+        elif op == "gated":
+            out = [new(rows, N // 2), new(rows, N)]
+            T.tpmlp_moe_matmul(x, src, off, w, None, *out, tokens, rows, e, K, N, act=T.ACT_SWIGLU)
+        elif op == "dx":
+            out = [new(rows, K)]
+            T.tpmlp_moe_matmul_dx(x, off, w, None, *out, rows, e, K, N)
+        elif op == "gated dx":
+            out = [new(rows, 2 * K)]
+            T.tpmlp_moe_matmul_dx(x, off, w, other, *out, rows, e, K, N, act=T.ACT_SWIGLU)
+        else:
+            out = [new(e, K, N, dtype=F32), new(e, N, dtype=F32)]
+            T.tpmlp_moe_matmul_dw(x, src, off, other, *out, tokens, rows, e, K, N)
+        return out
+
+    for at in (0, rows):
+        for o in call(torch.full((e + 1,), at, dtype=I32, device="cuda")):
+            assert (o == (0.0 if op == "dw" else 7.0)).all()
+    # the last rows on two experts, those ahead on none
+    first = rows - min(rows, 41)
+    mid = (first + rows) // 2
+    off = torch.tensor([first] * (e // 2 + 1) + [mid] * (e - e // 2 - 1) + [rows], dtype=I32, device="cuda")
+    off = off[: e + 1] if e > 1 else torch.tensor([first, rows], dtype=I32, device="cuda")
+    off[-1] = rows
+    got = call(off)
+    if op == "dw":
+        xs = x if src is None else x[src.long()]
+        ref, size, rb, sb = R.dw(xs, off, other, e)
+        R.close(got[0], ref, R.product_bound(41) * size, "dW")
+        R.close(got[1], rb, 64 * 2.0**-24 * sb, "dbias")
+    else:
+        for o in got:
+            assert (o[:first] == 7.0).all() and not (o[first:] == 7.0).all(1).any()
+    assert T.tpmlp_device_status(check=False) == T.OK
